@@ -425,6 +425,169 @@ long long moe_launch_count(void);
  */
 moe_status moe_selftest_wait_timeout(void* ws, size_t ws_bytes, int limit_us, void* stream);
 
+/*
+ * ---------------------------------------------------------------- around the experts
+ * The operators of a routed-expert block next to the experts themselves:
+ * scored routing, the norms with the residual stream, dense products, and
+ * the gradient of each.  The conventions at the top of this file hold.  Row
+ * strides (ld_*) count elements and may exceed the row length, so that a
+ * slice of columns of a larger matrix can be passed.
+ */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1 } moe_dtype;
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/*
+ * moe_route_scored - router top-k over scores.
+ *   logits   device [T, E], fp32 or bf16, rows ld_logits apart
+ *   score    s_e = softmax over all E (its normaliser summed by halves of
+ *            the index range, a fixed order) or 1 / (1 + exp(-l_e)); fp32
+ *   bias     device fp32 [E] or NULL: choice c_e = s_e + bias_e in fp32.  It
+ *            moves the choice only, never the weights.  An expert whose
+ *            logit is -inf or NaN, or whose bias is -inf or NaN, is masked
+ *            (c_e = -inf).
+ *   n_group  > 1: the experts form n_group groups of E / n_group neighbours;
+ *            a group's score is the sum of its group_top (1 or 2) largest
+ *            unmasked c_e, and only the topk_group best groups (equal
+ *            scores: the lower group) keep their c_e, the others' is -inf
+ *   topk_idx device int32 [T, k] out: the k largest c_e in descending order,
+ *            equal ones by ascending expert index
+ *   topk_w   device fp32 [T, k] out: the chosen s_e (0 where c_e = -inf); if
+ *            renormalise != 0 divided by their sum (1/k in every slot where
+ *            that sum is 0); then times scale
+ * 1 <= k <= min(E, 32), E <= 1024, n_group <= 32 divides E, 1 <= topk_group <=
+ * n_group, topk_group * (E / n_group) >= k (else MOE_ERR_UNSUPPORTED).
+ * T = 0 is a no-op.
+ */
+moe_status moe_route_scored(const void* logits, moe_dtype dt, int64_t ld_logits, int T, int E,
+                            int k, moe_score score, const float* bias, int n_group,
+                            int topk_group, int group_top, int renormalise, float scale,
+                            int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
+ * moe_route_scored_backward - gradient of topk_w with respect to the logits.
+ *   logits, score, bias, renormalise, scale   as passed to moe_route_scored
+ *   topk_idx, topk_w   what it returned (the indices of a row distinct)
+ *   grad_w        device fp32 [T, k]: dL/d topk_w
+ *   grad_logits   device [T, E] of the logits' type, rows ld_grad apart, out:
+ *                 fully written.  The choice itself has no gradient; a slot
+ *                 whose weight is 0, whose expert is masked or whose index is
+ *                 outside [0, E) contributes none.
+ */
+moe_status moe_route_scored_backward(const void* logits, moe_dtype dt, int64_t ld_logits, int T,
+                                     int E, int k, moe_score score, const float* bias,
+                                     int renormalise, float scale, const int32_t* topk_idx,
+                                     const float* topk_w, const float* grad_w,
+                                     void* grad_logits, int64_t ld_grad, void* stream);
+
+/* What a block's gate has one value for.  The gate multiplies the block's
+ * (normed) output before it joins the residual stream. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1, /* [H]    */
+  MOE_GATE_TOKEN = 2,   /* [T]    */
+  MOE_GATE_ELEMENT = 3  /* [T, H] */
+} moe_gate;
+
+/*
+ * moe_block_norm - the norm after a block, its gate and residual scale, the
+ * residual sum and the norm before the next block in one pass:
+ *   z = post_norm ? y / rms(y) * post_weight : y
+ *   residual_out = residual + scale * gate * z
+ *   normed       = residual_out / rms(residual_out) * pre_weight
+ * with rms(v) = sqrt(mean(v^2) + eps) over a row.  Sums and residual_out are
+ * held in fp32 and rounded once on their way out; normed is made from the
+ * unrounded residual_out.
+ *   residual      device [T, H], bf16 or fp32 (res_dt)
+ *   y             device bf16 [T, H], or NULL: residual_out = residual is not
+ *                 written, only normed is
+ *   gate          device bf16 or fp32 (gate_dt), shape by gate_kind; NULL for
+ *                 MOE_GATE_NONE.  ld_gate only for MOE_GATE_ELEMENT.
+ *   post_weight, pre_weight   device [H] bf16 or fp32 (weight_dt), or NULL: 1
+ *   residual_out  device [T, H] of residual's type, rows H apart; may be
+ *                 residual itself where ld_res = H
+ *   normed        device bf16 [T, H], rows H apart; NULL iff pre_norm == 0
+ * 1 <= H <= 16384 (else MOE_ERR_UNSUPPORTED), any strides >= H, buffers
+ * aligned to 16 bytes; rows that are not (H or a stride not a multiple of 8)
+ * take a path of narrower loads.  T = 0 is a no-op.
+ */
+moe_status moe_block_norm(const void* residual, moe_dtype res_dt, int64_t ld_res, const void* y,
+                          int64_t ld_y, const void* gate, moe_gate gate_kind, moe_dtype gate_dt,
+                          int64_t ld_gate, float scale, int post_norm, const void* post_weight,
+                          int pre_norm, const void* pre_weight, moe_dtype weight_dt, float eps,
+                          int T, int H, void* residual_out, void* normed, void* stream);
+
+/*
+ * moe_block_norm_backward - gradients of moe_block_norm.
+ *   grad_residual  dL/d residual_out, of res_dt, or NULL (zero)
+ *   grad_normed    dL/d normed, bf16, or NULL (no norm before the next block)
+ *   residual       the residual_out that was stored (NULL iff grad_normed is)
+ *   y, gate, scale, post_norm, post_weight, pre_weight, eps  as in the forward
+ *   d_residual     out, dL/d residual, of res_dt, rows H apart; or NULL.  May be
+ *                  grad_residual itself where ld_gres = H
+ *   d_y            out, bf16 [T, H]; required with y
+ *   d_gate         out: fp32 [H] for MOE_GATE_CHANNEL (summed over tokens), else
+ *                  the gate's type and shape
+ *   d_post_weight, d_pre_weight   out, fp32 [H], summed over tokens; or NULL
+ *   ws             at least moe_block_norm_backward_workspace_size(H) bytes,
+ *                  256-byte aligned (partial sums; its first 256 bytes, a
+ *                  workspace's error words, are left alone)
+ * The sums over tokens are added in a fixed order.  T = 0 writes zeros to them.
+ */
+size_t moe_block_norm_backward_workspace_size(int H);
+moe_status moe_block_norm_backward(const void* grad_residual, int64_t ld_gres,
+                                   const void* grad_normed, int64_t ld_gn, const void* residual,
+                                   moe_dtype res_dt, int64_t ld_res, const void* y, int64_t ld_y,
+                                   const void* gate, moe_gate gate_kind, moe_dtype gate_dt,
+                                   int64_t ld_gate, float scale, int post_norm,
+                                   const void* post_weight, const void* pre_weight,
+                                   moe_dtype weight_dt, float eps, int T, int H,
+                                   void* d_residual, void* d_y, void* d_gate,
+                                   float* d_post_weight, float* d_pre_weight, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Activation argument of the linear operators: a moe_activation, or none. */
+#define MOE_ACT_NONE (-1)
+
+/*
+ * moe_linear - out = residual + act(x w^T + bias).
+ *   x         device bf16 [T, K];  w  device bf16 [N, K]
+ *   bias      device [N] bf16 or fp32 (bias_dt), or NULL
+ *   act       MOE_ACT_NONE, or a moe_activation applied to x w^T + bias
+ *   residual  device [T, N] of out's type, or NULL; may be out itself
+ *   out       device [T, N] bf16 or fp32 (out_dt), rounded once from fp32
+ *   preact    device [T, N] of out's type and row stride, or NULL: out,
+ *             x w^T + bias (what the backward pass of an activation needs)
+ *   ws        device scratch, 256-byte aligned, at least 256 bytes: only its
+ *             error word is used, as in moe_experts_forward
+ * K % 8 == 0 and strides of x and w multiples of 8 (16-byte rows), else
+ * MOE_ERR_UNSUPPORTED; any T, N.  T = 0 or N = 0 is a no-op.
+ */
+moe_status moe_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, const void* bias,
+                      moe_dtype bias_dt, int act, const void* residual, int64_t ld_res, int T,
+                      int K, int N, void* out, moe_dtype out_dt, int64_t ld_out, void* preact,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_linear_backward - gradients of moe_linear.  With dz = grad_y *
+ * act'(preact): dx = dz w, dw = dz^T x, dbias = sum over tokens of dz; the
+ * residual's gradient is grad_y itself.  dz enters the two products rounded
+ * to bf16, and dbias unrounded.
+ *   grad_y   device [T, N] of the forward's out type (y_dt)
+ *   preact   device [T, N] of that type, as moe_linear stored it; NULL iff
+ *            act is MOE_ACT_NONE
+ *   dx       out, bf16 [T, K], rows K apart, or NULL
+ *   dw       out, bf16 [N, K], rows K apart, or NULL
+ *   dbias    out, fp32 [N], or NULL
+ *   ws       at least moe_linear_backward_workspace_size() bytes, 256-byte
+ *            aligned, head as above
+ * The same requirements as moe_linear.  T = 0 writes zeros to dw and dbias.
+ */
+size_t moe_linear_backward_workspace_size(int T, int N);
+moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy, const void* x,
+                               int64_t ld_x, const void* w, int64_t ld_w, int act,
+                               const void* preact, int64_t ld_z, int T, int K, int N, void* dx,
+                               void* dw, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

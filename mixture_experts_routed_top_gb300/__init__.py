@@ -24,6 +24,7 @@ __all__ = [
     "get_block_scaled_mma", "set_fp4_gemv_rows", "get_fp4_gemv_rows", "set_decode_single",
     "get_decode_single", "set_tile_group", "get_tile_group", "set_pair_gemm", "get_pair_gemm", "set_down_l2_hints", "get_down_l2_hints", "set_down_phases",
     "get_down_phases",
+    "route_scored", "route_scored_backward", "block_norm", "block_norm_backward", "linear", "linear_backward",
     "Workspace", "STATUS", "STAGES", "W_BF16", "W_FP8_E4M3", "W_FP4_E2M1", "SCALE_NONE", "SCALE_F32",
     "SCALE_UE8M0", "ACTIVATIONS",
 ]
@@ -45,6 +46,7 @@ class MoEError(RuntimeError):
 
 _LIB = None
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F = ctypes.c_int64, ctypes.c_float
 _SIGS = {
     "moe_version": ([], _I),
     "moe_last_error": ([], ctypes.c_char_p),
@@ -83,6 +85,17 @@ _SIGS = {
     "moe_get_decode_single": ([], _I),
     "moe_set_fp4_gemv_rows": ([_I], None),
     "moe_get_fp4_gemv_rows": ([], _I),
+    "moe_route_scored": ([_P, _I, _L, _I, _I, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P, _P], _I),
+    "moe_route_scored_backward": ([_P, _I, _L, _I, _I, _I, _I, _P, _I, _F, _P, _P, _P, _P, _L, _P], _I),
+    "moe_block_norm": ([_P, _I, _L, _P, _L, _P, _I, _I, _L, _F, _I, _P, _I, _P, _I, _F, _I, _I, _P,
+                        _P, _P], _I),
+    "moe_block_norm_backward_workspace_size": ([_I], _SZ),
+    "moe_block_norm_backward": ([_P, _L, _P, _L, _P, _I, _L, _P, _L, _P, _I, _I, _L, _F, _I, _P, _P,
+                                 _I, _F, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "moe_linear": ([_P, _L, _P, _L, _P, _I, _I, _P, _L, _I, _I, _I, _P, _I, _L, _P, _P, _SZ, _P], _I),
+    "moe_linear_backward_workspace_size": ([_I, _I], _SZ),
+    "moe_linear_backward": ([_P, _I, _L, _P, _L, _P, _L, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _SZ,
+                             _P], _I),
 }
 
 
@@ -268,6 +281,325 @@ def default_workspace(device="cuda") -> Workspace:
     if d.index is None:
         d = torch.device("cuda", torch.cuda.current_device())
     return _DEFAULT_WS.setdefault(d, Workspace(d))
+
+
+# ------------------------------------------------------------------ around the experts
+# Activations, logits and their gradients may have rows further apart than
+# they are long (a slice of columns of a larger matrix); everything else is
+# contiguous.  Each call is asynchronous on the current stream (or stream=).
+_BF16, _F32 = torch.bfloat16, torch.float32
+_DT = {_BF16: 0, _F32: 1}
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_ACT_NONE = -1
+
+
+def _mat(name: str, t: torch.Tensor, dtypes, rows: Optional[int] = None, cols: Optional[int] = None) -> int:
+    """Checks a CUDA matrix whose rows are contiguous; -> its row stride."""
+    if not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d)[6:] for d in dtypes)}")
+    n, c = t.shape
+    if (rows is not None and n != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must be [{rows if rows is not None else n}, {cols if cols is not None else c}], "
+                         f"not {list(t.shape)}")
+    sn, sc = t.stride()
+    if sc != 1 and c > 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return sn if n > 1 else max(c, 1)
+
+
+def _vec(name: str, t: Optional[torch.Tensor], dtypes, n: int):
+    if t is not None and (not t.is_cuda or t.dtype not in dtypes or t.dim() != 1 or t.shape[0] != n
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor [{n}] of {' or '.join(str(d)[6:] for d in dtypes)}")
+
+
+def _same_device(device, *ts):
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _out(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
+    """A contiguous output: the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on {device}")
+    return t
+
+
+def _p(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+class _on:
+    """The device of a call's tensors made current around it."""
+
+    __slots__ = ("prev",)
+
+    def __init__(self, device):
+        cur = torch.cuda.current_device()
+        self.prev = None if device.index == cur else cur
+        if self.prev is not None:
+            torch.cuda.set_device(device)
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+
+
+def _workspace(workspace: Optional[Workspace], device, nbytes: int) -> torch.Tensor:
+    if workspace is None:
+        workspace = _DEFAULT_WS.get(device)
+        if workspace is None:
+            workspace = _DEFAULT_WS.setdefault(device, Workspace(device))
+    return workspace.get(nbytes)
+
+
+def route_scored(logits: torch.Tensor, k: int, *, score: str = "sigmoid",
+                 bias: Optional[torch.Tensor] = None, n_group: int = 1, topk_group: int = 1,
+                 group_top: int = 2, renormalise: bool = True, scale: float = 1.0,
+                 out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Top-k routing by scores -> (topk_idx int32 [T,k], topk_w fp32 [T,k]).
+
+    logits fp32 or bf16 [T,E]; score 'sigmoid' or 'softmax'; bias fp32 [E],
+    added to the scores for the choice only; n_group > 1: only the topk_group
+    best groups are eligible, a group's score being the sum of its group_top
+    (1 or 2) best; the chosen scores are divided by their sum if renormalise,
+    then multiplied by scale.  Experts with a logit of -inf or NaN are masked.
+    out: (topk_idx, topk_w) to write into."""
+    ld = _mat("logits", logits, (_F32, _BF16))
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _vec("bias", bias, (_F32,), E)
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    idx = _out("topk_idx", None if out is None else out[0], (T, k), torch.int32, dev)
+    w = _out("topk_w", None if out is None else out[1], (T, k), _F32, dev)
+    _same_device(dev, bias)
+    with _on(dev):
+        _check(lib().moe_route_scored(logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _SCORES[score],
+                                      _p(bias), n_group, topk_group, group_top, bool(renormalise), scale,
+                                      idx.data_ptr(), w.data_ptr(), _stream(stream)))
+    return idx, w
+
+
+def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                          grad_w: torch.Tensor, *, score: str = "sigmoid",
+                          bias: Optional[torch.Tensor] = None, renormalise: bool = True,
+                          scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """Gradient of route_scored's weights -> grad_logits [T,E] of the logits' type.
+
+    logits, score, bias, renormalise, scale as route_scored was called with;
+    topk_idx, topk_w what it returned; grad_w fp32 [T,k]."""
+    ld = _mat("logits", logits, (_F32, _BF16))
+    T, E = logits.shape
+    dev = logits.device
+    _need_cuda(topk_idx, topk_w, grad_w)
+    k = topk_idx.shape[1] if topk_idx.dim() == 2 else 0
+    for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_w", topk_w, _F32), ("grad_w", grad_w, _F32)):
+        if t.dtype != dt or t.shape != (T, k):
+            raise ValueError(f"{name} must be {str(dt)[6:]} [T, k]")
+    _vec("bias", bias, (_F32,), E)
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    g = _out("out", out, (T, E), logits.dtype, dev)
+    _same_device(dev, topk_idx, topk_w, grad_w, bias)
+    with _on(dev):
+        _check(lib().moe_route_scored_backward(
+            logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _SCORES[score], _p(bias), bool(renormalise),
+            scale, topk_idx.data_ptr(), topk_w.data_ptr(), grad_w.data_ptr(), g.data_ptr(), max(E, 1),
+            _stream(stream)))
+    return g
+
+
+def _gate_of(gate: Optional[torch.Tensor], T: int, H: int):
+    """-> (moe_gate kind, dtype, row stride): [H] per channel, [T] or [T,1]
+    per token, [T,H] per element.  A 1-D gate where T = H is per channel."""
+    if gate is None:
+        return 0, 0, 0
+    if not gate.is_cuda or gate.dtype not in _DT:
+        raise ValueError("gate must be a CUDA tensor of bfloat16 or float32")
+    dt, shape = _DT[gate.dtype], gate.shape
+    if gate.dim() == 2 and shape[0] == T and shape[1] == H and H != 1:
+        return 3, dt, _mat("gate", gate, (gate.dtype,), T, H)
+    if not gate.is_contiguous():
+        raise ValueError("gate must be contiguous")
+    if shape == (H,):
+        return 1, dt, 0
+    if shape == (T,) or shape == (T, 1):
+        return 2, dt, 0
+    raise ValueError("gate must be [H] (per channel), [T] or [T, 1] (per token), or [T, H]")
+
+
+def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+               gate: Optional[torch.Tensor] = None, scale: float = 1.0, post_norm: bool = False,
+               post_weight: Optional[torch.Tensor] = None, pre_norm: bool = True,
+               pre_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               out: Optional[Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]] = None,
+               stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """The norms after and before a block in one pass -> (residual_out, normed).
+
+    z = y / rms(y) * post_weight if post_norm else y;
+    residual_out = residual + scale * gate * z;
+    normed = residual_out / rms(residual_out) * pre_weight, or None if not pre_norm.
+
+    residual bf16 or fp32 [T,H] (residual_out alike); y bf16 [T,H], or None:
+    only the norm, and residual itself is returned; normed bf16; gate [H],
+    [T] / [T,1] or [T,H], bf16 or fp32; weights [H], both bf16 or both fp32.
+    out: (residual_out, normed) to write into; residual_out may be residual."""
+    ld_r = _mat("residual", residual, (_BF16, _F32))
+    T, H = residual.shape
+    dev = residual.device
+    ld_y = 0 if y is None else _mat("y", y, (_BF16,), T, H)
+    kind, gate_dt, ld_g = _gate_of(gate, T, H)
+    wdt = None
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None:
+            _vec(name, t, (_BF16, _F32), H)
+            if wdt is not None and t.dtype != wdt:
+                raise ValueError("post_weight and pre_weight must have one dtype")
+            wdt = t.dtype
+    _same_device(dev, y, gate, post_weight, pre_weight)
+    res = residual if y is None else _out("residual_out", None if out is None else out[0], (T, H), residual.dtype, dev)
+    n = _out("normed", None if out is None else out[1], (T, H), _BF16, dev) if pre_norm else None
+    with _on(dev):
+        _check(lib().moe_block_norm(
+            residual.data_ptr(), _DT[residual.dtype], ld_r, _p(y), ld_y, _p(gate), kind, gate_dt, ld_g, scale,
+            bool(post_norm), _p(post_weight), bool(pre_norm), _p(pre_weight), 0 if wdt is None else _DT[wdt],
+            eps, T, H, None if y is None else res.data_ptr(), _p(n), _stream(stream)))
+    return res, n
+
+
+def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Optional[torch.Tensor],
+                        residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                        gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                        post_norm: bool = False, post_weight: Optional[torch.Tensor] = None,
+                        pre_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        workspace: Optional[Workspace] = None, stream=None):
+    """Gradients of block_norm -> (d_residual, d_y, d_gate, d_post_weight, d_pre_weight).
+
+    grad_residual: dL/d residual_out [T,H] or None; grad_normed: dL/d normed
+    bf16 [T,H], or None where pre_norm was off; residual: the residual_out that
+    block_norm returned; the rest as it was called with.  What does not apply
+    comes back as None.  d_gate is fp32 for a per-channel gate, else of the
+    gate's type; the weights' gradients are fp32 [H]."""
+    ld_r = _mat("residual", residual, (_BF16, _F32))
+    T, H = residual.shape
+    dev = residual.device
+    ld_gr = 0 if grad_residual is None else _mat("grad_residual", grad_residual, (residual.dtype,), T, H)
+    ld_gn = 0 if grad_normed is None else _mat("grad_normed", grad_normed, (_BF16,), T, H)
+    ld_y = 0 if y is None else _mat("y", y, (_BF16,), T, H)
+    kind, gate_dt, ld_g = _gate_of(gate, T, H)
+    wdt = None
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None:
+            _vec(name, t, (_BF16, _F32), H)
+            if wdt is not None and t.dtype != wdt:
+                raise ValueError("post_weight and pre_weight must have one dtype")
+            wdt = t.dtype
+    _same_device(dev, grad_residual, grad_normed, y, gate, post_weight, pre_weight)
+    d_res = torch.empty(T, H, dtype=residual.dtype, device=dev)
+    d_y = None if y is None else torch.empty(T, H, dtype=_BF16, device=dev)
+    d_gate = None
+    if gate is not None:
+        d_gate = torch.empty(gate.shape, dtype=_F32 if kind == 1 else gate.dtype, device=dev)
+    d_post = torch.empty(H, dtype=_F32, device=dev) if post_weight is not None else None
+    d_pre = torch.empty(H, dtype=_F32, device=dev) if pre_weight is not None else None
+    L = lib()
+    with _on(dev):
+        ws = _workspace(workspace, dev, L.moe_block_norm_backward_workspace_size(H))
+        _check(L.moe_block_norm_backward(
+            _p(grad_residual), ld_gr, _p(grad_normed), ld_gn,
+            residual.data_ptr() if grad_normed is not None else None, _DT[residual.dtype], ld_r, _p(y), ld_y,
+            _p(gate), kind, gate_dt, ld_g, scale, bool(post_norm), _p(post_weight), _p(pre_weight),
+            0 if wdt is None else _DT[wdt], eps, T, H, d_res.data_ptr(), _p(d_y), _p(d_gate), _p(d_post),
+            _p(d_pre), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return d_res, d_y, d_gate, d_post, d_pre
+
+
+def _act(activation: Optional[str]) -> int:
+    if activation is None:
+        return _ACT_NONE
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be None or one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[activation]
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+           activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+           out_dtype: torch.dtype = torch.bfloat16, preact: bool = False,
+           out: Optional[torch.Tensor] = None, workspace: Optional[Workspace] = None, stream=None):
+    """residual + act(x w^T + bias) -> [T,N], or (that, x w^T + bias) if preact.
+
+    x bf16 [T,K]; w bf16 [N,K]; K a multiple of 8; bias [N] bf16 or fp32;
+    activation None, 'silu', 'gelu' (exact) or 'relu'; out_dtype bf16 or fp32
+    (router logits), which residual and the pre-activation share.  out: the
+    tensor to write into (rows contiguous); it may be residual."""
+    ld_x = _mat("x", x, (_BF16,))
+    T, K = x.shape
+    ld_w = _mat("w", w, (_BF16,), None, K)
+    N = w.shape[0]
+    dev = x.device
+    if bias is not None:
+        _vec("bias", bias, (_BF16, _F32), N)
+    act = _act(activation)
+    if out is None:
+        out = torch.empty(T, N, dtype=out_dtype, device=dev)
+    dt = out.dtype
+    ld_o = _mat("out", out, (_BF16, _F32), T, N)
+    ld_r = 0 if residual is None else _mat("residual", residual, (dt,), T, N)
+    # the pre-activation has out's row stride
+    z = torch.empty_strided((T, N), (ld_o, 1), dtype=dt, device=dev) if preact else None
+    _same_device(dev, w, bias, residual, out)
+    with _on(dev):
+        ws = _workspace(workspace, dev, 1024)
+        _check(lib().moe_linear(
+            x.data_ptr(), ld_x, w.data_ptr(), ld_w, _p(bias), 0 if bias is None else _DT[bias.dtype], act,
+            _p(residual), ld_r, T, K, N, out.data_ptr(), _DT[dt], ld_o, _p(z), ws.data_ptr(), ws.numel(),
+            _stream(stream)))
+    return (out, z) if preact else out
+
+
+def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
+                    bias: Optional[torch.Tensor] = None, activation: Optional[str] = None,
+                    preact: Optional[torch.Tensor] = None, need_x: bool = True, need_w: bool = True,
+                    workspace: Optional[Workspace] = None, stream=None):
+    """Gradients of linear -> (dx bf16 [T,K], dw bf16 [N,K], dbias fp32 [N]).
+
+    grad_y [T,N] of linear's output type (it is also the residual's gradient);
+    preact: what linear(..., preact=True) returned, with an activation; bias:
+    as passed to linear (None: dbias is None).  need_x / need_w = False leave
+    that gradient out (None)."""
+    ld_x = _mat("x", x, (_BF16,))
+    T, K = x.shape
+    ld_w = _mat("w", w, (_BF16,), None, K)
+    N = w.shape[0]
+    dev = x.device
+    ld_g = _mat("grad_y", grad_y, (_BF16, _F32), T, N)
+    act = _act(activation)
+    if (preact is None) != (act == _ACT_NONE):
+        raise ValueError("an activation and its preact go together")
+    ld_z = 0 if preact is None else _mat("preact", preact, (grad_y.dtype,), T, N)
+    if bias is not None:
+        _vec("bias", bias, (_BF16, _F32), N)
+    _same_device(dev, grad_y, w, preact, bias)
+    dx = torch.empty(T, K, dtype=_BF16, device=dev) if need_x else None
+    dw = torch.empty(N, K, dtype=_BF16, device=dev) if need_w else None
+    db = torch.empty(N, dtype=_F32, device=dev) if bias is not None else None
+    L = lib()
+    with _on(dev):
+        ws = _workspace(workspace, dev, L.moe_linear_backward_workspace_size(T, N))
+        _check(L.moe_linear_backward(
+            grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(), ld_w, act,
+            _p(preact), ld_z, T, K, N, _p(dx), _p(dw), _p(db), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return dx, dw, db
 
 
 # ------------------------------------------------------------------ FP8

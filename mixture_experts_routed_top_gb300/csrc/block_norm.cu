@@ -1,0 +1,422 @@
+// The norms after and before a block in one pass, with the block's gate and
+// residual scale, and their gradient.
+//
+// Forward, for one token's stream r, block output y [H]:
+//   z  = y / rms(y) * w_post            (or y: no norm after the block)
+//   r' = r + scale * g * z              g: per channel, per token, per element or 1
+//   n  = r' / rms(r') * w_pre           rms(v) = sqrt(mean v^2 + eps)
+// r' and n leave rounded once each; n is made from the unrounded r'.
+//
+// Backward, from dL/dr' (dr) and dL/dn (dn), with the r' that was stored:
+//   q   = dn * w_pre / rms(r'),   d  = dr + q - r' mean(q r') / rms(r')^2   (dL/dr)
+//   dz  = scale * g * d,          dg = scale * z * d, summed over what shares g
+//   q2  = dz * w_post / rms(y),   dy = q2 - y mean(q2 y) / rms(y)^2
+//   dw_pre = sum_t dn r' / rms(r'),   dw_post = sum_t dz y / rms(y)
+// The norms' statistics are computed again from the rows, which have to be
+// read anyway: two more sums in reductions that run in any case, against
+// storing and loading them.
+//
+// Both are bound by memory: a row is read once into registers, every
+// reduction runs over the registers, and sums are held in fp32.
+#include <math.h>
+
+#include "moe_device.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+// Eight consecutive elements of a row as floats.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint4 u;
+  u.x = pack_bf16x2(v[0], v[1]);
+  u.y = pack_bf16x2(v[2], v[3]);
+  u.z = pack_bf16x2(v[4], v[5]);
+  u.w = pack_bf16x2(v[6], v[7]);
+  *reinterpret_cast<uint4*>(p) = u;
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ float get(const float* p) { return *p; }
+__device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// The columns of a row that a thread holds: NV pieces of 8.  VEC: piece v is
+// columns 8 (tx + TX v) .. +7, moved in 16-byte vectors (H % 8 == 0, rows
+// 16-byte aligned); otherwise single columns TX apart, for any H and stride.
+template <bool VEC, int NV>
+struct Cols {
+  int tx, TX, H;
+  __device__ __forceinline__ int col(int v, int e) const {
+    return VEC ? (tx + TX * v) * 8 + e : tx + TX * (v * 8 + e);
+  }
+  template <typename T>
+  __device__ __forceinline__ void load(const T* row, int v, float (&x)[8], float fill) const {
+    if (VEC) {
+      if (col(v, 0) < H) {
+        load8(row + col(v, 0), x);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fill;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = col(v, e) < H ? get(row + col(v, e)) : fill;
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(T* row, int v, const float (&x)[8]) const {
+    if (VEC) {
+      if (col(v, 0) < H) store8(row + col(v, 0), x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col(v, e) < H) put(row + col(v, e), x[e]);
+    }
+  }
+  // a vector of fp32 or bf16 weights (16-byte aligned where VEC)
+  __device__ __forceinline__ void load_any(const void* p, bool bf16, int v, float (&x)[8],
+                                           float fill) const {
+    if (bf16) load(static_cast<const __nv_bfloat16*>(p), v, x, fill);
+    else load(static_cast<const float*>(p), v, x, fill);
+  }
+};
+
+// Sums of N values over the TX threads of one row (TX a multiple of 32; the
+// block's other rows take part in the barriers).  Every thread gets the
+// same bits: the warps' sums are added in warp order.
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* s_red, int warps, int row_warp0) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], off);
+  if (warps == 1) return;
+  const int warp = (threadIdx.x + threadIdx.y * blockDim.x) >> 5;
+  __syncthreads();  // the previous sums have been read
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) s_red[warp * N + n] = v[n];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = 0.f;
+  for (int w = 0; w < warps; ++w)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += s_red[(row_warp0 + w) * N + n];
+}
+
+constexpr int kMaxRed = 32 * 4;  // warps of a block x values of a reduction
+
+template <typename RT, bool VEC, int NV>
+__global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a) {
+  pdl_launch_dependents();
+  __shared__ float s_red[kMaxRed];
+  const Cols<VEC, NV> c{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.H};
+  const int warps = blockDim.x >> 5, warp0 = threadIdx.y * warps;
+  const float inv_h = 1.f / static_cast<float>(a.H);
+  pdl_wait();
+  const long t_raw = static_cast<long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool on = t_raw < a.T;  // a row past the end still meets the barriers
+  const long t = on ? t_raw : a.T - 1;
+  const RT* r_in = static_cast<const RT*>(a.residual) + t * a.ld_res;
+  const __nv_bfloat16* y_in =
+      a.y ? static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y : nullptr;
+  float r[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) c.load(r_in, v, r[v], 0.f);
+  if (y_in != nullptr) {
+    float y[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) c.load(y_in, v, y[v], 0.f);
+    float coef = a.scale;
+    if (a.gate_kind == MOE_GATE_TOKEN)
+      coef *= a.gate_bf16 ? get(static_cast<const __nv_bfloat16*>(a.gate) + t)
+                          : get(static_cast<const float*>(a.gate) + t);
+    float rstd = 1.f;
+    if (a.post_norm) {
+      float sum[1] = {0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[0] += y[v][e] * y[v][e];
+      row_sums<1>(sum, s_red, warps, warp0);
+      rstd = rsqrtf(sum[0] * inv_h + a.eps);
+    }
+    coef *= rstd;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float m[8];
+      if (a.post_norm && a.post_weight != nullptr) {
+        c.load_any(a.post_weight, a.weight_bf16, v, m, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[v][e] *= m[e];
+      }
+      if (a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_ELEMENT) {
+        const long off = a.gate_kind == MOE_GATE_ELEMENT ? t * a.ld_gate : 0;
+        const void* g = a.gate_bf16
+                            ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.gate) + off)
+                            : static_cast<const void*>(static_cast<const float*>(a.gate) + off);
+        c.load_any(g, a.gate_bf16, v, m, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[v][e] *= m[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[v][e] += coef * y[v][e];
+      if (on) c.store(static_cast<RT*>(a.residual_out) + t * a.H, v, r[v]);
+    }
+  }
+  if (a.pre_norm) {
+    float sum[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[0] += r[v][e] * r[v][e];
+    row_sums<1>(sum, s_red, warps, warp0);
+    const float rstd = rsqrtf(sum[0] * inv_h + a.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float m[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r[v][e] *= rstd;
+      if (a.pre_weight != nullptr) {
+        c.load_any(a.pre_weight, a.weight_bf16, v, m, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] *= m[e];
+      }
+      if (on) c.store(static_cast<__nv_bfloat16*>(a.normed) + t * a.H, v, r[v]);
+    }
+  }
+}
+
+// Backward.  One block per row at a time, blocks striding over the rows;
+// each thread keeps the sums over its rows for its own columns (dw_pre,
+// dw_post and a per-channel dg) and leaves them as one partial row per
+// block; block_norm_partials_kernel adds those in block order, so the
+// result does not depend on timing.
+template <typename RT, bool VEC, int NV>
+__global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNormBwdArgs a) {
+  pdl_launch_dependents();
+  __shared__ float s_red[kMaxRed];
+  const Cols<VEC, NV> c{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.H};
+  const int warps = blockDim.x >> 5;
+  const float inv_h = 1.f / static_cast<float>(a.H);
+  float acc_pre[NV][8] = {}, acc_post[NV][8] = {}, acc_gate[NV][8] = {};
+  pdl_wait();
+  for (long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    float d[NV][8], r[NV][8];
+    if (a.grad_res != nullptr) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        c.load(static_cast<const RT*>(a.grad_res) + t * a.ld_gres, v, d[v], 0.f);
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[v][e] = 0.f;
+    }
+    if (a.grad_normed != nullptr) {
+      float q[NV][8], sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float m[8];
+        c.load(static_cast<const RT*>(a.residual) + t * a.ld_res, v, r[v], 0.f);
+        c.load(static_cast<const __nv_bfloat16*>(a.grad_normed) + t * a.ld_gn, v, q[v], 0.f);
+        if (a.pre_weight != nullptr) c.load_any(a.pre_weight, a.weight_bf16, v, m, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          sum[0] += r[v][e] * r[v][e];
+          sum[1] += q[v][e] * r[v][e] * (a.pre_weight != nullptr ? m[e] : 1.f);
+        }
+      }
+      row_sums<2>(sum, s_red, warps, 0);
+      const float rstd = rsqrtf(sum[0] * inv_h + a.eps);
+      const float corr = sum[1] * inv_h * rstd * rstd * rstd;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float m[8];
+        if (a.pre_weight != nullptr) c.load_any(a.pre_weight, a.weight_bf16, v, m, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float qn = q[v][e] * rstd;
+          acc_pre[v][e] += qn * r[v][e];
+          d[v][e] += qn * (a.pre_weight != nullptr ? m[e] : 1.f) - r[v][e] * corr;
+        }
+      }
+    }
+    if (a.d_res != nullptr) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) c.store(static_cast<RT*>(a.d_res) + t * a.H, v, d[v]);
+    }
+    if (a.y == nullptr) continue;
+    // dz (without the gate and scale: coef and m below), and the sums
+    //   0: y^2   1: dz w_post y (the norm's projection)   2: z' d (a per-token dg)
+    float y[NV][8], sum[3] = {0.f, 0.f, 0.f};
+    float gt = 1.f;
+    if (a.gate_kind == MOE_GATE_TOKEN)
+      gt = a.gate_bf16 ? get(static_cast<const __nv_bfloat16*>(a.gate) + t)
+                       : get(static_cast<const float*>(a.gate) + t);
+    const long goff = a.gate_kind == MOE_GATE_ELEMENT ? t * a.ld_gate : 0;
+    const void* grow = a.gate_bf16
+                           ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.gate) + goff)
+                           : static_cast<const void*>(static_cast<const float*>(a.gate) + goff);
+    const bool gvec = a.gate_kind == MOE_GATE_CHANNEL || a.gate_kind == MOE_GATE_ELEMENT;
+    const bool pw = a.post_norm && a.post_weight != nullptr;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float m[8], w[8];
+      c.load(static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y, v, y[v], 0.f);
+      if (gvec) c.load_any(grow, a.gate_bf16, v, m, 0.f);
+      if (pw) c.load_any(a.post_weight, a.weight_bf16, v, w, 0.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float wd = d[v][e] * (pw ? w[e] : 1.f);
+        sum[0] += y[v][e] * y[v][e];
+        sum[2] += wd * y[v][e];
+        sum[1] += wd * y[v][e] * (gvec ? m[e] : 1.f);
+      }
+    }
+    float rstd = 1.f;
+    if (a.post_norm || a.gate_kind == MOE_GATE_TOKEN) row_sums<3>(sum, s_red, warps, 0);
+    if (a.post_norm) rstd = rsqrtf(sum[0] * inv_h + a.eps);
+    if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) {
+      const float dg = a.scale * rstd * sum[2];
+      if (a.gate_bf16) put(static_cast<__nv_bfloat16*>(a.d_gate) + t, dg);
+      else put(static_cast<float*>(a.d_gate) + t, dg);
+    }
+    const float coef = a.scale * gt * rstd;  // dL/d(y * w_post) per unit of g d
+    const float corr = a.post_norm ? sum[1] * inv_h * rstd * rstd * coef : 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float m[8], w[8], dgv[8];
+      if (gvec) c.load_any(grow, a.gate_bf16, v, m, 0.f);
+      if (pw) c.load_any(a.post_weight, a.weight_bf16, v, w, 0.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float gd = d[v][e] * (gvec ? m[e] : 1.f) * coef;
+        const float wv = pw ? w[e] : 1.f;
+        dgv[e] = a.scale * rstd * y[v][e] * wv * d[v][e];
+        acc_post[v][e] += gd * y[v][e];
+        acc_gate[v][e] += dgv[e];
+        y[v][e] = gd * wv - y[v][e] * corr;
+      }
+      c.store(static_cast<__nv_bfloat16*>(a.d_y) + t * a.H, v, y[v]);
+      if (a.gate_kind == MOE_GATE_ELEMENT) {
+        if (a.gate_bf16) c.store(static_cast<__nv_bfloat16*>(a.d_gate) + t * a.H, v, dgv);
+        else c.store(static_cast<float*>(a.d_gate) + t * a.H, v, dgv);
+      }
+    }
+  }
+  float* part = a.partials + static_cast<long>(blockIdx.x) * a.n_part * a.H;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    int p = 0;
+    if (a.d_pre != nullptr) c.store(part + static_cast<long>(p++) * a.H, v, acc_pre[v]);
+    if (a.d_post != nullptr) c.store(part + static_cast<long>(p++) * a.H, v, acc_post[v]);
+    if (a.gate_kind == MOE_GATE_CHANNEL) c.store(part + static_cast<long>(p++) * a.H, v, acc_gate[v]);
+  }
+}
+
+// Sums of the blocks' partial rows: 32 columns x 8 slices of the blocks per
+// thread block, each slice added in block order, then the 8 slices in order.
+__global__ void __launch_bounds__(256)
+    block_norm_partials_kernel(const float* __restrict__ partials, int blocks, int n_part, int H,
+                               float* o0, float* o1, float* o2) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ float s[8][33];
+  const int x = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + x, p = blockIdx.y;
+  float sum = 0.f;
+  if (col < H)
+    for (int b = sl; b < blocks; b += 8)
+      sum += partials[(static_cast<long>(b) * n_part + p) * H + col];
+  s[sl][x] = sum;
+  __syncthreads();
+  if (sl == 0 && col < H) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) sum += s[i][x];
+    (p == 0 ? o0 : p == 1 ? o1 : o2)[col] = sum;
+  }
+}
+
+template <typename RT, bool VEC>
+cudaError_t fwd(const BlockNormArgs& a, cudaStream_t s) {
+  // one piece of 8 columns per thread up to 8192 columns, two above
+  const int pieces = ceil_div(a.H, 8);
+  const int nv = pieces <= 1024 ? 1 : 2;
+  const int tx = ceil_div(ceil_div(pieces, nv), 32) * 32;
+  const int ty = tx >= 256 ? 1 : 256 / tx;
+  const dim3 grid(ceil_div(a.T, ty)), block(tx, ty);
+  return nv == 1 ? launch_pdl(block_norm_kernel<RT, VEC, 1>, grid, block, 0, s, a)
+                 : launch_pdl(block_norm_kernel<RT, VEC, 2>, grid, block, 0, s, a);
+}
+
+template <typename RT, bool VEC>
+cudaError_t bwd(const BlockNormBwdArgs& a, int blocks, cudaStream_t s) {
+  const int pieces = ceil_div(a.H, 8);
+  const int nv = pieces <= 512 ? 1 : pieces <= 1024 ? 2 : 4;
+  const dim3 block(ceil_div(ceil_div(pieces, nv), 32) * 32);
+  if (nv == 1) return launch_pdl(block_norm_backward_kernel<RT, VEC, 1>, dim3(blocks), block, 0, s, a);
+  if (nv == 2) return launch_pdl(block_norm_backward_kernel<RT, VEC, 2>, dim3(blocks), block, 0, s, a);
+  return launch_pdl(block_norm_backward_kernel<RT, VEC, 4>, dim3(blocks), block, 0, s, a);
+}
+
+}  // namespace
+
+int block_norm_backward_blocks(long T, int num_sms) {
+  return static_cast<int>(T < 2L * num_sms ? T : 2L * num_sms);
+}
+
+cudaError_t launch_block_norm(const BlockNormArgs& a, bool res_bf16, bool vec, cudaStream_t s) {
+  cudaError_t e;
+  if (res_bf16) e = vec ? fwd<__nv_bfloat16, true>(a, s) : fwd<__nv_bfloat16, false>(a, s);
+  else e = vec ? fwd<float, true>(a, s) : fwd<float, false>(a, s);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_block_norm_backward(const BlockNormBwdArgs& a, bool res_bf16, bool vec,
+                                       int blocks, cudaStream_t s) {
+  cudaError_t e;
+  if (res_bf16)
+    e = vec ? bwd<__nv_bfloat16, true>(a, blocks, s) : bwd<__nv_bfloat16, false>(a, blocks, s);
+  else
+    e = vec ? bwd<float, true>(a, blocks, s) : bwd<float, false>(a, blocks, s);
+  count_launches(1);
+  if (e != cudaSuccess) return e;
+  if (a.n_part > 0) {
+    float* o[3] = {nullptr, nullptr, nullptr};
+    int p = 0;
+    if (a.d_pre != nullptr) o[p++] = a.d_pre;
+    if (a.d_post != nullptr) o[p++] = a.d_post;
+    if (a.gate_kind == MOE_GATE_CHANNEL) o[p++] = static_cast<float*>(a.d_gate);
+    e = launch_pdl(block_norm_partials_kernel, dim3(ceil_div(a.H, 32), a.n_part), dim3(256), 0, s,
+                   static_cast<const float*>(a.partials), blocks, a.n_part, a.H, o[0], o[1], o[2]);
+    count_launches(1);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace moe

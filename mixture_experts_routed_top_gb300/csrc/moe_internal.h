@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -300,5 +301,129 @@ cudaError_t launch_fp4_down(const Fp4DecodeArgs& a, cudaStream_t s);
 // bf16 [rows, cols] -> packed e2m1 [rows, cols/2] + UE8M0 bytes [rows, cols/32]
 cudaError_t launch_quantize_fp4(const void* w, long rows, int cols, uint8_t* q, uint8_t* scale,
                                 int num_sms, cudaStream_t s);
+
+// ---- operators around the experts: scored routing, block norms, linear
+// (route_scored.cu, block_norm.cu, linear.cu; entry points in block_abi.cu)
+moe_status cuda_error(cudaError_t e, const char* what);   // records and returns MOE_ERR_CUDA
+int device_sms();
+bool ptr_aligned(const void* p, size_t a);
+// 2-D bf16 matrix of `outer` rows of `inner` elements, `ld` elements apart;
+// box box_inner (64) x box_outer, 128-byte swizzle, zeros outside.
+moe_status make_map_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                            uint64_t ld, uint32_t box_inner, uint32_t box_outer);
+
+struct RouteScoredArgs {
+  const void* logits;
+  long ld;
+  const float* bias;       // or null
+  int T, E, k, n_group, topk_group, group_top;
+  bool softmax, renorm, vec;
+  float scale;
+  int32_t* idx;
+  float* w;
+};
+cudaError_t launch_route_scored(const RouteScoredArgs& a, bool bf16, cudaStream_t s);
+
+struct RouteScoredBwdArgs {
+  const void* logits;
+  long ld;
+  const int32_t* idx;
+  const float* w;
+  const float* grad_w;
+  const float* bias;       // or null
+  int T, E, k;
+  bool softmax, renorm, vec, vec_out;
+  float scale;
+  void* grad_logits;
+  long ldo;
+};
+cudaError_t launch_route_scored_backward(const RouteScoredBwdArgs& a, bool bf16, cudaStream_t s);
+
+struct BlockNormArgs {
+  const void* residual;
+  const void* y;
+  const void* gate;
+  const void* post_weight;
+  const void* pre_weight;
+  void* residual_out;      // [T, H], null without y
+  void* normed;            // [T, H], null without the norm before the next block
+  long ld_res, ld_y, ld_gate;
+  int T, H, gate_kind;
+  bool gate_bf16, weight_bf16, post_norm, pre_norm;
+  float scale, eps;
+};
+cudaError_t launch_block_norm(const BlockNormArgs& a, bool res_bf16, bool vec, cudaStream_t s);
+
+struct BlockNormBwdArgs {
+  const void* grad_res;    // or null
+  const void* grad_normed; // or null
+  const void* residual;    // the stored r'
+  const void* y;           // or null
+  const void* gate;
+  const void* post_weight;
+  const void* pre_weight;
+  void* d_res;
+  void* d_y;
+  void* d_gate;
+  float* d_post;
+  float* d_pre;
+  float* partials;         // [blocks, n_part, H]
+  long ld_gres, ld_gn, ld_res, ld_y, ld_gate;
+  int T, H, gate_kind, n_part;
+  bool gate_bf16, weight_bf16, post_norm;
+  float scale, eps;
+};
+constexpr int kNormMaxH = 16384;
+constexpr int kNormBwdBlocks = 304;   // most blocks of the backward pass (2 per SM of 152)
+int block_norm_backward_blocks(long T, int num_sms);
+cudaError_t launch_block_norm_backward(const BlockNormBwdArgs& a, bool res_bf16, bool vec,
+                                       int blocks, cudaStream_t s);
+
+// Epilogue of the linear kernels.
+struct LinearEpi {
+  const void* bias;        // [N] or null
+  const void* residual;    // [M, N] of the output's type, or null
+  void* out;
+  void* preact;            // [M, N] of the output's type and row stride, or null
+  long ld_res, ld_out;
+  int M, N, act;           // act: a moe_activation or MOE_ACT_NONE
+  bool bias_bf16, out_f32, vec;
+};
+struct LinearDev {
+  LinearEpi epi;
+  int K;                   // contraction length
+  int split, group;
+  int* err;
+};
+struct LinearPath {
+  bool pair;
+  int split;
+};
+LinearPath linear_path(long M, long N, long K, int num_sms);
+// D[M, N] = A B^T with the operands' orders (a_mn, b_mn: false, false /
+// false, true / true, true); the maps' boxes are those linear_boxes names.
+cudaError_t launch_linear(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const LinearDev& p,
+                          bool a_mn, bool b_mn, const LinearPath& path, cudaStream_t s);
+struct LinearGemvArgs {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* w;
+  long ld_x, ld_w;
+  int K;
+  LinearEpi epi;
+};
+constexpr int kLinearGemvRows = 8;    // tokens at or below: the weights stream through CUDA cores
+cudaError_t launch_linear_gemv(const LinearGemvArgs& a, int num_sms, cudaStream_t s);
+struct LinearDzArgs {
+  const void* dy;
+  const void* preact;      // null: dz = dy
+  __nv_bfloat16* dz;       // or null: only the column sums
+  float* partials;         // [slices, N] or null
+  long ld_dy, ld_z, ld_dz;
+  int T, N, act;
+  bool f32, vec;
+};
+constexpr int kLinearDzSlices = 608;
+int linear_dz_slices(long T, long N, int num_sms);
+cudaError_t launch_linear_dz(const LinearDzArgs& a, int slices, float* dbias, cudaStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,394 @@
+// Routing by scores: softmax or sigmoid scores of the router's logits, a
+// balance bias that moves the choice but not the weights, expert groups of
+// which only the best are eligible, top-k, weights renormalised and scaled;
+// and the gradient of the weights with respect to the logits.
+//
+// Forward, for one token with logits l_e:
+//   s_e = 1 / (1 + exp(-l_e))               sigmoid scores, or
+//   s_e = exp(l_e - max l) / S              softmax scores; S sums the E terms
+//         by halves (term i + term i + P/2, and so on, P = E rounded up to a
+//         power of two), a fixed tree, so the scores do not depend on how
+//         the terms are spread over threads
+//   c_e = s_e + b_e in 32 bits; -inf where the expert is masked (l_e or b_e
+//         -inf, or NaN)
+//   a group's score is the sum of its one or two largest live c_e; the
+//   topk_group best groups (ties: lower group) keep their c, the others' is
+//   -inf; the k largest c are taken, ties to the lower expert index
+//   w_j = s_j (0 where c_j = -inf), divided by their sum if renormalised
+//         (1/k each where that sum is 0), times scale
+// The scores use expf and IEEE division, not the fast forms: the choice
+// compares them bit by bit, so that a tie and a near-tie come out the same
+// in any implementation of the formulas in 32 bits.
+#include <math.h>
+
+#include "moe_device.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kWarps = 8;  // tokens (warps) per block
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_f(float v, float* o) { *o = v; }
+__device__ __forceinline__ void from_f(float v, __nv_bfloat16* o) { *o = __float2bfloat16_rn(v); }
+
+// Order-preserving map of floats (no NaN, no -0) to unsigned; -inf maps to
+// 0x007fffff, and 0 is below every float.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+constexpr uint32_t kKeyNegInf = 0x007fffffu;
+
+__device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) {
+  return __reduce_max_sync(0xffffffffu, v);
+}
+
+// Lane l holds the NPL consecutive experts l * NPL + i, so the lower lane
+// always holds the lower expert index, an aligned group of experts is a run
+// of lanes, and a row is read in 16-byte vectors.
+template <typename T, int NPL>
+__device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane, bool vec,
+                                         float (&v)[NPL]) {
+  constexpr int PV = 16 / sizeof(T);  // elements per 16-byte vector
+  const int e0 = lane * NPL;
+  if (NPL >= PV && vec) {  // E % PV == 0: a vector is inside the row or outside it
+#pragma unroll
+    for (int i = 0; i < NPL; i += PV) {
+      T t[PV];
+      if (e0 + i < E) {
+        *reinterpret_cast<uint4*>(t) = __ldg(reinterpret_cast<const uint4*>(row + e0 + i));
+      } else {
+#pragma unroll
+        for (int j = 0; j < PV; ++j) t[j] = T(0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < PV && i + j < NPL; ++j) v[i + j] = to_f(t[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = e0 + i < E ? to_f(row[e0 + i]) : 0.f;
+  }
+}
+
+// Softmax numerators of a row (NaN and -inf count as masked: 0; the largest
+// logit gives 1 even when it is +inf) and their sum by halves.
+template <int NPL>
+__device__ __forceinline__ float softmax_terms(float (&v)[NPL], int E, int lane) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (lane * NPL + i < E) m = fmaxf(m, v[i]);  // fmaxf drops NaN
+  const uint32_t mk = warp_max_u32(order_key(m + 0.f));
+  m = __uint_as_float(mk & 0x80000000u ? mk ^ 0x80000000u : ~mk);
+  float t[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const bool live = lane * NPL + i < E && v[i] > -INFINITY;
+    v[i] = live ? expf(v[i] == m ? 0.f : __fsub_rn(v[i], m)) : 0.f;
+    t[i] = v[i];
+  }
+  // halves: the upper index bits are the lane's, the lower ones i's
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) t[i] = __fadd_rn(t[i], __shfl_xor_sync(0xffffffffu, t[i], off));
+#pragma unroll
+  for (int n = NPL / 2; n > 0; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) t[i] = __fadd_rn(t[i], t[i + n]);
+  return t[0];
+}
+
+__device__ __forceinline__ float sigmoid_score(float x) {
+  return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x)));
+}
+
+template <typename T, int NPL>
+__global__ void __launch_bounds__(kWarps * 32)
+    route_scored_kernel(const RouteScoredArgs a) {
+  pdl_launch_dependents();
+  __shared__ int s_idx[kWarps][kMaxK];
+  __shared__ float s_val[kWarps][kMaxK];
+  extern __shared__ float s_row[];  // [kWarps][32 * NPL]: groups that are no run of lanes
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long t = static_cast<long>(blockIdx.x) * kWarps + warp;
+  pdl_wait();
+  if (t >= a.T) return;
+  const int E = a.E, e0 = lane * NPL;
+  float s[NPL];
+  load_row<T, NPL>(static_cast<const T*>(a.logits) + t * a.ld, E, lane, a.vec, s);
+  uint32_t dead = 0;  // bit i: expert e0 + i is masked (or there is none)
+#pragma unroll
+  for (int i = 0; i < NPL; ++i)
+    if (e0 + i >= E || !(s[i] > -INFINITY)) dead |= 1u << i;
+  if (a.softmax) {
+    const float sum = softmax_terms<NPL>(s, E, lane);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) s[i] = (dead >> i) & 1u ? 0.f : __fdiv_rn(s[i], sum);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) s[i] = (dead >> i) & 1u ? 0.f : sigmoid_score(s[i]);
+  }
+  uint32_t key[NPL];  // 0: no expert, or taken already
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    float c = s[i];
+    if (a.bias != nullptr && e0 + i < E) c = __fadd_rn(c, __ldg(a.bias + e0 + i));
+    if (((dead >> i) & 1u) || !(c > -INFINITY)) c = -INFINITY;
+    key[i] = e0 + i < E ? order_key(c + 0.f) : 0u;
+  }
+  if (a.n_group > 1) {
+    const int gs = E / a.n_group;
+    float g = -INFINITY;  // this lane's group's score (lane < n_group in the second form)
+    auto value = [](uint32_t k) {
+      return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+    };
+    auto score_of = [&](float t1, float t2) {  // a masked second expert adds nothing
+      return a.group_top == 2 && t2 > -INFINITY ? __fadd_rn(t1, t2) : t1;
+    };
+    const int span = gs / NPL;  // lanes a group covers
+    const bool runs = gs % NPL == 0 && (span & (span - 1)) == 0;
+    if (runs) {
+      // the two largest of a lane, then of its run of lanes by xor shuffles
+      uint32_t t1 = kKeyNegInf, t2 = kKeyNegInf;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        const uint32_t kx = key[i];
+        t2 = max(t2, min(t1, kx));
+        t1 = max(t1, kx);
+      }
+      for (int off = 1; off < span; off <<= 1) {
+        const uint32_t o1 = __shfl_xor_sync(0xffffffffu, t1, off);
+        const uint32_t o2 = __shfl_xor_sync(0xffffffffu, t2, off);
+        t2 = max(max(t2, o2), min(t1, o1));
+        t1 = max(t1, o1);
+      }
+      g = score_of(value(t1), value(t2));
+      const int mine = e0 / gs;
+      int rank = 0;  // groups that come before this lane's
+      for (int q = 0; q < a.n_group; ++q) {
+        const float og = __shfl_sync(0xffffffffu, g, q * span);
+        rank += og > g || (og == g && q < mine);
+      }
+      if (rank >= a.topk_group) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) key[i] = min(key[i], kKeyNegInf);
+      }
+    } else {
+      // any other group size: the row in shared memory, a lane per group
+      uint32_t* row = reinterpret_cast<uint32_t*>(s_row) + warp * 32 * NPL;
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) row[e0 + i] = key[i];
+      __syncwarp();
+      if (lane < a.n_group) {
+        uint32_t t1 = kKeyNegInf, t2 = kKeyNegInf;
+        for (int j = 0; j < gs; ++j) {
+          const uint32_t kx = row[lane * gs + j];
+          t2 = max(t2, min(t1, kx));
+          t1 = max(t1, kx);
+        }
+        g = score_of(value(t1), value(t2));
+      }
+      int rank = 0;
+      for (int q = 0; q < a.n_group; ++q) {
+        const float og = __shfl_sync(0xffffffffu, g, q);
+        rank += og > g || (og == g && q < lane);
+      }
+      const uint32_t kept = __ballot_sync(0xffffffffu, lane < a.n_group && rank < a.topk_group);
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (e0 + i < E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = min(key[i], kKeyNegInf);
+    }
+  }
+  // k rounds: the warp's largest key; its lowest lane, and there the lowest
+  // i, is the lowest expert index among equals
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) best = max(best, key[i]);
+    const uint32_t top = warp_max_u32(best);
+    const uint32_t who = __ballot_sync(0xffffffffu, best == top);
+    if (lane == __ffs(who) - 1) {
+      int at = 0;
+      float sv = 0.f;
+#pragma unroll
+      for (int i = NPL - 1; i >= 0; --i)
+        if (key[i] == top) {
+          at = i;
+          sv = s[i];
+        }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (i == at) key[i] = 0u;
+      s_idx[warp][j] = e0 + at;
+      s_val[warp][j] = top == kKeyNegInf ? 0.f : sv;
+    }
+  }
+  __syncwarp();
+  const bool has = lane < a.k;
+  float w = has ? s_val[warp][lane] : 0.f;
+  if (a.renorm) {
+    float sum = w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    w = sum > 0.f ? w / sum : 1.f / static_cast<float>(a.k);
+  }
+  if (has) {
+    a.idx[t * a.k + lane] = s_idx[warp][lane];
+    a.w[t * a.k + lane] = w * a.scale;
+  }
+}
+
+// Gradient.  With g_j = scale * dL/dw_j, r_j = s_j / sum of the chosen s,
+// D = sum_j g_j r_j:
+//   renormalised, sigmoid   dl_j = (g_j - D) r_j (1 - s_j)
+//   renormalised, softmax   dl_j = (g_j - D) r_j    (the softmax's own
+//                           denominator cancels: only the chosen logits count)
+//   as they are, sigmoid    dl_j = g_j s_j (1 - s_j)
+//   as they are, softmax    dl_e = s_e ([e chosen] g_e - sum_j g_j s_j), every e
+// A slot whose weight is 0, or whose expert is masked, has no gradient.
+// One warp per token; lane j holds slot j.  Three of the four forms read
+// only the chosen logits and write one row, whose zeros and values are put
+// together in shared memory so that the row leaves in 16-byte vectors.
+template <typename T, int NPL>
+__global__ void __launch_bounds__(kWarps * 32)
+    route_scored_backward_kernel(const RouteScoredBwdArgs a) {
+  pdl_launch_dependents();
+  extern __shared__ float s_row[];  // [kWarps][32 * NPL]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long t = static_cast<long>(blockIdx.x) * kWarps + warp;
+  pdl_wait();
+  if (t >= a.T) return;
+  const int E = a.E, k = a.k, e0 = lane * NPL;
+  const T* lrow = static_cast<const T*>(a.logits) + t * a.ld;
+  float* row = s_row + warp * 32 * NPL;
+  int e = -1;
+  float g = 0.f, x = -INFINITY;
+  if (lane < k) {
+    e = __ldg(a.idx + t * k + lane);
+    const float w = __ldg(a.w + t * k + lane);
+    g = a.scale * __ldg(a.grad_w + t * k + lane);
+    if (e < 0 || e >= E || w == 0.f) e = -1;
+    if (e >= 0) x = to_f(lrow[e]);
+    if (e >= 0 && a.bias != nullptr && !(__ldg(a.bias + e) > -INFINITY)) e = -1;
+    if (!(x > -INFINITY)) e = -1;
+    if (e < 0) g = 0.f;
+  }
+  const bool has = e >= 0;
+  auto sum32 = [](float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  };
+  const bool dense = a.softmax && !a.renorm;
+  float d = 0.f;
+  if (!dense) {
+    float s = 0.f, rest = 1.f;  // score (softmax: up to the common factor), 1 - s
+    if (a.softmax) {
+      float m = has ? x : -INFINITY;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      s = has ? expf(x == m ? 0.f : x - m) : 0.f;
+    } else if (has) {
+      s = sigmoid_score(x);
+      rest = sigmoid_score(-x);  // 1 - s without its cancellation
+    }
+    if (a.renorm) {
+      const float total = sum32(s);
+      const float r = total > 0.f ? s / total : 0.f;
+      d = (g - sum32(g * r)) * r * rest;
+    } else {
+      d = g * s * rest;
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) row[i * 32 + lane] = 0.f;
+    __syncwarp();
+    if (has) row[e] = d;
+    __syncwarp();
+  } else {
+    float p[NPL];
+    load_row<T, NPL>(lrow, E, lane, a.vec, p);
+    const float sum = softmax_terms<NPL>(p, E, lane);
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      p[i] = p[i] > 0.f ? p[i] / sum : 0.f;
+      row[e0 + i] = p[i];
+    }
+    __syncwarp();
+    const float ps = has ? row[e] : 0.f;
+    const float dot = sum32(g * ps);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) row[e0 + i] = -p[i] * dot;
+    __syncwarp();
+    if (has) row[e] = ps * (g - dot);
+    __syncwarp();
+  }
+  T* out = static_cast<T*>(a.grad_logits) + t * a.ldo;
+  constexpr int PV = 16 / sizeof(T);
+  if (a.vec_out) {
+    for (int c = lane * PV; c < E; c += 32 * PV) {
+      T o[PV];
+#pragma unroll
+      for (int j = 0; j < PV; ++j) from_f(row[c + j], &o[j]);
+      *reinterpret_cast<uint4*>(out + c) = *reinterpret_cast<const uint4*>(o);
+    }
+  } else {
+    for (int c = lane; c < E; c += 32) from_f(row[c], out + c);
+  }
+}
+
+template <typename T, int NPL>
+cudaError_t fwd(const RouteScoredArgs& a, cudaStream_t s) {
+  // shared rows only for groups that are no power-of-two run of lanes
+  const int gs = a.E / a.n_group, span = gs / NPL;
+  const bool runs = gs % NPL == 0 && (span & (span - 1)) == 0;
+  const size_t smem = a.n_group > 1 && !runs ? sizeof(float) * kWarps * 32 * NPL : 0;
+  return launch_pdl(route_scored_kernel<T, NPL>, dim3(ceil_div(a.T, kWarps)), dim3(kWarps * 32),
+                    smem, s, a);
+}
+template <typename T, int NPL>
+cudaError_t bwd(const RouteScoredBwdArgs& a, cudaStream_t s) {
+  return launch_pdl(route_scored_backward_kernel<T, NPL>, dim3(ceil_div(a.T, kWarps)),
+                    dim3(kWarps * 32), sizeof(float) * kWarps * 32 * NPL, s, a);
+}
+
+template <typename T>
+cudaError_t fwd_t(const RouteScoredArgs& a, cudaStream_t s) {
+  const int npl = ceil_div(a.E, 32);
+  if (npl <= 1) return fwd<T, 1>(a, s);
+  if (npl <= 2) return fwd<T, 2>(a, s);
+  if (npl <= 4) return fwd<T, 4>(a, s);
+  if (npl <= 8) return fwd<T, 8>(a, s);
+  if (npl <= 16) return fwd<T, 16>(a, s);
+  return fwd<T, 32>(a, s);
+}
+template <typename T>
+cudaError_t bwd_t(const RouteScoredBwdArgs& a, cudaStream_t s) {
+  const int npl = ceil_div(a.E, 32);
+  if (npl <= 1) return bwd<T, 1>(a, s);
+  if (npl <= 2) return bwd<T, 2>(a, s);
+  if (npl <= 4) return bwd<T, 4>(a, s);
+  if (npl <= 8) return bwd<T, 8>(a, s);
+  if (npl <= 16) return bwd<T, 16>(a, s);
+  return bwd<T, 32>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_route_scored(const RouteScoredArgs& a, bool bf16, cudaStream_t s) {
+  const cudaError_t e = bf16 ? fwd_t<__nv_bfloat16>(a, s) : fwd_t<float>(a, s);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_route_scored_backward(const RouteScoredBwdArgs& a, bool bf16, cudaStream_t s) {
+  const cudaError_t e = bf16 ? bwd_t<__nv_bfloat16>(a, s) : bwd_t<float>(a, s);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace moe
