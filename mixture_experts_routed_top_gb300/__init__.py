@@ -131,9 +131,19 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without the Python object around it, which
+# costs 3 of the 12 microseconds of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+if _raw_stream is None or _raw_device is None:
+    _raw_device = torch.cuda.current_device
+
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return _raw_stream(_raw_device()) if stream is None else stream.cuda_stream
 
 
 def _need_cuda(*ts):
@@ -290,65 +300,59 @@ def default_workspace(device="cuda") -> Workspace:
 _BF16, _F32 = torch.bfloat16, torch.float32
 _DT = {_BF16: 0, _F32: 1}
 _SCORES = {"softmax": 0, "sigmoid": 1}
+_ONLY_F32, _ONLY_BF16 = (_F32,), (_BF16,)
 _ACT_NONE = -1
 
 
-def _mat(name: str, t: torch.Tensor, dtypes, rows: Optional[int] = None, cols: Optional[int] = None) -> int:
-    """Checks a CUDA matrix whose rows are contiguous; -> its row stride."""
-    if not t.is_cuda or t.dim() != 2 or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d)[6:] for d in dtypes)}")
-    n, c = t.shape
-    if (rows is not None and n != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{name} must be [{rows if rows is not None else n}, {cols if cols is not None else c}], "
-                         f"not {list(t.shape)}")
-    sn, sc = t.stride()
-    if sc != 1 and c > 1:
-        raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return sn if n > 1 else max(c, 1)
+def _bad(name: str, what: str):
+    raise ValueError(f"{name} must be {what}")
 
 
-def _vec(name: str, t: Optional[torch.Tensor], dtypes, n: int):
-    if t is not None and (not t.is_cuda or t.dtype not in dtypes or t.dim() != 1 or t.shape[0] != n
-                          or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor [{n}] of {' or '.join(str(d)[6:] for d in dtypes)}")
+def _names(dtypes) -> str:
+    return " or ".join(str(d)[6:] for d in dtypes)
 
 
-def _same_device(device, *ts):
-    for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError("all tensors must be on one device")
+def _mat(name: str, t: torch.Tensor, dtypes, rows: int, cols: int, dev: int) -> int:
+    """Checks a matrix [rows, cols] on device dev, its rows contiguous; -> its row stride."""
+    if t.shape != (rows, cols) or t.dtype not in dtypes or t.get_device() != dev:
+        _bad(name, f"a tensor [{rows}, {cols}] of {_names(dtypes)} on CUDA device {dev}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        _bad(name, "contiguous along its rows")
+    return ld if rows > 1 else cols
 
 
-def _out(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> torch.Tensor:
-    """A contiguous output: the caller's, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor {list(shape)} on {device}")
-    return t
+def _vec(name: str, t: torch.Tensor, dtypes, n: int, dev: int):
+    if t.shape != (n,) or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
+        _bad(name, f"a contiguous tensor [{n}] of {_names(dtypes)} on CUDA device {dev}")
+
+
+def _out(name: str, t: torch.Tensor, shape, dtype, dev: int):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        _bad(name, f"a contiguous tensor {list(shape)} of {str(dtype)[6:]} on CUDA device {dev}")
+
+
+def _device_of(name: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0 or t.dim() != 2:
+        _bad(name, "a 2-D CUDA tensor")
+    return dev
+
+
+def _call(fn, dev: int, stream, args):
+    """The C call on `dev`: the stream appended, the device made current."""
+    cur = _raw_device()
+    if cur == dev:
+        status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if status:
+        _check(status)
 
 
 def _p(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
-
-
-class _on:
-    """The device of a call's tensors made current around it."""
-
-    __slots__ = ("prev",)
-
-    def __init__(self, device):
-        cur = torch.cuda.current_device()
-        self.prev = None if device.index == cur else cur
-        if self.prev is not None:
-            torch.cuda.set_device(device)
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
 
 
 def _workspace(workspace: Optional[Workspace], device, nbytes: int) -> torch.Tensor:
@@ -372,20 +376,23 @@ def route_scored(logits: torch.Tensor, k: int, *, score: str = "sigmoid",
     (1 or 2) best; the chosen scores are divided by their sum if renormalise,
     then multiplied by scale.  Experts with a logit of -inf or NaN are masked.
     out: (topk_idx, topk_w) to write into."""
-    ld = _mat("logits", logits, (_F32, _BF16))
+    dev = _device_of("logits", logits)
     T, E = logits.shape
-    dev = logits.device
+    ld = _mat("logits", logits, _DT, T, E, dev)
     if bias is not None:
-        _vec("bias", bias, (_F32,), E)
+        _vec("bias", bias, _ONLY_F32, E, dev)
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
-    idx = _out("topk_idx", None if out is None else out[0], (T, k), torch.int32, dev)
-    w = _out("topk_w", None if out is None else out[1], (T, k), _F32, dev)
-    _same_device(dev, bias)
-    with _on(dev):
-        _check(lib().moe_route_scored(logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _SCORES[score],
-                                      _p(bias), n_group, topk_group, group_top, bool(renormalise), scale,
-                                      idx.data_ptr(), w.data_ptr(), _stream(stream)))
+    if out is None:
+        idx = logits.new_empty((T, k), dtype=torch.int32)
+        w = logits.new_empty((T, k), dtype=_F32)
+    else:
+        idx, w = out
+        _out("topk_idx", idx, (T, k), torch.int32, dev)
+        _out("topk_w", w, (T, k), _F32, dev)
+    _call((_LIB or lib()).moe_route_scored, dev, stream,
+          (logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _SCORES[score], _p(bias), n_group, topk_group,
+           group_top, renormalise, scale, idx.data_ptr(), w.data_ptr()))
     return idx, w
 
 
@@ -397,45 +404,62 @@ def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: 
     """Gradient of route_scored's weights -> grad_logits [T,E] of the logits' type.
 
     logits, score, bias, renormalise, scale as route_scored was called with;
-    topk_idx, topk_w what it returned; grad_w fp32 [T,k]."""
-    ld = _mat("logits", logits, (_F32, _BF16))
+    topk_idx, topk_w what it returned; grad_w fp32 [T,k].  out: a tensor to
+    write into, its rows contiguous."""
+    dev = _device_of("logits", logits)
     T, E = logits.shape
-    dev = logits.device
-    _need_cuda(topk_idx, topk_w, grad_w)
-    k = topk_idx.shape[1] if topk_idx.dim() == 2 else 0
-    for name, t, dt in (("topk_idx", topk_idx, torch.int32), ("topk_w", topk_w, _F32), ("grad_w", grad_w, _F32)):
-        if t.dtype != dt or t.shape != (T, k):
-            raise ValueError(f"{name} must be {str(dt)[6:]} [T, k]")
-    _vec("bias", bias, (_F32,), E)
+    ld = _mat("logits", logits, _DT, T, E, dev)
+    if topk_idx.dim() != 2:
+        _bad("topk_idx", "2-D")
+    k = topk_idx.shape[1]
+    _out("topk_idx", topk_idx, (T, k), torch.int32, dev)
+    _out("topk_w", topk_w, (T, k), _F32, dev)
+    _out("grad_w", grad_w, (T, k), _F32, dev)
+    if bias is not None:
+        _vec("bias", bias, _ONLY_F32, E, dev)
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}")
-    g = _out("out", out, (T, E), logits.dtype, dev)
-    _same_device(dev, topk_idx, topk_w, grad_w, bias)
-    with _on(dev):
-        _check(lib().moe_route_scored_backward(
-            logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _SCORES[score], _p(bias), bool(renormalise),
-            scale, topk_idx.data_ptr(), topk_w.data_ptr(), grad_w.data_ptr(), g.data_ptr(), max(E, 1),
-            _stream(stream)))
-    return g
+    if out is None:
+        out = logits.new_empty((T, E))
+        ldo = E
+    else:
+        ldo = _mat("out", out, (logits.dtype,), T, E, dev)
+    _call((_LIB or lib()).moe_route_scored_backward, dev, stream,
+          (logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _SCORES[score], _p(bias), renormalise, scale,
+           topk_idx.data_ptr(), topk_w.data_ptr(), grad_w.data_ptr(), out.data_ptr(), ldo))
+    return out
 
 
-def _gate_of(gate: Optional[torch.Tensor], T: int, H: int):
+def _gate_of(gate: Optional[torch.Tensor], T: int, H: int, dev: int):
     """-> (moe_gate kind, dtype, row stride): [H] per channel, [T] or [T,1]
     per token, [T,H] per element.  A 1-D gate where T = H is per channel."""
     if gate is None:
         return 0, 0, 0
-    if not gate.is_cuda or gate.dtype not in _DT:
-        raise ValueError("gate must be a CUDA tensor of bfloat16 or float32")
-    dt, shape = _DT[gate.dtype], gate.shape
-    if gate.dim() == 2 and shape[0] == T and shape[1] == H and H != 1:
-        return 3, dt, _mat("gate", gate, (gate.dtype,), T, H)
+    dt = _DT.get(gate.dtype)
+    if dt is None or gate.get_device() != dev:
+        _bad("gate", f"a tensor of {_names(_DT)} on CUDA device {dev}")
+    shape = gate.shape
+    if shape == (T, H) and H != 1:
+        return 3, dt, _mat("gate", gate, _DT, T, H, dev)
     if not gate.is_contiguous():
-        raise ValueError("gate must be contiguous")
+        _bad("gate", "contiguous")
     if shape == (H,):
         return 1, dt, 0
     if shape == (T,) or shape == (T, 1):
         return 2, dt, 0
-    raise ValueError("gate must be [H] (per channel), [T] or [T, 1] (per token), or [T, H]")
+    return _bad("gate", "[H] (per channel), [T] or [T, 1] (per token), or [T, H]")
+
+
+def _norm_weights(post_weight, pre_weight, H: int, dev: int) -> int:
+    """-> the dtype of the norms' weights."""
+    if post_weight is not None:
+        _vec("post_weight", post_weight, _DT, H, dev)
+        if pre_weight is not None and pre_weight.dtype != post_weight.dtype:
+            raise ValueError("post_weight and pre_weight must have one dtype")
+    if pre_weight is not None:
+        _vec("pre_weight", pre_weight, _DT, H, dev)
+        return _DT[pre_weight.dtype]
+    return 0 if post_weight is None else _DT[post_weight.dtype]
 
 
 def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
@@ -453,27 +477,31 @@ def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     residual bf16 or fp32 [T,H] (residual_out alike); y bf16 [T,H], or None:
     only the norm, and residual itself is returned; normed bf16; gate [H],
     [T] / [T,1] or [T,H], bf16 or fp32; weights [H], both bf16 or both fp32.
-    out: (residual_out, normed) to write into; residual_out may be residual."""
-    ld_r = _mat("residual", residual, (_BF16, _F32))
+    out: (residual_out, normed) to write into, either of them None for a new
+    tensor; residual_out may be residual."""
+    dev = _device_of("residual", residual)
     T, H = residual.shape
-    dev = residual.device
-    ld_y = 0 if y is None else _mat("y", y, (_BF16,), T, H)
-    kind, gate_dt, ld_g = _gate_of(gate, T, H)
-    wdt = None
-    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if t is not None:
-            _vec(name, t, (_BF16, _F32), H)
-            if wdt is not None and t.dtype != wdt:
-                raise ValueError("post_weight and pre_weight must have one dtype")
-            wdt = t.dtype
-    _same_device(dev, y, gate, post_weight, pre_weight)
-    res = residual if y is None else _out("residual_out", None if out is None else out[0], (T, H), residual.dtype, dev)
-    n = _out("normed", None if out is None else out[1], (T, H), _BF16, dev) if pre_norm else None
-    with _on(dev):
-        _check(lib().moe_block_norm(
-            residual.data_ptr(), _DT[residual.dtype], ld_r, _p(y), ld_y, _p(gate), kind, gate_dt, ld_g, scale,
-            bool(post_norm), _p(post_weight), bool(pre_norm), _p(pre_weight), 0 if wdt is None else _DT[wdt],
-            eps, T, H, None if y is None else res.data_ptr(), _p(n), _stream(stream)))
+    ld_r = _mat("residual", residual, _DT, T, H, dev)
+    ld_y = 0 if y is None else _mat("y", y, _ONLY_BF16, T, H, dev)
+    kind, gate_dt, ld_g = _gate_of(gate, T, H, dev)
+    wdt = _norm_weights(post_weight, pre_weight, H, dev)
+    res, n = (None, None) if out is None else out
+    if y is None:
+        res = residual
+    elif res is None:
+        res = residual.new_empty((T, H))
+    else:
+        _out("residual_out", res, (T, H), residual.dtype, dev)
+    if not pre_norm:
+        n = None
+    elif n is None:
+        n = residual.new_empty((T, H), dtype=_BF16)
+    else:
+        _out("normed", n, (T, H), _BF16, dev)
+    _call((_LIB or lib()).moe_block_norm, dev, stream,
+          (residual.data_ptr(), _DT[residual.dtype], ld_r, _p(y), ld_y, _p(gate), kind, gate_dt, ld_g, scale,
+           post_norm, _p(post_weight), pre_norm, _p(pre_weight), wdt, eps, T, H,
+           None if y is None else res.data_ptr(), _p(n)))
     return res, n
 
 
@@ -490,37 +518,28 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
     block_norm returned; the rest as it was called with.  What does not apply
     comes back as None.  d_gate is fp32 for a per-channel gate, else of the
     gate's type; the weights' gradients are fp32 [H]."""
-    ld_r = _mat("residual", residual, (_BF16, _F32))
+    dev = _device_of("residual", residual)
     T, H = residual.shape
-    dev = residual.device
-    ld_gr = 0 if grad_residual is None else _mat("grad_residual", grad_residual, (residual.dtype,), T, H)
-    ld_gn = 0 if grad_normed is None else _mat("grad_normed", grad_normed, (_BF16,), T, H)
-    ld_y = 0 if y is None else _mat("y", y, (_BF16,), T, H)
-    kind, gate_dt, ld_g = _gate_of(gate, T, H)
-    wdt = None
-    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if t is not None:
-            _vec(name, t, (_BF16, _F32), H)
-            if wdt is not None and t.dtype != wdt:
-                raise ValueError("post_weight and pre_weight must have one dtype")
-            wdt = t.dtype
-    _same_device(dev, grad_residual, grad_normed, y, gate, post_weight, pre_weight)
-    d_res = torch.empty(T, H, dtype=residual.dtype, device=dev)
-    d_y = None if y is None else torch.empty(T, H, dtype=_BF16, device=dev)
+    ld_r = _mat("residual", residual, _DT, T, H, dev)
+    ld_gr = 0 if grad_residual is None else _mat("grad_residual", grad_residual, (residual.dtype,), T, H, dev)
+    ld_gn = 0 if grad_normed is None else _mat("grad_normed", grad_normed, _ONLY_BF16, T, H, dev)
+    ld_y = 0 if y is None else _mat("y", y, _ONLY_BF16, T, H, dev)
+    kind, gate_dt, ld_g = _gate_of(gate, T, H, dev)
+    wdt = _norm_weights(post_weight, pre_weight, H, dev)
+    d_res = residual.new_empty((T, H))
+    d_y = None if y is None else residual.new_empty((T, H), dtype=_BF16)
     d_gate = None
-    if gate is not None:
-        d_gate = torch.empty(gate.shape, dtype=_F32 if kind == 1 else gate.dtype, device=dev)
-    d_post = torch.empty(H, dtype=_F32, device=dev) if post_weight is not None else None
-    d_pre = torch.empty(H, dtype=_F32, device=dev) if pre_weight is not None else None
-    L = lib()
-    with _on(dev):
-        ws = _workspace(workspace, dev, L.moe_block_norm_backward_workspace_size(H))
-        _check(L.moe_block_norm_backward(
-            _p(grad_residual), ld_gr, _p(grad_normed), ld_gn,
-            residual.data_ptr() if grad_normed is not None else None, _DT[residual.dtype], ld_r, _p(y), ld_y,
-            _p(gate), kind, gate_dt, ld_g, scale, bool(post_norm), _p(post_weight), _p(pre_weight),
-            0 if wdt is None else _DT[wdt], eps, T, H, d_res.data_ptr(), _p(d_y), _p(d_gate), _p(d_post),
-            _p(d_pre), ws.data_ptr(), ws.numel(), _stream(stream)))
+    if kind:
+        d_gate = gate.new_empty(gate.shape, dtype=_F32 if kind == 1 else gate.dtype)
+    d_post = None if post_weight is None else residual.new_empty(H, dtype=_F32)
+    d_pre = None if pre_weight is None else residual.new_empty(H, dtype=_F32)
+    L = _LIB or lib()
+    ws = _workspace(workspace, residual.device, L.moe_block_norm_backward_workspace_size(H))
+    _call(L.moe_block_norm_backward, dev, stream,
+          (_p(grad_residual), ld_gr, _p(grad_normed), ld_gn,
+           None if grad_normed is None else residual.data_ptr(), _DT[residual.dtype], ld_r, _p(y), ld_y,
+           _p(gate), kind, gate_dt, ld_g, scale, post_norm, _p(post_weight), _p(pre_weight), wdt, eps, T, H,
+           d_res.data_ptr(), _p(d_y), _p(d_gate), _p(d_post), _p(d_pre), ws.data_ptr(), ws.numel()))
     return d_res, d_y, d_gate, d_post, d_pre
 
 
@@ -530,6 +549,19 @@ def _act(activation: Optional[str]) -> int:
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be None or one of {sorted(ACTIVATIONS)}")
     return ACTIVATIONS[activation]
+
+
+def _x_and_w(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor]):
+    dev = _device_of("x", x)
+    T, K = x.shape
+    ld_x = _mat("x", x, _ONLY_BF16, T, K, dev)
+    if w.dim() != 2:
+        _bad("w", "2-D")
+    N = w.shape[0]
+    ld_w = _mat("w", w, _ONLY_BF16, N, K, dev)
+    if bias is not None:
+        _vec("bias", bias, _DT, N, dev)
+    return dev, T, K, N, ld_x, ld_w
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
@@ -542,28 +574,23 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
     activation None, 'silu', 'gelu' (exact) or 'relu'; out_dtype bf16 or fp32
     (router logits), which residual and the pre-activation share.  out: the
     tensor to write into (rows contiguous); it may be residual."""
-    ld_x = _mat("x", x, (_BF16,))
-    T, K = x.shape
-    ld_w = _mat("w", w, (_BF16,), None, K)
-    N = w.shape[0]
-    dev = x.device
-    if bias is not None:
-        _vec("bias", bias, (_BF16, _F32), N)
+    dev, T, K, N, ld_x, ld_w = _x_and_w(x, w, bias)
     act = _act(activation)
     if out is None:
-        out = torch.empty(T, N, dtype=out_dtype, device=dev)
-    dt = out.dtype
-    ld_o = _mat("out", out, (_BF16, _F32), T, N)
-    ld_r = 0 if residual is None else _mat("residual", residual, (dt,), T, N)
+        if out_dtype not in _DT:
+            _bad("out_dtype", _names(_DT))
+        out = x.new_empty((T, N), dtype=out_dtype)
+        ld_o, dt = N, out_dtype
+    else:
+        dt = out.dtype
+        ld_o = _mat("out", out, _DT, T, N, dev)
+    ld_r = 0 if residual is None else _mat("residual", residual, (dt,), T, N, dev)
     # the pre-activation has out's row stride
-    z = torch.empty_strided((T, N), (ld_o, 1), dtype=dt, device=dev) if preact else None
-    _same_device(dev, w, bias, residual, out)
-    with _on(dev):
-        ws = _workspace(workspace, dev, 1024)
-        _check(lib().moe_linear(
-            x.data_ptr(), ld_x, w.data_ptr(), ld_w, _p(bias), 0 if bias is None else _DT[bias.dtype], act,
-            _p(residual), ld_r, T, K, N, out.data_ptr(), _DT[dt], ld_o, _p(z), ws.data_ptr(), ws.numel(),
-            _stream(stream)))
+    z = torch.empty_strided((T, N), (ld_o, 1), dtype=dt, device=x.device) if preact else None
+    ws = _workspace(workspace, x.device, 1024)
+    _call((_LIB or lib()).moe_linear, dev, stream,
+          (x.data_ptr(), ld_x, w.data_ptr(), ld_w, _p(bias), 0 if bias is None else _DT[bias.dtype], act,
+           _p(residual), ld_r, T, K, N, out.data_ptr(), _DT[dt], ld_o, _p(z), ws.data_ptr(), ws.numel()))
     return (out, z) if preact else out
 
 
@@ -577,28 +604,20 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
     preact: what linear(..., preact=True) returned, with an activation; bias:
     as passed to linear (None: dbias is None).  need_x / need_w = False leave
     that gradient out (None)."""
-    ld_x = _mat("x", x, (_BF16,))
-    T, K = x.shape
-    ld_w = _mat("w", w, (_BF16,), None, K)
-    N = w.shape[0]
-    dev = x.device
-    ld_g = _mat("grad_y", grad_y, (_BF16, _F32), T, N)
+    dev, T, K, N, ld_x, ld_w = _x_and_w(x, w, bias)
+    ld_g = _mat("grad_y", grad_y, _DT, T, N, dev)
     act = _act(activation)
     if (preact is None) != (act == _ACT_NONE):
         raise ValueError("an activation and its preact go together")
-    ld_z = 0 if preact is None else _mat("preact", preact, (grad_y.dtype,), T, N)
-    if bias is not None:
-        _vec("bias", bias, (_BF16, _F32), N)
-    _same_device(dev, grad_y, w, preact, bias)
-    dx = torch.empty(T, K, dtype=_BF16, device=dev) if need_x else None
-    dw = torch.empty(N, K, dtype=_BF16, device=dev) if need_w else None
-    db = torch.empty(N, dtype=_F32, device=dev) if bias is not None else None
-    L = lib()
-    with _on(dev):
-        ws = _workspace(workspace, dev, L.moe_linear_backward_workspace_size(T, N))
-        _check(L.moe_linear_backward(
-            grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(), ld_w, act,
-            _p(preact), ld_z, T, K, N, _p(dx), _p(dw), _p(db), ws.data_ptr(), ws.numel(), _stream(stream)))
+    ld_z = 0 if preact is None else _mat("preact", preact, (grad_y.dtype,), T, N, dev)
+    dx = x.new_empty((T, K)) if need_x else None
+    dw = w.new_empty((N, K)) if need_w else None
+    db = None if bias is None else x.new_empty(N, dtype=_F32)
+    L = _LIB or lib()
+    ws = _workspace(workspace, x.device, L.moe_linear_backward_workspace_size(T, N))
+    _call(L.moe_linear_backward, dev, stream,
+          (grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(), ld_w, act,
+           _p(preact), ld_z, T, K, N, _p(dx), _p(dw), _p(db), ws.data_ptr(), ws.numel()))
     return dx, dw, db
 
 

@@ -287,7 +287,7 @@ moe_status moe_block_norm(const void* residual, moe_dtype res_dt, int64_t ld_res
   const bool vec = H % 8 == 0 && ld_res % 8 == 0 && (!y || ld_y % 8 == 0) &&
                    (gate_kind != MOE_GATE_ELEMENT || ld_gate % 8 == 0);
   const cudaError_t e =
-      launch_block_norm(a, res_dt == MOE_DT_BF16, vec, static_cast<cudaStream_t>(stream));
+      launch_block_norm(a, res_dt == MOE_DT_BF16, vec, device_sms(), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
 }
 
@@ -374,8 +374,7 @@ moe_status moe_block_norm_backward(const void* grad_residual, int64_t ld_gres,
   const bool vec = H % 8 == 0 && (!grad_residual || ld_gres % 8 == 0) &&
                    (!grad_normed || (ld_gn % 8 == 0 && ld_res % 8 == 0)) &&
                    (!y || ld_y % 8 == 0) && (gate_kind != MOE_GATE_ELEMENT || ld_gate % 8 == 0);
-  const int blocks = std::min(block_norm_backward_blocks(T, device_sms()), kNormBwdBlocks);
-  const cudaError_t e = launch_block_norm_backward(a, res_dt == MOE_DT_BF16, vec, blocks,
+  const cudaError_t e = launch_block_norm_backward(a, res_dt == MOE_DT_BF16, vec, device_sms(),
                                                    static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
 }

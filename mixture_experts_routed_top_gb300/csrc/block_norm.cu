@@ -20,6 +20,9 @@
 // reduction runs over the registers, and sums are held in fp32.
 #include <math.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "moe_device.cuh"
 #include "moe_internal.h"
 
@@ -361,8 +364,506 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// ------------------------------------------------------------ streamed rows
+// Rows of H % 8 == 0, H <= 8192 columns with 16-byte row starts.  Blocks of up
+// to 512 threads stay on their SM and walk over the rows; a thread holds the
+// same NV pieces of 8 columns of every row (so weights and sums over tokens
+// stay in registers) and copies its own pieces of the next rows into its own
+// slots of a ring in shared memory (cp.async), so loads run while the block
+// computes.  No thread reads another's slots, so the ring needs no barrier;
+// the block meets only for the sums.
+constexpr int kRingBytes = 200 * 1024;   // rings of an SM's blocks together, at most
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// A thread's 16-byte pieces of one stage: piece p lies blockDim.x *
+// blockDim.y pieces after piece p - 1.
+struct Slots {
+  uint4* at;
+  int stride;
+  // 8 elements of bf16 (one piece) or fp32 (two)
+  template <typename T>
+  __device__ __forceinline__ void fetch8(int p, const T* src) const {
+    cp_async16(smem_u32(at + p * stride), src);
+    if (sizeof(T) == 4) cp_async16(smem_u32(at + (p + 1) * stride), src + 4);
+  }
+  __device__ __forceinline__ void fetch8_any(int p, const void* src, long off, bool bf16) const {
+    if (bf16) fetch8(p, static_cast<const __nv_bfloat16*>(src) + off);
+    else fetch8(p, static_cast<const float*>(src) + off);
+  }
+  __device__ __forceinline__ void read8(int p, bool f32, float (&v)[8]) const {
+    const uint4 a = at[p * stride];
+    if (f32) {
+      const uint4 b = at[(p + 1) * stride];
+      v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y);
+      v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+      v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y);
+      v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+    } else {
+      unpack8(a, v);
+    }
+  }
+};
+
+// Sums of N <= 2 values over a row's warps, one barrier each: two buffers in
+// turn, so a buffer is written again only after a barrier that follows its
+// reads.  s_red: [2][2][rows][16], zero from the row's warp count on.
+constexpr int kRedFloats = 2 * 2 * 8 * 16;  // at most 8 rows of two to 16 warps in a block
+template <int N>
+__device__ __forceinline__ void ring_sums(float (&v)[N], float* s_red, int& turn) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], off);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return;
+  float* buf = s_red + turn * (kRedFloats / 2) + threadIdx.y * 16;
+  turn ^= 1;
+  constexpr int kStep = 8 * 16;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) buf[n * kStep + (threadIdx.x >> 5)] = v[n];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    float4 t = *reinterpret_cast<const float4*>(buf + n * kStep);
+    for (int w = 4; w < warps; w += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(buf + n * kStep + w);
+      t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
+    }
+    v[n] = (t.x + t.y) + (t.z + t.w);
+  }
+}
+
+template <typename RT, int NV, int STAGES>
+__global__ void __launch_bounds__(512, 2) block_norm_ring_kernel(const BlockNormArgs a) {
+  pdl_launch_dependents();
+  extern __shared__ uint4 s_ring[];
+  __shared__ __align__(16) float s_red[kRedFloats];
+  constexpr bool R32 = sizeof(RT) == 4;
+  constexpr int PR = R32 ? 2 : 1;                 // pieces of a residual row
+  const bool has_y = a.y != nullptr;
+  const bool elem = a.gate_kind == MOE_GATE_ELEMENT;
+  const int nthr = blockDim.x * blockDim.y, tid = threadIdx.x + threadIdx.y * blockDim.x;
+  const int pv = PR + (has_y ? 1 : 0) + (elem ? (a.gate_bf16 ? 1 : 2) : 0);  // pieces of 8 columns
+  for (int i = tid; i < kRedFloats; i += nthr) s_red[i] = 0.f;
+  __syncthreads();
+  const Cols<true, NV> c{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.H};
+  const float inv_h = 1.f / static_cast<float>(a.H);
+  const long step = static_cast<long>(gridDim.x) * blockDim.y;
+  auto fetch = [&](long t, int st) {
+    if (t < a.T) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int col = c.col(v, 0);
+        if (col < a.H) {
+          const Slots sl{s_ring + (st * NV + v) * pv * nthr + tid, nthr};
+          sl.fetch8(0, static_cast<const RT*>(a.residual) + t * a.ld_res + col);
+          if (has_y) sl.fetch8(PR, static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y + col);
+          if (elem) sl.fetch8_any(PR + 1, a.gate, t * a.ld_gate + col, a.gate_bf16);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  pdl_wait();
+  long t = static_cast<long>(blockIdx.x) * blockDim.y + threadIdx.y;
+#pragma unroll
+  for (int st = 0; st < STAGES - 1; ++st) fetch(t + st * step, st);
+  // weights of this thread's columns: m = post_weight * per-channel gate
+  float m[NV][8], wp[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[v][e] = wp[v][e] = 1.f;
+    if (a.post_weight != nullptr) c.load_any(a.post_weight, a.weight_bf16, v, m[v], 0.f);
+    if (a.gate_kind == MOE_GATE_CHANNEL) {
+      c.load_any(a.gate, a.gate_bf16, v, wp[v], 0.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[v][e] *= wp[v][e], wp[v][e] = 1.f;
+    }
+    if (a.pre_weight != nullptr) c.load_any(a.pre_weight, a.weight_bf16, v, wp[v], 0.f);
+  }
+  int st = 0, turn = 0;
+  for (long base = static_cast<long>(blockIdx.x) * blockDim.y; base < a.T; base += step, t += step) {
+    fetch(t + (STAGES - 1) * step, st == 0 ? STAGES - 1 : st - 1);
+    cp_async_wait<STAGES - 1>();
+    const bool on = t < a.T;
+    uint4* const slot = s_ring + st * NV * pv * nthr + tid;
+    if (++st == STAGES) st = 0;
+    float r[NV][8];
+    if (has_y) {
+      float coef = a.scale;
+      if (a.gate_kind == MOE_GATE_TOKEN && on)
+        coef *= a.gate_bf16 ? get(static_cast<const __nv_bfloat16*>(a.gate) + t)
+                            : get(static_cast<const float*>(a.gate) + t);
+      if (a.post_norm) {
+        float sum[1] = {0.f};
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          if (on && c.col(v, 0) < a.H) {
+            float y[8];
+            Slots{slot + v * pv * nthr, nthr}.read8(PR, false, y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[0] += y[e] * y[e];
+          }
+        }
+        ring_sums<1>(sum, s_red, turn);
+        coef *= rsqrtf(sum[0] * inv_h + a.eps);
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const Slots sl{slot + v * pv * nthr, nthr};
+        if (on && c.col(v, 0) < a.H) {
+          float y[8];
+          sl.read8(0, R32, r[v]);
+          sl.read8(PR, false, y);
+          if (elem) {
+            float g[8];
+            sl.read8(PR + 1, !a.gate_bf16, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] *= g[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] += coef * (y[e] * m[v][e]);
+          store8(static_cast<RT*>(a.residual_out) + t * a.H + c.col(v, 0), r[v]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) r[v][e] = 0.f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] = 0.f;
+        if (on && c.col(v, 0) < a.H) Slots{slot + v * pv * nthr, nthr}.read8(0, R32, r[v]);
+      }
+    }
+    if (a.pre_norm) {
+      float sum[1] = {0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[0] += r[v][e] * r[v][e];
+      ring_sums<1>(sum, s_red, turn);
+      const float rstd = rsqrtf(sum[0] * inv_h + a.eps);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[v][e] = r[v][e] * rstd * wp[v][e];
+        if (on) c.store(static_cast<__nv_bfloat16*>(a.normed) + t * a.H, v, r[v]);
+      }
+    }
+  }
+}
+
+// Backward on the same ring, one block per SM.  Two sums over tokens stay in
+// registers per column: acc_pre = sum dn r' / rms(r'), and acc = sum g_t d y /
+// rms(y) (g_t: the per-token or per-element gate), of which a per-channel
+// gate's dg = scale * w_post * acc and dw_post = scale * g * acc are
+// multiples, since w_post and that gate do not depend on the token.
+template <typename RT, int NV, int STAGES>
+__global__ void __launch_bounds__(512, 1)
+    block_norm_backward_ring_kernel(const BlockNormBwdArgs a) {
+  pdl_launch_dependents();
+  extern __shared__ uint4 s_ring[];
+  __shared__ __align__(16) float s_red[kRedFloats];
+  constexpr bool R32 = sizeof(RT) == 4;
+  constexpr int PR = R32 ? 2 : 1;
+  const bool has_y = a.y != nullptr, has_gr = a.grad_res != nullptr, has_gn = a.grad_normed != nullptr;
+  const bool elem = a.gate_kind == MOE_GATE_ELEMENT, gch = a.gate_kind == MOE_GATE_CHANNEL;
+  // pieces: residual, grad_residual, grad_normed, y, gate
+  const int p_gr = has_gn ? PR : 0, p_gn = p_gr + (has_gr ? PR : 0), p_y = p_gn + (has_gn ? 1 : 0),
+            p_g = p_y + (has_y ? 1 : 0);
+  const int pv = p_g + (elem ? (a.gate_bf16 ? 1 : 2) : 0);
+  const int nthr = blockDim.x * blockDim.y, tid = threadIdx.x + threadIdx.y * blockDim.x;
+  for (int i = tid; i < kRedFloats; i += nthr) s_red[i] = 0.f;
+  __syncthreads();
+  const Cols<true, NV> c{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.H};
+  const float inv_h = 1.f / static_cast<float>(a.H);
+  const long step = static_cast<long>(gridDim.x) * blockDim.y;
+  auto fetch = [&](long t, int st) {
+    if (t < a.T) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int col = c.col(v, 0);
+        if (col < a.H) {
+          const Slots sl{s_ring + (st * NV + v) * pv * nthr + tid, nthr};
+          if (has_gn) {
+            sl.fetch8(0, static_cast<const RT*>(a.residual) + t * a.ld_res + col);
+            sl.fetch8(p_gn, static_cast<const __nv_bfloat16*>(a.grad_normed) + t * a.ld_gn + col);
+          }
+          if (has_gr) sl.fetch8(p_gr, static_cast<const RT*>(a.grad_res) + t * a.ld_gres + col);
+          if (has_y) sl.fetch8(p_y, static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y + col);
+          if (elem) sl.fetch8_any(p_g, a.gate, t * a.ld_gate + col, a.gate_bf16);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  pdl_wait();
+  long t = static_cast<long>(blockIdx.x) * blockDim.y + threadIdx.y;
+#pragma unroll
+  for (int st = 0; st < STAGES - 1; ++st) fetch(t + st * step, st);
+  const bool pw = a.post_norm && a.post_weight != nullptr;
+  float m[NV][8], wp[NV][8];  // post_weight * per-channel gate, pre_weight
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m[v][e] = wp[v][e] = 1.f;
+    if (pw) c.load_any(a.post_weight, a.weight_bf16, v, m[v], 0.f);
+    if (gch) {
+      c.load_any(a.gate, a.gate_bf16, v, wp[v], 0.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[v][e] *= wp[v][e], wp[v][e] = 1.f;
+    }
+    if (a.pre_weight != nullptr) c.load_any(a.pre_weight, a.weight_bf16, v, wp[v], 0.f);
+  }
+  float acc_pre[NV][8] = {}, acc[NV][8] = {};
+  int st = 0, turn = 0;
+  for (long base = static_cast<long>(blockIdx.x) * blockDim.y; base < a.T; base += step, t += step) {
+    fetch(t + (STAGES - 1) * step, st == 0 ? STAGES - 1 : st - 1);
+    cp_async_wait<STAGES - 1>();
+    const bool on = t < a.T;
+    uint4* const slot = s_ring + st * NV * pv * nthr + tid;
+    if (++st == STAGES) st = 0;
+    float rstd = 1.f, corr = 0.f;
+    if (has_gn) {
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (on && c.col(v, 0) < a.H) {
+          const Slots sl{slot + v * pv * nthr, nthr};
+          float r[8], q[8];
+          sl.read8(0, R32, r);
+          sl.read8(p_gn, false, q);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            sum[0] += r[e] * r[e];
+            sum[1] += q[e] * wp[v][e] * r[e];
+          }
+        }
+      }
+      ring_sums<2>(sum, s_red, turn);
+      rstd = rsqrtf(sum[0] * inv_h + a.eps);
+      corr = sum[1] * inv_h * rstd * rstd * rstd;
+    }
+    float d[NV][8];
+    float sum[2] = {0.f, 0.f};  // y^2; the norm's projection, which a per-token dg also needs
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const Slots sl{slot + v * pv * nthr, nthr};
+      const bool in = on && c.col(v, 0) < a.H;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[v][e] = 0.f;
+      if (in) {
+        if (has_gr) sl.read8(p_gr, R32, d[v]);
+        if (has_gn) {
+          float r[8], q[8];
+          sl.read8(0, R32, r);
+          sl.read8(p_gn, false, q);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float qn = q[e] * rstd;
+            acc_pre[v][e] += qn * r[e];
+            d[v][e] += qn * wp[v][e] - r[e] * corr;
+          }
+        }
+        if (a.d_res != nullptr) store8(static_cast<RT*>(a.d_res) + t * a.H + c.col(v, 0), d[v]);
+        if (has_y) {
+          float y[8];
+          sl.read8(p_y, false, y);
+          float g[8];
+          if (elem) {
+            sl.read8(p_g, !a.gate_bf16, g);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = 1.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            sum[0] += y[e] * y[e];
+            sum[1] += d[v][e] * m[v][e] * (y[e] * g[e]);
+          }
+        }
+      }
+    }
+    if (!has_y) continue;
+    float gt = 1.f;
+    rstd = 1.f, corr = 0.f;
+    if (a.gate_kind == MOE_GATE_TOKEN && on)
+      gt = a.gate_bf16 ? get(static_cast<const __nv_bfloat16*>(a.gate) + t)
+                       : get(static_cast<const float*>(a.gate) + t);
+    if (a.post_norm || a.gate_kind == MOE_GATE_TOKEN) {
+      ring_sums<2>(sum, s_red, turn);
+      if (a.post_norm) {
+        rstd = rsqrtf(sum[0] * inv_h + a.eps);
+        corr = sum[1] * inv_h * rstd * rstd * a.scale * gt * rstd;
+      }
+      if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0 && on) {
+        const float dg = a.scale * rstd * sum[1];
+        if (a.gate_bf16) put(static_cast<__nv_bfloat16*>(a.d_gate) + t, dg);
+        else put(static_cast<float*>(a.d_gate) + t, dg);
+      }
+    }
+    const float gr = gt * rstd;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const Slots sl{slot + v * pv * nthr, nthr};
+      if (!(on && c.col(v, 0) < a.H)) continue;
+      float y[8];
+      sl.read8(p_y, false, y);
+      if (elem) {
+        float g[8], dg[8];
+        sl.read8(p_g, !a.gate_bf16, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dg[e] = a.scale * rstd * m[v][e] * y[e] * d[v][e];
+          d[v][e] *= g[e];
+        }
+        if (a.gate_bf16) store8(static_cast<__nv_bfloat16*>(a.d_gate) + t * a.H + c.col(v, 0), dg);
+        else store8(static_cast<float*>(a.d_gate) + t * a.H + c.col(v, 0), dg);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float gd = gr * d[v][e];
+        acc[v][e] += gd * y[e];
+        y[e] = a.scale * m[v][e] * gd - y[e] * corr;
+      }
+      store8(static_cast<__nv_bfloat16*>(a.d_y) + t * a.H + c.col(v, 0), y);
+    }
+  }
+  if (a.n_part == 0) return;
+  // the block's rows side by side added in order, through the ring's memory
+  cp_async_wait<0>();
+  float* sum = reinterpret_cast<float*>(s_ring);   // [threads in y][n_part][H]
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (c.col(v, 0) >= a.H) continue;
+    float* to = sum + static_cast<long>(threadIdx.y) * a.n_part * a.H + c.col(v, 0);
+    float w[8];
+    if (a.d_pre != nullptr) {
+      store8(to, acc_pre[v]);
+      to += a.H;
+    }
+    if (a.d_post != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 1.f;
+      if (gch) c.load_any(a.gate, a.gate_bf16, v, w, 0.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= a.scale * acc[v][e];
+      store8(to, w);
+      to += a.H;
+    }
+    if (gch) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 1.f;
+      if (pw) c.load_any(a.post_weight, a.weight_bf16, v, w, 0.f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= a.scale * acc[v][e];
+      store8(to, w);
+    }
+  }
+  __syncthreads();
+  float* part = a.partials + static_cast<long>(blockIdx.x) * a.n_part * a.H;
+  const int total = a.n_part * a.H;
+  for (int i = tid * 4; i < total; i += nthr * 4) {   // H % 8 == 0
+    float4 v = *reinterpret_cast<const float4*>(sum + i);
+    for (int y = 1; y < blockDim.y; ++y) {
+      const float4 o = *reinterpret_cast<const float4*>(sum + static_cast<long>(y) * total + i);
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    *reinterpret_cast<float4*>(part + i) = v;
+  }
+}
+
+// Threads of a row and rows of a block: NV = 1 up to 2048 columns, 2 above; rows
+// side by side up to 512 threads, fewer where that would leave blocks idle.
+dim3 ring_block(int T, int H, int nv, int blocks) {
+  const int tx = ceil_div(H, 256 * nv) * 32;
+  const int most = tx == 32 ? 16 : std::min(512 / tx, 8);
+  const int ty = std::max(1, std::min(most, ceil_div(T, blocks)));
+  return dim3(tx, ty);
+}
+
+template <typename K>
+cudaError_t ring_ready(K kern, std::atomic<int>* ready) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    ready[dev].store(1, std::memory_order_release);
+  }
+  return cudaSuccess;
+}
+
+template <typename RT, int NV, int STAGES>
+cudaError_t fwd_ring(const BlockNormArgs& a, dim3 block, size_t stage, int grid, cudaStream_t s) {
+  static std::atomic<int> ready[64] = {};
+  const cudaError_t e = ring_ready(block_norm_ring_kernel<RT, NV, STAGES>, ready);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(block_norm_ring_kernel<RT, NV, STAGES>, dim3(grid), block, stage * STAGES, s, a);
+}
+template <typename RT, int NV, int STAGES>
+cudaError_t bwd_ring(const BlockNormBwdArgs& a, dim3 block, size_t smem, int grid, cudaStream_t s) {
+  static std::atomic<int> ready[64] = {};
+  const cudaError_t e = ring_ready(block_norm_backward_ring_kernel<RT, NV, STAGES>, ready);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(block_norm_backward_ring_kernel<RT, NV, STAGES>, dim3(grid), block, smem, s, a);
+}
+
+template <typename RT, int NV>
+cudaError_t fwd_nv(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
+  dim3 block = ring_block(a.T, a.H, NV, 2 * num_sms);
+  const int pv = static_cast<int>(sizeof(RT) / 2) + (a.y != nullptr) +
+                 (a.gate_kind == MOE_GATE_ELEMENT ? (a.gate_bf16 ? 1 : 2) : 0);
+  const size_t stage = static_cast<size_t>(pv) * NV * block.x * block.y * 16;
+  // two blocks per SM share the ring's memory; 3 stages, or 2 of wide rows
+  const int grid = std::min(2 * num_sms, ceil_div(a.T, block.y));
+  return 3 * stage <= kRingBytes / 2 ? fwd_ring<RT, NV, 3>(a, block, stage, grid, s)
+                                     : fwd_ring<RT, NV, 2>(a, block, stage, grid, s);
+}
+template <typename RT, int NV>
+cudaError_t bwd_nv(const BlockNormBwdArgs& a, int num_sms, int pv, int* blocks, cudaStream_t s) {
+  dim3 block = ring_block(a.T, a.H, NV, num_sms);
+  const size_t row = static_cast<size_t>(pv) * NV * block.x * 16;  // of one stage, <= kRingBytes / 2
+  block.y = std::max<unsigned>(1, std::min<unsigned>(block.y, kRingBytes / (2 * row)));
+  const size_t stage = row * block.y;
+  const size_t sums = static_cast<size_t>(block.y) * a.n_part * a.H * 4;  // <= 96 KB
+  const int grid = *blocks = std::min(std::min(num_sms, kNormBwdBlocks), ceil_div(a.T, block.y));
+  return 3 * stage <= kRingBytes
+             ? bwd_ring<RT, NV, 3>(a, block, std::max(3 * stage, sums), grid, s)
+             : bwd_ring<RT, NV, 2>(a, block, std::max(2 * stage, sums), grid, s);
+}
+
 template <typename RT, bool VEC>
-cudaError_t fwd(const BlockNormArgs& a, cudaStream_t s) {
+cudaError_t fwd(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
+  if (VEC && a.H <= 8192)
+    return a.H <= 2048 ? fwd_nv<RT, 1>(a, num_sms, s) : fwd_nv<RT, 2>(a, num_sms, s);
   // one piece of 8 columns per thread up to 8192 columns, two above
   const int pieces = ceil_div(a.H, 8);
   const int nv = pieces <= 1024 ? 1 : 2;
@@ -374,7 +875,18 @@ cudaError_t fwd(const BlockNormArgs& a, cudaStream_t s) {
 }
 
 template <typename RT, bool VEC>
-cudaError_t bwd(const BlockNormBwdArgs& a, int blocks, cudaStream_t s) {
+cudaError_t bwd(const BlockNormBwdArgs& a, int num_sms, int* blocks_used, cudaStream_t s) {
+  if (VEC && a.H <= 8192) {
+    const int pr = static_cast<int>(sizeof(RT) / 2);
+    const int pv = (a.grad_normed ? pr + 1 : 0) + (a.grad_res ? pr : 0) + (a.y != nullptr) +
+                   (a.gate_kind == MOE_GATE_ELEMENT ? (a.gate_bf16 ? 1 : 2) : 0);
+    // two stages of one row fit: all but the widest rows of fp32 streams and gates
+    if (static_cast<size_t>(pv) * ceil_div(a.H, 512) * 512 * 2 <= kRingBytes / 2)
+      return a.H <= 2048 ? bwd_nv<RT, 1>(a, num_sms, pv, blocks_used, s)
+                         : bwd_nv<RT, 2>(a, num_sms, pv, blocks_used, s);
+  }
+  const int blocks = *blocks_used =
+      static_cast<int>(std::min<long>(std::min(2 * num_sms, kNormBwdBlocks), a.T));
   const int pieces = ceil_div(a.H, 8);
   const int nv = pieces <= 512 ? 1 : pieces <= 1024 ? 2 : 4;
   const dim3 block(ceil_div(ceil_div(pieces, nv), 32) * 32);
@@ -385,25 +897,26 @@ cudaError_t bwd(const BlockNormBwdArgs& a, int blocks, cudaStream_t s) {
 
 }  // namespace
 
-int block_norm_backward_blocks(long T, int num_sms) {
-  return static_cast<int>(T < 2L * num_sms ? T : 2L * num_sms);
-}
-
-cudaError_t launch_block_norm(const BlockNormArgs& a, bool res_bf16, bool vec, cudaStream_t s) {
+cudaError_t launch_block_norm(const BlockNormArgs& a, bool res_bf16, bool vec, int num_sms,
+                              cudaStream_t s) {
   cudaError_t e;
-  if (res_bf16) e = vec ? fwd<__nv_bfloat16, true>(a, s) : fwd<__nv_bfloat16, false>(a, s);
-  else e = vec ? fwd<float, true>(a, s) : fwd<float, false>(a, s);
+  if (res_bf16)
+    e = vec ? fwd<__nv_bfloat16, true>(a, num_sms, s) : fwd<__nv_bfloat16, false>(a, num_sms, s);
+  else
+    e = vec ? fwd<float, true>(a, num_sms, s) : fwd<float, false>(a, num_sms, s);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_block_norm_backward(const BlockNormBwdArgs& a, bool res_bf16, bool vec,
-                                       int blocks, cudaStream_t s) {
+                                       int num_sms, cudaStream_t s) {
   cudaError_t e;
+  int blocks = 0;
   if (res_bf16)
-    e = vec ? bwd<__nv_bfloat16, true>(a, blocks, s) : bwd<__nv_bfloat16, false>(a, blocks, s);
+    e = vec ? bwd<__nv_bfloat16, true>(a, num_sms, &blocks, s)
+            : bwd<__nv_bfloat16, false>(a, num_sms, &blocks, s);
   else
-    e = vec ? bwd<float, true>(a, blocks, s) : bwd<float, false>(a, blocks, s);
+    e = vec ? bwd<float, true>(a, num_sms, &blocks, s) : bwd<float, false>(a, num_sms, &blocks, s);
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (a.n_part > 0) {

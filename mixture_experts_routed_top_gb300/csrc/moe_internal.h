@@ -352,7 +352,8 @@ struct BlockNormArgs {
   bool gate_bf16, weight_bf16, post_norm, pre_norm;
   float scale, eps;
 };
-cudaError_t launch_block_norm(const BlockNormArgs& a, bool res_bf16, bool vec, cudaStream_t s);
+cudaError_t launch_block_norm(const BlockNormArgs& a, bool res_bf16, bool vec, int num_sms,
+                              cudaStream_t s);
 
 struct BlockNormBwdArgs {
   const void* grad_res;    // or null
@@ -375,9 +376,8 @@ struct BlockNormBwdArgs {
 };
 constexpr int kNormMaxH = 16384;
 constexpr int kNormBwdBlocks = 304;   // most blocks of the backward pass (2 per SM of 152)
-int block_norm_backward_blocks(long T, int num_sms);
 cudaError_t launch_block_norm_backward(const BlockNormBwdArgs& a, bool res_bf16, bool vec,
-                                       int blocks, cudaStream_t s);
+                                       int num_sms, cudaStream_t s);
 
 // Epilogue of the linear kernels.
 struct LinearEpi {
