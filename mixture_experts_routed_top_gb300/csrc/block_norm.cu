@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(256)
   const int col = blockIdx.x * 32 + x, p = blockIdx.y;
   float sum = 0.f;
   if (col < H)
+#pragma unroll 8
     for (int b = sl; b < blocks; b += 8)
       sum += partials[(static_cast<long>(b) * n_part + p) * H + col];
   s[sl][x] = sum;
@@ -385,40 +386,92 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Pairs of floats, for the packed fp32 instructions (two lanes of work in one
+// issue slot: these kernels are held back by issue as much as by memory).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ float2 parts(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+  const float2 p = parts(a);
+  return p.x + p.y;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const F2 (&v)[4]) {
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const float2 q = parts(v[i]);
+    w[i] = pack_bf16x2(q.x, q.y);
   }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const F2 (&v)[4]) {
+  const float2 a = parts(v[0]), b = parts(v[1]), c = parts(v[2]), d = parts(v[3]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
+}
+// 8 weights (or per-channel gates) of a thread's columns; 1 where p is null
+// and 0 past the row's end.
+__device__ __forceinline__ void weights8(const void* p, bool bf16, int col, int H, F2 (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = col < H ? 1.f : 0.f;
+  if (p != nullptr && col < H) {
+    if (bf16) load8(static_cast<const __nv_bfloat16*>(p) + col, f);
+    else load8(static_cast<const float*>(p) + col, f);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = f2(f[2 * e], f[2 * e + 1]);
 }
 
-// A thread's 16-byte pieces of one stage: piece p lies blockDim.x *
-// blockDim.y pieces after piece p - 1.
+// A thread's 16-byte pieces of one stage; piece p lies p * kRingThreads pieces
+// further on (a constant, so that offsets are part of the instructions).
+constexpr int kRingThreads = 512;
 struct Slots {
   uint4* at;
-  int stride;
   // 8 elements of bf16 (one piece) or fp32 (two)
   template <typename T>
   __device__ __forceinline__ void fetch8(int p, const T* src) const {
-    cp_async16(smem_u32(at + p * stride), src);
-    if (sizeof(T) == 4) cp_async16(smem_u32(at + (p + 1) * stride), src + 4);
+    cp_async16(smem_u32(at + p * kRingThreads), src);
+    if (sizeof(T) == 4) cp_async16(smem_u32(at + (p + 1) * kRingThreads), src + 4);
   }
   __device__ __forceinline__ void fetch8_any(int p, const void* src, long off, bool bf16) const {
     if (bf16) fetch8(p, static_cast<const __nv_bfloat16*>(src) + off);
     else fetch8(p, static_cast<const float*>(src) + off);
   }
-  __device__ __forceinline__ void read8(int p, bool f32, float (&v)[8]) const {
-    const uint4 a = at[p * stride];
+  __device__ __forceinline__ void read8(int p, bool f32, F2 (&v)[4]) const {
+    const uint4 a = at[p * kRingThreads];
     if (f32) {
-      const uint4 b = at[(p + 1) * stride];
-      v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y);
-      v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-      v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y);
-      v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+      const uint4 b = at[(p + 1) * kRingThreads];
+      v[0] = f2(__uint_as_float(a.x), __uint_as_float(a.y));
+      v[1] = f2(__uint_as_float(a.z), __uint_as_float(a.w));
+      v[2] = f2(__uint_as_float(b.x), __uint_as_float(b.y));
+      v[3] = f2(__uint_as_float(b.z), __uint_as_float(b.w));
     } else {
-      unpack8(a, v);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
   }
 };
@@ -454,32 +507,35 @@ __device__ __forceinline__ void ring_sums(float (&v)[N], float* s_red, int& turn
   }
 }
 
-template <typename RT, int NV, int STAGES>
-__global__ void __launch_bounds__(512, 2) block_norm_ring_kernel(const BlockNormArgs a) {
+// MID: a call between two blocks (y given, norm before the next block, no
+// gate per element), whose options are then constants of the code.
+template <typename RT, int NV, int STAGES, bool MID>
+__global__ void __launch_bounds__(kRingThreads, 2) block_norm_ring_kernel(const BlockNormArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint4 s_ring[];
   __shared__ __align__(16) float s_red[kRedFloats];
   constexpr bool R32 = sizeof(RT) == 4;
   constexpr int PR = R32 ? 2 : 1;                 // pieces of a residual row
-  const bool has_y = a.y != nullptr;
-  const bool elem = a.gate_kind == MOE_GATE_ELEMENT;
+  const bool has_y = MID || a.y != nullptr, pre_norm = MID || a.pre_norm;
+  const bool elem = !MID && a.gate_kind == MOE_GATE_ELEMENT;
   const int nthr = blockDim.x * blockDim.y, tid = threadIdx.x + threadIdx.y * blockDim.x;
-  const int pv = PR + (has_y ? 1 : 0) + (elem ? (a.gate_bf16 ? 1 : 2) : 0);  // pieces of 8 columns
+  // pieces of 8 columns: residual, y, gate
+  const int pv = PR + (has_y ? 1 : 0) + (elem ? (a.gate_bf16 ? 1 : 2) : 0);
   for (int i = tid; i < kRedFloats; i += nthr) s_red[i] = 0.f;
   __syncthreads();
-  const Cols<true, NV> c{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.H};
-  const float inv_h = 1.f / static_cast<float>(a.H);
+  const int H = a.H;
+  auto col = [&](int v) { return static_cast<int>(threadIdx.x + blockDim.x * v) * 8; };
+  const float inv_h = 1.f / static_cast<float>(H);
   const long step = static_cast<long>(gridDim.x) * blockDim.y;
   auto fetch = [&](long t, int st) {
     if (t < a.T) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int col = c.col(v, 0);
-        if (col < a.H) {
-          const Slots sl{s_ring + (st * NV + v) * pv * nthr + tid, nthr};
-          sl.fetch8(0, static_cast<const RT*>(a.residual) + t * a.ld_res + col);
-          if (has_y) sl.fetch8(PR, static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y + col);
-          if (elem) sl.fetch8_any(PR + 1, a.gate, t * a.ld_gate + col, a.gate_bf16);
+        if (col(v) < H) {
+          const Slots sl{s_ring + (st * NV + v) * pv * kRingThreads + tid};
+          sl.fetch8(0, static_cast<const RT*>(a.residual) + t * a.ld_res + col(v));
+          if (has_y) sl.fetch8(PR, static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y + col(v));
+          if (elem) sl.fetch8_any(PR + 1, a.gate, t * a.ld_gate + col(v), a.gate_bf16);
         }
       }
     }
@@ -490,88 +546,83 @@ __global__ void __launch_bounds__(512, 2) block_norm_ring_kernel(const BlockNorm
 #pragma unroll
   for (int st = 0; st < STAGES - 1; ++st) fetch(t + st * step, st);
   // weights of this thread's columns: m = post_weight * per-channel gate
-  float m[NV][8], wp[NV][8];
+  F2 m[NV][4], wp[NV][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m[v][e] = wp[v][e] = 1.f;
-    if (a.post_weight != nullptr) c.load_any(a.post_weight, a.weight_bf16, v, m[v], 0.f);
+    weights8(a.post_weight, a.weight_bf16, col(v), H, m[v]);
     if (a.gate_kind == MOE_GATE_CHANNEL) {
-      c.load_any(a.gate, a.gate_bf16, v, wp[v], 0.f);
+      weights8(a.gate, a.gate_bf16, col(v), H, wp[v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m[v][e] *= wp[v][e], wp[v][e] = 1.f;
+      for (int e = 0; e < 4; ++e) m[v][e] = mul2(m[v][e], wp[v][e]);
     }
-    if (a.pre_weight != nullptr) c.load_any(a.pre_weight, a.weight_bf16, v, wp[v], 0.f);
+    weights8(a.pre_weight, a.weight_bf16, col(v), H, wp[v]);
   }
   int st = 0, turn = 0;
   for (long base = static_cast<long>(blockIdx.x) * blockDim.y; base < a.T; base += step, t += step) {
     fetch(t + (STAGES - 1) * step, st == 0 ? STAGES - 1 : st - 1);
     cp_async_wait<STAGES - 1>();
     const bool on = t < a.T;
-    uint4* const slot = s_ring + st * NV * pv * nthr + tid;
+    uint4* const slot = s_ring + st * NV * pv * kRingThreads + tid;
     if (++st == STAGES) st = 0;
-    float r[NV][8];
+    F2 r[NV][4];
+    float coef = a.scale;
     if (has_y) {
-      float coef = a.scale;
       if (a.gate_kind == MOE_GATE_TOKEN && on)
         coef *= a.gate_bf16 ? get(static_cast<const __nv_bfloat16*>(a.gate) + t)
                             : get(static_cast<const float*>(a.gate) + t);
       if (a.post_norm) {
-        float sum[1] = {0.f};
+        F2 sq = f2(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          if (on && c.col(v, 0) < a.H) {
-            float y[8];
-            Slots{slot + v * pv * nthr, nthr}.read8(PR, false, y);
+          if (on && col(v) < H) {
+            F2 y[4];
+            Slots{slot + v * pv * kRingThreads}.read8(PR, false, y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[0] += y[e] * y[e];
+            for (int e = 0; e < 4; ++e) sq = fma2(y[e], y[e], sq);
           }
         }
+        float sum[1] = {sum2(sq)};
         ring_sums<1>(sum, s_red, turn);
         coef *= rsqrtf(sum[0] * inv_h + a.eps);
       }
+    }
+    F2 sq = f2(0.f);
+    const F2 coef2 = f2(coef);
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const Slots sl{slot + v * pv * nthr, nthr};
-        if (on && c.col(v, 0) < a.H) {
-          float y[8];
-          sl.read8(0, R32, r[v]);
+    for (int v = 0; v < NV; ++v) {
+      const Slots sl{slot + v * pv * kRingThreads};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[v][e] = f2(0.f);
+      if (on && col(v) < H) {
+        sl.read8(0, R32, r[v]);
+        if (has_y) {
+          F2 y[4];
           sl.read8(PR, false, y);
           if (elem) {
-            float g[8];
+            F2 g[4];
             sl.read8(PR + 1, !a.gate_bf16, g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] *= g[e];
+            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], g[e]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] += coef * (y[e] * m[v][e]);
-          store8(static_cast<RT*>(a.residual_out) + t * a.H + c.col(v, 0), r[v]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) r[v][e] = 0.f;
+          for (int e = 0; e < 4; ++e) r[v][e] = fma2(coef2, mul2(y[e], m[v][e]), r[v][e]);
+          store8(static_cast<RT*>(a.residual_out) + t * H + col(v), r[v]);
         }
-      }
-    } else {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[v][e] = 0.f;
-        if (on && c.col(v, 0) < a.H) Slots{slot + v * pv * nthr, nthr}.read8(0, R32, r[v]);
+        for (int e = 0; e < 4; ++e) sq = fma2(r[v][e], r[v][e], sq);
       }
     }
-    if (a.pre_norm) {
-      float sum[1] = {0.f};
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[0] += r[v][e] * r[v][e];
+    if (pre_norm) {
+      float sum[1] = {sum2(sq)};
       ring_sums<1>(sum, s_red, turn);
-      const float rstd = rsqrtf(sum[0] * inv_h + a.eps);
+      const F2 rstd = f2(rsqrtf(sum[0] * inv_h + a.eps));
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
+        if (on && col(v) < H) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[v][e] = r[v][e] * rstd * wp[v][e];
-        if (on) c.store(static_cast<__nv_bfloat16*>(a.normed) + t * a.H, v, r[v]);
+          for (int e = 0; e < 4; ++e) r[v][e] = mul2(mul2(r[v][e], rstd), wp[v][e]);
+          store8(static_cast<__nv_bfloat16*>(a.normed) + t * H + col(v), r[v]);
+        }
       }
     }
   }
@@ -582,16 +633,19 @@ __global__ void __launch_bounds__(512, 2) block_norm_ring_kernel(const BlockNorm
 // rms(y) (g_t: the per-token or per-element gate), of which a per-channel
 // gate's dg = scale * w_post * acc and dw_post = scale * g * acc are
 // multiples, since w_post and that gate do not depend on the token.
-template <typename RT, int NV, int STAGES>
-__global__ void __launch_bounds__(512, 1)
+// MID: both gradients and y given, no gate per element.
+template <typename RT, int NV, int STAGES, bool MID>
+__global__ void __launch_bounds__(kRingThreads, 1)
     block_norm_backward_ring_kernel(const BlockNormBwdArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint4 s_ring[];
   __shared__ __align__(16) float s_red[kRedFloats];
   constexpr bool R32 = sizeof(RT) == 4;
   constexpr int PR = R32 ? 2 : 1;
-  const bool has_y = a.y != nullptr, has_gr = a.grad_res != nullptr, has_gn = a.grad_normed != nullptr;
-  const bool elem = a.gate_kind == MOE_GATE_ELEMENT, gch = a.gate_kind == MOE_GATE_CHANNEL;
+  const bool has_y = MID || a.y != nullptr, has_gr = MID || a.grad_res != nullptr,
+             has_gn = MID || a.grad_normed != nullptr;
+  const bool elem = !MID && a.gate_kind == MOE_GATE_ELEMENT;
+  const bool gch = a.gate_kind == MOE_GATE_CHANNEL;
   // pieces: residual, grad_residual, grad_normed, y, gate
   const int p_gr = has_gn ? PR : 0, p_gn = p_gr + (has_gr ? PR : 0), p_y = p_gn + (has_gn ? 1 : 0),
             p_g = p_y + (has_y ? 1 : 0);
@@ -599,23 +653,23 @@ __global__ void __launch_bounds__(512, 1)
   const int nthr = blockDim.x * blockDim.y, tid = threadIdx.x + threadIdx.y * blockDim.x;
   for (int i = tid; i < kRedFloats; i += nthr) s_red[i] = 0.f;
   __syncthreads();
-  const Cols<true, NV> c{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.H};
-  const float inv_h = 1.f / static_cast<float>(a.H);
+  const int H = a.H;
+  auto col = [&](int v) { return static_cast<int>(threadIdx.x + blockDim.x * v) * 8; };
+  const float inv_h = 1.f / static_cast<float>(H);
   const long step = static_cast<long>(gridDim.x) * blockDim.y;
   auto fetch = [&](long t, int st) {
     if (t < a.T) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int col = c.col(v, 0);
-        if (col < a.H) {
-          const Slots sl{s_ring + (st * NV + v) * pv * nthr + tid, nthr};
+        if (col(v) < H) {
+          const Slots sl{s_ring + (st * NV + v) * pv * kRingThreads + tid};
           if (has_gn) {
-            sl.fetch8(0, static_cast<const RT*>(a.residual) + t * a.ld_res + col);
-            sl.fetch8(p_gn, static_cast<const __nv_bfloat16*>(a.grad_normed) + t * a.ld_gn + col);
+            sl.fetch8(0, static_cast<const RT*>(a.residual) + t * a.ld_res + col(v));
+            sl.fetch8(p_gn, static_cast<const __nv_bfloat16*>(a.grad_normed) + t * a.ld_gn + col(v));
           }
-          if (has_gr) sl.fetch8(p_gr, static_cast<const RT*>(a.grad_res) + t * a.ld_gres + col);
-          if (has_y) sl.fetch8(p_y, static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y + col);
-          if (elem) sl.fetch8_any(p_g, a.gate, t * a.ld_gate + col, a.gate_bf16);
+          if (has_gr) sl.fetch8(p_gr, static_cast<const RT*>(a.grad_res) + t * a.ld_gres + col(v));
+          if (has_y) sl.fetch8(p_y, static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y + col(v));
+          if (elem) sl.fetch8_any(p_g, a.gate, t * a.ld_gate + col(v), a.gate_bf16);
         }
       }
     }
@@ -625,86 +679,86 @@ __global__ void __launch_bounds__(512, 1)
   long t = static_cast<long>(blockIdx.x) * blockDim.y + threadIdx.y;
 #pragma unroll
   for (int st = 0; st < STAGES - 1; ++st) fetch(t + st * step, st);
-  const bool pw = a.post_norm && a.post_weight != nullptr;
-  float m[NV][8], wp[NV][8];  // post_weight * per-channel gate, pre_weight
+  const void* post_w = a.post_norm ? a.post_weight : nullptr;
+  F2 m[NV][4], wp[NV][4];  // scale * post_weight * per-channel gate, pre_weight
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
+    weights8(post_w, a.weight_bf16, col(v), H, m[v]);
+    weights8(gch ? a.gate : nullptr, a.gate_bf16, col(v), H, wp[v]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m[v][e] = wp[v][e] = 1.f;
-    if (pw) c.load_any(a.post_weight, a.weight_bf16, v, m[v], 0.f);
-    if (gch) {
-      c.load_any(a.gate, a.gate_bf16, v, wp[v], 0.f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m[v][e] *= wp[v][e], wp[v][e] = 1.f;
-    }
-    if (a.pre_weight != nullptr) c.load_any(a.pre_weight, a.weight_bf16, v, wp[v], 0.f);
+    for (int e = 0; e < 4; ++e) m[v][e] = mul2(f2(a.scale), mul2(m[v][e], wp[v][e]));
+    weights8(a.pre_weight, a.weight_bf16, col(v), H, wp[v]);
   }
-  float acc_pre[NV][8] = {}, acc[NV][8] = {};
+  F2 acc_pre[NV][4], acc[NV][4];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc_pre[v][e] = acc[v][e] = f2(0.f);
   int st = 0, turn = 0;
   for (long base = static_cast<long>(blockIdx.x) * blockDim.y; base < a.T; base += step, t += step) {
     fetch(t + (STAGES - 1) * step, st == 0 ? STAGES - 1 : st - 1);
     cp_async_wait<STAGES - 1>();
     const bool on = t < a.T;
-    uint4* const slot = s_ring + st * NV * pv * nthr + tid;
+    uint4* const slot = s_ring + st * NV * pv * kRingThreads + tid;
     if (++st == STAGES) st = 0;
     float rstd = 1.f, corr = 0.f;
     if (has_gn) {
-      float sum[2] = {0.f, 0.f};
+      F2 s0 = f2(0.f), s1 = f2(0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        if (on && c.col(v, 0) < a.H) {
-          const Slots sl{slot + v * pv * nthr, nthr};
-          float r[8], q[8];
+        if (on && col(v) < H) {
+          const Slots sl{slot + v * pv * kRingThreads};
+          F2 r[4], q[4];
           sl.read8(0, R32, r);
           sl.read8(p_gn, false, q);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum[0] += r[e] * r[e];
-            sum[1] += q[e] * wp[v][e] * r[e];
+          for (int e = 0; e < 4; ++e) {
+            s0 = fma2(r[e], r[e], s0);
+            s1 = fma2(mul2(q[e], wp[v][e]), r[e], s1);
           }
         }
       }
+      float sum[2] = {sum2(s0), sum2(s1)};
       ring_sums<2>(sum, s_red, turn);
       rstd = rsqrtf(sum[0] * inv_h + a.eps);
       corr = sum[1] * inv_h * rstd * rstd * rstd;
     }
-    float d[NV][8];
-    float sum[2] = {0.f, 0.f};  // y^2; the norm's projection, which a per-token dg also needs
+    F2 d[NV][4];
+    F2 s0 = f2(0.f), s1 = f2(0.f);  // y^2; scale * the norm's projection, which a per-token dg needs too
+    {
+      const F2 rstd2 = f2(rstd), ncorr = f2(-corr);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const Slots sl{slot + v * pv * nthr, nthr};
-      const bool in = on && c.col(v, 0) < a.H;
+      for (int v = 0; v < NV; ++v) {
+        const Slots sl{slot + v * pv * kRingThreads};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[v][e] = 0.f;
-      if (in) {
+        for (int e = 0; e < 4; ++e) d[v][e] = f2(0.f);
+        if (!(on && col(v) < H)) continue;
         if (has_gr) sl.read8(p_gr, R32, d[v]);
         if (has_gn) {
-          float r[8], q[8];
+          F2 r[4], q[4];
           sl.read8(0, R32, r);
           sl.read8(p_gn, false, q);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float qn = q[e] * rstd;
-            acc_pre[v][e] += qn * r[e];
-            d[v][e] += qn * wp[v][e] - r[e] * corr;
+          for (int e = 0; e < 4; ++e) {
+            const F2 qn = mul2(q[e], rstd2);
+            acc_pre[v][e] = fma2(qn, r[e], acc_pre[v][e]);
+            d[v][e] = fma2(qn, wp[v][e], fma2(r[e], ncorr, d[v][e]));
           }
         }
-        if (a.d_res != nullptr) store8(static_cast<RT*>(a.d_res) + t * a.H + c.col(v, 0), d[v]);
+        if (a.d_res != nullptr) store8(static_cast<RT*>(a.d_res) + t * H + col(v), d[v]);
         if (has_y) {
-          float y[8];
+          F2 y[4];
           sl.read8(p_y, false, y);
-          float g[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s0 = fma2(y[e], y[e], s0);
           if (elem) {
+            F2 g[4];
             sl.read8(p_g, !a.gate_bf16, g);
-          } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = 1.f;
+            for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], g[e]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            sum[0] += y[e] * y[e];
-            sum[1] += d[v][e] * m[v][e] * (y[e] * g[e]);
-          }
+          for (int e = 0; e < 4; ++e) s1 = fma2(mul2(d[v][e], m[v][e]), y[e], s1);
         }
       }
     }
@@ -715,42 +769,43 @@ __global__ void __launch_bounds__(512, 1)
       gt = a.gate_bf16 ? get(static_cast<const __nv_bfloat16*>(a.gate) + t)
                        : get(static_cast<const float*>(a.gate) + t);
     if (a.post_norm || a.gate_kind == MOE_GATE_TOKEN) {
+      float sum[2] = {sum2(s0), sum2(s1)};
       ring_sums<2>(sum, s_red, turn);
       if (a.post_norm) {
         rstd = rsqrtf(sum[0] * inv_h + a.eps);
-        corr = sum[1] * inv_h * rstd * rstd * a.scale * gt * rstd;
+        corr = sum[1] * inv_h * rstd * rstd * gt * rstd;
       }
       if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0 && on) {
-        const float dg = a.scale * rstd * sum[1];
+        const float dg = rstd * sum[1];
         if (a.gate_bf16) put(static_cast<__nv_bfloat16*>(a.d_gate) + t, dg);
         else put(static_cast<float*>(a.d_gate) + t, dg);
       }
     }
-    const float gr = gt * rstd;
+    const F2 gr = f2(gt * rstd), ncorr = f2(-corr);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const Slots sl{slot + v * pv * nthr, nthr};
-      if (!(on && c.col(v, 0) < a.H)) continue;
-      float y[8];
+      const Slots sl{slot + v * pv * kRingThreads};
+      if (!(on && col(v) < H)) continue;
+      F2 y[4];
       sl.read8(p_y, false, y);
       if (elem) {
-        float g[8], dg[8];
+        F2 g[4], dg[4];
         sl.read8(p_g, !a.gate_bf16, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dg[e] = a.scale * rstd * m[v][e] * y[e] * d[v][e];
-          d[v][e] *= g[e];
+        for (int e = 0; e < 4; ++e) {
+          dg[e] = mul2(mul2(gr, m[v][e]), mul2(y[e], d[v][e]));
+          d[v][e] = mul2(d[v][e], g[e]);
         }
-        if (a.gate_bf16) store8(static_cast<__nv_bfloat16*>(a.d_gate) + t * a.H + c.col(v, 0), dg);
-        else store8(static_cast<float*>(a.d_gate) + t * a.H + c.col(v, 0), dg);
+        if (a.gate_bf16) store8(static_cast<__nv_bfloat16*>(a.d_gate) + t * H + col(v), dg);
+        else store8(static_cast<float*>(a.d_gate) + t * H + col(v), dg);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float gd = gr * d[v][e];
-        acc[v][e] += gd * y[e];
-        y[e] = a.scale * m[v][e] * gd - y[e] * corr;
+      for (int e = 0; e < 4; ++e) {
+        const F2 gd = mul2(gr, d[v][e]);
+        acc[v][e] = fma2(gd, y[e], acc[v][e]);
+        y[e] = fma2(m[v][e], gd, mul2(y[e], ncorr));
       }
-      store8(static_cast<__nv_bfloat16*>(a.d_y) + t * a.H + c.col(v, 0), y);
+      store8(static_cast<__nv_bfloat16*>(a.d_y) + t * H + col(v), y);
     }
   }
   if (a.n_part == 0) return;
@@ -760,34 +815,30 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (c.col(v, 0) >= a.H) continue;
-    float* to = sum + static_cast<long>(threadIdx.y) * a.n_part * a.H + c.col(v, 0);
-    float w[8];
+    if (col(v) >= H) continue;
+    float* to = sum + static_cast<long>(threadIdx.y) * a.n_part * H + col(v);
+    F2 w[4];
     if (a.d_pre != nullptr) {
       store8(to, acc_pre[v]);
-      to += a.H;
+      to += H;
     }
     if (a.d_post != nullptr) {
+      weights8(gch ? a.gate : nullptr, a.gate_bf16, col(v), H, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.f;
-      if (gch) c.load_any(a.gate, a.gate_bf16, v, w, 0.f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] *= a.scale * acc[v][e];
+      for (int e = 0; e < 4; ++e) w[e] = mul2(mul2(f2(a.scale), w[e]), acc[v][e]);
       store8(to, w);
-      to += a.H;
+      to += H;
     }
     if (gch) {
+      weights8(post_w, a.weight_bf16, col(v), H, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 1.f;
-      if (pw) c.load_any(a.post_weight, a.weight_bf16, v, w, 0.f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] *= a.scale * acc[v][e];
+      for (int e = 0; e < 4; ++e) w[e] = mul2(mul2(f2(a.scale), w[e]), acc[v][e]);
       store8(to, w);
     }
   }
   __syncthreads();
-  float* part = a.partials + static_cast<long>(blockIdx.x) * a.n_part * a.H;
-  const int total = a.n_part * a.H;
+  float* part = a.partials + static_cast<long>(blockIdx.x) * a.n_part * H;
+  const int total = a.n_part * H;
   for (int i = tid * 4; i < total; i += nthr * 4) {   // H % 8 == 0
     float4 v = *reinterpret_cast<const float4*>(sum + i);
     for (int y = 1; y < blockDim.y; ++y) {
@@ -821,43 +872,50 @@ cudaError_t ring_ready(K kern, std::atomic<int>* ready) {
   return cudaSuccess;
 }
 
-template <typename RT, int NV, int STAGES>
-cudaError_t fwd_ring(const BlockNormArgs& a, dim3 block, size_t stage, int grid, cudaStream_t s) {
+template <typename RT, int NV, int STAGES, bool MID>
+cudaError_t fwd_ring(const BlockNormArgs& a, dim3 block, size_t smem, int grid, cudaStream_t s) {
   static std::atomic<int> ready[64] = {};
-  const cudaError_t e = ring_ready(block_norm_ring_kernel<RT, NV, STAGES>, ready);
+  const cudaError_t e = ring_ready(block_norm_ring_kernel<RT, NV, STAGES, MID>, ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl(block_norm_ring_kernel<RT, NV, STAGES>, dim3(grid), block, stage * STAGES, s, a);
+  return launch_pdl(block_norm_ring_kernel<RT, NV, STAGES, MID>, dim3(grid), block, smem, s, a);
 }
-template <typename RT, int NV, int STAGES>
+template <typename RT, int NV, int STAGES, bool MID>
 cudaError_t bwd_ring(const BlockNormBwdArgs& a, dim3 block, size_t smem, int grid, cudaStream_t s) {
   static std::atomic<int> ready[64] = {};
-  const cudaError_t e = ring_ready(block_norm_backward_ring_kernel<RT, NV, STAGES>, ready);
+  const cudaError_t e = ring_ready(block_norm_backward_ring_kernel<RT, NV, STAGES, MID>, ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl(block_norm_backward_ring_kernel<RT, NV, STAGES>, dim3(grid), block, smem, s, a);
+  return launch_pdl(block_norm_backward_ring_kernel<RT, NV, STAGES, MID>, dim3(grid), block, smem, s,
+                    a);
 }
+
+// Bytes of one stage: pv pieces for each of the NV column sets of a thread.
+size_t stage_bytes(int pv, int nv) { return static_cast<size_t>(pv) * nv * kRingThreads * 16; }
 
 template <typename RT, int NV>
 cudaError_t fwd_nv(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
-  dim3 block = ring_block(a.T, a.H, NV, 2 * num_sms);
-  const int pv = static_cast<int>(sizeof(RT) / 2) + (a.y != nullptr) +
-                 (a.gate_kind == MOE_GATE_ELEMENT ? (a.gate_bf16 ? 1 : 2) : 0);
-  const size_t stage = static_cast<size_t>(pv) * NV * block.x * block.y * 16;
-  // two blocks per SM share the ring's memory; 3 stages, or 2 of wide rows
+  const dim3 block = ring_block(a.T, a.H, NV, 2 * num_sms);
+  const bool elem = a.gate_kind == MOE_GATE_ELEMENT;
+  const size_t stage = stage_bytes(
+      static_cast<int>(sizeof(RT) / 2) + (a.y != nullptr) + (elem ? (a.gate_bf16 ? 1 : 2) : 0), NV);
+  // two blocks per SM share the ring's memory: 3 stages, or 2 of wide rows
   const int grid = std::min(2 * num_sms, ceil_div(a.T, block.y));
-  return 3 * stage <= kRingBytes / 2 ? fwd_ring<RT, NV, 3>(a, block, stage, grid, s)
-                                     : fwd_ring<RT, NV, 2>(a, block, stage, grid, s);
+  if (a.y != nullptr && a.pre_norm && !elem)
+    return 3 * stage <= kRingBytes / 2 ? fwd_ring<RT, NV, 3, true>(a, block, 3 * stage, grid, s)
+                                       : fwd_ring<RT, NV, 2, true>(a, block, 2 * stage, grid, s);
+  return fwd_ring<RT, NV, 2, false>(a, block, 2 * stage, grid, s);
 }
 template <typename RT, int NV>
 cudaError_t bwd_nv(const BlockNormBwdArgs& a, int num_sms, int pv, int* blocks, cudaStream_t s) {
-  dim3 block = ring_block(a.T, a.H, NV, num_sms);
-  const size_t row = static_cast<size_t>(pv) * NV * block.x * 16;  // of one stage, <= kRingBytes / 2
-  block.y = std::max<unsigned>(1, std::min<unsigned>(block.y, kRingBytes / (2 * row)));
-  const size_t stage = row * block.y;
+  const dim3 block = ring_block(a.T, a.H, NV, num_sms);
+  const size_t stage = stage_bytes(pv, NV);
   const size_t sums = static_cast<size_t>(block.y) * a.n_part * a.H * 4;  // <= 96 KB
   const int grid = *blocks = std::min(std::min(num_sms, kNormBwdBlocks), ceil_div(a.T, block.y));
-  return 3 * stage <= kRingBytes
-             ? bwd_ring<RT, NV, 3>(a, block, std::max(3 * stage, sums), grid, s)
-             : bwd_ring<RT, NV, 2>(a, block, std::max(2 * stage, sums), grid, s);
+  if (a.grad_res != nullptr && a.grad_normed != nullptr && a.y != nullptr &&
+      a.gate_kind != MOE_GATE_ELEMENT)
+    return 3 * stage <= kRingBytes
+               ? bwd_ring<RT, NV, 3, true>(a, block, std::max(3 * stage, sums), grid, s)
+               : bwd_ring<RT, NV, 2, true>(a, block, std::max(2 * stage, sums), grid, s);
+  return bwd_ring<RT, NV, 2, false>(a, block, std::max(2 * stage, sums), grid, s);
 }
 
 template <typename RT, bool VEC>
@@ -880,8 +938,8 @@ cudaError_t bwd(const BlockNormBwdArgs& a, int num_sms, int* blocks_used, cudaSt
     const int pr = static_cast<int>(sizeof(RT) / 2);
     const int pv = (a.grad_normed ? pr + 1 : 0) + (a.grad_res ? pr : 0) + (a.y != nullptr) +
                    (a.gate_kind == MOE_GATE_ELEMENT ? (a.gate_bf16 ? 1 : 2) : 0);
-    // two stages of one row fit: all but the widest rows of fp32 streams and gates
-    if (static_cast<size_t>(pv) * ceil_div(a.H, 512) * 512 * 2 <= kRingBytes / 2)
+    // two stages fit: every case but wide rows with fp32 streams and fp32 element gates
+    if (2 * stage_bytes(pv, a.H <= 2048 ? 1 : 2) <= kRingBytes)
       return a.H <= 2048 ? bwd_nv<RT, 1>(a, num_sms, pv, blocks_used, s)
                          : bwd_nv<RT, 2>(a, num_sms, pv, blocks_used, s);
   }
