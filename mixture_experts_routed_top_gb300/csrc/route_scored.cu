@@ -102,8 +102,100 @@ __device__ __forceinline__ float softmax_terms(float (&v)[NPL], int E, int lane)
   return t[0];
 }
 
+// __frcp_rn is the correctly rounded 1 / v, the same bits as IEEE division.
 __device__ __forceinline__ float sigmoid_score(float x) {
-  return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x)));
+  return __frcp_rn(__fadd_rn(1.f, expf(-x)));
+}
+
+// The k largest of the warp's keys in (key descending, expert ascending)
+// order, written to s_idx / s_val; value 0 where the key is that of -inf.
+//
+// Up to kRankK of them by rank: the k-th largest of the 32 lane maxima is a
+// bound that at least k keys reach and few others do; those are gathered (at
+// most one per lane) and each lane counts how many come before its own.  At
+// 256 experts and k = 8 about 12 keys are gathered, and the whole selection
+// takes some 190 instructions, against 600 for k rounds of a warp-wide
+// maximum that remove one key each, which remain for the other cases: more
+// than kRankK, or more than 32 keys at the bound (ties, masked experts).
+constexpr int kRankK = 16;
+template <int NPL>
+__device__ __forceinline__ void select_top(uint32_t (&key)[NPL], const float (&s)[NPL], int k,
+                                           int lane, uint32_t* s_key, float* s_cand, int* s_expert,
+                                           int* s_idx, float* s_val) {
+  const int e0 = lane * NPL;
+  if (k <= kRankK) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) best = max(best, key[i]);
+    uint32_t bound = 0;
+    for (int taken = 0; taken < k;) {  // equal maxima leave together
+      bound = warp_max_u32(best);
+      const bool mine = best == bound;
+      taken += __popc(__ballot_sync(0xffffffffu, mine));
+      if (mine) best = 0u;
+      if (bound == 0u) break;  // fewer lanes than k hold an expert
+    }
+    int n = 0;
+    uint32_t at[NPL];
+    bool fits = bound != 0u;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+      const bool in = key[i] >= bound;
+      const uint32_t b = __ballot_sync(0xffffffffu, in);
+      at[i] = in ? n + __popc(b & ((1u << lane) - 1u)) : 32u;
+      n += __popc(b);
+    }
+    fits = fits && n <= 32;
+    if (fits) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i) {
+        if (at[i] < 32u) {
+          s_key[at[i]] = key[i];
+          s_cand[at[i]] = s[i];
+          s_expert[at[i]] = e0 + i;
+        }
+      }
+      __syncwarp();
+      const uint32_t mk = lane < n ? s_key[lane] : 0u;
+      const int me = lane < n ? s_expert[lane] : 0x7fffffff;
+      int rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const uint32_t ok = s_key[j];
+        rank += ok > mk || (ok == mk && s_expert[j] < me);
+      }
+      if (lane < n && rank < k) {
+        s_idx[rank] = me;
+        s_val[rank] = mk == kKeyNegInf ? 0.f : s_cand[lane];
+      }
+      __syncwarp();
+      return;
+    }
+  }
+  // k rounds: the warp's largest key; its lowest lane, and there the lowest
+  // i, is the lowest expert index among equals
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) best = max(best, key[i]);
+    const uint32_t top = warp_max_u32(best);
+    const uint32_t who = __ballot_sync(0xffffffffu, best == top);
+    if (lane == __ffs(who) - 1) {
+      int at = 0;
+      float sv = 0.f;
+#pragma unroll
+      for (int i = NPL - 1; i >= 0; --i)
+        if (key[i] == top) {
+          at = i;
+          sv = s[i];
+        }
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (i == at) key[i] = 0u;
+      s_idx[j] = e0 + at;
+      s_val[j] = top == kKeyNegInf ? 0.f : sv;
+    }
+  }
+  __syncwarp();
 }
 
 template <typename T, int NPL>
@@ -112,6 +204,9 @@ __global__ void __launch_bounds__(kWarps * 32)
   pdl_launch_dependents();
   __shared__ int s_idx[kWarps][kMaxK];
   __shared__ float s_val[kWarps][kMaxK];
+  __shared__ uint32_t s_key[kWarps][32];
+  __shared__ float s_cand[kWarps][32];
+  __shared__ int s_expert[kWarps][32];
   extern __shared__ float s_row[];  // [kWarps][32 * NPL]: groups that are no run of lanes
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long t = static_cast<long>(blockIdx.x) * kWarps + warp;
@@ -203,31 +298,8 @@ __global__ void __launch_bounds__(kWarps * 32)
         if (e0 + i < E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = min(key[i], kKeyNegInf);
     }
   }
-  // k rounds: the warp's largest key; its lowest lane, and there the lowest
-  // i, is the lowest expert index among equals
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) best = max(best, key[i]);
-    const uint32_t top = warp_max_u32(best);
-    const uint32_t who = __ballot_sync(0xffffffffu, best == top);
-    if (lane == __ffs(who) - 1) {
-      int at = 0;
-      float sv = 0.f;
-#pragma unroll
-      for (int i = NPL - 1; i >= 0; --i)
-        if (key[i] == top) {
-          at = i;
-          sv = s[i];
-        }
-#pragma unroll
-      for (int i = 0; i < NPL; ++i)
-        if (i == at) key[i] = 0u;
-      s_idx[warp][j] = e0 + at;
-      s_val[warp][j] = top == kKeyNegInf ? 0.f : sv;
-    }
-  }
-  __syncwarp();
+  select_top<NPL>(key, s, a.k, lane, s_key[warp], s_cand[warp], s_expert[warp], s_idx[warp],
+                  s_val[warp]);
   const bool has = lane < a.k;
   float w = has ? s_val[warp][lane] : 0.f;
   if (a.renorm) {
