@@ -557,11 +557,13 @@ moe_status moe_block_norm_backward(const void* grad_residual, int64_t ld_gres,
  *   out       device [T, N] bf16 or fp32 (out_dt), rounded once from fp32
  *   preact    device [T, N] of out's type and row stride, or NULL: out,
  *             x w^T + bias (what the backward pass of an activation needs)
- *   ws        device scratch, 256-byte aligned, at least 256 bytes: only its
- *             error word is used, as in moe_experts_forward
+ *   ws        device scratch, 256-byte aligned, at least
+ *             moe_linear_workspace_size() bytes (20 MB: the partial sums of a
+ *             split contraction); head and ordering as in moe_experts_forward
  * K % 8 == 0 and strides of x and w multiples of 8 (16-byte rows), else
  * MOE_ERR_UNSUPPORTED; any T, N.  T = 0 or N = 0 is a no-op.
  */
+size_t moe_linear_workspace_size(void);
 moe_status moe_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, const void* bias,
                       moe_dtype bias_dt, int act, const void* residual, int64_t ld_res, int T,
                       int K, int N, void* out, moe_dtype out_dt, int64_t ld_out, void* preact,

@@ -92,6 +92,7 @@ _SIGS = {
     "moe_block_norm_backward_workspace_size": ([_I], _SZ),
     "moe_block_norm_backward": ([_P, _L, _P, _L, _P, _I, _L, _P, _L, _P, _I, _I, _L, _F, _I, _P, _P,
                                  _I, _F, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "moe_linear_workspace_size": ([], _SZ),
     "moe_linear": ([_P, _L, _P, _L, _P, _I, _I, _P, _L, _I, _I, _I, _P, _I, _L, _P, _P, _SZ, _P], _I),
     "moe_linear_backward_workspace_size": ([_I, _I], _SZ),
     "moe_linear_backward": ([_P, _I, _L, _P, _L, _P, _L, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _SZ,
@@ -302,6 +303,7 @@ _DT = {_BF16: 0, _F32: 1}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _ONLY_F32, _ONLY_BF16 = (_F32,), (_BF16,)
 _ACT_NONE = -1
+_LINEAR_WS = 0  # the library's constant, once it is loaded
 
 
 def _bad(name: str, what: str):
@@ -587,8 +589,11 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
     ld_r = 0 if residual is None else _mat("residual", residual, (dt,), T, N, dev)
     # the pre-activation has out's row stride
     z = torch.empty_strided((T, N), (ld_o, 1), dtype=dt, device=x.device) if preact else None
-    ws = _workspace(workspace, x.device, 1024)
-    _call((_LIB or lib()).moe_linear, dev, stream,
+    global _LINEAR_WS
+    L = _LIB or lib()
+    _LINEAR_WS = _LINEAR_WS or L.moe_linear_workspace_size()
+    ws = _workspace(workspace, x.device, _LINEAR_WS)
+    _call(L.moe_linear, dev, stream,
           (x.data_ptr(), ld_x, w.data_ptr(), ld_w, _p(bias), 0 if bias is None else _DT[bias.dtype], act,
            _p(residual), ld_r, T, K, N, out.data_ptr(), _DT[dt], ld_o, _p(z), ws.data_ptr(), ws.numel()))
     return (out, z) if preact else out

@@ -130,8 +130,8 @@ moe_status check_linear(const char* fn, int64_t ld_x, int64_t ld_w, int act, int
 moe_status run_linear(const void* a, int64_t ld_a, bool a_mn, const void* b, int64_t ld_b,
                       bool b_mn, const LinearDev& p, cudaStream_t s, const char* what) {
   const int M = p.epi.M, N = p.epi.N, K = p.K;
-  const LinearPath path = linear_path(M, N, K, device_sms());
-  const uint32_t lines = path.pair ? 128 : 64;  // contraction lines of an MN-major box
+  const LinearPath path = linear_path(M, N, K, p.epi.out_f32, device_sms());
+  const uint32_t lines = path.kind == LinearPath::kTile ? 64 : 128;  // contraction lines of an MN-major box
   CUtensorMap ta, tb;
   moe_status st = a_mn ? make_map_bf16_2d(&ta, a, M, K, ld_a, 64, lines)
                        : make_map_bf16_2d(&ta, a, K, M, ld_a, 64, 128);
@@ -150,7 +150,7 @@ struct LinearWs {
 LinearWs linear_ws(int T, int N) {
   LinearWs w;
   w.ld_dz = (static_cast<int64_t>(N) + 7) / 8 * 8;
-  w.dz = 1024;
+  w.dz = kLinearWsBytes;
   w.partials = (w.dz + static_cast<size_t>(T) * w.ld_dz * 2 + 1023) / 1024 * 1024;
   w.total = w.partials + static_cast<size_t>(kLinearDzSlices) * N * 4;
   return w;
@@ -398,7 +398,7 @@ moe_status moe_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, 
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: preact needs a buffer of its own", fn);
   if (!all16(x, w, bias, residual, out, preact))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
-  if ((st = check_ws(fn, ws, ws_bytes, 256)) != MOE_OK) return st;
+  if ((st = check_ws(fn, ws, ws_bytes, kLinearWsBytes)) != MOE_OK) return st;
   LinearEpi e;
   e.bias = bias;
   e.residual = residual;
@@ -431,8 +431,11 @@ moe_status moe_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, 
   p.split = 1;
   p.group = 0;
   p.err = static_cast<int*>(ws);
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 1024);
   return run_linear(x, ld_x, false, w, ld_w, false, p, s, fn);
 }
+
+size_t moe_linear_workspace_size(void) { return kLinearWsBytes; }
 
 size_t moe_linear_backward_workspace_size(int T, int N) {
   return T < 0 || N < 0 ? 0 : linear_ws(T, N).total;
@@ -508,6 +511,7 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
   e.vec = true;  // K % 8 == 0
   LinearDev p{};
   p.err = static_cast<int*>(ws);
+  p.parts = reinterpret_cast<float*>(wsb + 1024);
   if (dx) {
     e.M = T;
     e.out = dx;

@@ -49,6 +49,37 @@ __host__ __device__ constexpr uint32_t idesc_bf16_order(int M, int N, bool a_mn,
   return idesc_bf16_f32(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 }
 
+// Bounded waits as mbar_wait_bounded, on the SM's cycle counter: reading the
+// global timer takes longer than most of these waits.  About a second; each
+// try itself blocks for a while.
+constexpr long long kWaitCycles = 2000000000ll, kDrainCycles = 40000000ll;
+template <bool kCluster>
+__device__ __forceinline__ bool wait_cycles(uint32_t bar, uint32_t parity, volatile int* abort,
+                                            int* err, int code, long long limit) {
+  long long t0 = 0;
+  for (int i = 0;; ++i) {
+    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if ((i & 15) == 15) {
+      if (*abort) return false;
+      const long long now = clock64();
+      if (i == 15) t0 = now;
+      else if (now - t0 > limit) {
+        atomicOr(err, code);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          int* err, int code, long long limit = kWaitCycles) {
+  return wait_cycles<true>(bar, parity, abort, err, code, limit);
+}
+__device__ __forceinline__ bool wait_cta(uint32_t bar, uint32_t parity, volatile int* abort,
+                                         int* err, int code, long long limit = kWaitCycles) {
+  return wait_cycles<false>(bar, parity, abort, err, code, limit);
+}
+
 // 2-D load counted on an mbarrier of either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar,
                                                  uint32_t dst, int x, int y) {
@@ -98,44 +129,193 @@ __device__ __forceinline__ void st8(void* p, long i, bool f32, const float (&v)[
   }
 }
 
-// The epilogue on 8 consecutive columns n.. of row m (m < M): pre-activation
-// z = v + bias, y = residual + act(z).  The activation is computed in fp32
-// with silu_f's fast division only where the result is rounded to bf16.
+// The activation in fp32; silu_f's fast division only where the result is
+// rounded to bf16.
 __device__ __forceinline__ float act_f(float z, int act, bool f32) {
   if (act == MOE_ACT_NONE) return z;
   if (act == MOE_ACT_SILU && f32) return z / (1.f + expf(-z));
   return gate_act(z, act);
 }
+// The epilogue on 8 consecutive columns n.. of row m (m < M): pre-activation
+// z = v + bias, y = residual + act(z).  ACT and F32 are constants of the code:
+// kernels hold several copies of this, and with every activation and type in
+// each the code was so long that fetching it took longer than a small
+// product (33 us for 64 x 256 x 256), while one copy called as a function
+// took 300 ns a call.
+template <int ACT, bool F32>
 __device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, float (&v)[8]) {
   if (n >= p.N) return;
   if (p.vec) {  // N % 8 == 0 and every row 16-byte aligned
-    float b[8];
+    float b[8], r[8];
+    if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !F32, r);
     if (p.bias != nullptr) {
       ld8(p.bias, n, p.bias_bf16, b);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] += b[j];
     }
-    if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, p.out_f32, v);
-    if (p.act != MOE_ACT_NONE) {
+    if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, F32, v);
+    if (ACT != MOE_ACT_NONE) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_f(v[j], p.act, p.out_f32);
+      for (int j = 0; j < 8; ++j) v[j] = act_f(v[j], ACT, F32);
     }
     if (p.residual != nullptr) {
-      ld8(p.residual, m * p.ld_res + n, !p.out_f32, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += b[j];
+      for (int j = 0; j < 8; ++j) v[j] += r[j];
     }
-    st8(p.out, m * p.ld_out + n, p.out_f32, v);
+    st8(p.out, m * p.ld_out + n, F32, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (n + j < p.N) {
         float z = v[j];
         if (p.bias != nullptr) z += ldf(p.bias, n + j, p.bias_bf16);
-        if (p.preact != nullptr) stf(p.preact, m * p.ld_out + n + j, p.out_f32, z);
-        z = act_f(z, p.act, p.out_f32);
-        if (p.residual != nullptr) z += ldf(p.residual, m * p.ld_res + n + j, !p.out_f32);
-        stf(p.out, m * p.ld_out + n + j, p.out_f32, z);
+        if (p.preact != nullptr) stf(p.preact, m * p.ld_out + n + j, F32, z);
+        z = act_f(z, ACT, F32);
+        if (p.residual != nullptr) z += ldf(p.residual, m * p.ld_res + n + j, !F32);
+        stf(p.out, m * p.ld_out + n + j, F32, z);
+      }
+    }
+  }
+}
+// 32 consecutive columns of row m from a thread's TMEM load.
+template <int ACT, bool F32>
+__device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
+                                           const uint32_t (&v)[32]) {
+  if (m >= p.M) return;
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[j + i]);
+    epilogue8<ACT, F32>(p, m, n + j, f);
+  }
+}
+
+// Joining a split contraction.  The CTAs of a cluster share a tile and each owns
+// some of its rows.  A CTA has its sums in its shared memory ([128][STRIDE]
+// floats); it writes the other owners' rows to its part of the workspace
+// ([CTA][128][8 * CHUNKS] floats, whole lines, into L2), and after a cluster
+// barrier each owner adds its rows over all CTAs in their order (so the
+// result does not depend on timing), its own from shared memory, and runs the
+// epilogue on them: 8 columns of a row per thread, neighbouring threads along
+// the row, the loads of two rows from up to four CTAs in flight together.
+// Through distributed shared memory instead, reading or writing, the same
+// exchange ran at 17 to 30 GB/s per SM and took 5 us of a router product of
+// 8192 tokens and 10 of a 256 x 2048 x 2048 one.
+template <int THREADS, int CHUNKS, int STRIDE>
+__device__ __forceinline__ void hand_over(const float* stg, float* part, int row0, int rows) {
+  constexpr int C4 = 2 * CHUNKS;  // float4s of a row
+  for (int i = threadIdx.x; i < (128 - rows) * C4; i += THREADS) {
+    int row = i / C4;
+    row += row >= row0 ? rows : 0;  // the rows before and after the CTA's own
+    const int c = (i % C4) * 4;
+    __stcg(reinterpret_cast<float4*>(part + row * (4 * C4) + c),
+           *reinterpret_cast<const float4*>(stg + row * STRIDE + c));
+  }
+}
+// v[row][8] += parts k0 .. k0 + PARTS - 1 of the first R of a thread's 4 rows,
+// `count` of which there are.  own: its columns of the rows in shared memory,
+// other: in the first CTA's part of the workspace, the next one's `step`
+// floats further on; `mine` is the part in shared memory.
+template <int R, int PARTS>
+__device__ __forceinline__ void add_parts(const float* own, int own_step, const float* other,
+                                          int other_step, long step, int k0, int mine, int count,
+                                          float (&v)[4][8]) {
+  float4 x[PARTS][R][2];
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      x[i][r][0] = x[i][r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r >= count) continue;
+      if (k0 + i == mine) {
+        const float4* q = reinterpret_cast<const float4*>(own + r * own_step);
+        x[i][r][0] = q[0];
+        x[i][r][1] = q[1];
+      } else {
+        const float4* q = reinterpret_cast<const float4*>(other + step * (k0 + i) + r * other_step);
+        x[i][r][0] = __ldcg(q);
+        x[i][r][1] = __ldcg(q + 1);
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      v[r][0] += x[i][r][0].x, v[r][1] += x[i][r][0].y, v[r][2] += x[i][r][0].z;
+      v[r][3] += x[i][r][0].w, v[r][4] += x[i][r][1].x, v[r][5] += x[i][r][1].y;
+      v[r][6] += x[i][r][1].z, v[r][7] += x[i][r][1].w;
+    }
+}
+// The rows row0 .. row0 + rows of a tile whose first row is m0, columns n0 ..
+// n0 + 8 * CHUNKS.  parts: number of CTAs (1, 2, 4 or 8), mine: this one's place
+// among them; part0: the first one's part of the workspace, the next ones'
+// `step` floats further on.
+template <int THREADS, int CHUNKS, int STRIDE>
+__device__ __forceinline__ void join_rows(const LinearEpi& p, const float* stg, const float* part0,
+                                          long step, int parts, int mine, int row0, int rows,
+                                          long m0, int n0) {
+  static_assert(THREADS % CHUNKS == 0, "a thread keeps its columns");
+  constexpr int STEP = THREADS / CHUNKS;
+  const int col = (threadIdx.x % CHUNKS) * 8, n = n0 + col;
+  if (n >= p.N) return;
+  float b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = 0.f;
+  if (p.bias != nullptr) {
+    if (p.vec) {
+      ld8(p.bias, n, p.bias_bf16, b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j < p.N) b[j] = ldf(p.bias, n + j, p.bias_bf16);
+    }
+  }
+  // rows in flight: 4 of up to two parts, 2 of four (twice as many measured slower)
+  const int R = parts <= 2 ? 4 : 2;
+  const int end = static_cast<int>(min(static_cast<long>(rows), p.M - m0 - row0));
+#pragma unroll 1
+  for (int i = threadIdx.x / CHUNKS; i < end; i += R * STEP) {
+    const int count = min(R, (end - i + STEP - 1) / STEP), ra = row0 + i;
+    const float* const own = stg + ra * STRIDE + col;
+    const float* const other = part0 + ra * (8 * CHUNKS) + col;
+    constexpr int OS = STEP * STRIDE, PS = STEP * 8 * CHUNKS;
+    float v[4][8];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[r][j] = 0.f;
+    if (parts == 1) add_parts<4, 1>(own, OS, other, PS, step, 0, mine, count, v);
+    else if (parts == 2) add_parts<4, 2>(own, OS, other, PS, step, 0, mine, count, v);
+    else
+      for (int k = 0; k < parts; k += 4)
+        add_parts<2, 4>(own, OS, other, PS, step, k, mine, count, v);
+#pragma unroll 1
+    for (int r = 0; r < count; ++r) {
+      const long m = m0 + ra + r * STEP;
+      float z[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        z[j] = (r == 0 ? v[0][j] : r == 1 ? v[1][j] : r == 2 ? v[2][j] : v[3][j]) + b[j];
+      if (p.vec) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = 0.f;
+        if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !p.out_f32, y);
+        if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, p.out_f32, z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] += act_f(z[j], p.act, p.out_f32);
+        st8(p.out, m * p.ld_out + n, p.out_f32, y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (n + j < p.N) {
+            const float y =
+                p.residual != nullptr ? ldf(p.residual, m * p.ld_res + n + j, !p.out_f32) : 0.f;
+            if (p.preact != nullptr) stf(p.preact, m * p.ld_out + n + j, p.out_f32, z[j]);
+            stf(p.out, m * p.ld_out + n + j, p.out_f32, y + act_f(z[j], p.act, p.out_f32));
+          }
+        }
       }
     }
   }
@@ -173,10 +353,10 @@ __device__ __forceinline__ void pair_tile(int tile, int mt, int nt, int group, i
   *mi = g * group + (r - *ni * rows);
 }
 
-template <bool A_MN, bool B_MN>
+template <bool A_MN, bool B_MN, int ACT>
 __global__ void __launch_bounds__(kPThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
-                       const __grid_constant__ CUtensorMap tm_b, const LinearDev p) {
+                       const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ LinearDev p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -234,7 +414,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int arow = mi * 256 + 128 * static_cast<int>(rank);
         const int brow = ni * 256 + 128 * static_cast<int>(rank);
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_bounded<true, true>(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err,
+          if (!wait_pair(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err,
                                              ERR_TIMEOUT_PRODUCER)) {
             ok = false;
             break;
@@ -266,8 +446,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if ((issued >> s) & 1u) {
           volatile int no_abort = 0;
           const uint32_t par = (last_par >> s) & 1u;
-          mbar_wait_bounded<true, true>(smem_u32(rank == 0 ? &full[s] : &empty[s]), par, &no_abort,
-                                        p.err, ERR_TIMEOUT_PRODUCER, 20000000ull);
+          wait_pair(smem_u32(rank == 0 ? &full[s] : &empty[s]), par, &no_abort,
+                                        p.err, ERR_TIMEOUT_PRODUCER, kDrainCycles);
         }
       }
     }
@@ -279,12 +459,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
       bool ok = true;
       for (int tile = cid; ok && tile < total; tile += ncl, ++it) {
         const int acc = it & 1;
-        if (!mbar_wait_bounded<true, true>(smem_u32(&tempty[acc]), ((it >> 1) & 1) ^ 1u, s_abort,
+        if (!wait_pair(smem_u32(&tempty[acc]), ((it >> 1) & 1) ^ 1u, s_abort,
                                            p.err, ERR_TIMEOUT_MMA))
           break;
         tc_fence_after();
         for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_bounded<true, true>(smem_u32(&full[stage]), ph, s_abort, p.err,
+          if (!wait_pair(smem_u32(&full[stage]), ph, s_abort, p.err,
                                              ERR_TIMEOUT_MMA)) {
             ok = false;
             break;
@@ -313,7 +493,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (it > 0) {
         umma_commit_pair_local(smem_u32(fin));
         volatile int no_abort = 0;
-        mbar_wait_bounded<true, true>(smem_u32(fin), 0, &no_abort, p.err, ERR_TIMEOUT_MMA);
+        wait_pair(smem_u32(fin), 0, &no_abort, p.err, ERR_TIMEOUT_MMA);
       }
     }
   } else {
@@ -326,7 +506,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int acc = it & 1;
       int ok = 1;
       if (lane == 0)
-        ok = mbar_wait_bounded<true, true>(smem_u32(&tfull[acc]), (it >> 1) & 1, s_abort, p.err,
+        ok = wait_pair(smem_u32(&tfull[acc]), (it >> 1) & 1, s_abort, p.err,
                                            ERR_TIMEOUT_EPILOGUE);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
@@ -346,15 +526,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             else mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
           }
         }
-        if (m < p.epi.M) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            float f[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[j + i]);
-            epilogue8(p.epi, m, n0 + 32 * s + j, f);
-          }
-        }
+        epilogue32<ACT, false>(p.epi, m, n0 + 32 * s, v);
       }
     }
   }
@@ -365,13 +537,304 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+// ========================================= CTA pairs, sums in registers
+// The same 256 x 256 pair tiles for two cases.
+//
+// fp32 results.  The tensor core truncates each addition into its fp32
+// accumulator, a bias toward zero that grows with the number of additions:
+// measured 1.0e-6 of the result per 1024 of the contraction (7.9e-6 at 7168,
+// where fp32 arithmetic has 0.9e-6).  So an accumulator takes 512 of the
+// contraction, and the epilogue warps add each such part in registers,
+// rounding to nearest, while the other accumulator is filled: 5e-7 at any
+// length, and the additions hide under the products.
+//
+// Few tiles.  A cluster of S pairs shares a tile: pair i takes the i-th part of
+// the contraction, and the pairs' sums are joined as said above.
+//
+// 320 threads: producer, MMA, 8 epilogue warps (a thread: one row, 128 columns).
+constexpr int kAThreads = 320;
+constexpr int kASeg = 4;          // stages (of 128) per part
+constexpr int kAStride = 260;     // floats per staged row: 256 + 4 (no bank conflicts)
+static_assert(128 * kAStride * 4 <= kPOffBar, "staged tile fits the ring");
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Arrive on the mbarrier at shared offset `bar` in the CTAs of `mask` when
+// this thread's tcgen05 operations so far have completed.
+__device__ __forceinline__ void umma_commit_pair_mask(uint32_t bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar), "h"(mask)
+      : "memory");
+}
+
+// ACT: the activation without a split (fp32 results); with one it is read from
+// the arguments, in the single copy of the joining epilogue.
+template <bool A_MN, bool B_MN, bool SPLIT, int ACT>
+__global__ void __launch_bounds__(kAThreads, 1)
+    linear_sums_kernel(const __grid_constant__ CUtensorMap tm_a,
+                       const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ LinearDev p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kPOffBar);
+  uint64_t* full = bars;                  // leader: both CTAs' loads of a stage landed
+  uint64_t* empty = bars + kPStages;      // both: the stage's MMAs are done
+  uint64_t* tfull = bars + 2 * kPStages;  // both: a part is complete
+  uint64_t* tempty = tfull + 2;           // leader: both CTAs have read it
+  uint64_t* fin = tempty + 2;             // leader: every MMA done
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kPOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kPOffMisc + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int crank = static_cast<int>(cluster_ctarank());
+  const int rank = crank & 1, pair = crank >> 1, S = SPLIT ? p.split : 1;
+  const uint32_t lead = static_cast<uint32_t>(crank & ~1);
+  const uint16_t both = static_cast<uint16_t>(3u << lead);
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&tfull[a]), 1);
+      mbar_init(smem_u32(&tempty[a]), 16);
+    }
+    mbar_init(smem_u32(fin), 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  cluster_sync_all();
+  if (warp == 1) tmem_alloc_pair(smem_u32(s_tmem), 512);
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  const int mt = (p.epi.M + 255) >> 8, nt = (p.epi.N + 255) >> 8;
+  const int total = mt * nt;
+  const int KB = (p.K + 2 * BK - 1) / (2 * BK);
+  const int kb0 = static_cast<int>(static_cast<long>(KB) * pair / S);
+  const int kb1 = static_cast<int>(static_cast<long>(KB) * (pair + 1) / S);
+  const int cid = blockIdx.x / (2 * S), ncl = gridDim.x / (2 * S);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < total; tile += ncl) {
+        int mi, ni;
+        pair_tile(tile, mt, nt, p.group, &mi, &ni);
+        const int arow = mi * 256 + 128 * rank, brow = ni * 256 + 128 * rank;
+        // tiles begin at different places of their part, so that the tiles in
+        // flight do not all ask for the same lines of the other operand at once
+        int kb = kb0 + static_cast<int>(static_cast<long>(tile) * 5 % (kb1 - kb0));
+        for (int left = kb1 - kb0; left > 0; --left) {
+          if (!wait_pair(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err,
+                                             ERR_TIMEOUT_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = smem_u32(&full[stage]);
+          if (rank == 0) mbar_arrive_expect_tx(fb_local, 2u * 2u * kPOper);
+          const uint32_t fb = mapa_shared(fb_local, lead);
+          const uint32_t a_dst = smem_u32(smem + stage * kPOper);
+          const uint32_t b_dst = smem_u32(smem + kPOffB + stage * kPOper);
+          const int k0 = kb * 2 * BK;
+          if (++kb == kb1) kb = kb0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (A_MN) tma_load_2d_pair(&tm_a, fb, a_dst + h * kPSlab, arow + BK * h, k0);
+            else tma_load_2d_pair(&tm_a, fb, a_dst + h * kPSlab, k0 + BK * h, arow);
+            if (B_MN) tma_load_2d_pair(&tm_b, fb, b_dst + h * kPSlab, brow + BK * h, k0);
+            else tma_load_2d_pair(&tm_b, fb, b_dst + h * kPSlab, k0 + BK * h, brow);
+          }
+          issued |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (ph << stage);
+          if (++stage == kPStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // drain: the leader until every issued stage's loads (both CTAs')
+      // landed, the other until its last loads of each stage were consumed
+      for (int s = 0; s < kPStages; ++s) {
+        if ((issued >> s) & 1u) {
+          volatile int no_abort = 0;
+          const uint32_t par = (last_par >> s) & 1u;
+          wait_pair(smem_u32(rank == 0 ? &full[s] : &empty[s]), par, &no_abort,
+                                        p.err, ERR_TIMEOUT_PRODUCER, kDrainCycles);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_bf16_order(256, 256, A_MN, B_MN);
+      int stage = 0, it = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < total; tile += ncl) {
+        for (int kb = kb0; ok && kb < kb1; ++it) {
+          const int acc = it & 1;
+          if (!wait_pair(smem_u32(&tempty[acc]), ((it >> 1) & 1) ^ 1u, s_abort,
+                                             p.err, ERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int end = min(kb + kASeg, kb1);
+          for (bool first = true; kb < end; ++kb, first = false) {
+            if (!wait_pair(smem_u32(&full[stage]), ph, s_abort, p.err,
+                                               ERR_TIMEOUT_MMA)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t as = smem_u32(smem + stage * kPOper);
+            const uint32_t bs = smem_u32(smem + kPOffB + stage * kPOper);
+            const uint64_t ad = A_MN ? sdesc_mn_sw128(as, kPSlab) : sdesc_k_sw128(as);
+            const uint64_t bd = B_MN ? sdesc_mn_sw128(bs, kPSlab) : sdesc_k_sw128(bs);
+#pragma unroll
+            for (int kk = 0; kk < 2 * BK / 16; ++kk) {
+              const uint32_t koff = ((kk >> 2) * kPSlab >> 4) + 2 * (kk & 3), moff = kk * 128;
+              umma_f16_pair(tmem + acc * 256, ad + (A_MN ? moff : koff), bd + (B_MN ? moff : koff),
+                            idesc, (!first || kk != 0) ? 1u : 0u);
+            }
+            umma_commit_pair_mask(smem_u32(&empty[stage]), both);
+            if (++stage == kPStages) {
+              stage = 0;
+              ph ^= 1u;
+            }
+          }
+          if (ok) umma_commit_pair_mask(smem_u32(&tfull[acc]), both);
+        }
+      }
+      if (it > 0) {
+        umma_commit_pair_local(smem_u32(fin));
+        volatile int no_abort = 0;
+        wait_pair(smem_u32(fin), 0, &no_abort, p.err, ERR_TIMEOUT_MMA);
+      }
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, column half
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 128 * half;
+    auto release = [&](int buf) {  // this warp has read the part
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(smem_u32(&tempty[buf]));
+        else mbar_arrive_remote(mapa_shared(smem_u32(&tempty[buf]), lead));
+      }
+    };
+    int it = 0;
+    for (int tile = cid; tile < total; tile += ncl) {
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      int ok = 1;
+#pragma unroll 1
+      for (int kb = kb0; kb < kb1; kb += kASeg, ++it) {
+        const int buf = it & 1;
+        if (lane == 0)
+          ok = wait_pair(smem_u32(&tfull[buf]), (it >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tl + buf * 256 + 32 * s, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[32 * s + i] += __uint_as_float(v[i]);
+        }
+        if (SPLIT || kb + kASeg < kb1) release(buf);
+      }
+      if (!ok) break;
+      if (SPLIT) {
+        // one tile per cluster: the last part has been read, so every load
+        // has landed and every product is done
+        float* row = reinterpret_cast<float*>(smem) + (32 * q + lane) * kAStride + 128 * half;
+#pragma unroll
+        for (int j = 0; j < 128; j += 4)
+          *reinterpret_cast<float4*>(row + j) =
+              make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+      } else {
+        // back into the last part's accumulator, so that the epilogue is a
+        // loop over TMEM columns (one copy of its code) and not over registers
+        const int buf = (it & 1) ^ 1;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * s + i]);
+          tmem_st_32x32b_x32(tl + buf * 256 + 32 * s, v);
+        }
+        tmem_st_wait();
+        int mi, ni;
+        pair_tile(tile, mt, nt, p.group, &mi, &ni);
+        const long m = static_cast<long>(mi) * 256 + 128 * rank + 32 * q + lane;
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(tl + buf * 256 + 32 * s, v);
+          tmem_ld_wait();
+          epilogue32<ACT, true>(p.epi, m, ni * 256 + 128 * half + 32 * s, v);
+        }
+        release(buf);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  const float* const stg = reinterpret_cast<const float*>(smem);
+  const int rows = 128 / S;
+  if (SPLIT)
+    hand_over<kAThreads, 32, kAStride>(stg, p.parts + static_cast<long>(blockIdx.x) * 128 * 256,
+                                       pair * rows, rows);
+  __syncwarp();
+  cluster_sync_all();  // sums handed over; without a split: nobody is still signalling
+  tc_fence_after();
+  if (SPLIT && !*s_abort) {
+    int mi, ni;
+    pair_tile(cid, mt, nt, p.group, &mi, &ni);
+    // the CTAs of this rank of each pair, two apart
+    join_rows<kAThreads, 32, kAStride>(
+        p.epi, stg, p.parts + static_cast<long>(blockIdx.x - 2 * pair) * 128 * 256, 2l * 128 * 256,
+        S, pair, pair * rows, rows, static_cast<long>(mi) * 256 + 128 * rank, ni * 256);
+  }
+  __syncwarp();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
 // ====================================================== split tile kernel
 // One 128 x 128 tile per cluster of S CTAs; CTA r takes the r-th part of the
-// contraction.  The parts are added through distributed shared memory: each
-// CTA leaves its accumulator in its own shared memory, and CTA r adds rows
-// r * 128/S .. of all S in rank order (so the result does not depend on
-// timing) and runs the epilogue on them.  No scratch in global memory, one
-// launch.
+// contraction (at least one stage), in two accumulators, which halves the
+// tensor core's truncation; the CTAs' sums are joined as said above.  Two CTAs
+// fit an SM (with 256 TMEM columns each).
 constexpr int kTStages = 3;
 constexpr int kTThreads = 192;
 constexpr int kTOper = 128 * BK * 2;             // 16 KB: one operand's part of a stage
@@ -383,19 +846,10 @@ constexpr int kTSmem = kTOffMisc + 16 + 1024;
 constexpr int kTStride = 132;                    // floats per staged row: 128 + 4 (no bank conflicts)
 static_assert(128 * kTStride * 4 <= kTOffBar, "staged tile fits the ring");
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 template <bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kTThreads)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
-                       const __grid_constant__ CUtensorMap tm_b, const LinearDev p) {
+                       const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ LinearDev p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -421,7 +875,7 @@ __global__ void __launch_bounds__(kTThreads)
     tma_prefetch_desc(&tm_a);
     tma_prefetch_desc(&tm_b);
   }
-  if (warp == 1) tmem_alloc(smem_u32(s_tmem), 128);
+  if (warp == 1) tmem_alloc(smem_u32(s_tmem), 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -433,13 +887,14 @@ __global__ void __launch_bounds__(kTThreads)
   const int KB = (p.K + BK - 1) / BK;
   const int kb0 = static_cast<int>(static_cast<long>(KB) * rank / S);
   const int kb1 = static_cast<int>(static_cast<long>(KB) * (rank + 1) / S);
+  const int kmid = kb0 + (kb1 - kb0 + 1) / 2;  // from here on the second accumulator
   int ok = 1;
   if (warp == 0) {
     if (lane == 0) {
       int stage = 0;
       uint32_t ph = 0, issued = 0, last_par = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded<true>(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err,
+        if (!wait_cta(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err,
                                      ERR_TIMEOUT_PRODUCER))
           break;
         const uint32_t fb = smem_u32(&full[stage]);
@@ -469,8 +924,8 @@ __global__ void __launch_bounds__(kTThreads)
       for (int s = 0; s < kTStages; ++s) {  // nothing in flight when the ring is reused
         if ((issued >> s) & 1u) {
           volatile int no_abort = 0;
-          mbar_wait_bounded<true>(smem_u32(&full[s]), (last_par >> s) & 1u, &no_abort, p.err,
-                                  ERR_TIMEOUT_PRODUCER, 20000000ull);
+          wait_cta(smem_u32(&full[s]), (last_par >> s) & 1u, &no_abort, p.err,
+                                  ERR_TIMEOUT_PRODUCER, kDrainCycles);
         }
       }
     }
@@ -480,7 +935,7 @@ __global__ void __launch_bounds__(kTThreads)
       int stage = 0;
       uint32_t ph = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded<true>(smem_u32(&full[stage]), ph, s_abort, p.err, ERR_TIMEOUT_MMA))
+        if (!wait_cta(smem_u32(&full[stage]), ph, s_abort, p.err, ERR_TIMEOUT_MMA))
           break;
         tc_fence_after();
         const uint32_t as = smem_u32(smem + stage * kTOper);
@@ -489,8 +944,9 @@ __global__ void __launch_bounds__(kTThreads)
         const uint64_t bd = B_MN ? sdesc_mn_sw128(bs, kTOper / 2) : sdesc_k_sw128(bs);
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          umma_f16(tmem, ad + (A_MN ? kk * 128 : kk * 2), bd + (B_MN ? kk * 128 : kk * 2), idesc,
-                   (kb > kb0 || kk > 0) ? 1u : 0u);
+          umma_f16(tmem + (kb < kmid ? 0 : 128), ad + (A_MN ? kk * 128 : kk * 2),
+                   bd + (B_MN ? kk * 128 : kk * 2), idesc,
+                   (kk > 0 || (kb != kb0 && kb != kmid)) ? 1u : 0u);
         umma_commit(smem_u32(&empty[stage]));
         if (++stage == kTStages) {
           stage = 0;
@@ -501,54 +957,50 @@ __global__ void __launch_bounds__(kTThreads)
     }
   }
   // every thread waits for the last product: after it the ring is free
-  if (!mbar_wait_bounded<true>(smem_u32(done), 0, s_abort, p.err, ERR_TIMEOUT_EPILOGUE) || *s_abort)
+  if (!wait_cta(smem_u32(done), 0, s_abort, p.err, ERR_TIMEOUT_EPILOGUE) || *s_abort)
     ok = 0;
   __syncthreads();
   __syncwarp();
   tc_fence_after();
-  float* stg = reinterpret_cast<float*>(smem);
   if (warp >= 2) {
     const int q = warp & 3;
-    const int row = 32 * q + lane;
-#pragma unroll
+    float* row = reinterpret_cast<float*>(smem) + (32 * q + lane) * kTStride;
+#pragma unroll 1
     for (int s = 0; s < 4; ++s) {
       uint32_t v[32];
       tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + 32 * s, v);
       tmem_ld_wait();
+      if (kmid < kb1) {
+        uint32_t u[32];
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + 128 + 32 * s, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+      }
 #pragma unroll
       for (int j = 0; j < 32; j += 4)
-        *reinterpret_cast<float4*>(stg + row * kTStride + 32 * s + j) =
-            kb1 > kb0 ? make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
-                                    __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]))
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(row + 32 * s + j) =
+            make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]),
+                        __uint_as_float(v[j + 3]));
     }
     tc_fence_before();
   }
-  __syncwarp();
-  if (S > 1) cluster_sync_all();
-  else __syncthreads();
-  if (ok) {
-    const int rows = 128 / S;
-    for (int i = threadIdx.x; i < rows * 16; i += kTThreads) {
-      const int row = rank * rows + (i >> 4), col = (i & 15) * 8;
-      const long m = static_cast<long>(mi) * 128 + row;
-      if (m >= p.epi.M || ni * 128 + col >= p.epi.N) continue;
-      const uint32_t at = smem_u32(stg + row * kTStride + col);
-      float f[8] = {};
-      for (int r = 0; r < S; ++r) {
-        const uint32_t o = mapa_shared(at, r);
-        const float4 a = ld_cluster_f4(o), b = ld_cluster_f4(o + 16);
-        f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
-        f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
-      }
-      epilogue8(p.epi, m, ni * 128 + col, f);
-    }
+  __syncthreads();
+  const float* const stg = reinterpret_cast<const float*>(smem);
+  const int rows = 128 / S;
+  if (S > 1) {
+    hand_over<kTThreads, 16, kTStride>(stg, p.parts + static_cast<long>(blockIdx.x) * 128 * 128,
+                                       rank * rows, rows);
+    __syncwarp();
+    cluster_sync_all();  // sums handed over
   }
-  __syncwarp();
-  if (S > 1) cluster_sync_all();  // the others have read this CTA's part
-  else __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 128);
+  if (warp == 1) tmem_dealloc(tmem, 256);
+  if (ok)
+    join_rows<kTThreads, 16, kTStride>(
+        p.epi, stg, p.parts + static_cast<long>(blockIdx.x - rank) * 128 * 128, 128l * 128, S, rank,
+        rank * rows, rows, static_cast<long>(mi) * 128, ni * 128);
 }
 
 // ====================================================== few tokens
@@ -712,10 +1164,10 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <bool A_MN, bool B_MN>
+template <bool A_MN, bool B_MN, int ACT>
 cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, LinearDev p,
                         cudaStream_t s) {
-  auto kern = linear_pair_kernel<A_MN, B_MN>;
+  auto kern = linear_pair_kernel<A_MN, B_MN, ACT>;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -746,6 +1198,53 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Linear
   const long tiles = static_cast<long>(ceil_div(p.epi.M, 256)) * ceil_div(p.epi.N, 256);
   p.group = 8;
   cfg.gridDim = dim3(2 * static_cast<int>(std::min<long>(nc, tiles)));
+  cfg.stream = s;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, kern, tm_a, tm_b, p);
+  count_launches(1);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <bool A_MN, bool B_MN, bool SPLIT, int ACT>
+cudaError_t launch_sums(const CUtensorMap& tm_a, const CUtensorMap& tm_b, LinearDev p, int split,
+                        cudaStream_t s) {
+  auto kern = linear_sums_kernel<A_MN, B_MN, SPLIT, ACT>;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * split);
+  cfg.blockDim = dim3(kAThreads);
+  cfg.dynamicSmemBytes = kPSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static std::atomic<int> max_clusters[64] = {};  // pairs without a split
+  int nc = max_clusters[dev].load(std::memory_order_acquire);
+  if (nc == 0) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
+    if (err != cudaSuccess) return err;
+    cfg.gridDim = dim3(2);
+    attr[0].val.clusterDim.x = 2;
+    err = cudaOccupancyMaxActiveClusters(&nc, kern, &cfg);
+    if (err != cudaSuccess) return err;
+    if (nc < 1) return cudaErrorLaunchOutOfResources;
+    max_clusters[dev].store(nc, std::memory_order_release);
+    attr[0].val.clusterDim.x = 2 * split;
+  }
+  const long tiles = static_cast<long>(ceil_div(p.epi.M, 256)) * ceil_div(p.epi.N, 256);
+  p.group = 8;
+  p.split = split;
+  // without a split the pairs stay and walk over the tiles; with one a
+  // cluster takes one tile
+  cfg.gridDim = dim3(2 * split * static_cast<int>(split > 1 ? tiles : std::min<long>(nc, tiles)));
   cfg.stream = s;
   cfg.numAttrs = 2;
   err = cudaLaunchKernelEx(&cfg, kern, tm_a, tm_b, p);
@@ -804,30 +1303,79 @@ cudaError_t launch_gemv_w(const LinearGemvArgs& a, int num_sms, cudaStream_t s) 
 
 }  // namespace
 
-// Tiles of 256 x 256 on CTA pairs from half a wave of them; below, 128 x 128
-// tiles whose contraction is split over up to 8 CTAs until the grid covers
-// the GPU twice (two such CTAs fit an SM), each part at least 4 stages long.
-LinearPath linear_path(long M, long N, long K, int num_sms) {
+// Which kernel, and how many parts of the contraction.  256 x 256 tiles on
+// persistent pairs from half a wave of them (measured, bf16: 512 x 2048 x 7168,
+// 56 tiles, 20.2 us against 21.6 in 128 x 128 tiles).  Below, 128 x 128 tiles
+// with the contraction split until the grid covers the GPU twice (two such
+// CTAs fit an SM), each part at least 4 stages long: 64 x 7168 x 4096 21 us
+// against 29 on split pairs, 1024 x 2048 x 2048 15.3 against 16.9.  Two pairs
+// per tile where that gives most of a wave of full tiles and the contraction
+// is long, so that reading the operands counts (8192 x 7168 x 256 34 us against
+// 36, but 8192 x 7168 x 64 31 against 28), or
+// where an fp32 result would have more than 1024 of the contraction in one
+// accumulator.
+LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms) {
   LinearPath r;
   const long big = static_cast<long>(ceil_div(M, 256)) * ceil_div(N, 256);
-  r.pair = big >= num_sms / 4;
+  const long pairs = std::min(num_sms, kLinearMaxParts / 2) / 2;
   r.split = 1;
+  if (big >= pairs / 2) {
+    r.kind = out_f32 ? LinearPath::kSums : LinearPath::kPair;
+    return r;
+  }
+  r.kind = LinearPath::kTile;
   const long tiles = static_cast<long>(ceil_div(M, 128)) * ceil_div(N, 128);
-  while (r.split < 8 && tiles * r.split * 2 <= 2L * num_sms && K / (r.split * 2) >= 4 * BK)
+  while (r.split < 8 && tiles * r.split * 2 <= 4 * pairs && K / (r.split * 2) >= 4 * BK)
     r.split *= 2;
+  if ((big * 8 >= pairs * 3 && 3 * big <= tiles && K >= 64 * BK) || (out_f32 && K / (2 * r.split) > 16 * BK && r.split < 8)) {
+    r.kind = LinearPath::kSums;  // 2 * big <= pairs here
+    r.split = 2;
+  }
   return r;
 }
 
 cudaError_t launch_linear(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const LinearDev& p,
                           bool a_mn, bool b_mn, const LinearPath& path, cudaStream_t s) {
-  if (path.pair) {
-    if (!a_mn && !b_mn) return launch_pair<false, false>(tm_a, tm_b, p, s);
-    if (!a_mn) return launch_pair<false, true>(tm_a, tm_b, p, s);
-    return launch_pair<true, true>(tm_a, tm_b, p, s);
+  constexpr int kNone = MOE_ACT_NONE;
+  const int act = p.epi.act;
+  // what each kernel supports, whatever chose the path: the CTA-pair kernel
+  // stores bf16, the register sums fp32 unless they are joined, a split has
+  // no empty part and its sums fit the workspace
+  const bool sums = path.kind == LinearPath::kSums;
+  const long parts = static_cast<long>(path.split) *
+                     (sums ? 4l * ceil_div(p.epi.M, 256) * ceil_div(p.epi.N, 256)
+                           : static_cast<long>(ceil_div(p.epi.M, 128)) * ceil_div(p.epi.N, 128));
+  const int stages = ceil_div(p.K, sums ? 2 * BK : BK);
+  if ((path.kind == LinearPath::kPair && p.epi.out_f32) ||
+      (sums && (path.split > 2 || (path.split == 1 && (!p.epi.out_f32 || a_mn || b_mn)))) ||
+      (path.split != 1 && path.split != 2 && path.split != 4 && path.split != 8) ||
+      (path.split > 1 && (path.split > stages || parts > kLinearMaxParts)))
+    return cudaErrorInvalidValue;
+  if (path.kind == LinearPath::kPair) {
+    if (a_mn) return launch_pair<true, true, kNone>(tm_a, tm_b, p, s);
+    if (b_mn) return launch_pair<false, true, kNone>(tm_a, tm_b, p, s);
+    if (act == MOE_ACT_SILU) return launch_pair<false, false, MOE_ACT_SILU>(tm_a, tm_b, p, s);
+    if (act == MOE_ACT_GELU) return launch_pair<false, false, MOE_ACT_GELU>(tm_a, tm_b, p, s);
+    if (act == MOE_ACT_RELU) return launch_pair<false, false, MOE_ACT_RELU>(tm_a, tm_b, p, s);
+    return launch_pair<false, false, kNone>(tm_a, tm_b, p, s);
   }
-  if (!a_mn && !b_mn) return launch_tile<false, false>(tm_a, tm_b, p, path.split, s);
-  if (!a_mn) return launch_tile<false, true>(tm_a, tm_b, p, path.split, s);
-  return launch_tile<true, true>(tm_a, tm_b, p, path.split, s);
+  if (path.kind == LinearPath::kSums) {
+    const int n = path.split;
+    // without a split only for fp32 results, which the gradients' products have not
+    if (a_mn) return launch_sums<true, true, true, kNone>(tm_a, tm_b, p, n, s);
+    if (b_mn) return launch_sums<false, true, true, kNone>(tm_a, tm_b, p, n, s);
+    if (n > 1) return launch_sums<false, false, true, kNone>(tm_a, tm_b, p, n, s);
+    if (act == MOE_ACT_SILU)
+      return launch_sums<false, false, false, MOE_ACT_SILU>(tm_a, tm_b, p, n, s);
+    if (act == MOE_ACT_GELU)
+      return launch_sums<false, false, false, MOE_ACT_GELU>(tm_a, tm_b, p, n, s);
+    if (act == MOE_ACT_RELU)
+      return launch_sums<false, false, false, MOE_ACT_RELU>(tm_a, tm_b, p, n, s);
+    return launch_sums<false, false, false, kNone>(tm_a, tm_b, p, n, s);
+  }
+  if (a_mn) return launch_tile<true, true>(tm_a, tm_b, p, path.split, s);
+  if (b_mn) return launch_tile<false, true>(tm_a, tm_b, p, path.split, s);
+  return launch_tile<false, false>(tm_a, tm_b, p, path.split, s);
 }
 
 cudaError_t launch_linear_gemv(const LinearGemvArgs& a, int num_sms, cudaStream_t s) {

@@ -389,17 +389,22 @@ struct LinearEpi {
   int M, N, act;           // act: a moe_activation or MOE_ACT_NONE
   bool bias_bf16, out_f32, vec;
 };
+// CTAs of 128 x 128 sums that a split contraction hands over, at most (a CTA
+// pair's CTA counts as two): two CTAs per SM of 152.
+constexpr int kLinearMaxParts = 304;
+constexpr size_t kLinearWsBytes = 1024 + static_cast<size_t>(kLinearMaxParts) * 128 * 128 * 4;
 struct LinearDev {
   LinearEpi epi;
   int K;                   // contraction length
   int split, group;
+  float* parts;            // the CTAs' sums of a split contraction: kLinearMaxParts x 128 x 128
   int* err;
 };
 struct LinearPath {
-  bool pair;
+  enum Kind { kPair, kSums, kTile } kind;
   int split;
 };
-LinearPath linear_path(long M, long N, long K, int num_sms);
+LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms);
 // D[M, N] = A B^T with the operands' orders (a_mn, b_mn: false, false /
 // false, true / true, true); the maps' boxes are those linear_boxes names.
 cudaError_t launch_linear(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const LinearDev& p,

@@ -77,7 +77,7 @@ def test_block_norm_backward(L, kw, status):
 
 
 def lin(L, x=P, ld_x=64, w=P, ld_w=64, bias=NUL, bdt=0, act=-1, res=NUL, ld_res=0, T=4, K=64, N=32, out=P, odt=0,
-        ld_out=32, z=NUL, ws=P, wsb=1024):
+        ld_out=32, z=NUL, ws=P, wsb=1 << 30):
     return L.moe_linear(x, ld_x, w, ld_w, bias, bdt, act, res, ld_res, T, K, N, out, odt, ld_out, z, ws, wsb, NUL)
 
 

@@ -289,6 +289,24 @@ def test_linear_and_gradient(moe, T, K, N, act):
     moe.workspace_status(moe.default_workspace())
 
 
+@pytest.mark.parametrize("T,K,N,act", [(1800, 4104, 1000, "silu"), (2300, 5000, 1030, "gelu"), (130, 7168, 260, None),
+                                       (600, 6152, 1500, "relu")])
+def test_linear_fp32_results_of_long_contractions(moe, T, K, N, act):
+    """fp32 results: at most 1024 of the contraction is added in one tensor-core
+    accumulator, whatever its length; the sums of those parts are fp32 (F32)."""
+    g = _rng(T, K, N)
+    x, w = _dev(g.normal(size=(T, K)), torch.bfloat16), _dev(g.normal(size=(N, K)) / K ** 0.5, torch.bfloat16)
+    b, r = _dev(g.normal(size=N)), _dev(g.normal(size=(T, N)))
+    ry, rz = B.linear(_np(x), _np(w), _np(b), act, _np(r))
+    y, z = moe.linear(x, w, bias=b, activation=act, residual=r, out_dtype=torch.float32, preact=True)
+    mag = np.abs(_np(x)) @ np.abs(_np(w)).T + np.abs(rz) + np.abs(_np(r))
+    _close(z, rz, mag, False, _acc(1024))
+    _close(y, ry, 1.2 * mag, False, _acc(1024) + 2.0 ** -21)
+    # truncation of 1024 / 16 additions, half a unit on average, is 2^-18 of the result at most
+    assert np.linalg.norm(_np(z) - rz) < 2.0 ** -18 * np.linalg.norm(rz)
+    moe.workspace_status(moe.default_workspace())
+
+
 def test_linear_strides_in_place_and_parts(moe):
     g = _rng(11)
     big = _dev(g.normal(size=(70, 400)), torch.bfloat16)
