@@ -590,6 +590,16 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
                                const void* preact, int64_t ld_z, int T, int K, int N, void* dx,
                                void* dw, float* dbias, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * moe_call_packed - one of the six calls above with its arguments in a block of
+ * 8-byte slots in the function's order: pointers and integers as int64_t,
+ * floats as double.  For bindings that pay per argument.
+ *   call   0 moe_route_scored, 1 moe_route_scored_backward, 2 moe_block_norm,
+ *          3 moe_block_norm_backward, 4 moe_linear, 5 moe_linear_backward;
+ *          any other: MOE_ERR_INVALID_ARG
+ */
+moe_status moe_call_packed(int call, const void* block);
+
 #ifdef __cplusplus
 }
 #endif

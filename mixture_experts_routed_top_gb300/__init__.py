@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -92,6 +93,7 @@ _SIGS = {
     "moe_block_norm_backward_workspace_size": ([_I], _SZ),
     "moe_block_norm_backward": ([_P, _L, _P, _L, _P, _I, _L, _P, _L, _P, _I, _I, _L, _F, _I, _P, _P,
                                  _I, _F, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P], _I),
+    "moe_call_packed": ([_I, ctypes.c_char_p], _I),
     "moe_linear_workspace_size": ([], _SZ),
     "moe_linear": ([_P, _L, _P, _L, _P, _I, _I, _P, _L, _I, _I, _I, _P, _I, _L, _P, _P, _SZ, _P], _I),
     "moe_linear_backward_workspace_size": ([_I, _I], _SZ),
@@ -301,9 +303,19 @@ def default_workspace(device="cuda") -> Workspace:
 _BF16, _F32 = torch.bfloat16, torch.float32
 _DT = {_BF16: 0, _F32: 1}
 _SCORES = {"softmax": 0, "sigmoid": 1}
-_ONLY_F32, _ONLY_BF16 = (_F32,), (_BF16,)
+_ONLY_F32, _ONLY_BF16, _ONLY_I32 = (_F32,), (_BF16,), (torch.int32,)
 _ACT_NONE = -1
 _LINEAR_WS = 0  # the library's constant, once it is loaded
+
+
+# Calls of moe_call_packed and the slots of their argument blocks (q integer or
+# pointer, d float); the stream is the last.
+_ROUTE = (0, struct.Struct("=12qd3q").pack)
+_ROUTE_BWD = (1, struct.Struct("=9qd6q").pack)
+_NORM = (2, struct.Struct("=9qd5qd5q").pack)
+_NORM_BWD = (3, struct.Struct("=13qd4qd10q").pack)
+_LINEAR = (4, struct.Struct("=19q").pack)
+_LINEAR_BWD = (5, struct.Struct("=19q").pack)
 
 
 def _bad(name: str, what: str):
@@ -314,47 +326,33 @@ def _names(dtypes) -> str:
     return " or ".join(str(d)[6:] for d in dtypes)
 
 
-def _mat(name: str, t: torch.Tensor, dtypes, rows: int, cols: int, dev: int) -> int:
-    """Checks a matrix [rows, cols] on device dev, its rows contiguous; -> its row stride."""
-    if t.shape != (rows, cols) or t.dtype not in dtypes or t.get_device() != dev:
-        _bad(name, f"a tensor [{rows}, {cols}] of {_names(dtypes)} on CUDA device {dev}")
+def _mat(name: str, t: torch.Tensor, dtypes, shape, dev: int) -> int:
+    """Checks a matrix of this shape on device dev, its rows contiguous; -> its row stride."""
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev:
+        _bad(name, f"a tensor {list(shape)} of {_names(dtypes)} on CUDA device {dev}")
     ld, one = t.stride()
-    if one != 1 and cols > 1:
+    if one != 1 and shape[1] > 1:
         _bad(name, "contiguous along its rows")
-    return ld if rows > 1 else cols
+    return ld if shape[0] > 1 else shape[1]
 
 
-def _vec(name: str, t: torch.Tensor, dtypes, n: int, dev: int):
-    if t.shape != (n,) or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
-        _bad(name, f"a contiguous tensor [{n}] of {_names(dtypes)} on CUDA device {dev}")
+def _dense(name: str, t: torch.Tensor, dtypes, shape, dev: int) -> int:
+    """Checks a contiguous tensor of this shape; -> its address."""
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
+        _bad(name, f"a contiguous tensor {list(shape)} of {_names(dtypes)} on CUDA device {dev}")
+    return t.data_ptr()
 
 
-def _out(name: str, t: torch.Tensor, shape, dtype, dev: int):
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
-        _bad(name, f"a contiguous tensor {list(shape)} of {str(dtype)[6:]} on CUDA device {dev}")
-
-
-def _device_of(name: str, t: torch.Tensor) -> int:
-    dev = t.get_device()
-    if dev < 0 or t.dim() != 2:
-        _bad(name, "a 2-D CUDA tensor")
-    return dev
-
-
-def _call(fn, dev: int, stream, args):
-    """The C call on `dev`: the stream appended, the device made current."""
-    cur = _raw_device()
-    if cur == dev:
-        status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+def _call(call, dev: int, stream, *args):
+    """One of the packed calls on device `dev`: the stream appended, the device made current."""
+    L = _LIB or lib()
+    if _raw_device() == dev:
+        status = L.moe_call_packed(call[0], call[1](*args, _raw_stream(dev) if stream is None else stream.cuda_stream))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+            status = L.moe_call_packed(call[0], call[1](*args, _raw_stream(dev) if stream is None else stream.cuda_stream))
     if status:
         _check(status)
-
-
-def _p(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
 
 
 def _workspace(workspace: Optional[Workspace], device, nbytes: int) -> torch.Tensor:
@@ -363,6 +361,21 @@ def _workspace(workspace: Optional[Workspace], device, nbytes: int) -> torch.Ten
         if workspace is None:
             workspace = _DEFAULT_WS.setdefault(device, Workspace(device))
     return workspace.get(nbytes)
+
+
+def _matrix_of(name: str, t: torch.Tensor):
+    """-> the device index and shape of a CUDA matrix."""
+    dev, shape = t.get_device(), t.shape
+    if dev < 0 or len(shape) != 2:
+        _bad(name, "a 2-D CUDA tensor")
+    return dev, shape
+
+
+def _score_of(score: str) -> int:
+    sc = _SCORES.get(score)
+    if sc is None:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    return sc
 
 
 def route_scored(logits: torch.Tensor, k: int, *, score: str = "sigmoid",
@@ -378,23 +391,20 @@ def route_scored(logits: torch.Tensor, k: int, *, score: str = "sigmoid",
     (1 or 2) best; the chosen scores are divided by their sum if renormalise,
     then multiplied by scale.  Experts with a logit of -inf or NaN are masked.
     out: (topk_idx, topk_w) to write into."""
-    dev = _device_of("logits", logits)
-    T, E = logits.shape
-    ld = _mat("logits", logits, _DT, T, E, dev)
-    if bias is not None:
-        _vec("bias", bias, _ONLY_F32, E, dev)
-    if score not in _SCORES:
-        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    dev, shape = _matrix_of("logits", logits)
+    ld = _mat("logits", logits, _DT, shape, dev)
+    T, E = shape
     if out is None:
         idx = logits.new_empty((T, k), dtype=torch.int32)
         w = logits.new_empty((T, k), dtype=_F32)
+        pi, pw = idx.data_ptr(), w.data_ptr()
     else:
         idx, w = out
-        _out("topk_idx", idx, (T, k), torch.int32, dev)
-        _out("topk_w", w, (T, k), _F32, dev)
-    _call((_LIB or lib()).moe_route_scored, dev, stream,
-          (logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _SCORES[score], _p(bias), n_group, topk_group,
-           group_top, renormalise, scale, idx.data_ptr(), w.data_ptr()))
+        pi = _dense("topk_idx", idx, _ONLY_I32, (T, k), dev)
+        pw = _dense("topk_w", w, _ONLY_F32, (T, k), dev)
+    _call(_ROUTE, dev, stream, logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _score_of(score),
+          0 if bias is None else _dense("bias", bias, _ONLY_F32, (E,), dev), n_group, topk_group, group_top,
+          renormalise, scale, pi, pw)
     return idx, w
 
 
@@ -408,60 +418,53 @@ def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: 
     logits, score, bias, renormalise, scale as route_scored was called with;
     topk_idx, topk_w what it returned; grad_w fp32 [T,k].  out: a tensor to
     write into, its rows contiguous."""
-    dev = _device_of("logits", logits)
-    T, E = logits.shape
-    ld = _mat("logits", logits, _DT, T, E, dev)
-    if topk_idx.dim() != 2:
-        _bad("topk_idx", "2-D")
-    k = topk_idx.shape[1]
-    _out("topk_idx", topk_idx, (T, k), torch.int32, dev)
-    _out("topk_w", topk_w, (T, k), _F32, dev)
-    _out("grad_w", grad_w, (T, k), _F32, dev)
-    if bias is not None:
-        _vec("bias", bias, _ONLY_F32, E, dev)
-    if score not in _SCORES:
-        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    dev, shape = _matrix_of("logits", logits)
+    ld = _mat("logits", logits, _DT, shape, dev)
+    T, E = shape
+    _, slots = _matrix_of("topk_idx", topk_idx)
+    if slots[0] != T:
+        _bad("topk_idx", "[T, k]")
     if out is None:
-        out = logits.new_empty((T, E))
+        out = logits.new_empty(shape)
         ldo = E
     else:
-        ldo = _mat("out", out, (logits.dtype,), T, E, dev)
-    _call((_LIB or lib()).moe_route_scored_backward, dev, stream,
-          (logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _SCORES[score], _p(bias), renormalise, scale,
-           topk_idx.data_ptr(), topk_w.data_ptr(), grad_w.data_ptr(), out.data_ptr(), ldo))
+        ldo = _mat("out", out, (logits.dtype,), shape, dev)
+    _call(_ROUTE_BWD, dev, stream, logits.data_ptr(), _DT[logits.dtype], ld, T, E, slots[1], _score_of(score),
+          0 if bias is None else _dense("bias", bias, _ONLY_F32, (E,), dev), renormalise, scale,
+          _dense("topk_idx", topk_idx, _ONLY_I32, slots, dev), _dense("topk_w", topk_w, _ONLY_F32, slots, dev),
+          _dense("grad_w", grad_w, _ONLY_F32, slots, dev), out.data_ptr(), ldo)
     return out
 
 
-def _gate_of(gate: Optional[torch.Tensor], T: int, H: int, dev: int):
-    """-> (moe_gate kind, dtype, row stride): [H] per channel, [T] or [T,1]
-    per token, [T,H] per element.  A 1-D gate where T = H is per channel."""
-    if gate is None:
-        return 0, 0, 0
+def _gate_of(gate: torch.Tensor, shape, dev: int):
+    """-> (address, moe_gate kind, dtype, row stride): [H] per channel, [T] or
+    [T,1] per token, [T,H] per element.  A 1-D gate where T = H is per channel."""
     dt = _DT.get(gate.dtype)
     if dt is None or gate.get_device() != dev:
         _bad("gate", f"a tensor of {_names(_DT)} on CUDA device {dev}")
-    shape = gate.shape
-    if shape == (T, H) and H != 1:
-        return 3, dt, _mat("gate", gate, _DT, T, H, dev)
+    T, H = shape
+    if gate.shape == shape and H != 1:
+        return gate.data_ptr(), 3, dt, _mat("gate", gate, _DT, shape, dev)
     if not gate.is_contiguous():
         _bad("gate", "contiguous")
-    if shape == (H,):
-        return 1, dt, 0
-    if shape == (T,) or shape == (T, 1):
-        return 2, dt, 0
+    if gate.shape == (H,):
+        return gate.data_ptr(), 1, dt, 0
+    if gate.shape == (T,) or gate.shape == (T, 1):
+        return gate.data_ptr(), 2, dt, 0
     return _bad("gate", "[H] (per channel), [T] or [T, 1] (per token), or [T, H]")
 
 
-def _norm_weights(post_weight, pre_weight, H: int, dev: int) -> int:
-    """-> the dtype of the norms' weights."""
+def _norm_weights(post_weight, pre_weight, H: int, dev: int):
+    """-> the addresses of the norms' weights (0: none), their dtype."""
+    post = pre = dt = 0
     if post_weight is not None:
-        _vec("post_weight", post_weight, _DT, H, dev)
-        if pre_weight is not None and pre_weight.dtype != post_weight.dtype:
-            raise ValueError("post_weight and pre_weight must have one dtype")
+        post, dt = _dense("post_weight", post_weight, _DT, (H,), dev), _DT[post_weight.dtype]
     if pre_weight is not None:
-        _vec("pre_weight", pre_weight, _DT, H, dev)
-        return _DT[pre_weight.dtype]
-    return 0 if post_weight is None else _DT[post_weight.dtype]
+        pre = _dense("pre_weight", pre_weight, _DT, (H,), dev)
+        if post and _DT[pre_weight.dtype] != dt:
+            raise ValueError("post_weight and pre_weight must have one dtype")
+        dt = _DT[pre_weight.dtype]
+    return post, pre, dt
 
 
 def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
@@ -481,29 +484,31 @@ def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     [T] / [T,1] or [T,H], bf16 or fp32; weights [H], both bf16 or both fp32.
     out: (residual_out, normed) to write into, either of them None for a new
     tensor; residual_out may be residual."""
-    dev = _device_of("residual", residual)
-    T, H = residual.shape
-    ld_r = _mat("residual", residual, _DT, T, H, dev)
-    ld_y = 0 if y is None else _mat("y", y, _ONLY_BF16, T, H, dev)
-    kind, gate_dt, ld_g = _gate_of(gate, T, H, dev)
-    wdt = _norm_weights(post_weight, pre_weight, H, dev)
+    dev, shape = _matrix_of("residual", residual)
+    ld_r = _mat("residual", residual, _DT, shape, dev)
+    T, H = shape
+    pg, kind, gate_dt, ld_g = (0, 0, 0, 0) if gate is None else _gate_of(gate, shape, dev)
+    post, pre, wdt = _norm_weights(post_weight, pre_weight, H, dev)
     res, n = (None, None) if out is None else out
+    py = ld_y = pres = pn = 0
     if y is None:
         res = residual
-    elif res is None:
-        res = residual.new_empty((T, H))
     else:
-        _out("residual_out", res, (T, H), residual.dtype, dev)
+        py, ld_y = y.data_ptr(), _mat("y", y, _ONLY_BF16, shape, dev)
+        if res is None:
+            res = residual.new_empty(shape)
+            pres = res.data_ptr()
+        else:
+            pres = _dense("residual_out", res, (residual.dtype,), shape, dev)
     if not pre_norm:
         n = None
     elif n is None:
-        n = residual.new_empty((T, H), dtype=_BF16)
+        n = residual.new_empty(shape, dtype=_BF16)
+        pn = n.data_ptr()
     else:
-        _out("normed", n, (T, H), _BF16, dev)
-    _call((_LIB or lib()).moe_block_norm, dev, stream,
-          (residual.data_ptr(), _DT[residual.dtype], ld_r, _p(y), ld_y, _p(gate), kind, gate_dt, ld_g, scale,
-           post_norm, _p(post_weight), pre_norm, _p(pre_weight), wdt, eps, T, H,
-           None if y is None else res.data_ptr(), _p(n)))
+        pn = _dense("normed", n, _ONLY_BF16, shape, dev)
+    _call(_NORM, dev, stream, residual.data_ptr(), _DT[residual.dtype], ld_r, py, ld_y, pg, kind, gate_dt, ld_g,
+          scale, post_norm, post, pre_norm, pre, wdt, eps, T, H, pres, pn)
     return res, n
 
 
@@ -520,28 +525,35 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
     block_norm returned; the rest as it was called with.  What does not apply
     comes back as None.  d_gate is fp32 for a per-channel gate, else of the
     gate's type; the weights' gradients are fp32 [H]."""
-    dev = _device_of("residual", residual)
-    T, H = residual.shape
-    ld_r = _mat("residual", residual, _DT, T, H, dev)
-    ld_gr = 0 if grad_residual is None else _mat("grad_residual", grad_residual, (residual.dtype,), T, H, dev)
-    ld_gn = 0 if grad_normed is None else _mat("grad_normed", grad_normed, _ONLY_BF16, T, H, dev)
-    ld_y = 0 if y is None else _mat("y", y, _ONLY_BF16, T, H, dev)
-    kind, gate_dt, ld_g = _gate_of(gate, T, H, dev)
-    wdt = _norm_weights(post_weight, pre_weight, H, dev)
-    d_res = residual.new_empty((T, H))
-    d_y = None if y is None else residual.new_empty((T, H), dtype=_BF16)
-    d_gate = None
+    dev, shape = _matrix_of("residual", residual)
+    ld_r = _mat("residual", residual, _DT, shape, dev)
+    T, H = shape
+    pgr = ld_gr = pgn = ld_gn = py = ld_y = pdy = pdg = pdpost = pdpre = 0
+    d_y = d_gate = d_post = d_pre = None
+    if grad_residual is not None:
+        pgr, ld_gr = grad_residual.data_ptr(), _mat("grad_residual", grad_residual, (residual.dtype,), shape, dev)
+    if grad_normed is not None:
+        pgn, ld_gn = grad_normed.data_ptr(), _mat("grad_normed", grad_normed, _ONLY_BF16, shape, dev)
+    if y is not None:
+        py, ld_y = y.data_ptr(), _mat("y", y, _ONLY_BF16, shape, dev)
+        d_y = residual.new_empty(shape, dtype=_BF16)
+        pdy = d_y.data_ptr()
+    pg, kind, gate_dt, ld_g = (0, 0, 0, 0) if gate is None else _gate_of(gate, shape, dev)
+    post, pre, wdt = _norm_weights(post_weight, pre_weight, H, dev)
+    d_res = residual.new_empty(shape)
     if kind:
         d_gate = gate.new_empty(gate.shape, dtype=_F32 if kind == 1 else gate.dtype)
-    d_post = None if post_weight is None else residual.new_empty(H, dtype=_F32)
-    d_pre = None if pre_weight is None else residual.new_empty(H, dtype=_F32)
-    L = _LIB or lib()
-    ws = _workspace(workspace, residual.device, L.moe_block_norm_backward_workspace_size(H))
-    _call(L.moe_block_norm_backward, dev, stream,
-          (_p(grad_residual), ld_gr, _p(grad_normed), ld_gn,
-           None if grad_normed is None else residual.data_ptr(), _DT[residual.dtype], ld_r, _p(y), ld_y,
-           _p(gate), kind, gate_dt, ld_g, scale, post_norm, _p(post_weight), _p(pre_weight), wdt, eps, T, H,
-           d_res.data_ptr(), _p(d_y), _p(d_gate), _p(d_post), _p(d_pre), ws.data_ptr(), ws.numel()))
+        pdg = d_gate.data_ptr()
+    if post:
+        d_post = residual.new_empty(H, dtype=_F32)
+        pdpost = d_post.data_ptr()
+    if pre:
+        d_pre = residual.new_empty(H, dtype=_F32)
+        pdpre = d_pre.data_ptr()
+    ws = _workspace(workspace, residual.device, (_LIB or lib()).moe_block_norm_backward_workspace_size(H))
+    _call(_NORM_BWD, dev, stream, pgr, ld_gr, pgn, ld_gn, residual.data_ptr() if pgn else 0, _DT[residual.dtype],
+          ld_r, py, ld_y, pg, kind, gate_dt, ld_g, scale, post_norm, post, pre, wdt, eps, T, H, d_res.data_ptr(),
+          pdy, pdg, pdpost, pdpre, ws.data_ptr(), ws.numel())
     return d_res, d_y, d_gate, d_post, d_pre
 
 
@@ -553,19 +565,6 @@ def _act(activation: Optional[str]) -> int:
     return ACTIVATIONS[activation]
 
 
-def _x_and_w(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor]):
-    dev = _device_of("x", x)
-    T, K = x.shape
-    ld_x = _mat("x", x, _ONLY_BF16, T, K, dev)
-    if w.dim() != 2:
-        _bad("w", "2-D")
-    N = w.shape[0]
-    ld_w = _mat("w", w, _ONLY_BF16, N, K, dev)
-    if bias is not None:
-        _vec("bias", bias, _DT, N, dev)
-    return dev, T, K, N, ld_x, ld_w
-
-
 def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
            activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
            out_dtype: torch.dtype = torch.bfloat16, preact: bool = False,
@@ -575,27 +574,39 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
     x bf16 [T,K]; w bf16 [N,K]; K a multiple of 8; bias [N] bf16 or fp32;
     activation None, 'silu', 'gelu' (exact) or 'relu'; out_dtype bf16 or fp32
     (router logits), which residual and the pre-activation share.  out: the
-    tensor to write into (rows contiguous); it may be residual."""
-    dev, T, K, N, ld_x, ld_w = _x_and_w(x, w, bias)
-    act = _act(activation)
-    if out is None:
-        if out_dtype not in _DT:
-            _bad("out_dtype", _names(_DT))
-        out = x.new_empty((T, N), dtype=out_dtype)
-        ld_o, dt = N, out_dtype
-    else:
-        dt = out.dtype
-        ld_o = _mat("out", out, _DT, T, N, dev)
-    ld_r = 0 if residual is None else _mat("residual", residual, (dt,), T, N, dev)
-    # the pre-activation has out's row stride
-    z = torch.empty_strided((T, N), (ld_o, 1), dtype=dt, device=x.device) if preact else None
+    tensor to write into (rows contiguous); it may be residual.  Calls that
+    share a workspace (by default all of a device) must be ordered on one
+    stream."""
     global _LINEAR_WS
-    L = _LIB or lib()
-    _LINEAR_WS = _LINEAR_WS or L.moe_linear_workspace_size()
+    dev, xs = _matrix_of("x", x)
+    T, K = xs
+    ld_x = _mat("x", x, _ONLY_BF16, xs, dev)
+    N = w.shape[0]
+    ld_w = _mat("w", w, _ONLY_BF16, (N, K), dev)
+    shape = (T, N)
+    if out is None:
+        dt = _DT.get(out_dtype)
+        if dt is None:
+            _bad("out_dtype", _names(_DT))
+        out = x.new_empty(shape, dtype=out_dtype)
+        ld_o = N
+    else:
+        ld_o = _mat("out", out, _DT, shape, dev)
+        out_dtype = out.dtype
+        dt = _DT[out_dtype]
+    pb = bdt = pr = ld_r = pz = 0
+    z = None
+    if bias is not None:
+        pb, bdt = _dense("bias", bias, _DT, (N,), dev), _DT[bias.dtype]
+    if residual is not None:
+        pr, ld_r = residual.data_ptr(), _mat("residual", residual, (out_dtype,), shape, dev)
+    if preact:  # it has out's row stride
+        z = torch.empty_strided(shape, (ld_o, 1), dtype=out_dtype, device=x.device)
+        pz = z.data_ptr()
+    _LINEAR_WS = _LINEAR_WS or lib().moe_linear_workspace_size()
     ws = _workspace(workspace, x.device, _LINEAR_WS)
-    _call(L.moe_linear, dev, stream,
-          (x.data_ptr(), ld_x, w.data_ptr(), ld_w, _p(bias), 0 if bias is None else _DT[bias.dtype], act,
-           _p(residual), ld_r, T, K, N, out.data_ptr(), _DT[dt], ld_o, _p(z), ws.data_ptr(), ws.numel()))
+    _call(_LINEAR, dev, stream, x.data_ptr(), ld_x, w.data_ptr(), ld_w, pb, bdt, _act(activation), pr, ld_r, T, K, N,
+          out.data_ptr(), dt, ld_o, pz, ws.data_ptr(), ws.numel())
     return (out, z) if preact else out
 
 
@@ -609,20 +620,33 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
     preact: what linear(..., preact=True) returned, with an activation; bias:
     as passed to linear (None: dbias is None).  need_x / need_w = False leave
     that gradient out (None)."""
-    dev, T, K, N, ld_x, ld_w = _x_and_w(x, w, bias)
-    ld_g = _mat("grad_y", grad_y, _DT, T, N, dev)
+    dev, xs = _matrix_of("x", x)
+    T, K = xs
+    ld_x = _mat("x", x, _ONLY_BF16, xs, dev)
+    N = w.shape[0]
+    ld_w = _mat("w", w, _ONLY_BF16, (N, K), dev)
+    shape = (T, N)
+    ld_g = _mat("grad_y", grad_y, _DT, shape, dev)
     act = _act(activation)
     if (preact is None) != (act == _ACT_NONE):
         raise ValueError("an activation and its preact go together")
-    ld_z = 0 if preact is None else _mat("preact", preact, (grad_y.dtype,), T, N, dev)
-    dx = x.new_empty((T, K)) if need_x else None
-    dw = w.new_empty((N, K)) if need_w else None
-    db = None if bias is None else x.new_empty(N, dtype=_F32)
-    L = _LIB or lib()
-    ws = _workspace(workspace, x.device, L.moe_linear_backward_workspace_size(T, N))
-    _call(L.moe_linear_backward, dev, stream,
-          (grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(), ld_w, act,
-           _p(preact), ld_z, T, K, N, _p(dx), _p(dw), _p(db), ws.data_ptr(), ws.numel()))
+    pz = ld_z = pdx = pdw = pdb = 0
+    dx = dw = db = None
+    if preact is not None:
+        pz, ld_z = preact.data_ptr(), _mat("preact", preact, (grad_y.dtype,), shape, dev)
+    if bias is not None:
+        _dense("bias", bias, _DT, (N,), dev)
+        db = x.new_empty(N, dtype=_F32)
+        pdb = db.data_ptr()
+    if need_x:
+        dx = x.new_empty(xs)
+        pdx = dx.data_ptr()
+    if need_w:
+        dw = w.new_empty((N, K))
+        pdw = dw.data_ptr()
+    ws = _workspace(workspace, x.device, (_LIB or lib()).moe_linear_backward_workspace_size(T, N))
+    _call(_LINEAR_BWD, dev, stream, grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(),
+          ld_w, act, pz, ld_z, T, K, N, pdx, pdw, pdb, ws.data_ptr(), ws.numel())
     return dx, dw, db
 
 

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstring>
 #include <mutex>
 
 #include "moe_internal.h"
@@ -527,6 +528,69 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
     if ((st = run_linear(dz, ld_dz, true, x, ld_x, true, p, s, fn)) != MOE_OK) return st;
   }
   return MOE_OK;
+}
+
+// The calls above with their arguments in one block of 8-byte slots (integers
+// and pointers as they are, floats as doubles), in the functions' order: the
+// Python binding's way in, since converting 14 to 29 arguments one by one took
+// longer there than launching the kernel.
+enum { CALL_ROUTE = 0, CALL_ROUTE_BWD = 1, CALL_NORM = 2, CALL_NORM_BWD = 3, CALL_LINEAR = 4, CALL_LINEAR_BWD = 5 };
+
+moe_status moe_call_packed(int call, const void* block) {
+  struct Slots {
+    const unsigned char* at;
+    int64_t i() {
+      int64_t v;
+      memcpy(&v, at, 8);
+      at += 8;
+      return v;
+    }
+    int n() { return static_cast<int>(i()); }
+    float f() {
+      double v;
+      memcpy(&v, at, 8);
+      at += 8;
+      return static_cast<float>(v);
+    }
+    void* p() { return reinterpret_cast<void*>(static_cast<uintptr_t>(i())); }
+    float* pf() { return static_cast<float*>(p()); }
+    int32_t* pi() { return static_cast<int32_t*>(p()); }
+    moe_dtype dt() { return static_cast<moe_dtype>(n()); }
+  } a{static_cast<const unsigned char*>(block)};
+  // an initialiser list evaluates its elements from left to right
+  switch (call) {
+    case CALL_ROUTE: {
+      struct { void* l; moe_dtype dt; int64_t ld; int T, E, k, sc; float* b; int ng, tg, gt, rn; float s; int32_t* idx; float* w; void* st; } q{
+          a.p(), a.dt(), a.i(), a.n(), a.n(), a.n(), a.n(), a.pf(), a.n(), a.n(), a.n(), a.n(), a.f(), a.pi(), a.pf(), a.p()};
+      return moe_route_scored(q.l, q.dt, q.ld, q.T, q.E, q.k, static_cast<moe_score>(q.sc), q.b, q.ng, q.tg, q.gt, q.rn, q.s, q.idx, q.w, q.st);
+    }
+    case CALL_ROUTE_BWD: {
+      struct { void* l; moe_dtype dt; int64_t ld; int T, E, k, sc; float* b; int rn; float s; int32_t* idx; float* w; float* gw; void* gl; int64_t ldg; void* st; } q{
+          a.p(), a.dt(), a.i(), a.n(), a.n(), a.n(), a.n(), a.pf(), a.n(), a.f(), a.pi(), a.pf(), a.pf(), a.p(), a.i(), a.p()};
+      return moe_route_scored_backward(q.l, q.dt, q.ld, q.T, q.E, q.k, static_cast<moe_score>(q.sc), q.b, q.rn, q.s, q.idx, q.w, q.gw, q.gl, q.ldg, q.st);
+    }
+    case CALL_NORM: {
+      struct { void* r; moe_dtype rd; int64_t ldr; void* y; int64_t ldy; void* g; int gk; moe_dtype gd; int64_t ldg; float sc; int po; void* pw; int pr; void* rw; moe_dtype wd; float eps; int T, H; void* ro; void* n; void* st; } q{
+          a.p(), a.dt(), a.i(), a.p(), a.i(), a.p(), a.n(), a.dt(), a.i(), a.f(), a.n(), a.p(), a.n(), a.p(), a.dt(), a.f(), a.n(), a.n(), a.p(), a.p(), a.p()};
+      return moe_block_norm(q.r, q.rd, q.ldr, q.y, q.ldy, q.g, static_cast<moe_gate>(q.gk), q.gd, q.ldg, q.sc, q.po, q.pw, q.pr, q.rw, q.wd, q.eps, q.T, q.H, q.ro, q.n, q.st);
+    }
+    case CALL_NORM_BWD: {
+      struct { void* gr; int64_t ldgr; void* gn; int64_t ldgn; void* r; moe_dtype rd; int64_t ldr; void* y; int64_t ldy; void* g; int gk; moe_dtype gd; int64_t ldg; float sc; int po; void* pw; void* rw; moe_dtype wd; float eps; int T, H; void* dr; void* dy; void* dg; float* dpo; float* dpr; void* ws; int64_t wsb; void* st; } q{
+          a.p(), a.i(), a.p(), a.i(), a.p(), a.dt(), a.i(), a.p(), a.i(), a.p(), a.n(), a.dt(), a.i(), a.f(), a.n(), a.p(), a.p(), a.dt(), a.f(), a.n(), a.n(), a.p(), a.p(), a.p(), a.pf(), a.pf(), a.p(), a.i(), a.p()};
+      return moe_block_norm_backward(q.gr, q.ldgr, q.gn, q.ldgn, q.r, q.rd, q.ldr, q.y, q.ldy, q.g, static_cast<moe_gate>(q.gk), q.gd, q.ldg, q.sc, q.po, q.pw, q.rw, q.wd, q.eps, q.T, q.H, q.dr, q.dy, q.dg, q.dpo, q.dpr, q.ws, static_cast<size_t>(q.wsb), q.st);
+    }
+    case CALL_LINEAR: {
+      struct { void* x; int64_t ldx; void* w; int64_t ldw; void* b; moe_dtype bd; int act; void* r; int64_t ldr; int T, K, N; void* o; moe_dtype od; int64_t ldo; void* z; void* ws; int64_t wsb; void* st; } q{
+          a.p(), a.i(), a.p(), a.i(), a.p(), a.dt(), a.n(), a.p(), a.i(), a.n(), a.n(), a.n(), a.p(), a.dt(), a.i(), a.p(), a.p(), a.i(), a.p()};
+      return moe_linear(q.x, q.ldx, q.w, q.ldw, q.b, q.bd, q.act, q.r, q.ldr, q.T, q.K, q.N, q.o, q.od, q.ldo, q.z, q.ws, static_cast<size_t>(q.wsb), q.st);
+    }
+    case CALL_LINEAR_BWD: {
+      struct { void* gy; moe_dtype yd; int64_t ldg; void* x; int64_t ldx; void* w; int64_t ldw; int act; void* z; int64_t ldz; int T, K, N; void* dx; void* dw; float* db; void* ws; int64_t wsb; void* st; } q{
+          a.p(), a.dt(), a.i(), a.p(), a.i(), a.p(), a.i(), a.n(), a.p(), a.i(), a.n(), a.n(), a.n(), a.p(), a.p(), a.pf(), a.p(), a.i(), a.p()};
+      return moe_linear_backward(q.gy, q.yd, q.ldg, q.x, q.ldx, q.w, q.ldw, q.act, q.z, q.ldz, q.T, q.K, q.N, q.dx, q.dw, q.db, q.ws, static_cast<size_t>(q.wsb), q.st);
+    }
+  }
+  return set_last_error(MOE_ERR_INVALID_ARG, "moe_call_packed: unknown call %d", call);
 }
 
 }  // extern "C"
