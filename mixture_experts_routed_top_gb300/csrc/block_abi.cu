@@ -192,7 +192,7 @@ moe_status moe_route_scored(const void* logits, moe_dtype dt, int64_t ld_logits,
   a.group_top = group_top;
   a.softmax = score == MOE_SCORE_SOFTMAX;
   a.renorm = renormalise != 0;
-  a.vec = rows16(ld_logits, size_of(dt)) && E * size_of(dt) % 16 == 0;
+  a.vec = ld_logits % 4 == 0 && E % 4 == 0;
   a.scale = scale;
   a.idx = topk_idx;
   a.w = topk_w;
@@ -228,7 +228,7 @@ moe_status moe_route_scored_backward(const void* logits, moe_dtype dt, int64_t l
   a.softmax = score == MOE_SCORE_SOFTMAX;
   a.renorm = renormalise != 0;
   const bool whole = E * size_of(dt) % 16 == 0;
-  a.vec = rows16(ld_logits, size_of(dt)) && whole;
+  a.vec = ld_logits % 4 == 0 && E % 4 == 0;
   a.vec_out = rows16(ld_grad, size_of(dt)) && whole;
   a.scale = scale;
   a.grad_logits = grad_logits;

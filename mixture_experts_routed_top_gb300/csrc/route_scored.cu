@@ -41,35 +41,49 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
 
 __device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) {
   return __reduce_max_sync(0xffffffffu, v);
 }
 
-// Lane l holds the NPL consecutive experts l * NPL + i, so the lower lane
-// always holds the lower expert index, an aligned group of experts is a run
-// of lanes, and a row is read in 16-byte vectors.
+// Where a lane's NPL values lie in a row: runs of C = min(NPL, 4) neighbours,
+// the lanes' runs next to each other, so that a row is read in whole lines
+// (16 bytes of fp32 or 8 of bf16 per lane).  Blocks of NPL neighbours per
+// lane instead ran 1024 experts 5 times slower: every load touched 32 lines.
+template <int NPL>
+struct Lay {
+  static constexpr int C = NPL < 4 ? NPL : 4;
+  static __device__ __forceinline__ int expert(int lane, int i) {
+    return (i / C) * (32 * C) + lane * C + i % C;
+  }
+};
+
 template <typename T, int NPL>
 __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int lane, bool vec,
                                          float (&v)[NPL]) {
-  constexpr int PV = 16 / sizeof(T);  // elements per 16-byte vector
-  const int e0 = lane * NPL;
-  if (NPL >= PV && vec) {  // E % PV == 0: a vector is inside the row or outside it
+  if (NPL >= 4 && vec) {  // E % 4 == 0: a run is inside the row or outside it
 #pragma unroll
-    for (int i = 0; i < NPL; i += PV) {
-      T t[PV];
-      if (e0 + i < E) {
-        *reinterpret_cast<uint4*>(t) = __ldg(reinterpret_cast<const uint4*>(row + e0 + i));
-      } else {
+    for (int i = 0; i < NPL; i += 4) {
+      const int e = Lay<NPL>::expert(lane, i);
+      T t[4];
 #pragma unroll
-        for (int j = 0; j < PV; ++j) t[j] = T(0.f);
+      for (int j = 0; j < 4; ++j) t[j] = T(0.f);
+      if (e < E) {
+        if (sizeof(T) == 4) *reinterpret_cast<uint4*>(t) = __ldg(reinterpret_cast<const uint4*>(row + e));
+        else *reinterpret_cast<uint2*>(t) = __ldg(reinterpret_cast<const uint2*>(row + e));
       }
 #pragma unroll
-      for (int j = 0; j < PV && i + j < NPL; ++j) v[i + j] = to_f(t[j]);
+      for (int j = 0; j < 4; ++j) v[i + j] = to_f(t[j]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) v[i] = e0 + i < E ? to_f(row[e0 + i]) : 0.f;
+    for (int i = 0; i < NPL; ++i) {
+      const int e = Lay<NPL>::expert(lane, i);
+      v[i] = e < E ? to_f(row[e]) : 0.f;
+    }
   }
 }
 
@@ -77,26 +91,31 @@ __device__ __forceinline__ void load_row(const T* __restrict__ row, int E, int l
 // logit gives 1 even when it is +inf) and their sum by halves.
 template <int NPL>
 __device__ __forceinline__ float softmax_terms(float (&v)[NPL], int E, int lane) {
+  constexpr int C = Lay<NPL>::C;
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
-    if (lane * NPL + i < E) m = fmaxf(m, v[i]);  // fmaxf drops NaN
-  const uint32_t mk = warp_max_u32(order_key(m + 0.f));
-  m = __uint_as_float(mk & 0x80000000u ? mk ^ 0x80000000u : ~mk);
+    if (Lay<NPL>::expert(lane, i) < E) m = fmaxf(m, v[i]);  // fmaxf drops NaN
+  m = key_value(warp_max_u32(order_key(m + 0.f)));
   float t[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    const bool live = lane * NPL + i < E && v[i] > -INFINITY;
+    const bool live = Lay<NPL>::expert(lane, i) < E && v[i] > -INFINITY;
     v[i] = live ? expf(v[i] == m ? 0.f : __fsub_rn(v[i], m)) : 0.f;
     t[i] = v[i];
   }
-  // halves: the upper index bits are the lane's, the lower ones i's
+  // halves: the highest bits of an expert's index are its run's, then the
+  // lane's, then its place in the run
+#pragma unroll
+  for (int n = NPL / 2; n >= C; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) t[i] = __fadd_rn(t[i], t[i + n]);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) t[i] = __fadd_rn(t[i], __shfl_xor_sync(0xffffffffu, t[i], off));
+    for (int i = 0; i < C; ++i) t[i] = __fadd_rn(t[i], __shfl_xor_sync(0xffffffffu, t[i], off));
 #pragma unroll
-  for (int n = NPL / 2; n > 0; n /= 2)
+  for (int n = C / 2; n > 0; n /= 2)
 #pragma unroll
     for (int i = 0; i < n; ++i) t[i] = __fadd_rn(t[i], t[i + n]);
   return t[0];
@@ -112,17 +131,19 @@ __device__ __forceinline__ float sigmoid_score(float x) {
 //
 // Up to kRankK of them by rank: the k-th largest of the 32 lane maxima is a
 // bound that at least k keys reach and few others do; those are gathered (at
-// most one per lane) and each lane counts how many come before its own.  At
-// 256 experts and k = 8 about 12 keys are gathered, and the whole selection
-// takes some 190 instructions, against 600 for k rounds of a warp-wide
-// maximum that remove one key each, which remain for the other cases: more
-// than kRankK, or more than 32 keys at the bound (ties, masked experts).
+// most 32) as one 64-bit number each, key above, complement of the expert
+// below, and each lane counts the numbers above its own.  At 256 experts and
+// k = 8 about 12 are gathered.  The other cases, more than kRankK or more
+// than 32 keys at the bound (ties, masked experts), take k rounds of a
+// warp-wide maximum that remove one key each, 2 us more at 8192 x 256.
 constexpr int kRankK = 16;
+struct __align__(16) Cand {
+  unsigned long long num[32];
+  float val[32];
+};
 template <int NPL>
 __device__ __forceinline__ void select_top(uint32_t (&key)[NPL], const float (&s)[NPL], int k,
-                                           int lane, uint32_t* s_key, float* s_cand, int* s_expert,
-                                           int* s_idx, float* s_val) {
-  const int e0 = lane * NPL;
+                                           int lane, Cand& c, int* s_idx, float* s_val) {
   if (k <= kRankK) {
     uint32_t best = key[0];
 #pragma unroll
@@ -135,90 +156,93 @@ __device__ __forceinline__ void select_top(uint32_t (&key)[NPL], const float (&s
       if (mine) best = 0u;
       if (bound == 0u) break;  // fewer lanes than k hold an expert
     }
+    c.num[lane] = 0ull;
+    __syncwarp();
     int n = 0;
-    uint32_t at[NPL];
-    bool fits = bound != 0u;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const bool in = key[i] >= bound;
-      const uint32_t b = __ballot_sync(0xffffffffu, in);
-      at[i] = in ? n + __popc(b & ((1u << lane) - 1u)) : 32u;
-      n += __popc(b);
-    }
-    fits = fits && n <= 32;
-    if (fits) {
+    const uint32_t below = (1u << lane) - 1u;
+    if (bound != 0u) {
 #pragma unroll
       for (int i = 0; i < NPL; ++i) {
-        if (at[i] < 32u) {
-          s_key[at[i]] = key[i];
-          s_cand[at[i]] = s[i];
-          s_expert[at[i]] = e0 + i;
+        const bool in = key[i] >= bound;
+        const uint32_t b = __ballot_sync(0xffffffffu, in);
+        const int at = n + __popc(b & below);
+        if (in && at < 32) {
+          c.num[at] = static_cast<unsigned long long>(key[i]) << 32 |
+                      static_cast<uint32_t>(~Lay<NPL>::expert(lane, i));
+          c.val[at] = s[i];
         }
+        n += __popc(b);
       }
-      __syncwarp();
-      const uint32_t mk = lane < n ? s_key[lane] : 0u;
-      const int me = lane < n ? s_expert[lane] : 0x7fffffff;
+    }
+    __syncwarp();
+    if (bound != 0u && n <= 32) {
+      const unsigned long long mine = c.num[lane];
       int rank = 0;
-      for (int j = 0; j < n; ++j) {
-        const uint32_t ok = s_key[j];
-        rank += ok > mk || (ok == mk && s_expert[j] < me);
+      for (int j = 0; j < n; j += 2) {  // 0 past the last
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(&c.num[j]);
+        rank += o.x > mine;
+        rank += o.y > mine;
       }
       if (lane < n && rank < k) {
-        s_idx[rank] = me;
-        s_val[rank] = mk == kKeyNegInf ? 0.f : s_cand[lane];
+        s_idx[rank] = static_cast<int>(~static_cast<uint32_t>(mine));
+        s_val[rank] = static_cast<uint32_t>(mine >> 32) == kKeyNegInf ? 0.f : c.val[lane];
       }
       __syncwarp();
       return;
     }
   }
-  // k rounds: the warp's largest key; its lowest lane, and there the lowest
-  // i, is the lowest expert index among equals
   for (int j = 0; j < k; ++j) {
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) best = max(best, key[i]);
     const uint32_t top = warp_max_u32(best);
-    const uint32_t who = __ballot_sync(0xffffffffu, best == top);
-    if (lane == __ffs(who) - 1) {
-      int at = 0;
+    int at = NPL;  // this lane's first value that is the maximum
+#pragma unroll
+    for (int i = NPL - 1; i >= 0; --i)
+      if (key[i] == top) at = i;
+    const uint32_t mine = at < NPL ? Lay<NPL>::expert(lane, at) : 0xffffffffu;
+    if (__reduce_min_sync(0xffffffffu, mine) == mine && at < NPL) {
       float sv = 0.f;
 #pragma unroll
-      for (int i = NPL - 1; i >= 0; --i)
-        if (key[i] == top) {
-          at = i;
-          sv = s[i];
-        }
-#pragma unroll
       for (int i = 0; i < NPL; ++i)
-        if (i == at) key[i] = 0u;
-      s_idx[j] = e0 + at;
+        if (i == at) {
+          sv = s[i];
+          key[i] = 0u;
+        }
+      s_idx[j] = static_cast<int>(mine);
       s_val[j] = top == kKeyNegInf ? 0.f : sv;
     }
   }
   __syncwarp();
 }
 
+// Shared rows have a gap after every 32 experts, so that groups of 32 do not
+// all begin in one bank.
+__device__ __forceinline__ int padded(int e) { return e + (e >> 5); }
+
 template <typename T, int NPL>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, NPL <= 8 ? 5 : NPL == 16 ? 4 : 2)
     route_scored_kernel(const RouteScoredArgs a) {
   pdl_launch_dependents();
   __shared__ int s_idx[kWarps][kMaxK];
   __shared__ float s_val[kWarps][kMaxK];
-  __shared__ uint32_t s_key[kWarps][32];
-  __shared__ float s_cand[kWarps][32];
-  __shared__ int s_expert[kWarps][32];
-  extern __shared__ float s_row[];  // [kWarps][32 * NPL]: groups that are no run of lanes
+  __shared__ Cand s_cand[kWarps];
+  extern __shared__ float s_row[];  // [kWarps][33 * NPL], with groups
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long t = static_cast<long>(blockIdx.x) * kWarps + warp;
   pdl_wait();
   if (t >= a.T) return;
-  const int E = a.E, e0 = lane * NPL;
-  float s[NPL];
+  const int E = a.E;
+  auto expert = [&](int i) { return Lay<NPL>::expert(lane, i); };
+  float s[NPL], b[NPL];
   load_row<T, NPL>(static_cast<const T*>(a.logits) + t * a.ld, E, lane, a.vec, s);
-  uint32_t dead = 0;  // bit i: expert e0 + i is masked (or there is none)
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) b[i] = 0.f;
+  if (a.bias != nullptr) load_row<float, NPL>(a.bias, E, lane, E % 4 == 0, b);
+  uint32_t dead = 0;  // bit i: the lane's i-th expert is masked (or there is none)
 #pragma unroll
   for (int i = 0; i < NPL; ++i)
-    if (e0 + i >= E || !(s[i] > -INFINITY)) dead |= 1u << i;
+    if (expert(i) >= E || !(s[i] > -INFINITY)) dead |= 1u << i;
   if (a.softmax) {
     const float sum = softmax_terms<NPL>(s, E, lane);
 #pragma unroll
@@ -230,76 +254,68 @@ __global__ void __launch_bounds__(kWarps * 32)
   uint32_t key[NPL];  // 0: no expert, or taken already
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
-    float c = s[i];
-    if (a.bias != nullptr && e0 + i < E) c = __fadd_rn(c, __ldg(a.bias + e0 + i));
-    if (((dead >> i) & 1u) || !(c > -INFINITY)) c = -INFINITY;
-    key[i] = e0 + i < E ? order_key(c + 0.f) : 0u;
+    const float c = __fadd_rn(s[i], b[i]);
+    const bool live = !((dead >> i) & 1u) && c > -INFINITY;
+    key[i] = expert(i) < E ? (live ? order_key(c + 0.f) : kKeyNegInf) : 0u;
   }
   if (a.n_group > 1) {
+    // 32 / n_group lanes (a power of two) per group look through its keys in
+    // shared memory and join their two largest by shuffles
     const int gs = E / a.n_group;
-    float g = -INFINITY;  // this lane's group's score (lane < n_group in the second form)
-    auto value = [](uint32_t k) {
-      return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-    };
-    auto score_of = [&](float t1, float t2) {  // a masked second expert adds nothing
-      return a.group_top == 2 && t2 > -INFINITY ? __fadd_rn(t1, t2) : t1;
-    };
-    const int span = gs / NPL;  // lanes a group covers
-    const bool runs = gs % NPL == 0 && (span & (span - 1)) == 0;
-    if (runs) {
-      // the two largest of a lane, then of its run of lanes by xor shuffles
-      uint32_t t1 = kKeyNegInf, t2 = kKeyNegInf;
+    const int lpg = 1 << (31 - __clz(32 / a.n_group));
+    constexpr int C = Lay<NPL>::C;
+    uint32_t* row = reinterpret_cast<uint32_t*>(s_row) + warp * 33 * NPL;
+    const int at0 = lane * C + (lane * C >> 5);  // padded(expert(i)), i's part a constant
 #pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const uint32_t kx = key[i];
+    for (int i = 0; i < NPL; ++i) row[at0 + (i / C) * (33 * C) + i % C] = key[i];
+    __syncwarp();
+    const int mine = lane / lpg;  // this lane's group
+    uint32_t t1 = kKeyNegInf, t2 = kKeyNegInf;
+    if (mine < a.n_group) {
+#pragma unroll 4
+      for (int j = lane % lpg; j < gs; j += lpg) {
+        const uint32_t kx = row[padded(mine * gs + j)];
         t2 = max(t2, min(t1, kx));
         t1 = max(t1, kx);
       }
-      for (int off = 1; off < span; off <<= 1) {
-        const uint32_t o1 = __shfl_xor_sync(0xffffffffu, t1, off);
-        const uint32_t o2 = __shfl_xor_sync(0xffffffffu, t2, off);
-        t2 = max(max(t2, o2), min(t1, o1));
-        t1 = max(t1, o1);
-      }
-      g = score_of(value(t1), value(t2));
-      const int mine = e0 / gs;
-      int rank = 0;  // groups that come before this lane's
-      for (int q = 0; q < a.n_group; ++q) {
-        const float og = __shfl_sync(0xffffffffu, g, q * span);
-        rank += og > g || (og == g && q < mine);
-      }
-      if (rank >= a.topk_group) {
+    }
+    for (int off = 1; off < lpg; off <<= 1) {
+      const uint32_t o1 = __shfl_xor_sync(0xffffffffu, t1, off);
+      const uint32_t o2 = __shfl_xor_sync(0xffffffffu, t2, off);
+      t2 = max(max(t2, o2), min(t1, o1));
+      t1 = max(t1, o1);
+    }
+    // a masked second expert adds nothing
+    float g = key_value(t1);
+    if (a.group_top == 2 && t2 > kKeyNegInf) g = __fadd_rn(g, key_value(t2));
+    // the topk_group largest, equal ones in group order; bit lpg * q: group q is kept
+    uint32_t gkey = mine < a.n_group && lane % lpg == 0 ? order_key(g + 0.f) : 0u, kept = 0;
+    for (int q = 0; q < a.topk_group; ++q) {
+      const uint32_t top = warp_max_u32(gkey);
+      const int first = __ffs(__ballot_sync(0xffffffffu, gkey == top)) - 1;
+      kept |= 1u << first;
+      if (lane == first) gkey = 0u;
+    }
+    // e / gs = e * ceil(2^20 / gs) >> 20 for e, gs <= 1024
+    const uint32_t magic = ((1u << 20) + gs - 1) / gs;
+    auto eligible = [&](int e) {
+      const uint32_t q = (static_cast<uint32_t>(e) * magic) >> 20;
+      return (kept >> min(q * lpg, 31u)) & 1u;
+    };
+    if (gs % C == 0) {  // a run lies in one group
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) key[i] = min(key[i], kKeyNegInf);
+      for (int i = 0; i < NPL; i += C) {
+        const uint32_t cap = eligible(expert(i)) ? 0xffffffffu : kKeyNegInf;
+#pragma unroll
+        for (int c = 0; c < C; ++c) key[i + c] = min(key[i + c], cap);
       }
     } else {
-      // any other group size: the row in shared memory, a lane per group
-      uint32_t* row = reinterpret_cast<uint32_t*>(s_row) + warp * 32 * NPL;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) row[e0 + i] = key[i];
-      __syncwarp();
-      if (lane < a.n_group) {
-        uint32_t t1 = kKeyNegInf, t2 = kKeyNegInf;
-        for (int j = 0; j < gs; ++j) {
-          const uint32_t kx = row[lane * gs + j];
-          t2 = max(t2, min(t1, kx));
-          t1 = max(t1, kx);
-        }
-        g = score_of(value(t1), value(t2));
-      }
-      int rank = 0;
-      for (int q = 0; q < a.n_group; ++q) {
-        const float og = __shfl_sync(0xffffffffu, g, q);
-        rank += og > g || (og == g && q < lane);
-      }
-      const uint32_t kept = __ballot_sync(0xffffffffu, lane < a.n_group && rank < a.topk_group);
 #pragma unroll
       for (int i = 0; i < NPL; ++i)
-        if (e0 + i < E && !((kept >> ((e0 + i) / gs)) & 1u)) key[i] = min(key[i], kKeyNegInf);
+        if (!eligible(expert(i))) key[i] = min(key[i], kKeyNegInf);
     }
   }
-  select_top<NPL>(key, s, a.k, lane, s_key[warp], s_cand[warp], s_expert[warp], s_idx[warp],
-                  s_val[warp]);
+  select_top<NPL>(key, s, a.k, lane, s_cand[warp], s_idx[warp], s_val[warp]);
   const bool has = lane < a.k;
   float w = has ? s_val[warp][lane] : 0.f;
   if (a.renorm) {
@@ -334,7 +350,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const long t = static_cast<long>(blockIdx.x) * kWarps + warp;
   pdl_wait();
   if (t >= a.T) return;
-  const int E = a.E, k = a.k, e0 = lane * NPL;
+  const int E = a.E, k = a.k;
   const T* lrow = static_cast<const T*>(a.logits) + t * a.ld;
   float* row = s_row + warp * 32 * NPL;
   int e = -1;
@@ -387,14 +403,14 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
       p[i] = p[i] > 0.f ? p[i] / sum : 0.f;
-      row[e0 + i] = p[i];
+      row[Lay<NPL>::expert(lane, i)] = p[i];
     }
     __syncwarp();
     const float ps = has ? row[e] : 0.f;
     const float dot = sum32(g * ps);
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) row[e0 + i] = -p[i] * dot;
+    for (int i = 0; i < NPL; ++i) row[Lay<NPL>::expert(lane, i)] = -p[i] * dot;
     __syncwarp();
     if (has) row[e] = ps * (g - dot);
     __syncwarp();
@@ -415,10 +431,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 template <typename T, int NPL>
 cudaError_t fwd(const RouteScoredArgs& a, cudaStream_t s) {
-  // shared rows only for groups that are no power-of-two run of lanes
-  const int gs = a.E / a.n_group, span = gs / NPL;
-  const bool runs = gs % NPL == 0 && (span & (span - 1)) == 0;
-  const size_t smem = a.n_group > 1 && !runs ? sizeof(float) * kWarps * 32 * NPL : 0;
+  const size_t smem = a.n_group > 1 ? sizeof(float) * kWarps * 33 * NPL : 0;
   return launch_pdl(route_scored_kernel<T, NPL>, dim3(ceil_div(a.T, kWarps)), dim3(kWarps * 32),
                     smem, s, a);
 }
