@@ -488,7 +488,6 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
     a.dy = grad_y;
     a.preact = preact;
     a.dz = direct || !products ? nullptr : reinterpret_cast<__nv_bfloat16*>(wsb + L.dz);
-    a.partials = dbias ? reinterpret_cast<float*>(wsb + L.partials) : nullptr;
     a.ld_dy = ld_gy;
     a.ld_z = ld_z;
     a.ld_dz = L.ld_dz;
@@ -498,6 +497,7 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
     a.f32 = y_dt == MOE_DT_F32;
     a.vec = N % 8 == 0 && rows16(ld_gy, size_of(y_dt)) && (!preact || rows16(ld_z, size_of(y_dt)));
     const int slices = std::min(linear_dz_slices(T, N, device_sms()), kLinearDzSlices);
+    a.partials = !dbias ? nullptr : slices == 1 ? dbias : reinterpret_cast<float*>(wsb + L.partials);
     const cudaError_t e = launch_linear_dz(a, slices, dbias, s);
     if (e != cudaSuccess) return cuda_error(e, fn);
     if (a.dz) {

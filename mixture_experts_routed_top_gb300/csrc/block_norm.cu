@@ -412,6 +412,11 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return r;
 }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 __device__ __forceinline__ float sum2(F2 a) {
   const float2 p = parts(a);
   return p.x + p.y;
@@ -476,35 +481,52 @@ struct Slots {
   }
 };
 
-// Sums of N <= 2 values over a row's warps, one barrier each: two buffers in
-// turn, so a buffer is written again only after a barrier that follows its
-// reads.  s_red: [2][2][rows][16], zero from the row's warp count on.
-constexpr int kRedFloats = 2 * 2 * 8 * 16;  // at most 8 rows of two to 16 warps in a block
-template <int N>
-__device__ __forceinline__ void ring_sums(float (&v)[N], float* s_red, int& turn) {
+// Sums over a row's warps, one barrier each: two buffers in turn, so a buffer
+// is written again only after a barrier that follows its reads.  s_red:
+// [2][rows][16] pairs, zero from the row's warp count on.  Two sums travel as
+// a pair: in the first shuffle each half of the warp hands over the sum that
+// the other half goes on with, so 5 shuffles do for both, and the warps' pairs
+// are added with packed instructions.
+constexpr int kRedPairs = 2 * 8 * 16;  // at most 8 rows of two to 16 warps in a block
+__device__ __forceinline__ F2 ring_sums2(float a, float b, F2* s_red, int& turn) {
+  const int lane = threadIdx.x & 31;
+  const bool low = lane < 16;
+  float v = (low ? a : b) + __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], off);
+  for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  // lanes 0..15 hold the sum of a, the others that of b
   const int warps = blockDim.x >> 5;
-  if (warps == 1) return;
-  float* buf = s_red + turn * (kRedFloats / 2) + threadIdx.y * 16;
+  if (warps == 1) return f2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+  F2* buf = s_red + (turn * 8 + threadIdx.y) * 16;
   turn ^= 1;
-  constexpr int kStep = 8 * 16;
-  if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-    for (int n = 0; n < N; ++n) buf[n * kStep + (threadIdx.x >> 5)] = v[n];
-  }
+  if ((lane & 15) == 0) reinterpret_cast<float*>(buf + (threadIdx.x >> 5))[lane >> 4] = v;
   __syncthreads();
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    float4 t = *reinterpret_cast<const float4*>(buf + n * kStep);
-    for (int w = 4; w < warps; w += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(buf + n * kStep + w);
-      t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
-    }
-    v[n] = (t.x + t.y) + (t.z + t.w);
+  ulonglong2 t = *reinterpret_cast<const ulonglong2*>(buf);
+  F2 x{t.x}, y{t.y};
+  for (int w = 2; w < warps; w += 2) {
+    t = *reinterpret_cast<const ulonglong2*>(buf + w);
+    x = add2(x, F2{t.x});
+    y = add2(y, F2{t.y});
   }
+  return add2(x, y);
+}
+__device__ __forceinline__ float ring_sum(float a, F2* s_red, int& turn) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return a;
+  float* buf = reinterpret_cast<float*>(s_red + (turn * 8 + threadIdx.y) * 16);
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = a;
+  __syncthreads();
+  ulonglong2 t = *reinterpret_cast<const ulonglong2*>(buf);
+  F2 x{t.x}, y{t.y};
+  for (int w = 4; w < warps; w += 4) {
+    t = *reinterpret_cast<const ulonglong2*>(buf + w);
+    x = add2(x, F2{t.x});
+    y = add2(y, F2{t.y});
+  }
+  return sum2(add2(x, y));
 }
 
 // MID: a call between two blocks (y given, norm before the next block, no
@@ -513,7 +535,7 @@ template <typename RT, int NV, int STAGES, bool MID>
 __global__ void __launch_bounds__(kRingThreads, 2) block_norm_ring_kernel(const BlockNormArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint4 s_ring[];
-  __shared__ __align__(16) float s_red[kRedFloats];
+  __shared__ __align__(16) F2 s_red[kRedPairs];
   constexpr bool R32 = sizeof(RT) == 4;
   constexpr int PR = R32 ? 2 : 1;                 // pieces of a residual row
   const bool has_y = MID || a.y != nullptr, pre_norm = MID || a.pre_norm;
@@ -521,7 +543,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) block_norm_ring_kernel(const 
   const int nthr = blockDim.x * blockDim.y, tid = threadIdx.x + threadIdx.y * blockDim.x;
   // pieces of 8 columns: residual, y, gate
   const int pv = PR + (has_y ? 1 : 0) + (elem ? (a.gate_bf16 ? 1 : 2) : 0);
-  for (int i = tid; i < kRedFloats; i += nthr) s_red[i] = 0.f;
+  for (int i = tid; i < kRedPairs; i += nthr) s_red[i] = f2(0.f);
   __syncthreads();
   const int H = a.H;
   auto col = [&](int v) { return static_cast<int>(threadIdx.x + blockDim.x * v) * 8; };
@@ -581,9 +603,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) block_norm_ring_kernel(const 
             for (int e = 0; e < 4; ++e) sq = fma2(y[e], y[e], sq);
           }
         }
-        float sum[1] = {sum2(sq)};
-        ring_sums<1>(sum, s_red, turn);
-        coef *= rsqrtf(sum[0] * inv_h + a.eps);
+        coef *= rsqrtf(ring_sum(sum2(sq), s_red, turn) * inv_h + a.eps);
       }
     }
     F2 sq = f2(0.f);
@@ -613,9 +633,7 @@ __global__ void __launch_bounds__(kRingThreads, 2) block_norm_ring_kernel(const 
       }
     }
     if (pre_norm) {
-      float sum[1] = {sum2(sq)};
-      ring_sums<1>(sum, s_red, turn);
-      const F2 rstd = f2(rsqrtf(sum[0] * inv_h + a.eps));
+      const F2 rstd = f2(rsqrtf(ring_sum(sum2(sq), s_red, turn) * inv_h + a.eps));
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         if (on && col(v) < H) {
@@ -639,7 +657,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     block_norm_backward_ring_kernel(const BlockNormBwdArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint4 s_ring[];
-  __shared__ __align__(16) float s_red[kRedFloats];
+  __shared__ __align__(16) F2 s_red[kRedPairs];
   constexpr bool R32 = sizeof(RT) == 4;
   constexpr int PR = R32 ? 2 : 1;
   const bool has_y = MID || a.y != nullptr, has_gr = MID || a.grad_res != nullptr,
@@ -651,7 +669,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             p_g = p_y + (has_y ? 1 : 0);
   const int pv = p_g + (elem ? (a.gate_bf16 ? 1 : 2) : 0);
   const int nthr = blockDim.x * blockDim.y, tid = threadIdx.x + threadIdx.y * blockDim.x;
-  for (int i = tid; i < kRedFloats; i += nthr) s_red[i] = 0.f;
+  for (int i = tid; i < kRedPairs; i += nthr) s_red[i] = f2(0.f);
   __syncthreads();
   const int H = a.H;
   auto col = [&](int v) { return static_cast<int>(threadIdx.x + blockDim.x * v) * 8; };
@@ -718,10 +736,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
           }
         }
       }
-      float sum[2] = {sum2(s0), sum2(s1)};
-      ring_sums<2>(sum, s_red, turn);
-      rstd = rsqrtf(sum[0] * inv_h + a.eps);
-      corr = sum[1] * inv_h * rstd * rstd * rstd;
+      const float2 sum = parts(ring_sums2(sum2(s0), sum2(s1), s_red, turn));
+      rstd = rsqrtf(sum.x * inv_h + a.eps);
+      corr = sum.y * inv_h * rstd * rstd * rstd;
     }
     F2 d[NV][4];
     F2 s0 = f2(0.f), s1 = f2(0.f);  // y^2; scale * the norm's projection, which a per-token dg needs too
@@ -769,14 +786,13 @@ __global__ void __launch_bounds__(kRingThreads, 1)
       gt = a.gate_bf16 ? get(static_cast<const __nv_bfloat16*>(a.gate) + t)
                        : get(static_cast<const float*>(a.gate) + t);
     if (a.post_norm || a.gate_kind == MOE_GATE_TOKEN) {
-      float sum[2] = {sum2(s0), sum2(s1)};
-      ring_sums<2>(sum, s_red, turn);
+      const float2 sum = parts(ring_sums2(sum2(s0), sum2(s1), s_red, turn));
       if (a.post_norm) {
-        rstd = rsqrtf(sum[0] * inv_h + a.eps);
-        corr = sum[1] * inv_h * rstd * rstd * gt * rstd;
+        rstd = rsqrtf(sum.x * inv_h + a.eps);
+        corr = sum.y * inv_h * rstd * rstd * gt * rstd;
       }
       if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0 && on) {
-        const float dg = rstd * sum[1];
+        const float dg = rstd * sum.y;
         if (a.gate_bf16) put(static_cast<__nv_bfloat16*>(a.d_gate) + t, dg);
         else put(static_cast<float*>(a.d_gate) + t, dg);
       }

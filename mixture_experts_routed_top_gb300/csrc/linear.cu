@@ -136,8 +136,8 @@ __device__ __forceinline__ float act_f(float z, int act, bool f32) {
   if (act == MOE_ACT_SILU && f32) return z / (1.f + expf(-z));
   return gate_act(z, act);
 }
-// The epilogue on 8 consecutive columns n.. of row m (m < M): pre-activation
-// z = v + bias, y = residual + act(z).  ACT and F32 are constants of the code:
+// The epilogue on 8 consecutive columns n.. of row m (m < M) where N % 8 == 0 and
+// every row is 16-byte aligned: pre-activation z = v + bias, y = residual + act(z).  ACT and F32 are constants of the code:
 // kernels hold several copies of this, and with every activation and type in
 // each the code was so long that fetching it took longer than a small
 // product (33 us for 64 x 256 x 256), while one copy called as a function
@@ -145,50 +145,64 @@ __device__ __forceinline__ float act_f(float z, int act, bool f32) {
 template <int ACT, bool F32>
 __device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, float (&v)[8]) {
   if (n >= p.N) return;
-  if (p.vec) {  // N % 8 == 0 and every row 16-byte aligned
-    float b[8], r[8];
-    if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !F32, r);
-    if (p.bias != nullptr) {
-      ld8(p.bias, n, p.bias_bf16, b);
+  float b[8], r[8];
+  if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !F32, r);
+  if (p.bias != nullptr) {
+    ld8(p.bias, n, p.bias_bf16, b);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += b[j];
-    }
-    if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, F32, v);
-    if (ACT != MOE_ACT_NONE) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = act_f(v[j], ACT, F32);
-    }
-    if (p.residual != nullptr) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += r[j];
-    }
-    st8(p.out, m * p.ld_out + n, F32, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (n + j < p.N) {
-        float z = v[j];
-        if (p.bias != nullptr) z += ldf(p.bias, n + j, p.bias_bf16);
-        if (p.preact != nullptr) stf(p.preact, m * p.ld_out + n + j, F32, z);
-        z = act_f(z, ACT, F32);
-        if (p.residual != nullptr) z += ldf(p.residual, m * p.ld_res + n + j, !F32);
-        stf(p.out, m * p.ld_out + n + j, F32, z);
-      }
-    }
+    for (int j = 0; j < 8; ++j) v[j] += b[j];
   }
+  if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, F32, v);
+  if (ACT != MOE_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = act_f(v[j], ACT, F32);
+  }
+  if (p.residual != nullptr) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += r[j];
+  }
+  st8(p.out, m * p.ld_out + n, F32, v);
 }
-// 32 consecutive columns of row m from a thread's TMEM load.
+// 32 consecutive columns of 32 rows from a warp's TMEM load (lane: row m, of
+// which `on` says whether it exists).  Where rows are not made of whole
+// aligned vectors (p.vec off), single columns straight from the lanes would
+// touch 32 lines per store; the values go through `buf` (32 x 33 floats of
+// this warp) so that lanes hold neighbouring columns of one row instead.
+// 6000 x 1024 x 300: 46 us without, see the figure at the kernels.
+constexpr int kOddBuf = 32 * 33;
 template <int ACT, bool F32>
 __device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
-                                           const uint32_t (&v)[32]) {
-  if (m >= p.M) return;
+                                           const uint32_t (&v)[32], float* buf) {
+  if (p.vec) {
+    if (m >= p.M) return;
 #pragma unroll
-  for (int j = 0; j < 32; j += 8) {
-    float f[8];
+    for (int j = 0; j < 32; j += 8) {
+      float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[j + i]);
-    epilogue8<ACT, F32>(p, m, n + j, f);
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[j + i]);
+      epilogue8<ACT, F32>(p, m, n + j, f);
+    }
+    return;
   }
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // the previous step's values have been read
+#pragma unroll
+  for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = __uint_as_float(v[i]);
+  __syncwarp();
+  const long m0 = m - lane;
+  const int rows = static_cast<int>(min(32l, p.M - m0)), col = n + lane;
+  if (col < p.N) {
+    const float b = p.bias != nullptr ? ldf(p.bias, col, p.bias_bf16) : 0.f;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const float z = buf[r * 33 + lane] + b;
+      const float res =
+          p.residual != nullptr ? ldf(p.residual, (m0 + r) * p.ld_res + col, !F32) : 0.f;
+      if (p.preact != nullptr) stf(p.preact, (m0 + r) * p.ld_out + col, F32, z);
+      stf(p.out, (m0 + r) * p.ld_out + col, F32, act_f(z, ACT, F32) + res);
+    }
+  }
+  __syncwarp();
 }
 
 // Joining a split contraction.  The CTAs of a cluster share a tile and each owns
@@ -339,8 +353,10 @@ constexpr int kPOffB = kPStages * kPOper;
 constexpr int kPOffBar = 2 * kPStages * kPOper;
 constexpr int kPBars = 2 * kPStages + 2 + 2 + 1;
 constexpr int kPOffMisc = kPOffBar + kPBars * 8;
-constexpr int kPSmem = kPOffMisc + 16 + 1024;
-static_assert(kPSmem <= 227 * 1024, "shared memory budget");
+constexpr int kPOffOdd = kPOffMisc + 16;    // a buffer per epilogue warp
+constexpr int kPSmem = kPOffOdd + 4 * kOddBuf * 4 + 1024;
+constexpr int kASmem = kPOffOdd + 8 * kOddBuf * 4 + 1024;  // of the kernel with 8 such warps
+static_assert(kASmem <= 227 * 1024, "shared memory budget");
 
 // Tile order: groups of `group` row tiles, all column tiles of a group
 // before the next, so the tiles in flight share operand rows in L2.
@@ -499,6 +515,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   } else {
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    float* const odd = reinterpret_cast<float*>(smem + kPOffOdd) + (warp - 2) * kOddBuf;
     int it = 0;
     for (int tile = cid; tile < total; tile += ncl, ++it) {
       int mi, ni;
@@ -526,7 +543,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             else mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
           }
         }
-        epilogue32<ACT, false>(p.epi, m, n0 + 32 * s, v);
+        epilogue32<ACT, false>(p.epi, m, n0 + 32 * s, v, odd);
       }
     }
   }
@@ -740,6 +757,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, column half
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 128 * half;
+    float* const odd = reinterpret_cast<float*>(smem + kPOffOdd) + (warp - 2) * kOddBuf;
     auto release = [&](int buf) {  // this warp has read the part
       tc_fence_before();
       __syncwarp();
@@ -801,7 +819,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
           uint32_t v[32];
           tmem_ld_32x32b_x32(tl + buf * 256 + 32 * s, v);
           tmem_ld_wait();
-          epilogue32<ACT, true>(p.epi, m, ni * 256 + 128 * half + 32 * s, v);
+          epilogue32<ACT, true>(p.epi, m, ni * 256 + 128 * half + 32 * s, v, odd);
         }
         release(buf);
       }
@@ -1223,13 +1241,13 @@ cudaError_t launch_sums(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Linear
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * split);
   cfg.blockDim = dim3(kAThreads);
-  cfg.dynamicSmemBytes = kPSmem;
+  cfg.dynamicSmemBytes = kASmem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static std::atomic<int> max_clusters[64] = {};  // pairs without a split
   int nc = max_clusters[dev].load(std::memory_order_acquire);
   if (nc == 0) {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kASmem);
     if (err != cudaSuccess) return err;
     cfg.gridDim = dim3(2);
     attr[0].val.clusterDim.x = 2;
@@ -1410,7 +1428,7 @@ cudaError_t launch_linear_dz(const LinearDzArgs& a, int slices, float* dbias, cu
     e = go(linear_dz_kernel<MOE_ACT_NONE, true>, linear_dz_kernel<MOE_ACT_NONE, false>);
   count_launches(1);
   if (e != cudaSuccess) return e;
-  if (dbias != nullptr) {
+  if (dbias != nullptr && slices > 1) {  // one slice has written dbias itself
     e = launch_pdl(linear_colsum_kernel, dim3(ceil_div(a.N, 32)), dim3(256), 0, s,
                    static_cast<const float*>(a.partials), slices, a.N, dbias);
     count_launches(1);
