@@ -529,10 +529,16 @@ __device__ __forceinline__ float ring_sum(float a, F2* s_red, int& turn) {
   return sum2(add2(x, y));
 }
 
+// Forward blocks on an SM: rows above 2048 columns fill a block by themselves, and
+// one block with a deep ring and registers for its weights is faster than two
+// (8192 x 7168 80 us against 86); shorter rows share one, and two are (4099 x
+// 2048 22 us against 29).
+constexpr int ring_blocks(int nv) { return nv == 1 ? 2 : 1; }
+
 // MID: a call between two blocks (y given, norm before the next block, no
 // gate per element), whose options are then constants of the code.
 template <typename RT, int NV, int STAGES, bool MID>
-__global__ void __launch_bounds__(kRingThreads, 2) block_norm_ring_kernel(const BlockNormArgs a) {
+__global__ void __launch_bounds__(kRingThreads, ring_blocks(NV)) block_norm_ring_kernel(const BlockNormArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint4 s_ring[];
   __shared__ __align__(16) F2 s_red[kRedPairs];
@@ -905,19 +911,22 @@ cudaError_t bwd_ring(const BlockNormBwdArgs& a, dim3 block, size_t smem, int gri
 }
 
 // Bytes of one stage: pv pieces for each of the NV column sets of a thread.
-size_t stage_bytes(int pv, int nv) { return static_cast<size_t>(pv) * nv * kRingThreads * 16; }
+constexpr size_t stage_bytes(int pv, int nv) { return static_cast<size_t>(pv) * nv * kRingThreads * 16; }
 
 template <typename RT, int NV>
 cudaError_t fwd_nv(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
-  const dim3 block = ring_block(a.T, a.H, NV, 2 * num_sms);
+  constexpr int PER_SM = ring_blocks(NV), PR = static_cast<int>(sizeof(RT) / 2);
+  const dim3 block = ring_block(a.T, a.H, NV, PER_SM * num_sms);
   const bool elem = a.gate_kind == MOE_GATE_ELEMENT;
-  const size_t stage = stage_bytes(
-      static_cast<int>(sizeof(RT) / 2) + (a.y != nullptr) + (elem ? (a.gate_bf16 ? 1 : 2) : 0), NV);
-  // two blocks per SM share the ring's memory: 3 stages, or 2 of wide rows
-  const int grid = std::min(2 * num_sms, ceil_div(a.T, block.y));
-  if (a.y != nullptr && a.pre_norm && !elem)
-    return 3 * stage <= kRingBytes / 2 ? fwd_ring<RT, NV, 3, true>(a, block, 3 * stage, grid, s)
-                                       : fwd_ring<RT, NV, 2, true>(a, block, 2 * stage, grid, s);
+  const int grid = std::min(PER_SM * num_sms, ceil_div(a.T, block.y));
+  if (a.y != nullptr && a.pre_norm && !elem) {
+    // 160 of 200 KB for bf16 rows; one stage more was slower at each width
+    // (81.7 against 80.2 us at 8192 x 7168, 23.2 against 22.0 at 4099 x 2048)
+    constexpr int ST = NV == 1 ? 3 : PR == 1 ? 5 : 4;
+    static_assert(ST * stage_bytes(PR + 1, NV) * PER_SM <= kRingBytes, "a ring");
+    return fwd_ring<RT, NV, ST, true>(a, block, ST * stage_bytes(PR + 1, NV), grid, s);
+  }
+  const size_t stage = stage_bytes(PR + (a.y != nullptr) + (elem ? (a.gate_bf16 ? 1 : 2) : 0), NV);
   return fwd_ring<RT, NV, 2, false>(a, block, 2 * stage, grid, s);
 }
 template <typename RT, int NV>
