@@ -163,39 +163,41 @@ __device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, flo
   }
   st8(p.out, m * p.ld_out + n, F32, v);
 }
-// 32 consecutive columns of 32 rows from a warp's TMEM load (lane: row m, of
-// which `on` says whether it exists).  Where rows are not made of whole
-// aligned vectors (p.vec off), single columns straight from the lanes would
-// touch 32 lines per store; the values go through `buf` (32 x 33 floats of
-// this warp) so that lanes hold neighbouring columns of one row instead.
-// 6000 x 1024 x 300: 46 us without, see the figure at the kernels.
-constexpr int kOddBuf = 32 * 33;
+// 32 consecutive columns of 32 rows from a warp's TMEM load (lane: row m).  The
+// values go through `buf` (32 x 32 floats of this warp, 16-byte pieces of a row
+// in the order of their index xor the row's, so that neither side meets a bank
+// twice), after which lanes hold neighbouring columns: 4 lanes of 8 columns a
+// row, or where rows are not whole aligned vectors (p.vec off) 32 of one.
+// Straight from the lanes every access touched 32 rows, and the epilogue of a
+// 256 x 256 tile took 6 us, as long as 1152 of the contraction.
+constexpr int kTurn = 32 * 32;
 template <int ACT, bool F32>
 __device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
                                            const uint32_t (&v)[32], float* buf) {
-  if (p.vec) {
-    if (m >= p.M) return;
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[j + i]);
-      epilogue8<ACT, F32>(p, m, n + j, f);
-    }
-    return;
-  }
   const int lane = threadIdx.x & 31;
   __syncwarp();  // the previous step's values have been read
 #pragma unroll
-  for (int i = 0; i < 32; ++i) buf[lane * 33 + i] = __uint_as_float(v[i]);
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(buf + lane * 32 + 4 * (c ^ (lane & 7))) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
   __syncwarp();
   const long m0 = m - lane;
-  const int rows = static_cast<int>(min(32l, p.M - m0)), col = n + lane;
-  if (col < p.N) {
+  if (p.vec) {
+    const int c = 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 8 * i + (lane >> 2);
+      const float4 x = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * (c ^ (row & 7)));
+      const float4 y = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * ((c + 1) ^ (row & 7)));
+      float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      if (m0 + row < p.M) epilogue8<ACT, F32>(p, m0 + row, n + 4 * c, f);
+    }
+  } else if (n + lane < p.N) {
+    const int rows = static_cast<int>(min(32l, p.M - m0)), col = n + lane;
     const float b = p.bias != nullptr ? ldf(p.bias, col, p.bias_bf16) : 0.f;
 #pragma unroll 4
     for (int r = 0; r < rows; ++r) {
-      const float z = buf[r * 33 + lane] + b;
+      const float z = buf[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
       const float res =
           p.residual != nullptr ? ldf(p.residual, (m0 + r) * p.ld_res + col, !F32) : 0.f;
       if (p.preact != nullptr) stf(p.preact, (m0 + r) * p.ld_out + col, F32, z);
@@ -338,25 +340,25 @@ __device__ __forceinline__ void join_rows(const LinearEpi& p, const float* stg, 
 // ====================================================== CTA-pair kernel
 // tcgen05.mma.cta_group::2, M = 256 (128 rows of A in each CTA), N = 256
 // (128 rows of B in each CTA), 128 of the contraction per stage.  Roles in
-// each CTA (192 threads): warp 0 TMA producer (ring of 3 stages, 32 KB of A
+// each CTA (320 threads): warp 0 TMA producer (ring of 3 stages, 32 KB of A
 // and of B each), warp 1 TMEM and, on rank 0, the MMA issuer (two
 // 256-column accumulators, so a tile's epilogue runs under the next tile's
-// products), warps 2-5 epilogue.  Both CTAs' loads complete on rank 0's stage
+// products), warps 2-9 epilogue (32 rows, half of the columns).  Both CTAs' loads complete on rank 0's stage
 // barrier; rank 0's commits arrive on both CTAs' stage-free and
 // accumulator-full barriers; both epilogues arrive on rank 0's
 // accumulator-free barrier.  Every mbarrier wait is bounded.
 constexpr int kPStages = 3;
-constexpr int kPThreads = 192;
+constexpr int kPThreads = 320;
 constexpr int kPSlab = 128 * BK * 2;        // 16 KB: 128 rows x 64, or 64 rows x 128
 constexpr int kPOper = 2 * kPSlab;          // one operand's part of a stage
 constexpr int kPOffB = kPStages * kPOper;
 constexpr int kPOffBar = 2 * kPStages * kPOper;
 constexpr int kPBars = 2 * kPStages + 2 + 2 + 1;
 constexpr int kPOffMisc = kPOffBar + kPBars * 8;
-constexpr int kPOffOdd = kPOffMisc + 16;    // a buffer per epilogue warp
-constexpr int kPSmem = kPOffOdd + 4 * kOddBuf * 4 + 1024;
-constexpr int kASmem = kPOffOdd + 8 * kOddBuf * 4 + 1024;  // of the kernel with 8 such warps
-static_assert(kASmem <= 227 * 1024, "shared memory budget");
+constexpr int kPOffTurn = kPOffMisc + 8 + 64;  // a buffer per epilogue warp
+static_assert(kPOffTurn % 16 == 0 && kPOffMisc % 8 == 0, "aligned");
+constexpr int kPSmem = kPOffTurn + 8 * kTurn * 4 + 1024;
+static_assert(kPSmem <= 227 * 1024, "shared memory budget");
 
 // Tile order: groups of `group` row tiles, all column tiles of a group
 // before the next, so the tiles in flight share operand rows in L2.
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(smem_u32(&tfull[a]), 1);
-      mbar_init(smem_u32(&tempty[a]), 8);
+      mbar_init(smem_u32(&tempty[a]), 16);
     }
     mbar_init(smem_u32(fin), 1);
     *s_abort = 0;
@@ -513,9 +515,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
     }
   } else {
-    const int q = warp & 3;  // TMEM lane quarter this warp may access
-    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    float* const odd = reinterpret_cast<float*>(smem + kPOffOdd) + (warp - 2) * kOddBuf;
+    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, column half
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 128 * half;
+    float* const turn = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 2) * kTurn;
     int it = 0;
     for (int tile = cid; tile < total; tile += ncl, ++it) {
       int mi, ni;
@@ -529,13 +531,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const long m = static_cast<long>(mi) * 256 + 128 * rank + 32 * q + lane;
-      const int n0 = ni * 256;
-      const int steps = min(8, (p.epi.N - n0 + 31) >> 5);
-      for (int s = 0; s < steps; ++s) {
+      const int n0 = ni * 256 + 128 * half;
+#pragma unroll 1
+      for (int s = 0; s < 4; ++s) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(tl + acc * 256 + 32 * s, v);
         tmem_ld_wait();
-        if (s == steps - 1) {  // every column read: hand the accumulator back
+        if (s == 3) {  // every column read: hand the accumulator back
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             else mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
           }
         }
-        epilogue32<ACT, false>(p.epi, m, n0 + 32 * s, v, odd);
+        if (n0 + 32 * s < p.epi.N) epilogue32<ACT, false>(p.epi, m, n0 + 32 * s, v, turn);
       }
     }
   }
@@ -560,9 +562,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
 // fp32 results.  The tensor core truncates each addition into its fp32
 // accumulator, a bias toward zero that grows with the number of additions:
 // measured 1.0e-6 of the result per 1024 of the contraction (7.9e-6 at 7168,
-// where fp32 arithmetic has 0.9e-6).  So an accumulator takes 512 of the
+// where fp32 arithmetic has 0.9e-6).  So an accumulator takes 768 of the
 // contraction, and the epilogue warps add each such part in registers,
-// rounding to nearest, while the other accumulator is filled: 5e-7 at any
+// rounding to nearest, while the other accumulator is filled: 7e-7 at any
 // length, and the additions hide under the products.
 //
 // Few tiles.  A cluster of S pairs shares a tile: pair i takes the i-th part of
@@ -570,25 +572,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
 //
 // 320 threads: producer, MMA, 8 epilogue warps (a thread: one row, 128 columns).
 constexpr int kAThreads = 320;
-constexpr int kASeg = 4;          // stages (of 128) per part
+constexpr int kASeg = 6;          // stages (of 128) per part; with 4 the parts cost 2 % more time
 constexpr int kAStride = 260;     // floats per staged row: 256 + 4 (no bank conflicts)
 static_assert(128 * kAStride * 4 <= kPOffBar, "staged tile fits the ring");
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
 // Arrive on the mbarrier at shared offset `bar` in the CTAs of `mask` when
 // this thread's tcgen05 operations so far have completed.
 __device__ __forceinline__ void umma_commit_pair_mask(uint32_t bar, uint16_t mask) {
@@ -757,7 +744,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, column half
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 128 * half;
-    float* const odd = reinterpret_cast<float*>(smem + kPOffOdd) + (warp - 2) * kOddBuf;
+    float* const turn = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 2) * kTurn;
     auto release = [&](int buf) {  // this warp has read the part
       tc_fence_before();
       __syncwarp();
@@ -788,7 +775,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[32 * s + i] += __uint_as_float(v[i]);
         }
-        if (SPLIT || kb + kASeg < kb1) release(buf);
+        release(buf);
       }
       if (!ok) break;
       if (SPLIT) {
@@ -800,28 +787,17 @@ __global__ void __launch_bounds__(kAThreads, 1)
           *reinterpret_cast<float4*>(row + j) =
               make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
       } else {
-        // back into the last part's accumulator, so that the epilogue is a
-        // loop over TMEM columns (one copy of its code) and not over registers
-        const int buf = (it & 1) ^ 1;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * s + i]);
-          tmem_st_32x32b_x32(tl + buf * 256 + 32 * s, v);
-        }
-        tmem_st_wait();
         int mi, ni;
         pair_tile(tile, mt, nt, p.group, &mi, &ni);
         const long m = static_cast<long>(mi) * 256 + 128 * rank + 32 * q + lane;
-#pragma unroll 1
-        for (int s = 0; s < 4; ++s) {
+        const int n0 = ni * 256 + 128 * half;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {  // the accumulators are free: the next tile runs on
           uint32_t v[32];
-          tmem_ld_32x32b_x32(tl + buf * 256 + 32 * s, v);
-          tmem_ld_wait();
-          epilogue32<ACT, true>(p.epi, m, ni * 256 + 128 * half + 32 * s, v, odd);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * s + i]);
+          if (n0 + 32 * s < p.epi.N) epilogue32<ACT, true>(p.epi, m, n0 + 32 * s, v, turn);
         }
-        release(buf);
       }
     }
   }
@@ -1241,13 +1217,13 @@ cudaError_t launch_sums(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Linear
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * split);
   cfg.blockDim = dim3(kAThreads);
-  cfg.dynamicSmemBytes = kASmem;
+  cfg.dynamicSmemBytes = kPSmem;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   static std::atomic<int> max_clusters[64] = {};  // pairs without a split
   int nc = max_clusters[dev].load(std::memory_order_acquire);
   if (nc == 0) {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kASmem);
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPSmem);
     if (err != cudaSuccess) return err;
     cfg.gridDim = dim3(2);
     attr[0].val.clusterDim.x = 2;
