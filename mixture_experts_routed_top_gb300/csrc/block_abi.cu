@@ -415,15 +415,15 @@ moe_status moe_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, 
   e.vec = N % 8 == 0 && rows16(ld_out, size_of(out_dt)) &&
           (!residual || rows16(ld_res, size_of(out_dt)));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (T <= kLinearGemvRows) {
-    LinearGemvArgs g;
+  if (linear_streams(T, N)) {
+    LinearStreamArgs g;
     g.x = static_cast<const __nv_bfloat16*>(x);
     g.w = static_cast<const __nv_bfloat16*>(w);
     g.ld_x = ld_x;
     g.ld_w = ld_w;
     g.K = K;
     g.epi = e;
-    const cudaError_t r = launch_linear_gemv(g, device_sms(), s);
+    const cudaError_t r = launch_linear_stream(g, device_sms(), s);
     return r == cudaSuccess ? MOE_OK : cuda_error(r, fn);
   }
   LinearDev p;

@@ -14,11 +14,12 @@
 // 64 (rows) x the contraction length of a stage; both land in 128-byte rows.
 // Edges in any direction read as zeros (TMA) and are not stored.
 //
-// Three kernels, chosen by linear_path():
+// The kernels, chosen by linear_streams() and linear_path():
 //   linear_pair_kernel   256 x 256 tiles on CTA pairs, persistent: large products
 //   linear_tile_kernel   128 x 128 tiles, the contraction split over the CTAs
 //                        of a cluster: few tiles
-//   linear_gemv_kernel   up to 8 tokens: the weights streamed through CUDA cores
+//   linear_stream_kernel a few tokens: the weights streamed into registers, and
+//   linear_vector_kernel for one token
 #include <algorithm>
 #include <atomic>
 
@@ -997,68 +998,199 @@ __global__ void __launch_bounds__(kTThreads)
         rank * rows, rows, static_cast<long>(mi) * 128, ni * 128);
 }
 
-// ====================================================== few tokens
-// Weights [N, K] streamed once by CUDA cores: WPR warps of a block share R
-// rows of w, each lane multiplying 16-byte pieces of them with the same
-// pieces of the TT tokens (read through L1).
-template <int TT, int WPR>
-__global__ void __launch_bounds__(256) linear_gemv_kernel(const LinearGemvArgs a) {
-  constexpr int R = 2;                // rows of w per warp: they share the token loads
+// ====================================================== one token
+// The weights [N, K] are read once, and that is what it costs: WPR warps of a
+// block share two rows of w, each lane multiplying 16-byte pieces of them with
+// the token's, and add their sums in order.
+template <int WPR>
+__global__ void __launch_bounds__(256)
+    linear_vector_kernel(const __grid_constant__ LinearStreamArgs a) {
+  constexpr int R = 2;                // rows of w per warp: they share the token's loads
   constexpr int GROUPS = 8 / WPR;     // row pairs per block
   pdl_launch_dependents();
-  __shared__ float s_part[8][R * TT];
+  __shared__ float s_part[8][R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp / WPR, part = warp % WPR;
   const int n0 = (blockIdx.x * GROUPS + grp) * R;
   pdl_wait();
-  float acc[R][TT] = {};
+  float acc[R] = {};
   const int chunks = a.K / 8;
   if (n0 < a.epi.N) {
     const __nv_bfloat16* w0 = a.w + static_cast<long>(n0) * a.ld_w;
     const __nv_bfloat16* w1 = a.w + static_cast<long>(min(n0 + 1, a.epi.N - 1)) * a.ld_w;
 #pragma unroll 4
     for (int c = part * 32 + lane; c < chunks; c += WPR * 32) {
-      float f[R][8];
+      float f[R][8], x[8];
       ld8(w0, c * 8, true, f[0]);
       ld8(w1, c * 8, true, f[1]);
+      ld8(a.x, c * 8, true, x);
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        if (t < a.epi.M) {
-          float x[8];
-          ld8(a.x, t * a.ld_x + c * 8, true, x);
+      for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(f[r][j], x[j], acc[r][t]);
-        }
-      }
+        for (int j = 0; j < 8; ++j) acc[r] = fmaf(f[r][j], x[j], acc[r]);
     }
   }
 #pragma unroll
-  for (int r = 0; r < R; ++r)
+  for (int r = 0; r < R; ++r) {
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1)
-        acc[r][t] += __shfl_xor_sync(0xffffffffu, acc[r][t], off);
-      if (lane == 0) s_part[warp][r * TT + t] = acc[r][t];
-    }
+    for (int off = 16; off > 0; off >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], off);
+    if (lane == 0) s_part[warp][r] = acc[r];
+  }
   __syncthreads();
-  if (threadIdx.x < GROUPS * R * TT) {
-    const int g = threadIdx.x / (R * TT), i = threadIdx.x % (R * TT);
-    const int r = i / TT, t = i % TT;
-    const int n = (blockIdx.x * GROUPS + g) * R + r;
-    if (n < a.epi.N && t < a.epi.M) {
-      float z = 0.f;
+  const int i = threadIdx.x, n = blockIdx.x * GROUPS * R + i;
+  if (i < GROUPS * R && n < a.epi.N) {
+    float z = 0.f;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) z += s_part[g * WPR + w][i];
-      const LinearEpi& p = a.epi;
-      if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
-      if (p.preact != nullptr) stf(p.preact, t * p.ld_out + n, p.out_f32, z);
-      z = act_f(z, p.act, p.out_f32);
-      if (p.residual != nullptr) z += ldf(p.residual, t * p.ld_res + n, !p.out_f32);
-      stf(p.out, t * p.ld_out + n, p.out_f32, z);
+    for (int w = 0; w < WPR; ++w) z += s_part[i / R * WPR + w][i % R];
+    const LinearEpi& p = a.epi;
+    if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
+    if (p.preact != nullptr) stf(p.preact, n, p.out_f32, z);
+    z = act_f(z, p.act, p.out_f32);
+    if (p.residual != nullptr) z += ldf(p.residual, n, !p.out_f32);
+    stf(p.out, n, p.out_f32, z);
+  }
+}
+
+// ====================================================== few tokens
+// 2 to 16 tokens, to 32 where there are few rows: the weights [N, K] are again
+// read once, straight from memory into the registers that multiply them.  So
+// no tiles in shared memory and no TMEM: a thread's 16-byte loads are operand
+// fragments of the warp-level product (16 weight rows x 8 tokens x 16), whose
+// contraction index may be counted in any order as long as both operands do
+// it alike: of 32 consecutive elements of a row, lane 4 g + t holds 8 t .. 8 t + 7
+// of row g (and of row g + 8, and of token g), the first four of them in one
+// instruction and the others in the next.  8 tokens at 2048 x 7168 (weights that
+// take 4.3 us to arrive) 9.4 us, against 24 on CUDA cores, most of it unpacking,
+// and 15 in tiles with a split contraction; 16 tokens 10.6 against 15; 32 tokens
+// at 256 x 7168 5.6 against 10.4, but at 7168 x 2048 14.3 against 13.4.
+//
+// A tile of 16 rows is shared by `wpr` warps of each of the S blocks of a cluster,
+// which take groups of 32 G of the contraction in turn and ask for a whole
+// group before they use any of it; the more of them, the more of the weights
+// are on their way at once.  After each group its sums are added to fp32
+// registers (the tensor core truncates its additions); at the end the warps'
+// sums are added in order, then the blocks', through the cluster's shared
+// memory (half a kilobyte each).
+__device__ __forceinline__ uint4 ld_stream(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void warp_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+constexpr int kStreamWarps = 8;
+// NT: groups of 8 tokens; G: steps of 32 of the contraction per group.
+template <int NT>
+struct StreamLay {
+  static constexpr int G = NT == 1 ? 8 : 4, TOK = 8 * NT;
+};
+template <int NT>
+__global__ void __launch_bounds__(kStreamWarps * 32)
+    linear_stream_kernel(const __grid_constant__ LinearStreamArgs a) {
+  constexpr int G = StreamLay<NT>::G, TOK = StreamLay<NT>::TOK;
+  pdl_launch_dependents();
+  __shared__ float s_part[kStreamWarps][TOK][17];
+  __shared__ float s_sum[kStreamWarps][TOK][16];  // of a tile, over this block's warps
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wpr = a.wpr, S = a.split, rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tiles = kStreamWarps / wpr;  // of a block
+  const int tile0 = blockIdx.x / S * tiles, part = rank * wpr + warp % wpr;
+  const int n0 = (tile0 + warp / wpr) * 16;
+  const int N = a.epi.N, T = a.epi.M, K = a.K;
+  pdl_wait();
+  float sum[NT][4] = {};
+  if (n0 < N) {
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const bool on0 = n0 + g < N, on1 = n0 + 8 + g < N;
+    const __nv_bfloat16* w0 = a.w + static_cast<long>(n0 + g) * a.ld_w;
+    const __nv_bfloat16* w1 = w0 + 8 * a.ld_w;
+#pragma unroll 1
+    for (int k0 = part * (32 * G); k0 < K; k0 += wpr * S * (32 * G)) {
+      uint4 wv[G][2], xv[G][NT];
+#pragma unroll
+      for (int s = 0; s < G; ++s) {
+        const int k = k0 + 32 * s + 8 * t;
+        wv[s][0] = on0 && k < K ? ld_stream(w0 + k) : zero;
+        wv[s][1] = on1 && k < K ? ld_stream(w1 + k) : zero;
+      }
+#pragma unroll
+      for (int s = 0; s < G; ++s) {
+        const int k = k0 + 32 * s + 8 * t;
+#pragma unroll
+        for (int q = 0; q < NT; ++q)
+          xv[s][q] = 8 * q + g < T && k < K
+                         ? __ldg(reinterpret_cast<const uint4*>(a.x + (8 * q + g) * a.ld_x + k))
+                         : zero;
+      }
+      float c[NT][4] = {};
+#pragma unroll
+      for (int s = 0; s < G; ++s)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          const uint4 lo = wv[s][0], hi = wv[s][1], x = xv[s][q];
+          warp_mma(c[q], lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+          warp_mma(c[q], lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+        }
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[q][i] += c[q][i];
     }
+  }
+  // a lane's sums: rows g and g + 8, tokens 2 t and 2 t + 1 of each 8
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_part[warp][8 * q + 2 * t + (i & 1)][g + 8 * (i >> 1)] = sum[q][i];
+  __syncthreads();
+  const LinearEpi& p = a.epi;
+  const int count = tiles * TOK * 16;  // (tile, token, row), the row fastest
+  if (S > 1) {
+    for (int i = threadIdx.x; i < count; i += kStreamWarps * 32) {
+      const int tl = i / (TOK * 16), tok = i / 16 % TOK, r = i % 16;
+      float z = 0.f;
+      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
+      (&s_sum[0][0][0])[i] = z;
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
+  // the blocks of a cluster share the results out among them
+  for (int i = threadIdx.x + rank * (kStreamWarps * 32); i < count; i += S * (kStreamWarps * 32)) {
+    const int tl = i / (TOK * 16), tok = i / 16 % TOK, r = i % 16, n = (tile0 + tl) * 16 + r;
+    if (n >= N || tok >= T) continue;
+    float z = 0.f;
+    if (S > 1) {
+      const uint32_t at = smem_u32(&s_sum[0][0][0] + i);
+#pragma unroll 8
+      for (int q = 0; q < S; ++q) z += ld_cluster_f32(mapa_shared(at, q));
+    } else {
+      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
+    }
+    if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
+    if (p.preact != nullptr) stf(p.preact, tok * p.ld_out + n, p.out_f32, z);
+    z = act_f(z, p.act, p.out_f32);
+    if (p.residual != nullptr) z += ldf(p.residual, tok * p.ld_res + n, !p.out_f32);
+    stf(p.out, tok * p.ld_out + n, p.out_f32, z);
+  }
+  if (S > 1) {
+    __syncwarp();
+    cluster_sync_all();  // the others have read this block's sums
   }
 }
 
@@ -1280,19 +1412,44 @@ cudaError_t launch_tile(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Linear
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-template <int TT, int WPR>
-cudaError_t launch_gemv_t(const LinearGemvArgs& a, cudaStream_t s) {
-  const int rows = 8 / WPR * 2;
-  return launch_pdl(linear_gemv_kernel<TT, WPR>, dim3(ceil_div(a.epi.N, rows)), dim3(256), 0, s, a);
+template <int WPR>
+cudaError_t launch_vector_w(const LinearStreamArgs& a, cudaStream_t s) {
+  return launch_pdl(linear_vector_kernel<WPR>, dim3(ceil_div(a.epi.N, 8 / WPR * 2)), dim3(256), 0, s, a);
 }
-template <int TT>
-cudaError_t launch_gemv_w(const LinearGemvArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_vector(const LinearStreamArgs& a, int num_sms, cudaStream_t s) {
   // warps per row pair: enough that every SM has 40 warps, at most 8
   const long pairs = (a.epi.N + 1) / 2, want = 40L * num_sms;
-  if (pairs >= want) return launch_gemv_t<TT, 1>(a, s);
-  if (2 * pairs >= want) return launch_gemv_t<TT, 2>(a, s);
-  if (4 * pairs >= want) return launch_gemv_t<TT, 4>(a, s);
-  return launch_gemv_t<TT, 8>(a, s);
+  if (pairs >= want) return launch_vector_w<1>(a, s);
+  if (2 * pairs >= want) return launch_vector_w<2>(a, s);
+  if (4 * pairs >= want) return launch_vector_w<4>(a, s);
+  return launch_vector_w<8>(a, s);
+}
+
+template <int NT>
+cudaError_t launch_stream(LinearStreamArgs a, int num_sms, cudaStream_t s) {
+  // warps of a block per tile, then blocks: until every SM has WANT warps, as
+  // long as each has a group of the contraction
+  constexpr long WANT = 16;
+  constexpr int kGroup = 32 * StreamLay<NT>::G;
+  const long tiles = ceil_div(a.epi.N, 16);
+  a.wpr = a.split = 1;
+  while (a.wpr < kStreamWarps && tiles * a.wpr < WANT * num_sms && a.wpr * kGroup < a.K) a.wpr *= 2;
+  while (a.split < 8 && tiles * a.wpr * a.split < WANT * num_sms && a.wpr * a.split * kGroup < a.K)
+    a.split *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(tiles, kStreamWarps / a.wpr) * a.split);
+  cfg.blockDim = dim3(kStreamWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<NT>, a);
 }
 
 }  // namespace
@@ -1372,12 +1529,14 @@ cudaError_t launch_linear(const CUtensorMap& tm_a, const CUtensorMap& tm_b, cons
   return launch_tile<false, false>(tm_a, tm_b, p, path.split, s);
 }
 
-cudaError_t launch_linear_gemv(const LinearGemvArgs& a, int num_sms, cudaStream_t s) {
+bool linear_streams(int T, int N) { return T <= 16 || (T <= 32 && N <= 1024); }
+
+cudaError_t launch_linear_stream(const LinearStreamArgs& a, int num_sms, cudaStream_t s) {
   cudaError_t e;
-  if (a.epi.M <= 1) e = launch_gemv_w<1>(a, num_sms, s);
-  else if (a.epi.M <= 2) e = launch_gemv_w<2>(a, num_sms, s);
-  else if (a.epi.M <= 4) e = launch_gemv_w<4>(a, num_sms, s);
-  else e = launch_gemv_w<8>(a, num_sms, s);
+  if (a.epi.M == 1) e = launch_vector(a, num_sms, s);
+  else if (a.epi.M <= 8) e = launch_stream<1>(a, num_sms, s);
+  else if (a.epi.M <= 16) e = launch_stream<2>(a, num_sms, s);
+  else e = launch_stream<4>(a, num_sms, s);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -409,15 +409,16 @@ LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms);
 // false, true / true, true); the maps' boxes are those linear_boxes names.
 cudaError_t launch_linear(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const LinearDev& p,
                           bool a_mn, bool b_mn, const LinearPath& path, cudaStream_t s);
-struct LinearGemvArgs {
+struct LinearStreamArgs {
   const __nv_bfloat16* x;
   const __nv_bfloat16* w;
   long ld_x, ld_w;
   int K;
+  int wpr, split;          // warps of a block and blocks that share a tile (set by the launcher)
   LinearEpi epi;
 };
-constexpr int kLinearGemvRows = 8;    // tokens at or below: the weights stream through CUDA cores
-cudaError_t launch_linear_gemv(const LinearGemvArgs& a, int num_sms, cudaStream_t s);
+bool linear_streams(int T, int N);     // few tokens: the weights stream into registers
+cudaError_t launch_linear_stream(const LinearStreamArgs& a, int num_sms, cudaStream_t s);
 struct LinearDzArgs {
   const void* dy;
   const void* preact;      // null: dz = dy

@@ -252,7 +252,8 @@ def _acc(K):
 
 
 LINEARS = [  # T, K, N: one tile and less, ragged edges, a split contraction, several tiles, both tile kernels
-    (1, 8, 1), (1, 2048, 512), (3, 264, 77), (8, 1024, 130), (9, 64, 1), (16, 7168, 256), (100, 72, 33),
+    (1, 8, 1), (1, 2048, 512), (2, 2056, 1000), (12, 7168, 40), (15, 136, 4001), (30, 1032, 700), (32, 64, 17),
+    (17, 512, 1025), (3, 264, 77), (8, 1024, 130), (9, 64, 1), (16, 7168, 256), (100, 72, 33),
     (129, 1024, 129), (300, 520, 264), (257, 136, 3), (2050, 192, 1536), (2049, 328, 1601),
     (1301, 2056, 2041)]
 
