@@ -132,6 +132,10 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* s_red, int warps,
 
 constexpr int kMaxRed = 32 * 4;  // warps of a block x values of a reduction
 
+// Forward, the rows that the streamed kernels below do not take (above 8192
+// columns): a row per group of TX threads, held in registers.  4778 x 12288 bf16
+// with both norms and a gate per channel 152 us (3.1 TB/s), bound by the
+// latency of its three dependent trips with one row per block in flight.
 template <typename RT, bool VEC, int NV>
 __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a) {
   pdl_launch_dependents();
@@ -217,7 +221,10 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
 // each thread keeps the sums over its rows for its own columns (dw_pre,
 // dw_post and a per-channel dg) and leaves them as one partial row per
 // block; block_norm_partials_kernel adds those in block order, so the
-// result does not depend on timing.
+// result does not depend on timing.  For rows above 8192 columns, and rows of fp32
+// with an fp32 gate per element whose ring would not fit.  4778 x 12288 bf16 with
+// both norms and a gate per channel 652 us (1.1 TB/s): a column's sums and values
+// take more registers than its threads have.
 template <typename RT, bool VEC, int NV>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNormBwdArgs a) {
   pdl_launch_dependents();
@@ -366,17 +373,22 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------ streamed rows
-// Rows of H % 8 == 0, H <= 8192 columns with 16-byte row starts.  Blocks of up
-// to 512 threads stay on their SM and walk over the rows; a thread holds the
-// same NV pieces of 8 columns of every row (so weights and sums over tokens
-// stay in registers) and copies its own pieces of the next rows into its own
-// slots of a ring in shared memory (cp.async), so loads run while the block
-// computes.  No thread reads another's slots, so the ring needs no barrier;
-// the block meets only for the sums.
+// Rows of H <= 8192 columns.  Blocks of up to 512 threads stay on their SM and
+// walk over the rows; a thread holds the same NV pieces of 8 columns of every
+// row (so weights and sums over tokens stay in registers), and the next rows
+// are copied into a ring in shared memory (cp.async), so loads run while the
+// block computes.  Where H % 8 == 0 and rows start at 16 bytes, a thread copies
+// its own pieces into its own slots: no thread reads another's, so the ring
+// needs no barrier; the block meets only for the sums.
 constexpr int kRingBytes = 200 * 1024;   // rings of an SM's blocks together, at most
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// `bytes` of the 16 from memory, zeros for the others.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -435,13 +447,22 @@ __device__ __forceinline__ void store8(float* p, const F2 (&v)[4]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(a.x, a.y, b.x, b.y);
   reinterpret_cast<float4*>(p)[1] = make_float4(c.x, c.y, d.x, d.y);
 }
-// 8 weights (or per-channel gates) of a thread's columns; 1 where p is null
-// and 0 past the row's end.
+// 8 weights (or per-channel gates) of a thread's columns, next to each other or
+// (EDGE) 32 apart; 1 where p is null and 0 past the row's end.
+template <bool EDGE>
 __device__ __forceinline__ void weights8(const void* p, bool bf16, int col, int H, F2 (&v)[4]) {
   float f[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) f[e] = col < H ? 1.f : 0.f;
-  if (p != nullptr && col < H) {
+  for (int e = 0; e < 8; ++e) f[e] = col + (EDGE ? 32 * e : 0) < H ? 1.f : 0.f;
+  if (EDGE) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = col + 32 * e;
+      if (p != nullptr && c < H)
+        f[e] = bf16 ? get(static_cast<const __nv_bfloat16*>(p) + c)
+                    : get(static_cast<const float*>(p) + c);
+    }
+  } else if (p != nullptr && col < H) {
     if (bf16) load8(static_cast<const __nv_bfloat16*>(p) + col, f);
     else load8(static_cast<const float*>(p) + col, f);
   }
@@ -480,6 +501,71 @@ struct Slots {
     }
   }
 };
+
+// Rows of any length and stride (EDGE).  They are copied as the aligned 16 bytes
+// that they touch, from the one in which the row begins (none lies before the
+// tensor, whose first row is aligned), into a ring of whole rows that the block
+// shares, and read from there element by element: a warp has 256 NV columns
+// side by side, a lane every 32nd of them, so that loads from the ring and
+// stores are runs of 32 elements whatever the alignment, in few instructions
+// (aligned vectors with the columns shifted into place took three times as
+// many and twice the time).  Past the row's end the ring holds zeros.
+__device__ __forceinline__ uint32_t byte_in_16(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 15u;
+}
+// Bytes in the ring of a row of `threads` times 8 NV elements.
+__host__ __device__ constexpr int edge_bytes(int threads, int nv, int size) {
+  return threads * 8 * nv * size + 16;
+}
+template <typename T>
+__device__ __forceinline__ void edge_fetch(char* to, const T* row, int H) {
+  const int lead = static_cast<int>(byte_in_16(row)), bytes = H * static_cast<int>(sizeof(T));
+  const char* from = reinterpret_cast<const char*>(row) - lead;
+  // as many pieces for every row, so that none keeps an earlier row's end
+  const int n = (16 - static_cast<int>(sizeof(T)) + bytes) / 16 + 1;
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    cp_async16(smem_u32(to + 16 * i), from + 16 * i, min(max(lead + bytes - 16 * i, 0), 16));
+}
+// 8 of a thread's columns of the row that begins at byte `sh` of the ring's row
+// at `at`.
+__device__ __forceinline__ void edge_read(const char* at, bool f32, uint32_t sh, int col,
+                                          F2 (&v)[4]) {
+  if (f32) {
+    const float* p = reinterpret_cast<const float*>(at + sh) + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2(p[64 * i], p[64 * i + 32]);
+  } else {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(at + sh) + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = f2(__uint_as_float(static_cast<uint32_t>(p[64 * i]) << 16),
+                __uint_as_float(static_cast<uint32_t>(p[64 * i + 32]) << 16));
+  }
+}
+// Columns col .. of a row: 8 next to each other, or (EDGE) 32 apart.
+template <bool EDGE, typename T>
+__device__ __forceinline__ void put8(T* row, int col, int H, const F2 (&v)[4]) {
+  if (!EDGE) {
+    store8(row + col, v);
+    return;
+  }
+  T* const to = row + col;
+  if ((col & ~31) + 256 <= H) {  // the same in a warp
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 q = parts(v[i]);
+      put(to + 64 * i, q.x);
+      put(to + 64 * i + 32, q.y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 q = parts(v[i]);
+      if (col + 64 * i < H) put(to + 64 * i, q.x);
+      if (col + 64 * i + 32 < H) put(to + 64 * i + 32, q.y);
+    }
+  }
+}
 
 // Sums over a row's warps, one barrier each: two buffers in turn, so a buffer
 // is written again only after a barrier that follows its reads.  s_red:
@@ -537,8 +623,14 @@ constexpr int ring_blocks(int nv) { return nv == 1 ? 2 : 1; }
 
 // MID: a call between two blocks (y given, norm before the next block, no
 // gate per element), whose options are then constants of the code.
-template <typename RT, int NV, int STAGES, bool MID>
-__global__ void __launch_bounds__(kRingThreads, ring_blocks(NV)) block_norm_ring_kernel(const BlockNormArgs a) {
+// 8192 x 7168 bf16 with both norms and a gate per channel: 80 us (470 MB, 5.9
+// TB/s, 86 % of a copy), bound by memory; 4099 x 2048 with an fp32 stream 18.5
+// (101 MB, 5.4 TB/s); one token 3.7, three dependent trips (row, two sums).
+// EDGE: 8192 x 7167 139 us (3.4 TB/s), bound by issue; a row per block without a
+// ring 309.
+template <typename RT, int NV, int STAGES, bool MID, bool EDGE>
+__global__ void __launch_bounds__(kRingThreads, ring_blocks(NV))
+    block_norm_ring_kernel(const BlockNormArgs a) {
   pdl_launch_dependents();
   extern __shared__ uint4 s_ring[];
   __shared__ __align__(16) F2 s_red[kRedPairs];
@@ -552,14 +644,40 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV)) block_norm_ring
   for (int i = tid; i < kRedPairs; i += nthr) s_red[i] = f2(0.f);
   __syncthreads();
   const int H = a.H;
-  auto col = [&](int v) { return static_cast<int>(threadIdx.x + blockDim.x * v) * 8; };
+  const RT* const res = static_cast<const RT*>(a.residual);
+  const __nv_bfloat16* const ys = static_cast<const __nv_bfloat16*>(a.y);
+  // EDGE: a row's tensors one behind the other
+  const int row32 = edge_bytes(blockDim.x, NV, 4), row16 = edge_bytes(blockDim.x, NV, 2);
+  const int o_y = R32 ? row32 : row16, o_g = o_y + (has_y ? row16 : 0),
+            row_bytes = o_g + (elem ? (a.gate_bf16 ? row16 : row32) : 0);
+  // EDGE: elements past the row's end read as zeros
+  auto col = [&](int v) {
+    return EDGE ? static_cast<int>(threadIdx.x >> 5) * (256 * NV) + (threadIdx.x & 31) + 256 * v
+                : static_cast<int>(threadIdx.x + blockDim.x * v) * 8;
+  };
+  auto in = [&](int v) { return EDGE || col(v) < H; };
   const float inv_h = 1.f / static_cast<float>(H);
   const long step = static_cast<long>(gridDim.x) * blockDim.y;
+  auto edge_row = [&](int st) {
+    return reinterpret_cast<char*>(s_ring) + (st * blockDim.y + threadIdx.y) * row_bytes;
+  };
+  if (EDGE) {
+    for (int i = tid; i < STAGES * static_cast<int>(blockDim.y) * row_bytes / 16; i += nthr)
+      s_ring[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
   auto fetch = [&](long t, int st) {
-    if (t < a.T) {
+    if (EDGE && t < a.T) {
+      char* const to = edge_row(st);
+      edge_fetch(to, res + t * a.ld_res, H);
+      if (has_y) edge_fetch(to + o_y, ys + t * a.ld_y, H);
+      if (elem && a.gate_bf16)
+        edge_fetch(to + o_g, static_cast<const __nv_bfloat16*>(a.gate) + t * a.ld_gate, H);
+      else if (elem) edge_fetch(to + o_g, static_cast<const float*>(a.gate) + t * a.ld_gate, H);
+    } else if (t < a.T) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        if (col(v) < H) {
+        if (in(v)) {
           const Slots sl{s_ring + (st * NV + v) * pv * kRingThreads + tid};
           sl.fetch8(0, static_cast<const RT*>(a.residual) + t * a.ld_res + col(v));
           if (has_y) sl.fetch8(PR, static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y + col(v));
@@ -577,20 +695,33 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV)) block_norm_ring
   F2 m[NV][4], wp[NV][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    weights8(a.post_weight, a.weight_bf16, col(v), H, m[v]);
+    weights8<EDGE>(a.post_weight, a.weight_bf16, col(v), H, m[v]);
     if (a.gate_kind == MOE_GATE_CHANNEL) {
-      weights8(a.gate, a.gate_bf16, col(v), H, wp[v]);
+      weights8<EDGE>(a.gate, a.gate_bf16, col(v), H, wp[v]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) m[v][e] = mul2(m[v][e], wp[v][e]);
     }
-    weights8(a.pre_weight, a.weight_bf16, col(v), H, wp[v]);
+    weights8<EDGE>(a.pre_weight, a.weight_bf16, col(v), H, wp[v]);
   }
+  auto gate_byte = [&](long t) {
+    return a.gate_bf16 ? byte_in_16(static_cast<const __nv_bfloat16*>(a.gate) + t * a.ld_gate)
+                       : byte_in_16(static_cast<const float*>(a.gate) + t * a.ld_gate);
+  };
+  auto read_y = [&](uint4* slot, const char* erow, int v, F2 (&y)[4]) {
+    if (EDGE) edge_read(erow + o_y, false, byte_in_16(ys + t * a.ld_y), col(v), y);
+    else Slots{slot + v * pv * kRingThreads}.read8(PR, false, y);
+  };
   int st = 0, turn = 0;
   for (long base = static_cast<long>(blockIdx.x) * blockDim.y; base < a.T; base += step, t += step) {
+    if (EDGE) {  // this row's copies, everyone's, and the last row is done with
+      cp_async_wait<STAGES - 2>();
+      __syncthreads();
+    }
     fetch(t + (STAGES - 1) * step, st == 0 ? STAGES - 1 : st - 1);
-    cp_async_wait<STAGES - 1>();
+    if (!EDGE) cp_async_wait<STAGES - 1>();
     const bool on = t < a.T;
     uint4* const slot = s_ring + st * NV * pv * kRingThreads + tid;
+    const char* const erow = edge_row(st);
     if (++st == STAGES) st = 0;
     F2 r[NV][4];
     float coef = a.scale;
@@ -602,9 +733,9 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV)) block_norm_ring
         F2 sq = f2(0.f);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          if (on && col(v) < H) {
+          if (on && in(v)) {
             F2 y[4];
-            Slots{slot + v * pv * kRingThreads}.read8(PR, false, y);
+            read_y(slot, erow, v, y);
 #pragma unroll
             for (int e = 0; e < 4; ++e) sq = fma2(y[e], y[e], sq);
           }
@@ -619,20 +750,22 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV)) block_norm_ring
       const Slots sl{slot + v * pv * kRingThreads};
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[v][e] = f2(0.f);
-      if (on && col(v) < H) {
-        sl.read8(0, R32, r[v]);
+      if (on && in(v)) {
+        if (EDGE) edge_read(erow, R32, byte_in_16(res + t * a.ld_res), col(v), r[v]);
+        else sl.read8(0, R32, r[v]);
         if (has_y) {
           F2 y[4];
-          sl.read8(PR, false, y);
+          read_y(slot, erow, v, y);
           if (elem) {
             F2 g[4];
-            sl.read8(PR + 1, !a.gate_bf16, g);
+            if (EDGE) edge_read(erow + o_g, !a.gate_bf16, gate_byte(t), col(v), g);
+            else sl.read8(PR + 1, !a.gate_bf16, g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], g[e]);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) r[v][e] = fma2(coef2, mul2(y[e], m[v][e]), r[v][e]);
-          store8(static_cast<RT*>(a.residual_out) + t * H + col(v), r[v]);
+          put8<EDGE>(static_cast<RT*>(a.residual_out) + t * H, col(v), H, r[v]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) sq = fma2(r[v][e], r[v][e], sq);
@@ -642,10 +775,10 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV)) block_norm_ring
       const F2 rstd = f2(rsqrtf(ring_sum(sum2(sq), s_red, turn) * inv_h + a.eps));
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        if (on && col(v) < H) {
+        if (on && in(v)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) r[v][e] = mul2(mul2(r[v][e], rstd), wp[v][e]);
-          store8(static_cast<__nv_bfloat16*>(a.normed) + t * H + col(v), r[v]);
+          put8<EDGE>(static_cast<__nv_bfloat16*>(a.normed) + t * H, col(v), H, r[v]);
         }
       }
     }
@@ -658,7 +791,11 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV)) block_norm_ring
 // gate's dg = scale * w_post * acc and dw_post = scale * g * acc are
 // multiples, since w_post and that gate do not depend on the token.
 // MID: both gradients and y given, no gate per element.
-template <typename RT, int NV, int STAGES, bool MID>
+// 8192 x 7168 bf16 with both norms and a gate per channel: 117 us and 7 for the
+// partial rows' sums (705 MB, 5.7 TB/s over both, 84 % of a copy), bound by
+// memory and nearly as much by issue.  EDGE: 8192 x 7167 255 us (2.8 TB/s), by
+// issue; without a ring 1684.
+template <typename RT, int NV, int STAGES, bool MID, bool EDGE>
 __global__ void __launch_bounds__(kRingThreads, 1)
     block_norm_backward_ring_kernel(const BlockNormBwdArgs a) {
   pdl_launch_dependents();
@@ -678,14 +815,48 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   for (int i = tid; i < kRedPairs; i += nthr) s_red[i] = f2(0.f);
   __syncthreads();
   const int H = a.H;
-  auto col = [&](int v) { return static_cast<int>(threadIdx.x + blockDim.x * v) * 8; };
+  const RT* const res = static_cast<const RT*>(a.residual);
+  const RT* const grs = static_cast<const RT*>(a.grad_res);
+  const __nv_bfloat16* const gns = static_cast<const __nv_bfloat16*>(a.grad_normed);
+  const __nv_bfloat16* const ys = static_cast<const __nv_bfloat16*>(a.y);
+  // EDGE: a row's tensors one behind the other
+  const int row32 = edge_bytes(blockDim.x, NV, 4), row16 = edge_bytes(blockDim.x, NV, 2);
+  const int rowR = R32 ? row32 : row16;
+  const int o_gr = has_gn ? rowR : 0, o_gn = o_gr + (has_gr ? rowR : 0),
+            o_y = o_gn + (has_gn ? row16 : 0), o_g = o_y + (has_y ? row16 : 0),
+            row_bytes = o_g + (elem ? (a.gate_bf16 ? row16 : row32) : 0);
+  // EDGE: elements past the row's end read as zeros
+  auto col = [&](int v) {
+    return EDGE ? static_cast<int>(threadIdx.x >> 5) * (256 * NV) + (threadIdx.x & 31) + 256 * v
+                : static_cast<int>(threadIdx.x + blockDim.x * v) * 8;
+  };
+  auto in = [&](int v) { return EDGE || col(v) < H; };
   const float inv_h = 1.f / static_cast<float>(H);
   const long step = static_cast<long>(gridDim.x) * blockDim.y;
+  auto edge_row = [&](int st) {
+    return reinterpret_cast<char*>(s_ring) + (st * blockDim.y + threadIdx.y) * row_bytes;
+  };
+  if (EDGE) {
+    for (int i = tid; i < STAGES * static_cast<int>(blockDim.y) * row_bytes / 16; i += nthr)
+      s_ring[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  }
   auto fetch = [&](long t, int st) {
-    if (t < a.T) {
+    if (EDGE && t < a.T) {
+      char* const to = edge_row(st);
+      if (has_gn) {
+        edge_fetch(to, res + t * a.ld_res, H);
+        edge_fetch(to + o_gn, gns + t * a.ld_gn, H);
+      }
+      if (has_gr) edge_fetch(to + o_gr, grs + t * a.ld_gres, H);
+      if (has_y) edge_fetch(to + o_y, ys + t * a.ld_y, H);
+      if (elem && a.gate_bf16)
+        edge_fetch(to + o_g, static_cast<const __nv_bfloat16*>(a.gate) + t * a.ld_gate, H);
+      else if (elem) edge_fetch(to + o_g, static_cast<const float*>(a.gate) + t * a.ld_gate, H);
+    } else if (t < a.T) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        if (col(v) < H) {
+        if (in(v)) {
           const Slots sl{s_ring + (st * NV + v) * pv * kRingThreads + tid};
           if (has_gn) {
             sl.fetch8(0, static_cast<const RT*>(a.residual) + t * a.ld_res + col(v));
@@ -707,34 +878,60 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   F2 m[NV][4], wp[NV][4];  // scale * post_weight * per-channel gate, pre_weight
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    weights8(post_w, a.weight_bf16, col(v), H, m[v]);
-    weights8(gch ? a.gate : nullptr, a.gate_bf16, col(v), H, wp[v]);
+    weights8<EDGE>(post_w, a.weight_bf16, col(v), H, m[v]);
+    weights8<EDGE>(gch ? a.gate : nullptr, a.gate_bf16, col(v), H, wp[v]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) m[v][e] = mul2(f2(a.scale), mul2(m[v][e], wp[v][e]));
-    weights8(a.pre_weight, a.weight_bf16, col(v), H, wp[v]);
+    weights8<EDGE>(a.pre_weight, a.weight_bf16, col(v), H, wp[v]);
   }
   F2 acc_pre[NV][4], acc[NV][4];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc_pre[v][e] = acc[v][e] = f2(0.f);
+  auto gate_byte = [&](long t) {
+    return a.gate_bf16 ? byte_in_16(static_cast<const __nv_bfloat16*>(a.gate) + t * a.ld_gate)
+                       : byte_in_16(static_cast<const float*>(a.gate) + t * a.ld_gate);
+  };
+  auto read_rq = [&](uint4* slot, const char* erow, int v, F2 (&r)[4], F2 (&q)[4]) {
+    if (EDGE) {
+      edge_read(erow, R32, byte_in_16(res + t * a.ld_res), col(v), r);
+      edge_read(erow + o_gn, false, byte_in_16(gns + t * a.ld_gn), col(v), q);
+    } else {
+      const Slots sl{slot + v * pv * kRingThreads};
+      sl.read8(0, R32, r);
+      sl.read8(p_gn, false, q);
+    }
+  };
+  auto read_y = [&](uint4* slot, const char* erow, int v, F2 (&y)[4]) {
+    if (EDGE) edge_read(erow + o_y, false, byte_in_16(ys + t * a.ld_y), col(v), y);
+    else Slots{slot + v * pv * kRingThreads}.read8(p_y, false, y);
+  };
+  auto read_g = [&](uint4* slot, const char* erow, int v, F2 (&g)[4]) {
+    if (EDGE) edge_read(erow + o_g, !a.gate_bf16, gate_byte(t), col(v), g);
+    else Slots{slot + v * pv * kRingThreads}.read8(p_g, !a.gate_bf16, g);
+  };
   int st = 0, turn = 0;
   for (long base = static_cast<long>(blockIdx.x) * blockDim.y; base < a.T; base += step, t += step) {
+    if (EDGE) {  // this row's copies, everyone's, and the last row is done with
+      cp_async_wait<STAGES - 2>();
+      __syncthreads();
+    }
     fetch(t + (STAGES - 1) * step, st == 0 ? STAGES - 1 : st - 1);
-    cp_async_wait<STAGES - 1>();
+    if (!EDGE) cp_async_wait<STAGES - 1>();
     const bool on = t < a.T;
     uint4* const slot = s_ring + st * NV * pv * kRingThreads + tid;
+    const char* const erow = edge_row(st);
     if (++st == STAGES) st = 0;
     float rstd = 1.f, corr = 0.f;
     if (has_gn) {
       F2 s0 = f2(0.f), s1 = f2(0.f);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        if (on && col(v) < H) {
+        if (on && in(v)) {
           const Slots sl{slot + v * pv * kRingThreads};
           F2 r[4], q[4];
-          sl.read8(0, R32, r);
-          sl.read8(p_gn, false, q);
+          read_rq(slot, erow, v, r, q);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             s0 = fma2(r[e], r[e], s0);
@@ -755,12 +952,13 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         const Slots sl{slot + v * pv * kRingThreads};
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[v][e] = f2(0.f);
-        if (!(on && col(v) < H)) continue;
-        if (has_gr) sl.read8(p_gr, R32, d[v]);
+        if (!(on && in(v))) continue;
+        if (has_gr && EDGE)
+          edge_read(erow + o_gr, R32, byte_in_16(grs + t * a.ld_gres), col(v), d[v]);
+        else if (has_gr) sl.read8(p_gr, R32, d[v]);
         if (has_gn) {
           F2 r[4], q[4];
-          sl.read8(0, R32, r);
-          sl.read8(p_gn, false, q);
+          read_rq(slot, erow, v, r, q);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const F2 qn = mul2(q[e], rstd2);
@@ -768,15 +966,15 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             d[v][e] = fma2(qn, wp[v][e], fma2(r[e], ncorr, d[v][e]));
           }
         }
-        if (a.d_res != nullptr) store8(static_cast<RT*>(a.d_res) + t * H + col(v), d[v]);
+        if (a.d_res != nullptr) put8<EDGE>(static_cast<RT*>(a.d_res) + t * H, col(v), H, d[v]);
         if (has_y) {
           F2 y[4];
-          sl.read8(p_y, false, y);
+          read_y(slot, erow, v, y);
 #pragma unroll
           for (int e = 0; e < 4; ++e) s0 = fma2(y[e], y[e], s0);
           if (elem) {
             F2 g[4];
-            sl.read8(p_g, !a.gate_bf16, g);
+            read_g(slot, erow, v, g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = mul2(y[e], g[e]);
           }
@@ -807,19 +1005,19 @@ __global__ void __launch_bounds__(kRingThreads, 1)
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const Slots sl{slot + v * pv * kRingThreads};
-      if (!(on && col(v) < H)) continue;
+      if (!(on && in(v))) continue;
       F2 y[4];
-      sl.read8(p_y, false, y);
+      read_y(slot, erow, v, y);
       if (elem) {
         F2 g[4], dg[4];
-        sl.read8(p_g, !a.gate_bf16, g);
+        read_g(slot, erow, v, g);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           dg[e] = mul2(mul2(gr, m[v][e]), mul2(y[e], d[v][e]));
           d[v][e] = mul2(d[v][e], g[e]);
         }
-        if (a.gate_bf16) store8(static_cast<__nv_bfloat16*>(a.d_gate) + t * H + col(v), dg);
-        else store8(static_cast<float*>(a.d_gate) + t * H + col(v), dg);
+        if (a.gate_bf16) put8<EDGE>(static_cast<__nv_bfloat16*>(a.d_gate) + t * H, col(v), H, dg);
+        else put8<EDGE>(static_cast<float*>(a.d_gate) + t * H, col(v), H, dg);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -827,7 +1025,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         acc[v][e] = fma2(gd, y[e], acc[v][e]);
         y[e] = fma2(m[v][e], gd, mul2(y[e], ncorr));
       }
-      store8(static_cast<__nv_bfloat16*>(a.d_y) + t * H + col(v), y);
+      put8<EDGE>(static_cast<__nv_bfloat16*>(a.d_y) + t * H, col(v), H, y);
     }
   }
   if (a.n_part == 0) return;
@@ -837,37 +1035,45 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (col(v) >= H) continue;
-    float* to = sum + static_cast<long>(threadIdx.y) * a.n_part * H + col(v);
+    if (!in(v)) continue;
+    float* to = sum + static_cast<long>(threadIdx.y) * a.n_part * H;
     F2 w[4];
     if (a.d_pre != nullptr) {
-      store8(to, acc_pre[v]);
+      put8<EDGE>(to, col(v), H, acc_pre[v]);
       to += H;
     }
     if (a.d_post != nullptr) {
-      weights8(gch ? a.gate : nullptr, a.gate_bf16, col(v), H, w);
+      weights8<EDGE>(gch ? a.gate : nullptr, a.gate_bf16, col(v), H, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = mul2(mul2(f2(a.scale), w[e]), acc[v][e]);
-      store8(to, w);
+      put8<EDGE>(to, col(v), H, w);
       to += H;
     }
     if (gch) {
-      weights8(post_w, a.weight_bf16, col(v), H, w);
+      weights8<EDGE>(post_w, a.weight_bf16, col(v), H, w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = mul2(mul2(f2(a.scale), w[e]), acc[v][e]);
-      store8(to, w);
+      put8<EDGE>(to, col(v), H, w);
     }
   }
   __syncthreads();
   float* part = a.partials + static_cast<long>(blockIdx.x) * a.n_part * H;
   const int total = a.n_part * H;
-  for (int i = tid * 4; i < total; i += nthr * 4) {   // H % 8 == 0
-    float4 v = *reinterpret_cast<const float4*>(sum + i);
-    for (int y = 1; y < blockDim.y; ++y) {
-      const float4 o = *reinterpret_cast<const float4*>(sum + static_cast<long>(y) * total + i);
-      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  if (EDGE) {
+    for (int i = tid; i < total; i += nthr) {
+      float v = sum[i];
+      for (int y = 1; y < blockDim.y; ++y) v += sum[y * total + i];
+      part[i] = v;
     }
-    *reinterpret_cast<float4*>(part + i) = v;
+  } else {
+    for (int i = tid * 4; i < total; i += nthr * 4) {  // H % 8 == 0
+      float4 v = *reinterpret_cast<const float4*>(sum + i);
+      for (int y = 1; y < blockDim.y; ++y) {
+        const float4 o = *reinterpret_cast<const float4*>(sum + static_cast<long>(y) * total + i);
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      }
+      *reinterpret_cast<float4*>(part + i) = v;
+    }
   }
 }
 
@@ -894,31 +1100,45 @@ cudaError_t ring_ready(K kern, std::atomic<int>* ready) {
   return cudaSuccess;
 }
 
-template <typename RT, int NV, int STAGES, bool MID>
+template <typename RT, int NV, int STAGES, bool MID, bool EDGE = false>
 cudaError_t fwd_ring(const BlockNormArgs& a, dim3 block, size_t smem, int grid, cudaStream_t s) {
   static std::atomic<int> ready[64] = {};
-  const cudaError_t e = ring_ready(block_norm_ring_kernel<RT, NV, STAGES, MID>, ready);
+  const cudaError_t e = ring_ready(block_norm_ring_kernel<RT, NV, STAGES, MID, EDGE>, ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl(block_norm_ring_kernel<RT, NV, STAGES, MID>, dim3(grid), block, smem, s, a);
+  return launch_pdl(block_norm_ring_kernel<RT, NV, STAGES, MID, EDGE>, dim3(grid), block, smem, s,
+                    a);
 }
-template <typename RT, int NV, int STAGES, bool MID>
+template <typename RT, int NV, int STAGES, bool MID, bool EDGE = false>
 cudaError_t bwd_ring(const BlockNormBwdArgs& a, dim3 block, size_t smem, int grid, cudaStream_t s) {
   static std::atomic<int> ready[64] = {};
-  const cudaError_t e = ring_ready(block_norm_backward_ring_kernel<RT, NV, STAGES, MID>, ready);
+  const cudaError_t e = ring_ready(block_norm_backward_ring_kernel<RT, NV, STAGES, MID, EDGE>, ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl(block_norm_backward_ring_kernel<RT, NV, STAGES, MID>, dim3(grid), block, smem, s,
-                    a);
+  return launch_pdl(block_norm_backward_ring_kernel<RT, NV, STAGES, MID, EDGE>, dim3(grid), block,
+                    smem, s, a);
 }
 
 // Bytes of one stage: pv pieces for each of the NV column sets of a thread.
 constexpr size_t stage_bytes(int pv, int nv) { return static_cast<size_t>(pv) * nv * kRingThreads * 16; }
 
-template <typename RT, int NV>
+// The same for EDGE: whole rows of n32 fp32 and n16 bf16 tensors.
+size_t edge_stage_bytes(int n32, int n16, int nv, dim3 block) {
+  return static_cast<size_t>(block.y) *
+         (static_cast<size_t>(n32) * edge_bytes(block.x, nv, 4) + n16 * edge_bytes(block.x, nv, 2));
+}
+
+template <typename RT, int NV, bool VEC>
 cudaError_t fwd_nv(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
   constexpr int PER_SM = ring_blocks(NV), PR = static_cast<int>(sizeof(RT) / 2);
   const dim3 block = ring_block(a.T, a.H, NV, PER_SM * num_sms);
   const bool elem = a.gate_kind == MOE_GATE_ELEMENT;
   const int grid = std::min(PER_SM * num_sms, ceil_div(a.T, block.y));
+  if (!VEC) {
+    const int g32 = elem && !a.gate_bf16, g16 = elem && a.gate_bf16, y16 = a.y != nullptr;
+    const size_t stage = edge_stage_bytes((PR == 2) + g32, (PR == 1) + y16 + g16, NV, block);
+    return 4 * stage * PER_SM <= kRingBytes
+               ? fwd_ring<RT, NV, 4, false, true>(a, block, 4 * stage, grid, s)
+               : fwd_ring<RT, NV, 2, false, true>(a, block, 2 * stage, grid, s);
+  }
   if (a.y != nullptr && a.pre_norm && !elem) {
     // 160 of 200 KB for bf16 rows; one stage more was slower at each width
     // (81.7 against 80.2 us at 8192 x 7168, 23.2 against 22.0 at 4099 x 2048)
@@ -929,12 +1149,24 @@ cudaError_t fwd_nv(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
   const size_t stage = stage_bytes(PR + (a.y != nullptr) + (elem ? (a.gate_bf16 ? 1 : 2) : 0), NV);
   return fwd_ring<RT, NV, 2, false>(a, block, 2 * stage, grid, s);
 }
-template <typename RT, int NV>
+size_t bwd_edge_stage(const BlockNormBwdArgs& a, bool r32, int nv, dim3 block) {
+  const bool elem = a.gate_kind == MOE_GATE_ELEMENT;
+  const int r = (a.grad_normed != nullptr) + (a.grad_res != nullptr);
+  return edge_stage_bytes((r32 ? r : 0) + (elem && !a.gate_bf16),
+                          (r32 ? 0 : r) + (a.grad_normed != nullptr) + (a.y != nullptr) +
+                              (elem && a.gate_bf16),
+                          nv, block);
+}
+template <typename RT, int NV, bool VEC>
 cudaError_t bwd_nv(const BlockNormBwdArgs& a, int num_sms, int pv, int* blocks, cudaStream_t s) {
   const dim3 block = ring_block(a.T, a.H, NV, num_sms);
-  const size_t stage = stage_bytes(pv, NV);
+  const size_t stage = VEC ? stage_bytes(pv, NV) : bwd_edge_stage(a, sizeof(RT) == 4, NV, block);
   const size_t sums = static_cast<size_t>(block.y) * a.n_part * a.H * 4;  // <= 96 KB
   const int grid = *blocks = std::min(std::min(num_sms, kNormBwdBlocks), ceil_div(a.T, block.y));
+  if (!VEC)
+    return 3 * stage <= kRingBytes
+               ? bwd_ring<RT, NV, 3, false, true>(a, block, std::max(3 * stage, sums), grid, s)
+               : bwd_ring<RT, NV, 2, false, true>(a, block, std::max(2 * stage, sums), grid, s);
   if (a.grad_res != nullptr && a.grad_normed != nullptr && a.y != nullptr &&
       a.gate_kind != MOE_GATE_ELEMENT)
     return 3 * stage <= kRingBytes
@@ -945,8 +1177,8 @@ cudaError_t bwd_nv(const BlockNormBwdArgs& a, int num_sms, int pv, int* blocks, 
 
 template <typename RT, bool VEC>
 cudaError_t fwd(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
-  if (VEC && a.H <= 8192)
-    return a.H <= 2048 ? fwd_nv<RT, 1>(a, num_sms, s) : fwd_nv<RT, 2>(a, num_sms, s);
+  if (a.H <= 8192)
+    return a.H <= 2048 ? fwd_nv<RT, 1, VEC>(a, num_sms, s) : fwd_nv<RT, 2, VEC>(a, num_sms, s);
   // one piece of 8 columns per thread up to 8192 columns, two above
   const int pieces = ceil_div(a.H, 8);
   const int nv = pieces <= 1024 ? 1 : 2;
@@ -959,14 +1191,18 @@ cudaError_t fwd(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
 
 template <typename RT, bool VEC>
 cudaError_t bwd(const BlockNormBwdArgs& a, int num_sms, int* blocks_used, cudaStream_t s) {
-  if (VEC && a.H <= 8192) {
+  if (a.H <= 8192) {
     const int pr = static_cast<int>(sizeof(RT) / 2);
     const int pv = (a.grad_normed ? pr + 1 : 0) + (a.grad_res ? pr : 0) + (a.y != nullptr) +
                    (a.gate_kind == MOE_GATE_ELEMENT ? (a.gate_bf16 ? 1 : 2) : 0);
     // two stages fit: every case but wide rows with fp32 streams and fp32 element gates
-    if (2 * stage_bytes(pv, a.H <= 2048 ? 1 : 2) <= kRingBytes)
-      return a.H <= 2048 ? bwd_nv<RT, 1>(a, num_sms, pv, blocks_used, s)
-                         : bwd_nv<RT, 2>(a, num_sms, pv, blocks_used, s);
+    const int nv = a.H <= 2048 ? 1 : 2;
+    const size_t stage =
+        VEC ? stage_bytes(pv, nv)
+            : bwd_edge_stage(a, pr == 2, nv, ring_block(a.T, a.H, nv, num_sms));
+    if (2 * stage <= kRingBytes)
+      return nv == 1 ? bwd_nv<RT, 1, VEC>(a, num_sms, pv, blocks_used, s)
+                     : bwd_nv<RT, 2, VEC>(a, num_sms, pv, blocks_used, s);
   }
   const int blocks = *blocks_used =
       static_cast<int>(std::min<long>(std::min(2 * num_sms, kNormBwdBlocks), a.T));

@@ -204,6 +204,41 @@ def test_block_norm_and_gradient(moe, T, H, stream, gate, post):
         assert a is None or torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,H,pad", [(2000, 77, 0), (3000, 7, 1), (1500, 1001, 3), (700, 264, 1), (500, 2051, 0),
+                                     (330, 7167, 2), (320, 8192, 5)])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gate", ["channel", "element"])
+def test_block_norm_ragged_rows(moe, T, H, pad, stream, gate):
+    """Several rows per block at every alignment of their starts; rows of a wider matrix."""
+    g, v = _norm_case(T, H, stream, torch.bfloat16, gate, True, 3)
+
+    def rows(t, extra):      # the same rows inside a matrix whose other columns are NaN
+        big = torch.full((T, H + extra), float("nan"), dtype=t.dtype, device="cuda")
+        big[:, :H] = t
+        return big[:, :H]
+
+    res, y = rows(v["residual"], pad), rows(v["y"], 2 * pad)
+    kw = dict(gate=rows(v["gate"], pad) if gate == "element" else v["gate"], scale=0.5, post_norm=True,
+              post_weight=v["post_weight"], pre_weight=v["pre_weight"])
+    nkw = {k: (_np(t) if torch.is_tensor(t) else t) for k, t in kw.items()}
+    r, n = moe.block_norm(res, y, **kw)
+    rr, rn = B.block_norm(_np(res), _np(y), **nkw)
+    bf = stream == torch.bfloat16
+    _close(r, rr, np.abs(rr) + np.abs(_np(res)) + 4, bf, 2.0 ** -20)
+    _close(n, rn, (np.abs(_np(res)) + 4) * np.abs(rn / np.where(rr == 0, 1, rr)), True, 2.0 ** -20)
+    gr, gn = rows(_dev(g.normal(size=(T, H)), stream), pad), rows(_dev(g.normal(size=(T, H)), torch.bfloat16), 3 * pad)
+    got = moe.block_norm_backward(gr, gn, rows(r, pad), y, **kw)
+    ref = B.block_norm_backward(_np(gr), _np(gn), _np(r), _np(y), **nkw)
+    d, gmax = np.abs(ref["d_residual"]).max() + 1, np.abs(nkw["gate"]).max() + 1
+    _close(got[0], ref["d_residual"], d, bf)
+    _close(got[1], ref["d_y"], np.abs(ref["d_y"]).max() + d * gmax, True)
+    _close(got[2], ref["d_gate"], d * 6 * (T if gate == "channel" else 1), gate == "element")
+    _close(got[3], ref["d_post_weight"], d * gmax * 6 * T, False)
+    _close(got[4], ref["d_pre_weight"], 6 * np.abs(_np(gn)).max() * T, False)
+    for a, b in zip(got, moe.block_norm_backward(gr, gn, rows(r, pad), y, **kw)):
+        assert torch.equal(a, b)
+
+
 def test_block_norm_parts(moe):
     g, v = _norm_case(7, 264, torch.bfloat16, torch.bfloat16, "none", False, 2)
     r, y, w = v["residual"], v["y"], v["pre_weight"]
