@@ -16,6 +16,8 @@
 //
 // The kernels, chosen by linear_streams() and linear_path():
 //   linear_pair_kernel   256 x 256 tiles on CTA pairs, persistent: large products
+//   linear_sums_kernel   the same tiles with sums in registers: large fp32
+//                        results, and tiles that two pairs share
 //   linear_tile_kernel   128 x 128 tiles, the contraction split over the CTAs
 //                        of a cluster: few tiles
 //   linear_stream_kernel a few tokens: the weights streamed into registers, and
@@ -138,11 +140,11 @@ __device__ __forceinline__ float act_f(float z, int act, bool f32) {
   return gate_act(z, act);
 }
 // The epilogue on 8 consecutive columns n.. of row m (m < M) where N % 8 == 0 and
-// every row is 16-byte aligned: pre-activation z = v + bias, y = residual + act(z).  ACT and F32 are constants of the code:
-// kernels hold several copies of this, and with every activation and type in
-// each the code was so long that fetching it took longer than a small
-// product (33 us for 64 x 256 x 256), while one copy called as a function
-// took 300 ns a call.
+// every row is 16-byte aligned: pre-activation z = v + bias, y = residual +
+// act(z).  ACT and F32 are constants of the code: kernels hold several copies of
+// this, and with every activation and type in each the code was so long that
+// fetching it took longer than a small product (33 us for 64 x 256 x 256),
+// while one copy called as a function took 300 ns a call.
 template <int ACT, bool F32>
 __device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, float (&v)[8]) {
   if (n >= p.N) return;
@@ -344,10 +346,17 @@ __device__ __forceinline__ void join_rows(const LinearEpi& p, const float* stg, 
 // each CTA (320 threads): warp 0 TMA producer (ring of 3 stages, 32 KB of A
 // and of B each), warp 1 TMEM and, on rank 0, the MMA issuer (two
 // 256-column accumulators, so a tile's epilogue runs under the next tile's
-// products), warps 2-9 epilogue (32 rows, half of the columns).  Both CTAs' loads complete on rank 0's stage
-// barrier; rank 0's commits arrive on both CTAs' stage-free and
-// accumulator-full barriers; both epilogues arrive on rank 0's
-// accumulator-free barrier.  Every mbarrier wait is bounded.
+// products), warps 2-9 epilogue (32 rows, half of the columns).  Both CTAs'
+// loads complete on rank 0's stage barrier; rank 0's commits arrive on both
+// CTAs' stage-free and accumulator-full barriers; both epilogues arrive on rank
+// 0's accumulator-free barrier.  Every mbarrier wait is bounded.
+//
+// Bound by the tensor cores, which are busy 88 % of the time: 8192 x 7168 x
+// 4096 with bias and gelu 254 us from a cool start (1.89 PFLOP/s) and 306 in an
+// endless loop, where the power limit lowers the clock.  Six stages of 64 keep
+// more loads in flight, but cost 2 % (a barrier and a commit per 4 products);
+// waits without cluster scope, streaming stores and groups of 4, 6, 11, 12, 16
+// or 32 row tiles are no faster.
 constexpr int kPStages = 3;
 constexpr int kPThreads = 320;
 constexpr int kPSlab = 128 * BK * 2;        // 16 KB: 128 rows x 64, or 64 rows x 128
@@ -566,10 +575,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
 // where fp32 arithmetic has 0.9e-6).  So an accumulator takes 768 of the
 // contraction, and the epilogue warps add each such part in registers,
 // rounding to nearest, while the other accumulator is filled: 7e-7 at any
-// length, and the additions hide under the products.
+// length.  8192 x 2048 x 7168 takes 157 us against 132 with bf16 results (whose
+// rounding hides the truncation, so linear_pair_kernel takes them).
 //
-// Few tiles.  A cluster of S pairs shares a tile: pair i takes the i-th part of
-// the contraction, and the pairs' sums are joined as said above.
+// Few tiles.  A cluster of two pairs shares a tile: pair i takes the i-th part
+// of the contraction, and the pairs' sums are joined as said above.  8192 x
+// 7168 x 256 34 us (0.88 PFLOP/s): 64 pairs, the tensor cores busy half of the
+// time, the rest first stages, the join and the epilogue.
 //
 // 320 threads: producer, MMA, 8 epilogue warps (a thread: one row, 128 columns).
 constexpr int kAThreads = 320;
@@ -829,7 +841,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
 // One 128 x 128 tile per cluster of S CTAs; CTA r takes the r-th part of the
 // contraction (at least one stage), in two accumulators, which halves the
 // tensor core's truncation; the CTAs' sums are joined as said above.  Two CTAs
-// fit an SM (with 256 TMEM columns each).
+// fit an SM (with 256 TMEM columns each).  Bound by latency: the way of the first
+// and the last stage, and the exchange of the sums.  1024 x 2048 x 2048 15.3 us
+// (0.56 PFLOP/s), 64 x 2048 x 7168 13.4, of which the weights take 4.3.
 constexpr int kTStages = 3;
 constexpr int kTThreads = 192;
 constexpr int kTOper = 128 * BK * 2;             // 16 KB: one operand's part of a stage
@@ -1001,7 +1015,8 @@ __global__ void __launch_bounds__(kTThreads)
 // ====================================================== one token
 // The weights [N, K] are read once, and that is what it costs: WPR warps of a
 // block share two rows of w, each lane multiplying 16-byte pieces of them with
-// the token's, and add their sums in order.
+// the token's, and add their sums in order.  2048 x 7168 6.3 us from memory
+// (4.7 TB/s, 2 us more than the bytes need), 3.7 from L2.
 template <int WPR>
 __global__ void __launch_bounds__(256)
     linear_vector_kernel(const __grid_constant__ LinearStreamArgs a) {
@@ -1203,7 +1218,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
 // a few units of 2^-22, far below the rounding of dz (2^-9 on average) and
 // averaged out in the sums.  With the accurate forms the kernel spent 57
 // instructions per element and took 40 us for 8191 x 2048, three times what
-// its loads and stores need.
+// its loads and stores need; now 21 (100 MB, 4.8 TB/s), bound by issue.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == MOE_ACT_SILU) {  // s (1 + z (1 - s)), 1 - s = e^-z s; e^-z kept finite
@@ -1462,9 +1477,9 @@ cudaError_t launch_stream(LinearStreamArgs a, int num_sms, cudaStream_t s) {
 // against 29 on split pairs, 1024 x 2048 x 2048 15.3 against 16.9.  Two pairs
 // per tile where that gives most of a wave of full tiles and the contraction
 // is long, so that reading the operands counts (8192 x 7168 x 256 34 us against
-// 36, but 8192 x 7168 x 64 31 against 28), or
-// where an fp32 result would have more than 1024 of the contraction in one
-// accumulator.
+// 36, but 8192 x 7168 x 64 31 against 28), or where an fp32 result would have more
+// than 1024 of the contraction in one accumulator (unless the split of the small
+// tiles is at its end: from K = 16384 on, with few tiles, it has more).
 LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms) {
   LinearPath r;
   const long big = static_cast<long>(ceil_div(M, 256)) * ceil_div(N, 256);
@@ -1478,7 +1493,8 @@ LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms) {
   const long tiles = static_cast<long>(ceil_div(M, 128)) * ceil_div(N, 128);
   while (r.split < 8 && tiles * r.split * 2 <= 4 * pairs && K / (r.split * 2) >= 4 * BK)
     r.split *= 2;
-  if ((big * 8 >= pairs * 3 && 3 * big <= tiles && K >= 64 * BK) || (out_f32 && K / (2 * r.split) > 16 * BK && r.split < 8)) {
+  if ((big * 8 >= pairs * 3 && 3 * big <= tiles && K >= 64 * BK) ||
+      (out_f32 && K / (2 * r.split) > 16 * BK && r.split < 8)) {
     r.kind = LinearPath::kSums;  // 2 * big <= pairs here
     r.split = 2;
   }
@@ -1551,7 +1567,8 @@ cudaError_t launch_linear_dz(const LinearDzArgs& a, int slices, float* dbias, cu
   const dim3 grid(ceil_div(a.N, 256), slices), block(256);
   cudaError_t e;
   auto go = [&](auto kern_f32, auto kern_bf16) {
-    return a.f32 ? launch_pdl(kern_f32, grid, block, 0, s, a) : launch_pdl(kern_bf16, grid, block, 0, s, a);
+    return a.f32 ? launch_pdl(kern_f32, grid, block, 0, s, a)
+                 : launch_pdl(kern_bf16, grid, block, 0, s, a);
   };
   if (a.act == MOE_ACT_SILU)
     e = go(linear_dz_kernel<MOE_ACT_SILU, true>, linear_dz_kernel<MOE_ACT_SILU, false>);

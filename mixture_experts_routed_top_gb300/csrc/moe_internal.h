@@ -406,7 +406,9 @@ struct LinearPath {
 };
 LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms);
 // D[M, N] = A B^T with the operands' orders (a_mn, b_mn: false, false /
-// false, true / true, true); the maps' boxes are those linear_boxes names.
+// false, true / true, true).  The maps' boxes: 64 of the contraction x 128 rows
+// of a K-major operand; 64 rows x 64 (kTile) or 128 of the contraction of an
+// MN-major one.
 cudaError_t launch_linear(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const LinearDev& p,
                           bool a_mn, bool b_mn, const LinearPath& path, cudaStream_t s);
 struct LinearStreamArgs {
