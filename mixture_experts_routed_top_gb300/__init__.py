@@ -395,8 +395,8 @@ def route_scored(logits: torch.Tensor, k: int, *, score: str = "sigmoid",
     ld = _mat("logits", logits, _DT, shape, dev)
     T, E = shape
     if out is None:
-        idx = logits.new_empty((T, k), dtype=torch.int32)
-        w = logits.new_empty((T, k), dtype=_F32)
+        idx = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        w = torch.empty((T, k), dtype=_F32, device=logits.device)
         pi, pw = idx.data_ptr(), w.data_ptr()
     else:
         idx, w = out
@@ -425,7 +425,7 @@ def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: 
     if slots[0] != T:
         _bad("topk_idx", "[T, k]")
     if out is None:
-        out = logits.new_empty(shape)
+        out = torch.empty(shape, dtype=logits.dtype, device=logits.device)
         ldo = E
     else:
         ldo = _mat("out", out, (logits.dtype,), shape, dev)
@@ -496,14 +496,14 @@ def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     else:
         py, ld_y = y.data_ptr(), _mat("y", y, _ONLY_BF16, shape, dev)
         if res is None:
-            res = residual.new_empty(shape)
+            res = torch.empty(shape, dtype=residual.dtype, device=residual.device)
             pres = res.data_ptr()
         else:
             pres = _dense("residual_out", res, (residual.dtype,), shape, dev)
     if not pre_norm:
         n = None
     elif n is None:
-        n = residual.new_empty(shape, dtype=_BF16)
+        n = torch.empty(shape, dtype=_BF16, device=residual.device)
         pn = n.data_ptr()
     else:
         pn = _dense("normed", n, _ONLY_BF16, shape, dev)
@@ -528,6 +528,7 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
     dev, shape = _matrix_of("residual", residual)
     ld_r = _mat("residual", residual, _DT, shape, dev)
     T, H = shape
+    device = residual.device
     pgr = ld_gr = pgn = ld_gn = py = ld_y = pdy = pdg = pdpost = pdpre = 0
     d_y = d_gate = d_post = d_pre = None
     if grad_residual is not None:
@@ -536,21 +537,21 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
         pgn, ld_gn = grad_normed.data_ptr(), _mat("grad_normed", grad_normed, _ONLY_BF16, shape, dev)
     if y is not None:
         py, ld_y = y.data_ptr(), _mat("y", y, _ONLY_BF16, shape, dev)
-        d_y = residual.new_empty(shape, dtype=_BF16)
+        d_y = torch.empty(shape, dtype=_BF16, device=device)
         pdy = d_y.data_ptr()
     pg, kind, gate_dt, ld_g = (0, 0, 0, 0) if gate is None else _gate_of(gate, shape, dev)
     post, pre, wdt = _norm_weights(post_weight, pre_weight, H, dev)
-    d_res = residual.new_empty(shape)
+    d_res = torch.empty(shape, dtype=residual.dtype, device=device)
     if kind:
-        d_gate = gate.new_empty(gate.shape, dtype=_F32 if kind == 1 else gate.dtype)
+        d_gate = torch.empty(gate.shape, dtype=_F32 if kind == 1 else gate.dtype, device=device)
         pdg = d_gate.data_ptr()
     if post:
-        d_post = residual.new_empty(H, dtype=_F32)
+        d_post = torch.empty(H, dtype=_F32, device=device)
         pdpost = d_post.data_ptr()
     if pre:
-        d_pre = residual.new_empty(H, dtype=_F32)
+        d_pre = torch.empty(H, dtype=_F32, device=device)
         pdpre = d_pre.data_ptr()
-    ws = _workspace(workspace, residual.device, (_LIB or lib()).moe_block_norm_backward_workspace_size(H))
+    ws = _workspace(workspace, device, (_LIB or lib()).moe_block_norm_backward_workspace_size(H))
     _call(_NORM_BWD, dev, stream, pgr, ld_gr, pgn, ld_gn, residual.data_ptr() if pgn else 0, _DT[residual.dtype],
           ld_r, py, ld_y, pg, kind, gate_dt, ld_g, scale, post_norm, post, pre, wdt, eps, T, H, d_res.data_ptr(),
           pdy, pdg, pdpost, pdpre, ws.data_ptr(), ws.numel())
@@ -588,7 +589,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
         dt = _DT.get(out_dtype)
         if dt is None:
             _bad("out_dtype", _names(_DT))
-        out = x.new_empty(shape, dtype=out_dtype)
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
         ld_o = N
     else:
         ld_o = _mat("out", out, _DT, shape, dev)
@@ -636,13 +637,13 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
         pz, ld_z = preact.data_ptr(), _mat("preact", preact, (grad_y.dtype,), shape, dev)
     if bias is not None:
         _dense("bias", bias, _DT, (N,), dev)
-        db = x.new_empty(N, dtype=_F32)
+        db = torch.empty(N, dtype=_F32, device=x.device)
         pdb = db.data_ptr()
     if need_x:
-        dx = x.new_empty(xs)
+        dx = torch.empty(xs, dtype=_BF16, device=x.device)
         pdx = dx.data_ptr()
     if need_w:
-        dw = w.new_empty((N, K))
+        dw = torch.empty((N, K), dtype=_BF16, device=x.device)
         pdw = dw.data_ptr()
     ws = _workspace(workspace, x.device, (_LIB or lib()).moe_linear_backward_workspace_size(T, N))
     _call(_LINEAR_BWD, dev, stream, grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(),

@@ -24,6 +24,7 @@
 //   linear_vector_kernel for one token
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "moe_device.cuh"
 #include "moe_internal.h"
@@ -198,13 +199,24 @@ __device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
   } else if (n + lane < p.N) {
     const int rows = static_cast<int>(min(32l, p.M - m0)), col = n + lane;
     const float b = p.bias != nullptr ? ldf(p.bias, col, p.bias_bf16) : 0.f;
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      const float z = buf[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)] + b;
-      const float res =
-          p.residual != nullptr ? ldf(p.residual, (m0 + r) * p.ld_res + col, !F32) : 0.f;
-      if (p.preact != nullptr) stf(p.preact, (m0 + r) * p.ld_out + col, F32, z);
-      stf(p.out, (m0 + r) * p.ld_out + col, F32, act_f(z, ACT, F32) + res);
+    using U = std::conditional_t<F32, uint32_t, uint16_t>;  // the residual's bits
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      U x[8] = {};
+      if (p.residual != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (r0 + k < rows) x[k] = static_cast<const U*>(p.residual)[(m0 + r0 + k) * p.ld_res + col];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = r0 + k;
+        if (r >= rows) break;
+        const float z = buf[r * 32 + 4 * ((lane >> 2) ^ k) + (lane & 3)] + b;
+        const float res = __uint_as_float(static_cast<uint32_t>(x[k]) << (F32 ? 0 : 16));
+        if (p.preact != nullptr) stf(p.preact, (m0 + r) * p.ld_out + col, F32, z);
+        stf(p.out, (m0 + r) * p.ld_out + col, F32, __fadd_rn(act_f(z, ACT, F32), res));
+      }
     }
   }
   __syncwarp();
@@ -266,19 +278,66 @@ __device__ __forceinline__ void add_parts(const float* own, int own_step, const 
       v[r][6] += x[i][r][1].z, v[r][7] += x[i][r][1].w;
     }
 }
+// RB rows of a warp, a lane every 32nd column: sums `from` (this lane's, rows
+// `stride` apart; -1: no row), bias b.  The type and whether there is an
+// activation are constants: tested per element they took most of its time.
+template <bool F32, bool ACT, int RB>
+__device__ __forceinline__ void single_rows(const LinearEpi& p, const float* from, int stride,
+                                            const int (&row)[RB], long m0, int n0,
+                                            const float (&b)[8]) {
+  constexpr int COLS = 8 / RB;
+  using T = std::conditional_t<F32, float, __nv_bfloat16>;
+  const int n = n0 + (threadIdx.x & 31);
+  // the residual's bits, every load on its way before the first is used (with the
+  // conversion beside the load each waited for its own, 7 us at 391 x 224 x 706)
+  using U = std::conditional_t<F32, uint32_t, uint16_t>;
+  U y[RB][COLS];
+#pragma unroll
+  for (int k = 0; k < RB; ++k)
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) y[k][j] = 0;
+  if (p.residual != nullptr) {
+#pragma unroll
+    for (int k = 0; k < RB; ++k)
+#pragma unroll
+      for (int j = 0; j < COLS; ++j)
+        if (row[k] >= 0 && n + 32 * j < p.N)
+          y[k][j] = static_cast<const U*>(p.residual)[(m0 + row[k]) * p.ld_res + n + 32 * j];
+  }
+#pragma unroll
+  for (int k = 0; k < RB; ++k) {
+    if (row[k] < 0) continue;
+    const float* const v = from + row[k] * stride;
+    const long at = (m0 + row[k]) * p.ld_out + n;
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) {
+      if (n + 32 * j >= p.N) continue;
+      const float z = v[32 * j] + b[j];
+      if (p.preact != nullptr) stf(static_cast<T*>(p.preact) + at, 32 * j, F32, z);
+      // not fused into the activation, which would depend on the other options
+      const float res = __uint_as_float(static_cast<uint32_t>(y[k][j]) << (F32 ? 0 : 16));
+      stf(static_cast<T*>(p.out) + at, 32 * j, F32, __fadd_rn(res, ACT ? act_f(z, p.act, F32) : z));
+    }
+  }
+}
+
 // The rows row0 .. row0 + rows of a tile whose first row is m0, columns n0 ..
 // n0 + 8 * CHUNKS.  parts: number of CTAs (1, 2, 4 or 8), mine: this one's place
 // among them; part0: the first one's part of the workspace, the next ones'
-// `step` floats further on.
+// `step` floats further on.  Rows that are not whole aligned vectors go back into
+// stg and leave it with a warp's lanes along a row (391 x 224 x 706 from the
+// threads' 8 columns 22.5 us, so 12.1; x 704 9.2).
 template <int THREADS, int CHUNKS, int STRIDE>
-__device__ __forceinline__ void join_rows(const LinearEpi& p, const float* stg, const float* part0,
+__device__ __forceinline__ void join_rows(const LinearEpi& p, float* stg, const float* part0,
                                           long step, int parts, int mine, int row0, int rows,
                                           long m0, int n0) {
-  static_assert(THREADS % CHUNKS == 0, "a thread keeps its columns");
-  constexpr int STEP = THREADS / CHUNKS;
+  static_assert(THREADS % CHUNKS == 0 && 32 % CHUNKS == 0, "a thread keeps its columns");
+  constexpr int STEP = THREADS / CHUNKS, WROWS = 32 / CHUNKS, WCOLS = CHUNKS / 4;
+  constexpr int RB = 8 / WCOLS;
+  const int lane = threadIdx.x & 31;
   const int col = (threadIdx.x % CHUNKS) * 8, n = n0 + col;
-  if (n >= p.N) return;
-  float b[8];
+  if (p.vec && n >= p.N) return;
+  float b[8];  // of the thread's columns; without vectors of lane, lane + 32, ..
 #pragma unroll
   for (int j = 0; j < 8; ++j) b[j] = 0.f;
   if (p.bias != nullptr) {
@@ -286,17 +345,18 @@ __device__ __forceinline__ void join_rows(const LinearEpi& p, const float* stg, 
       ld8(p.bias, n, p.bias_bf16, b);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (n + j < p.N) b[j] = ldf(p.bias, n + j, p.bias_bf16);
+      for (int j = 0; j < WCOLS; ++j)
+        if (n0 + lane + 32 * j < p.N) b[j] = ldf(p.bias, n0 + lane + 32 * j, p.bias_bf16);
     }
   }
   // rows in flight: 4 of up to two parts, 2 of four (twice as many measured slower)
   const int R = parts <= 2 ? 4 : 2;
   const int end = static_cast<int>(min(static_cast<long>(rows), p.M - m0 - row0));
 #pragma unroll 1
-  for (int i = threadIdx.x / CHUNKS; i < end; i += R * STEP) {
-    const int count = min(R, (end - i + STEP - 1) / STEP), ra = row0 + i;
-    const float* const own = stg + ra * STRIDE + col;
+  for (int iw = threadIdx.x / 32 * WROWS; iw < end; iw += R * STEP) {  // the warp's first row
+    const int i = iw + lane / CHUNKS;
+    const int count = max(0, min(R, (end - i + STEP - 1) / STEP)), ra = row0 + i;
+    float* const own = stg + ra * STRIDE + col;
     const float* const other = part0 + ra * (8 * CHUNKS) + col;
     constexpr int OS = STEP * STRIDE, PS = STEP * 8 * CHUNKS;
     float v[4][8];
@@ -309,33 +369,47 @@ __device__ __forceinline__ void join_rows(const LinearEpi& p, const float* stg, 
     else
       for (int k = 0; k < parts; k += 4)
         add_parts<2, 4>(own, OS, other, PS, step, k, mine, count, v);
+    if (!p.vec) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if (r >= count) continue;
+        float4* q = reinterpret_cast<float4*>(own + r * OS);
+        q[0] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
+        q[1] = make_float4(v[r][4], v[r][5], v[r][6], v[r][7]);
+      }
+      __syncwarp();
+      for (int r = 0; r < R * WROWS; r += RB) {
+        int rows_at[RB];
+#pragma unroll
+        for (int k = 0; k < RB; ++k) {
+          const int row = iw + (r + k) / WROWS * STEP + (r + k) % WROWS;
+          rows_at[k] = row < end ? row0 + row : -1;
+        }
+        const float* from = stg + lane;
+        if (p.out_f32) {
+          if (p.act == MOE_ACT_NONE) single_rows<true, false>(p, from, STRIDE, rows_at, m0, n0, b);
+          else single_rows<true, true>(p, from, STRIDE, rows_at, m0, n0, b);
+        } else {
+          if (p.act == MOE_ACT_NONE) single_rows<false, false>(p, from, STRIDE, rows_at, m0, n0, b);
+          else single_rows<false, true>(p, from, STRIDE, rows_at, m0, n0, b);
+        }
+      }
+      continue;
+    }
 #pragma unroll 1
     for (int r = 0; r < count; ++r) {
       const long m = m0 + ra + r * STEP;
-      float z[8];
+      float z[8], y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 8; ++j) {
         z[j] = (r == 0 ? v[0][j] : r == 1 ? v[1][j] : r == 2 ? v[2][j] : v[3][j]) + b[j];
-      if (p.vec) {
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = 0.f;
-        if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !p.out_f32, y);
-        if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, p.out_f32, z);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] += act_f(z[j], p.act, p.out_f32);
-        st8(p.out, m * p.ld_out + n, p.out_f32, y);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (n + j < p.N) {
-            const float y =
-                p.residual != nullptr ? ldf(p.residual, m * p.ld_res + n + j, !p.out_f32) : 0.f;
-            if (p.preact != nullptr) stf(p.preact, m * p.ld_out + n + j, p.out_f32, z[j]);
-            stf(p.out, m * p.ld_out + n + j, p.out_f32, y + act_f(z[j], p.act, p.out_f32));
-          }
-        }
+        y[j] = 0.f;
       }
+      if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !p.out_f32, y);
+      if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, p.out_f32, z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] += act_f(z[j], p.act, p.out_f32);
+      st8(p.out, m * p.ld_out + n, p.out_f32, y);
     }
   }
 }
@@ -817,7 +891,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  const float* const stg = reinterpret_cast<const float*>(smem);
+  float* const stg = reinterpret_cast<float*>(smem);
   const int rows = 128 / S;
   if (SPLIT)
     hand_over<kAThreads, 32, kAStride>(stg, p.parts + static_cast<long>(blockIdx.x) * 128 * 256,
@@ -996,7 +1070,7 @@ __global__ void __launch_bounds__(kTThreads)
     tc_fence_before();
   }
   __syncthreads();
-  const float* const stg = reinterpret_cast<const float*>(smem);
+  float* const stg = reinterpret_cast<float*>(smem);
   const int rows = 128 / S;
   if (S > 1) {
     hand_over<kTThreads, 16, kTStride>(stg, p.parts + static_cast<long>(blockIdx.x) * 128 * 128,
