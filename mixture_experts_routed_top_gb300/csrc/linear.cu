@@ -140,28 +140,35 @@ __device__ __forceinline__ float act_f(float z, int act, bool f32) {
   if (act == MOE_ACT_SILU && f32) return z / (1.f + expf(-z));
   return gate_act(z, act);
 }
+// 8 elements from 16 bytes of bf16 or 32 of fp32.
+template <bool F32>
+__device__ __forceinline__ void bits8(const uint4 (&x)[F32 ? 2 : 1], float (&v)[8]) {
+  const uint4 a = x[0], b = x[F32 ? 1 : 0];
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = __uint_as_float(F32 ? w[j] : j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+}
 // The epilogue on 8 consecutive columns n.. of row m (m < M) where N % 8 == 0 and
 // every row is 16-byte aligned: pre-activation z = v + bias, y = residual +
 // act(z).  ACT and F32 are constants of the code: kernels hold several copies of
 // this, and with every activation and type in each the code was so long that
 // fetching it took longer than a small product (33 us for 64 x 256 x 256),
 // while one copy called as a function took 300 ns a call.
+// b: the bias there; x: the residual's bits.
 template <int ACT, bool F32>
-__device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, float (&v)[8]) {
-  if (n >= p.N) return;
-  float b[8], r[8];
-  if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !F32, r);
-  if (p.bias != nullptr) {
-    ld8(p.bias, n, p.bias_bf16, b);
+__device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, const float (&b)[8],
+                                          const uint4 (&x)[F32 ? 2 : 1], float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += b[j];
-  }
+  for (int j = 0; j < 8; ++j) v[j] += b[j];
   if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, F32, v);
   if (ACT != MOE_ACT_NONE) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = act_f(v[j], ACT, F32);
   }
   if (p.residual != nullptr) {
+    float r[8];
+    bits8<F32>(x, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += r[j];
   }
@@ -179,13 +186,33 @@ template <int ACT, bool F32>
 __device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
                                            const uint32_t (&v)[32], float* buf) {
   const int lane = threadIdx.x & 31;
+  const long m0 = m - lane;
+  // bias and residual of 8 columns of 4 rows, every load on its way before the
+  // first store, which the compiler may not move loads across
+  const int nv = n + 8 * (lane & 3);
+  float bv[8] = {};
+  uint4 xv[4][F32 ? 2 : 1] = {};
+  if (p.vec && nv < p.N) {
+    if (p.residual != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long row = m0 + 8 * i + (lane >> 2);
+        if (row < p.M) {
+          const uint4* q = reinterpret_cast<const uint4*>(
+              static_cast<const char*>(p.residual) + (row * p.ld_res + nv) * (F32 ? 4 : 2));
+          xv[i][0] = q[0];
+          if (F32) xv[i][F32 ? 1 : 0] = q[1];
+        }
+      }
+    }
+    if (p.bias != nullptr) ld8(p.bias, nv, p.bias_bf16, bv);
+  }
   __syncwarp();  // the previous step's values have been read
 #pragma unroll
   for (int c = 0; c < 8; ++c)
     *reinterpret_cast<uint4*>(buf + lane * 32 + 4 * (c ^ (lane & 7))) =
         make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
   __syncwarp();
-  const long m0 = m - lane;
   if (p.vec) {
     const int c = 2 * (lane & 3);
 #pragma unroll
@@ -194,7 +221,7 @@ __device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
       const float4 x = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * (c ^ (row & 7)));
       const float4 y = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * ((c + 1) ^ (row & 7)));
       float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      if (m0 + row < p.M) epilogue8<ACT, F32>(p, m0 + row, n + 4 * c, f);
+      if (m0 + row < p.M && nv < p.N) epilogue8<ACT, F32>(p, m0 + row, nv, bv, xv[i], f);
     }
   } else if (n + lane < p.N) {
     const int rows = static_cast<int>(min(32l, p.M - m0)), col = n + lane;
