@@ -597,6 +597,7 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
  *   call   0 moe_route_scored, 1 moe_route_scored_backward, 2 moe_block_norm,
  *          3 moe_block_norm_backward, 4 moe_linear, 5 moe_linear_backward;
  *          any other: MOE_ERR_INVALID_ARG
+ *   block  the slots; a size that no int holds: MOE_ERR_UNSUPPORTED
  */
 moe_status moe_call_packed(int call, const void* block);
 

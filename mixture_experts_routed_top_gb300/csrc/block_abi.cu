@@ -9,6 +9,8 @@
 #include <atomic>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
+#include <utility>
 
 #include "moe_internal.h"
 
@@ -156,6 +158,43 @@ LinearWs linear_ws(int T, int N) {
   w.total = w.partials + static_cast<size_t>(kLinearDzSlices) * N * 4;
   return w;
 }
+
+}  // namespace
+
+namespace {
+
+// A call's arguments in 8-byte slots, in the function's order.
+struct Packed {
+  const unsigned char* block;
+  template <typename T>
+  T slot(size_t i) const {
+    if constexpr (std::is_floating_point_v<T>) {
+      double v;
+      memcpy(&v, block + 8 * i, 8);
+      return static_cast<T>(v);
+    } else {
+      int64_t v;
+      memcpy(&v, block + 8 * i, 8);
+      if constexpr (std::is_pointer_v<T>) return reinterpret_cast<T>(static_cast<uintptr_t>(v));
+      else return static_cast<T>(v);
+    }
+  }
+  // an int's slot holds a value that an int can
+  template <typename T>
+  bool fits(size_t i) const {
+    return !std::is_same_v<T, int> || slot<int64_t>(i) == slot<int>(i);
+  }
+  template <typename... A, size_t... I>
+  moe_status call(moe_status (*fn)(A...), std::index_sequence<I...>) const {
+    if (!(fits<A>(I) && ...))
+      return set_last_error(MOE_ERR_UNSUPPORTED, "moe_call_packed: a size above 2^31 - 1");
+    return fn(slot<A>(I)...);
+  }
+  template <typename... A>
+  moe_status call(moe_status (*fn)(A...)) const {
+    return call(fn, std::index_sequence_for<A...>{});
+  }
+};
 
 }  // namespace
 
@@ -530,65 +569,19 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
   return MOE_OK;
 }
 
-// The calls above with their arguments in one block of 8-byte slots (integers
-// and pointers as they are, floats as doubles), in the functions' order: the
-// Python binding's way in, since converting 14 to 29 arguments one by one took
-// longer there than launching the kernel.
-enum { CALL_ROUTE = 0, CALL_ROUTE_BWD = 1, CALL_NORM = 2, CALL_NORM_BWD = 3, CALL_LINEAR = 4, CALL_LINEAR_BWD = 5 };
-
+// The Python binding's way in: converting 14 to 29 arguments one by one took longer
+// there than launching the kernel.
 moe_status moe_call_packed(int call, const void* block) {
-  struct Slots {
-    const unsigned char* at;
-    int64_t i() {
-      int64_t v;
-      memcpy(&v, at, 8);
-      at += 8;
-      return v;
-    }
-    int n() { return static_cast<int>(i()); }
-    float f() {
-      double v;
-      memcpy(&v, at, 8);
-      at += 8;
-      return static_cast<float>(v);
-    }
-    void* p() { return reinterpret_cast<void*>(static_cast<uintptr_t>(i())); }
-    float* pf() { return static_cast<float*>(p()); }
-    int32_t* pi() { return static_cast<int32_t*>(p()); }
-    moe_dtype dt() { return static_cast<moe_dtype>(n()); }
-  } a{static_cast<const unsigned char*>(block)};
-  // an initialiser list evaluates its elements from left to right
+  if (block == nullptr)
+    return set_last_error(MOE_ERR_INVALID_ARG, "moe_call_packed: null block");
+  const Packed a{static_cast<const unsigned char*>(block)};
   switch (call) {
-    case CALL_ROUTE: {
-      struct { void* l; moe_dtype dt; int64_t ld; int T, E, k, sc; float* b; int ng, tg, gt, rn; float s; int32_t* idx; float* w; void* st; } q{
-          a.p(), a.dt(), a.i(), a.n(), a.n(), a.n(), a.n(), a.pf(), a.n(), a.n(), a.n(), a.n(), a.f(), a.pi(), a.pf(), a.p()};
-      return moe_route_scored(q.l, q.dt, q.ld, q.T, q.E, q.k, static_cast<moe_score>(q.sc), q.b, q.ng, q.tg, q.gt, q.rn, q.s, q.idx, q.w, q.st);
-    }
-    case CALL_ROUTE_BWD: {
-      struct { void* l; moe_dtype dt; int64_t ld; int T, E, k, sc; float* b; int rn; float s; int32_t* idx; float* w; float* gw; void* gl; int64_t ldg; void* st; } q{
-          a.p(), a.dt(), a.i(), a.n(), a.n(), a.n(), a.n(), a.pf(), a.n(), a.f(), a.pi(), a.pf(), a.pf(), a.p(), a.i(), a.p()};
-      return moe_route_scored_backward(q.l, q.dt, q.ld, q.T, q.E, q.k, static_cast<moe_score>(q.sc), q.b, q.rn, q.s, q.idx, q.w, q.gw, q.gl, q.ldg, q.st);
-    }
-    case CALL_NORM: {
-      struct { void* r; moe_dtype rd; int64_t ldr; void* y; int64_t ldy; void* g; int gk; moe_dtype gd; int64_t ldg; float sc; int po; void* pw; int pr; void* rw; moe_dtype wd; float eps; int T, H; void* ro; void* n; void* st; } q{
-          a.p(), a.dt(), a.i(), a.p(), a.i(), a.p(), a.n(), a.dt(), a.i(), a.f(), a.n(), a.p(), a.n(), a.p(), a.dt(), a.f(), a.n(), a.n(), a.p(), a.p(), a.p()};
-      return moe_block_norm(q.r, q.rd, q.ldr, q.y, q.ldy, q.g, static_cast<moe_gate>(q.gk), q.gd, q.ldg, q.sc, q.po, q.pw, q.pr, q.rw, q.wd, q.eps, q.T, q.H, q.ro, q.n, q.st);
-    }
-    case CALL_NORM_BWD: {
-      struct { void* gr; int64_t ldgr; void* gn; int64_t ldgn; void* r; moe_dtype rd; int64_t ldr; void* y; int64_t ldy; void* g; int gk; moe_dtype gd; int64_t ldg; float sc; int po; void* pw; void* rw; moe_dtype wd; float eps; int T, H; void* dr; void* dy; void* dg; float* dpo; float* dpr; void* ws; int64_t wsb; void* st; } q{
-          a.p(), a.i(), a.p(), a.i(), a.p(), a.dt(), a.i(), a.p(), a.i(), a.p(), a.n(), a.dt(), a.i(), a.f(), a.n(), a.p(), a.p(), a.dt(), a.f(), a.n(), a.n(), a.p(), a.p(), a.p(), a.pf(), a.pf(), a.p(), a.i(), a.p()};
-      return moe_block_norm_backward(q.gr, q.ldgr, q.gn, q.ldgn, q.r, q.rd, q.ldr, q.y, q.ldy, q.g, static_cast<moe_gate>(q.gk), q.gd, q.ldg, q.sc, q.po, q.pw, q.rw, q.wd, q.eps, q.T, q.H, q.dr, q.dy, q.dg, q.dpo, q.dpr, q.ws, static_cast<size_t>(q.wsb), q.st);
-    }
-    case CALL_LINEAR: {
-      struct { void* x; int64_t ldx; void* w; int64_t ldw; void* b; moe_dtype bd; int act; void* r; int64_t ldr; int T, K, N; void* o; moe_dtype od; int64_t ldo; void* z; void* ws; int64_t wsb; void* st; } q{
-          a.p(), a.i(), a.p(), a.i(), a.p(), a.dt(), a.n(), a.p(), a.i(), a.n(), a.n(), a.n(), a.p(), a.dt(), a.i(), a.p(), a.p(), a.i(), a.p()};
-      return moe_linear(q.x, q.ldx, q.w, q.ldw, q.b, q.bd, q.act, q.r, q.ldr, q.T, q.K, q.N, q.o, q.od, q.ldo, q.z, q.ws, static_cast<size_t>(q.wsb), q.st);
-    }
-    case CALL_LINEAR_BWD: {
-      struct { void* gy; moe_dtype yd; int64_t ldg; void* x; int64_t ldx; void* w; int64_t ldw; int act; void* z; int64_t ldz; int T, K, N; void* dx; void* dw; float* db; void* ws; int64_t wsb; void* st; } q{
-          a.p(), a.dt(), a.i(), a.p(), a.i(), a.p(), a.i(), a.n(), a.p(), a.i(), a.n(), a.n(), a.n(), a.p(), a.p(), a.pf(), a.p(), a.i(), a.p()};
-      return moe_linear_backward(q.gy, q.yd, q.ldg, q.x, q.ldx, q.w, q.ldw, q.act, q.z, q.ldz, q.T, q.K, q.N, q.dx, q.dw, q.db, q.ws, static_cast<size_t>(q.wsb), q.st);
-    }
+    case 0: return a.call(moe_route_scored);
+    case 1: return a.call(moe_route_scored_backward);
+    case 2: return a.call(moe_block_norm);
+    case 3: return a.call(moe_block_norm_backward);
+    case 4: return a.call(moe_linear);
+    case 5: return a.call(moe_linear_backward);
   }
   return set_last_error(MOE_ERR_INVALID_ARG, "moe_call_packed: unknown call %d", call);
 }

@@ -1,6 +1,7 @@
 """Refusals of the operators around the experts, checked without a GPU: every
 bad argument comes back as a status before anything touches the device."""
 import ctypes
+import struct
 
 import pytest
 
@@ -113,3 +114,20 @@ def test_the_bindings_refuse_host_tensors():
                  lambda: m.linear_backward(t, t, t), lambda: m.block_norm_backward(t, t, t)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_packed_calls(L):
+    """One block of 8-byte slots stands for the arguments; each call's own refusals come back."""
+    def block(*v):
+        return struct.pack("=" + "".join("d" if isinstance(x, float) else "q" for x in v), *v)
+
+    p = P.value
+    route_args = [p, 1, 8, 4, 8, 2, 1, 0, 1, 1, 2, 1, 1.0, p, p, 0]
+    for call, at, value, status in [(0, 3, -1, INVALID), (0, 5, 9, UNSUPPORTED), (0, 3, 1 << 32, UNSUPPORTED),
+                                    (0, 13, 0, INVALID), (0, 3, 0, OK), (6, 3, 0, INVALID), (-1, 3, 0, INVALID)]:
+        a = list(route_args)
+        a[at] = value
+        assert L.moe_call_packed(call, block(*a)) == status
+    # T, K, N of a product: a length that is no multiple of 8
+    assert L.moe_call_packed(4, block(p, 12, p, 12, 0, 0, -1, 0, 0, 4, 12, 8, p, 0, 8, 0, p, 1 << 25, 0)) == UNSUPPORTED
+    assert L.moe_call_packed(0, None) == INVALID
