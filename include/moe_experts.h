@@ -573,7 +573,7 @@ moe_status moe_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w, 
  * moe_linear_backward - gradients of moe_linear.  With dz = grad_y *
  * act'(preact): dx = dz w, dw = dz^T x, dbias = sum over tokens of dz; the
  * residual's gradient is grad_y itself.  dz enters the two products rounded
- * to bf16, and dbias unrounded.
+ * to bf16 (up to 1024 of them, T * N, as the sum of two), and dbias unrounded.
  *   grad_y   device [T, N] of the forward's out type (y_dt)
  *   preact   device [T, N] of that type, as moe_linear stored it; NULL iff
  *            act is MOE_ACT_NONE

@@ -148,13 +148,22 @@ moe_status run_linear(const void* a, int64_t ld_a, bool a_mn, const void* b, int
 
 struct LinearWs {
   int64_t ld_dz;
-  size_t dz, partials, total;
+  size_t dz, dz_lo, partials, total;
 };
+// dz is rounded to bf16 for the products of the gradient.  Over many dz that adds
+// to the error of a gradient what its own rounding to bf16 does, 1.41 times in
+// all; of a few dz the roundings do not average out (T = 1, N = 24: 1.53 times),
+// and the products are small.  So up to this many dz the rest of the rounding is
+// kept too and multiplied first, and the gradients are as those of an fp32 dz.
+constexpr int64_t kLinearDzSplit = 1024;
 LinearWs linear_ws(int T, int N) {
   LinearWs w;
   w.ld_dz = (static_cast<int64_t>(N) + 7) / 8 * 8;
   w.dz = kLinearWsBytes;
-  w.partials = (w.dz + static_cast<size_t>(T) * w.ld_dz * 2 + 1023) / 1024 * 1024;
+  const size_t bytes = static_cast<size_t>(T) * w.ld_dz * 2;
+  const bool split = static_cast<int64_t>(T) * N <= kLinearDzSplit;
+  w.dz_lo = w.dz + (bytes + 15) / 16 * 16;
+  w.partials = (w.dz_lo + (split ? bytes : 0) + 1023) / 1024 * 1024;
   w.total = w.partials + static_cast<size_t>(kLinearDzSlices) * N * 4;
   return w;
 }
@@ -520,13 +529,18 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
   // sums its columns
   const bool direct = act == MOE_ACT_NONE && y_dt == MOE_DT_BF16 && ld_gy % 8 == 0 && N % 8 == 0;
   const bool products = dx || dw;
+  // exact in bf16: a bf16 gradient times 0 or 1
+  const bool exact = y_dt == MOE_DT_BF16 && (act == MOE_ACT_NONE || act == MOE_ACT_RELU);
+  const bool split = products && !exact && static_cast<int64_t>(T) * N <= kLinearDzSplit;
   const void* dz = grad_y;
+  const void* dz_lo = nullptr;
   int64_t ld_dz = ld_gy;
   if (!(direct || !products) || dbias) {
     LinearDzArgs a;
     a.dy = grad_y;
     a.preact = preact;
     a.dz = direct || !products ? nullptr : reinterpret_cast<__nv_bfloat16*>(wsb + L.dz);
+    a.dz_lo = split ? reinterpret_cast<__nv_bfloat16*>(wsb + L.dz_lo) : nullptr;
     a.ld_dy = ld_gy;
     a.ld_z = ld_z;
     a.ld_dz = L.ld_dz;
@@ -539,6 +553,7 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
     a.partials = !dbias ? nullptr : slices == 1 ? dbias : reinterpret_cast<float*>(wsb + L.partials);
     const cudaError_t e = launch_linear_dz(a, slices, dbias, s);
     if (e != cudaSuccess) return cuda_error(e, fn);
+    dz_lo = a.dz_lo;
     if (a.dz) {
       dz = a.dz;
       ld_dz = L.ld_dz;
@@ -552,20 +567,25 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
   LinearDev p{};
   p.err = static_cast<int*>(ws);
   p.parts = reinterpret_cast<float*>(wsb + 1024);
-  if (dx) {
-    e.M = T;
-    e.out = dx;
+  e.ld_res = K;
+  // dz_lo's product first, then dz's on top of it
+  auto product = [&](void* out, int M, int contraction, bool a_mn, const void* b, int64_t ld_b) {
+    e.M = M;
+    e.out = out;
+    p.K = contraction;
+    moe_status r = MOE_OK;
+    if (dz_lo) {
+      e.residual = nullptr;
+      p.epi = e;
+      r = run_linear(dz_lo, ld_dz, a_mn, b, ld_b, true, p, s, fn);
+      if (r != MOE_OK) return r;
+    }
+    e.residual = dz_lo ? out : nullptr;
     p.epi = e;
-    p.K = N;
-    if ((st = run_linear(dz, ld_dz, false, w, ld_w, true, p, s, fn)) != MOE_OK) return st;
-  }
-  if (dw) {
-    e.M = N;
-    e.out = dw;
-    p.epi = e;
-    p.K = T;
-    if ((st = run_linear(dz, ld_dz, true, x, ld_x, true, p, s, fn)) != MOE_OK) return st;
-  }
+    return run_linear(dz, ld_dz, a_mn, b, ld_b, true, p, s, fn);
+  };
+  if (dx && (st = product(dx, T, N, false, w, ld_w)) != MOE_OK) return st;
+  if (dw && (st = product(dw, N, T, true, x, ld_x)) != MOE_OK) return st;
   return MOE_OK;
 }
 

@@ -1349,6 +1349,11 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzArgs a) {
       sum[j] += d[j];
     }
     if (a.dz != nullptr) st8(a.dz, t * a.ld_dz + n, false, d);  // rows padded to 8: always whole
+    if (a.dz_lo != nullptr) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] -= __bfloat162float(__float2bfloat16_rn(d[j]));
+      st8(a.dz_lo, t * a.ld_dz + n, false, d);
+    }
   };
   if (n < a.N && a.vec) {
 #pragma unroll 4

@@ -425,6 +425,7 @@ struct LinearDzArgs {
   const void* dy;
   const void* preact;      // null: dz = dy
   __nv_bfloat16* dz;       // or null: only the column sums
+  __nv_bfloat16* dz_lo;    // what dz's rounding left, laid out as dz, or null
   float* partials;         // [slices, N] or null
   long ld_dy, ld_z, ld_dz;
   int T, N, act;

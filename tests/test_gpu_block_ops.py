@@ -325,6 +325,23 @@ def test_linear_and_gradient(moe, T, K, N, act):
     moe.workspace_status(moe.default_workspace())
 
 
+@pytest.mark.parametrize("T,K,N", [(1, 5392, 24), (2, 136, 512), (3, 64, 7), (1024, 72, 1), (31, 2048, 33)])
+@pytest.mark.parametrize("act,dt", [("silu", torch.bfloat16), ("gelu", torch.bfloat16), ("relu", torch.float32),
+                                    (None, torch.float32)])
+def test_linear_gradient_of_few_dz(moe, T, K, N, act, dt):
+    """Up to 1024 dz enter the products as two bf16 numbers: 2^-17 of dz is left, and
+    2^-18 of rounding the smaller product, beside the result's own rounding."""
+    g = _rng(T, K, N, 11)
+    x, w = _dev(g.normal(size=(T, K)), torch.bfloat16), _dev(g.normal(size=(N, K)) / K ** 0.5, torch.bfloat16)
+    gy = _dev(g.normal(size=(T, N)), dt)
+    z = None if act is None else _dev(g.normal(size=(T, N)) * 2, dt)
+    dx, dw, _ = moe.linear_backward(gy, x, w, activation=act, preact=z)
+    rdx, rdw, _, dz = B.linear_backward(_np(gy), _np(x), _np(w), act, None if z is None else _np(z))
+    az = np.abs(dz) + 2.0 ** -5 * np.abs(_np(gy))      # the slope's terms cancel where it crosses zero
+    _close(dx, rdx, az @ np.abs(_np(w)), True, _acc(N) + 2.0 ** -16)
+    _close(dw, rdw, az.T @ np.abs(_np(x)), True, _acc(T) + 2.0 ** -16)
+
+
 @pytest.mark.parametrize("T,K,N,act", [(1800, 4104, 1000, "silu"), (2300, 5000, 1030, "gelu"), (130, 7168, 260, None),
                                        (600, 6152, 1500, "relu")])
 def test_linear_fp32_results_of_long_contractions(moe, T, K, N, act):
