@@ -446,11 +446,12 @@ __device__ __forceinline__ float silu_f(float g) {
 
 // Gate activation of the gated MLP, `act` a moe_activation value (uniform
 // across the kernel, so the branch never diverges): silu, exact GELU
-// x/2 (1 + erf(x / sqrt 2)), or max(x, 0).
+// x/2 (1 + erf(x / sqrt 2)), or max(x, 0), a NaN staying one (fmaxf would
+// make it 0 and hide a diverged row).
 __device__ __forceinline__ float gate_act(float g, int act) {
   if (act == MOE_ACT_SILU) return silu_f(g);
   if (act == MOE_ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
-  return fmaxf(g, 0.0f);
+  return !(g <= 0.0f) ? g : 0.0f;
 }
 
 // Smallest power of two >= q (q > 0, fp32), read from q's bits (exact, no

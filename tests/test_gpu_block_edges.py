@@ -1,0 +1,56 @@
+"""The operators around the experts on values that are not finite or far from one,
+against the float64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_oracle as B
+
+pytestmark = pytest.mark.gpu
+
+# a token, few tokens, split tiles, whole vectors and not, CTA pairs, pairs with sums in registers
+SHAPES = [(1, 64, 24), (5, 64, 24), (5, 72, 7), (40, 64, 24), (40, 1032, 33), (2050, 64, 1536)]
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_routed_top_gb300 as m
+    m.lib()
+    return m
+
+
+def _np(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+@pytest.mark.parametrize("T,K,N", SHAPES)
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_relu_keeps_nan(moe, T, K, N, dt):
+    """max(z, 0) of a NaN is a NaN: a diverged row or weight shows in the result."""
+    g = np.random.default_rng([T, K, N])
+    x = torch.from_numpy(g.normal(size=(T, K))).bfloat16().cuda()
+    w = torch.from_numpy(g.normal(size=(N, K))).bfloat16().cuda()
+    w[N // 2, K - 1] = float("nan")
+    x[T // 2, 3] = float("nan")
+    y, z = moe.linear(x, w, activation="relu", out_dtype=dt, preact=True)
+    want = np.zeros((T, N), bool)
+    want[T // 2], want[:, N // 2] = True, True
+    assert np.array_equal(np.isnan(_np(z)), want)
+    assert np.array_equal(np.isnan(_np(y)), want)
+    rest = ~want
+    assert np.array_equal(_np(y)[rest], np.maximum(_np(z)[rest], 0.0))
+
+
+@pytest.mark.parametrize("T", [2, 300])      # the small-token kernels and the grouped products
+def test_reglu_experts_keep_nan(moe, T):
+    """A NaN that only the gate has: the rows of that expert show it."""
+    g = np.random.default_rng(5)
+    H, I, E = 128, 128, 2
+    x = torch.from_numpy(g.normal(size=(T, H))).bfloat16().cuda()
+    wgu = torch.from_numpy(g.normal(size=(E, 2 * I, H)) / H ** 0.5).bfloat16().cuda()
+    wd = torch.from_numpy(g.normal(size=(E, H, I)) / I ** 0.5).bfloat16().cuda()
+    wgu[1, 7, 5] = float("nan")
+    idx = (torch.arange(T, dtype=torch.int32, device="cuda") % 2)[:, None].contiguous()
+    y = moe.experts_forward(x, idx, torch.ones(T, 1, device="cuda"), wgu, wd, activation="relu")
+    moe.workspace_status(moe.default_workspace())
+    assert torch.isnan(y[1::2]).all() and torch.isfinite(y[0::2]).all()
