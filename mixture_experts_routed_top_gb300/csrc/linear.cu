@@ -1322,8 +1322,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
 // its loads and stores need; now 21 (100 MB, 4.8 TB/s), bound by issue.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
-  if (ACT == MOE_ACT_SILU) {  // s (1 + z (1 - s)), 1 - s = e^-z s; e^-z kept finite
-    const float e = __expf(fminf(-z, 80.f)), s = __fdividef(1.f, 1.f + e);
+  if (ACT == MOE_ACT_SILU) {  // s (1 + z (1 - s)), 1 - s = e^-z s; below -80 (-1.4e-33) as at -80
+    z = z < -80.f ? -80.f : z;
+    const float e = __expf(-z), s = __fdividef(1.f, 1.f + e);
     return s * fmaf(z, e * s, 1.f);
   }
   if (ACT == MOE_ACT_GELU)  // Phi(z) + z phi(z); the second term is 0 long before z^2 overflows

@@ -438,10 +438,11 @@ __device__ __forceinline__ void tmem_ld_wait_x8x2(uint32_t (&a)[8], uint32_t (&b
 // silu(g) = g / (1 + e^-g).  The fast division (2 ulp of fp32 for divisors
 // below 2^126) replaces the IEEE one: the result is rounded to bf16 or
 // e4m3 next, and the division was the costliest step of the gate/up
-// epilogue.  -g is clamped at 80 so the divisor stays in that range; below
-// g = -80 the result is under 2^-100 * |g| either way.
+// epilogue.  A divisor above 2^126 (g below -87.3) gives 0, where the result
+// is under 2^-119; with the exponent held at 80 instead a g of -1e36 came
+// out as -18.
 __device__ __forceinline__ float silu_f(float g) {
-  return __fdividef(g, 1.0f + __expf(fminf(-g, 80.0f)));
+  return __fdividef(g, 1.0f + __expf(-g));
 }
 
 // Gate activation of the gated MLP, `act` a moe_activation value (uniform

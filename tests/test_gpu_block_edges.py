@@ -54,3 +54,27 @@ def test_reglu_experts_keep_nan(moe, T):
     y = moe.experts_forward(x, idx, torch.ones(T, 1, device="cuda"), wgu, wd, activation="relu")
     moe.workspace_status(moe.default_workspace())
     assert torch.isnan(y[1::2]).all() and torch.isfinite(y[0::2]).all()
+
+
+@pytest.mark.parametrize("T,K,N", SHAPES)
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_silu_far_from_zero(moe, T, K, N, dt):
+    """silu and its slope go to 0 on the left and to z and 1 on the right, as far as the type goes."""
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    far = [-3e38, -1e36, -1e33, -1e20, -1000.0, -88.5, -87.0, -80.5, -79.0, -20.0, 0.0, 20.0, 90.0, 1000.0, 1e33, 3e38]
+    x[:, 0] = 1
+    w[:, 0] = torch.tensor([far[i % len(far)] for i in range(N)]).bfloat16()
+    y, z = moe.linear(x, w, activation="silu", out_dtype=dt, preact=True)
+    assert torch.equal(z, w[:, 0].to(dt).expand(T, N))
+    with np.errstate(over="ignore"):
+        ry = _np(z) / (1 + np.exp(-_np(z)))
+        p = 1 / (1 + np.exp(-_np(z)))
+        slope = np.where(_np(z) < -700, 0.0, p * (1 + _np(z) * (1 - p)))
+    # a result of 8 bits or fp32 arithmetic, and where e^-z leaves fp32 (|z| above 87) less than 88 e^-87
+    tol = (2.0 ** -8 if dt == torch.bfloat16 else 2.0 ** -18) * np.abs(ry) + 88 * np.exp(-80.0)
+    assert (np.abs(_np(y) - ry) <= tol).all()
+    gy = torch.ones(T, N, dtype=dt, device="cuda")
+    _, dw, db = moe.linear_backward(gy, x, w, bias=torch.zeros(N, device="cuda"), activation="silu", preact=z)
+    assert (np.abs(_np(db) - T * slope[0]) <= T * (2.0 ** -18 * np.abs(slope[0]) + 81 * np.exp(-80.0))).all()
+    assert (np.abs(_np(dw)[:, 0] - T * slope[0]) <= T * (2.0 ** -7 * np.abs(slope[0]) + 81 * np.exp(-80.0))).all()
