@@ -149,6 +149,13 @@ __device__ __forceinline__ void bits8(const uint4 (&x)[F32 ? 2 : 1], float (&v)[
   for (int j = 0; j < 8; ++j)
     v[j] = __uint_as_float(F32 ? w[j] : j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
 }
+// A result and the residual.  REST (the gradients' products): the residual is the
+// product of what rounding an operand left, and it joins only finite results.  Times
+// an infinity that rest, 0 or of either sign, would make the infinite result a NaN.
+template <bool REST>
+__device__ __forceinline__ float plus(float v, float r) {
+  return REST && !(fabsf(v) < INFINITY) ? v : v + r;
+}
 // The epilogue on 8 consecutive columns n.. of row m (m < M) where N % 8 == 0 and
 // every row is 16-byte aligned: pre-activation z = v + bias, y = residual +
 // act(z).  ACT and F32 are constants of the code: kernels hold several copies of
@@ -156,7 +163,7 @@ __device__ __forceinline__ void bits8(const uint4 (&x)[F32 ? 2 : 1], float (&v)[
 // fetching it took longer than a small product (33 us for 64 x 256 x 256),
 // while one copy called as a function took 300 ns a call.
 // b: the bias there; x: the residual's bits.
-template <int ACT, bool F32>
+template <int ACT, bool F32, bool REST>
 __device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, const float (&b)[8],
                                           const uint4 (&x)[F32 ? 2 : 1], float (&v)[8]) {
 #pragma unroll
@@ -170,7 +177,7 @@ __device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, con
     float r[8];
     bits8<F32>(x, r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += r[j];
+    for (int j = 0; j < 8; ++j) v[j] = plus<REST>(v[j], r[j]);
   }
   st8(p.out, m * p.ld_out + n, F32, v);
 }
@@ -182,7 +189,7 @@ __device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, con
 // Straight from the lanes every access touched 32 rows, and the epilogue of a
 // 256 x 256 tile took 6 us, as long as 1152 of the contraction.
 constexpr int kTurn = 32 * 32;
-template <int ACT, bool F32>
+template <int ACT, bool F32, bool REST>
 __device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
                                            const uint32_t (&v)[32], float* buf) {
   const int lane = threadIdx.x & 31;
@@ -221,7 +228,7 @@ __device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
       const float4 x = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * (c ^ (row & 7)));
       const float4 y = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * ((c + 1) ^ (row & 7)));
       float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      if (m0 + row < p.M && nv < p.N) epilogue8<ACT, F32>(p, m0 + row, nv, bv, xv[i], f);
+      if (m0 + row < p.M && nv < p.N) epilogue8<ACT, F32, REST>(p, m0 + row, nv, bv, xv[i], f);
     }
   } else if (n + lane < p.N) {
     const int rows = static_cast<int>(min(32l, p.M - m0)), col = n + lane;
@@ -354,7 +361,7 @@ __device__ __forceinline__ void single_rows(const LinearEpi& p, const float* fro
 // `step` floats further on.  Rows that are not whole aligned vectors go back into
 // stg and leave it with a warp's lanes along a row (391 x 224 x 706 from the
 // threads' 8 columns 22.5 us, so 12.1; x 704 9.2).
-template <int THREADS, int CHUNKS, int STRIDE>
+template <int THREADS, int CHUNKS, int STRIDE, bool REST>
 __device__ __forceinline__ void join_rows(const LinearEpi& p, float* stg, const float* part0,
                                           long step, int parts, int mine, int row0, int rows,
                                           long m0, int n0) {
@@ -435,7 +442,7 @@ __device__ __forceinline__ void join_rows(const LinearEpi& p, float* stg, const 
       if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !p.out_f32, y);
       if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, p.out_f32, z);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] += act_f(z[j], p.act, p.out_f32);
+      for (int j = 0; j < 8; ++j) y[j] = plus<REST>(act_f(z[j], p.act, p.out_f32), y[j]);
       st8(p.out, m * p.ld_out + n, p.out_f32, y);
     }
   }
@@ -656,7 +663,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             else mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
           }
         }
-        if (n0 + 32 * s < p.epi.N) epilogue32<ACT, false>(p.epi, m, n0 + 32 * s, v, turn);
+        if (n0 + 32 * s < p.epi.N) epilogue32<ACT, false, B_MN>(p.epi, m, n0 + 32 * s, v, turn);
       }
     }
   }
@@ -910,7 +917,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
           uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * s + i]);
-          if (n0 + 32 * s < p.epi.N) epilogue32<ACT, true>(p.epi, m, n0 + 32 * s, v, turn);
+          if (n0 + 32 * s < p.epi.N) epilogue32<ACT, true, false>(p.epi, m, n0 + 32 * s, v, turn);
         }
       }
     }
@@ -930,7 +937,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     int mi, ni;
     pair_tile(cid, mt, nt, p.group, &mi, &ni);
     // the CTAs of this rank of each pair, two apart
-    join_rows<kAThreads, 32, kAStride>(
+    join_rows<kAThreads, 32, kAStride, B_MN>(
         p.epi, stg, p.parts + static_cast<long>(blockIdx.x - 2 * pair) * 128 * 256, 2l * 128 * 256,
         S, pair, pair * rows, rows, static_cast<long>(mi) * 256 + 128 * rank, ni * 256);
   }
@@ -1108,7 +1115,7 @@ __global__ void __launch_bounds__(kTThreads)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 256);
   if (ok)
-    join_rows<kTThreads, 16, kTStride>(
+    join_rows<kTThreads, 16, kTStride, B_MN>(
         p.epi, stg, p.parts + static_cast<long>(blockIdx.x - rank) * 128 * 128, 128l * 128, S, rank,
         rank * rows, rows, static_cast<long>(mi) * 128, ni * 128);
 }
@@ -1352,7 +1359,10 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzArgs a) {
     if (a.dz != nullptr) st8(a.dz, t * a.ld_dz + n, false, d);  // rows padded to 8: always whole
     if (a.dz_lo != nullptr) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] -= __bfloat162float(__float2bfloat16_rn(d[j]));
+      for (int j = 0; j < 8; ++j) {  // nothing is left of one that bf16 has no finite value for
+        const float hi = __bfloat162float(__float2bfloat16_rn(d[j]));
+        d[j] = fabsf(hi) < INFINITY ? d[j] - hi : 0.f;
+      }
       st8(a.dz_lo, t * a.ld_dz + n, false, d);
     }
   };

@@ -78,3 +78,41 @@ def test_silu_far_from_zero(moe, T, K, N, dt):
     _, dw, db = moe.linear_backward(gy, x, w, bias=torch.zeros(N, device="cuda"), activation="silu", preact=z)
     assert (np.abs(_np(db) - T * slope[0]) <= T * (2.0 ** -18 * np.abs(slope[0]) + 81 * np.exp(-80.0))).all()
     assert (np.abs(_np(dw)[:, 0] - T * slope[0]) <= T * (2.0 ** -7 * np.abs(slope[0]) + 81 * np.exp(-80.0))).all()
+
+
+@pytest.mark.parametrize("T,N", [(16, 64), (17, 64), (1, 1024), (1, 1032), (3, 7)])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), 3.4e38])
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_infinite_gradients_of_few_and_many_dz(moe, T, N, value, act):
+    """A gradient beyond bf16 makes its row of dx and of dw infinite, with the signs of what it
+    multiplies, on either side of the number of dz that enter the products in two parts."""
+    K = 72
+    g = np.random.default_rng([T, N])
+    x, w = (torch.from_numpy(np.where(g.random(s) < 0.5, -1, 1) * (0.5 + g.random(s))).bfloat16().cuda()
+            for s in ((T, K), (N, K)))
+    gy = torch.from_numpy(g.normal(size=(T, N))).float().cuda()
+    gy[T // 2, N // 3] = value
+    z = torch.full((T, N), 20.0, device="cuda") if act else None     # silu's slope is 1 there, to 2^-24
+    dx, dw, _ = moe.linear_backward(gy, x, w, activation=act, preact=z)
+    big = torch.full((K,), float("inf"), device="cuda") * (1 if value > 0 else -1)
+    assert torch.equal(dx[T // 2].float(), big * w[N // 3].float())
+    assert torch.equal(dw[N // 3].float(), big * x[T // 2].float())
+    gy[T // 2, N // 3] = 0
+    zdx, zdw, _ = moe.linear_backward(gy, x, w, activation=act, preact=z)
+    rows, cols = torch.arange(T, device="cuda") != T // 2, torch.arange(N, device="cuda") != N // 3
+    assert torch.equal(dx[rows], zdx[rows]) and torch.equal(dw[cols], zdw[cols])
+
+
+@pytest.mark.parametrize("T,N", [(16, 64), (17, 64), (1, 1024), (1, 1032), (3, 7), (1024, 1), (1100, 1)])
+@pytest.mark.parametrize("K", [72, 4104])
+def test_infinite_operands_of_few_and_many_dz(moe, T, N, K):
+    """An infinite token or weight makes infinities of what it is multiplied into and no NaN."""
+    g = np.random.default_rng([T, N, K])
+    x, w = (torch.from_numpy(g.normal(size=s)).bfloat16().cuda() for s in ((T, K), (N, K)))
+    gy = torch.from_numpy(np.where(g.random((T, N)) < 0.5, -1, 1) * (0.5 + g.random((T, N)))).float().cuda()
+    x[T // 2, 5], w[N // 3, 9] = float("inf"), -float("inf")
+    dx, dw, _ = moe.linear_backward(gy, x, w)
+    assert torch.equal(dx[:, 9].float(), -gy[:, N // 3] * float("inf"))
+    assert torch.equal(dw[:, 5].float(), gy[T // 2] * float("inf"))
+    cols = torch.arange(K, device="cuda")
+    assert torch.isfinite(dx[:, cols != 9]).all() and torch.isfinite(dw[:, cols != 5]).all()
