@@ -199,18 +199,48 @@ def workspace_size(T: int, H: int, I: int, E: int, k: int, wdtype: int = W_BF16)
     return int(lib().moe_workspace_size(T, H, I, E, k, wdtype))
 
 
+def _capturing() -> bool:
+    """Whether the current stream is being captured (the default stream cannot be)."""
+    return _raw_stream(_raw_device()) != 0 and torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
-    """Caller-owned device scratch for experts_forward, grown on demand.
-    The first 256 bytes hold the device error word; they start zeroed."""
+    """Caller-owned device scratch, grown on demand.  The first 256 bytes of a
+    buffer hold the device error word; they start zeroed.
+
+    buf is the buffer of calls that run at once.  A buffer that a call under
+    CUDA-graph capture was given stays allocated as long as the workspace,
+    whatever later calls need, since the graph goes on writing to it.  A
+    buffer that a capture had to allocate belongs to its graph, which zeroes
+    it in each replay: make the call once before, as capturing asks for."""
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
         self.buf = None
+        self.captured = []      # buffers that graphs use
+
+    def buffers(self):
+        """Every buffer whose error word may be set."""
+        own = [] if self.buf is None or any(b is self.buf for b in self.captured) else [self.buf]
+        return own + self.captured
 
     def get(self, nbytes: int) -> torch.Tensor:
+        if _capturing():
+            return self._for_graph(nbytes)
         if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.zeros(max(nbytes, 1024), dtype=torch.uint8, device=self.device)
+            self.buf = self._new(nbytes)
         return self.buf
+
+    def _new(self, nbytes: int) -> torch.Tensor:
+        return torch.zeros(max(nbytes, 1024), dtype=torch.uint8, device=self.device)
+
+    def _for_graph(self, nbytes: int) -> torch.Tensor:
+        buf = next((b for b in self.buffers() if b.numel() >= nbytes), None)
+        if buf is None:
+            buf = self._new(nbytes)
+        if not any(b is buf for b in self.captured):
+            self.captured.append(buf)
+        return buf
 
 
 _DEFAULT_WS = {}
@@ -272,9 +302,11 @@ def experts_forward(hidden: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.
 
 
 def workspace_status(workspace, stream=None):
-    """Synchronise and raise MoEError if a kernel flagged an error in ws."""
-    ws = workspace.buf if isinstance(workspace, Workspace) else workspace
-    _check(lib().moe_workspace_status(_ptr(ws), _stream(stream)))
+    """Synchronise and raise MoEError if a kernel flagged an error in ws (a
+    Workspace: in any of its buffers, those of captured graphs among them)."""
+    bufs = (workspace.buffers() or [None]) if isinstance(workspace, Workspace) else [workspace]
+    for ws in bufs:
+        _check(lib().moe_workspace_status(_ptr(ws), _stream(stream)))
 
 
 def accumulator(workspace, T: int, H: int, I: int, E: int, k: int,
@@ -282,9 +314,10 @@ def accumulator(workspace, T: int, H: int, I: int, E: int, k: int,
     """fp32 [T, H] view of the workspace's output accumulator: after a
     grouped-path forward with these sizes it holds the un-rounded output
     (see moe_workspace_accumulator_offset)."""
-    ws = workspace.buf if isinstance(workspace, Workspace) else workspace
     off = int(lib().moe_workspace_accumulator_offset(T, H, I, E, k, wdtype))
-    if off == 0 or off + T * H * 4 > ws.numel():
+    bufs = workspace.buffers() if isinstance(workspace, Workspace) else [workspace]
+    ws = next((b for b in bufs if off + T * H * 4 <= b.numel()), None)
+    if off == 0 or ws is None:
         raise ValueError("workspace too small for these sizes")
     return ws[off:off + T * H * 4].view(torch.float32).view(T, H)
 

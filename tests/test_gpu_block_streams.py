@@ -1,0 +1,56 @@
+"""Workspaces and tensors of the calls under graphs and on several streams."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_routed_top_gb300 as m
+    m.lib()
+    return m
+
+
+def _randn(*shape, seed=0, dtype=torch.bfloat16):
+    g = torch.Generator("cuda")
+    g.manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("default", [True, False])
+def test_a_graph_keeps_its_workspace_when_a_larger_call_follows(moe, default, monkeypatch):
+    """Captured, then a call that needs more, then other tensors in whatever memory is free,
+    then replays: the results are the same and nobody else's memory has changed."""
+    monkeypatch.setattr(moe, "_DEFAULT_WS", {})
+    ws = None if default else moe.Workspace("cuda")
+    x, w = _randn(64, 4096, seed=1), _randn(256, 4096, seed=2)
+    gy = _randn(64, 256, seed=3)
+
+    def step():
+        y = moe.linear(x, w, workspace=ws)                       # the contraction is split: partial sums
+        return y, *moe.linear_backward(gy, x, w, bias=x[0, :256], workspace=ws)
+
+    want = [t.clone() for t in step()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    used = (moe.default_workspace() if default else ws).buffers()
+    big = torch.full((4096, 8192), 2.0, dtype=torch.bfloat16, device="cuda")     # 67 MB of dz
+    moe.linear_backward(big, _randn(4096, 64, seed=4), _randn(8192, 64, seed=5), activation="silu", preact=big,
+                        workspace=ws)
+    torch.cuda.synchronize()
+    after = moe.default_workspace() if default else ws
+    assert after.buf.numel() > 67 * 2 ** 20 and all(any(b is c for c in after.buffers()) for b in after.captured)
+    assert any(b is c for b in used for c in after.captured)
+    others = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in [b.numel() for b in used] * 2 + [1 << 20] * 8]
+    for t in got:
+        t.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert all(bool((o == 7).all()) for o in others)
+    moe.workspace_status(after)

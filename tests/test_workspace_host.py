@@ -1,0 +1,61 @@
+"""The workspace's bookkeeping, without a GPU: its buffers are host tensors here and the
+state of the stream is the test's."""
+import weakref
+
+import pytest
+import torch
+
+import mixture_experts_routed_top_gb300 as moe
+
+
+@pytest.fixture
+def stream(monkeypatch):
+    """Whether the current stream is being captured, as the test sets it."""
+    state = dict(capturing=False)
+    monkeypatch.setattr(moe, "_capturing", lambda: state["capturing"], raising=False)
+    return state
+
+
+def test_a_captured_buffer_outlives_growth(stream):
+    """A graph keeps the address it was captured with: a larger call gets another
+    buffer, and the graph's is not given back."""
+    ws = moe.Workspace("cpu")
+    first = ws.get(2000)
+    assert ws.get(100) is first
+    stream["capturing"] = True
+    assert ws.get(1500) is first              # the graph's from now on
+    stream["capturing"] = False
+    assert ws.get(1500) is first
+    first = weakref.ref(first)                # nobody but the workspace holds it
+    large = ws.get(50000)
+    assert first() is not None and large is not first() and ws.buf is large
+    assert any(b is first() for b in ws.buffers()) and any(b is large for b in ws.buffers())
+    stream["capturing"] = True
+    assert ws.get(40000) is large             # another graph, a larger call
+    stream["capturing"] = False
+    ws.get(90000)
+    assert {b.numel() for b in ws.buffers()} == {2000, 50000, 90000}
+
+
+def test_a_buffer_that_was_not_captured_is_given_back(stream):
+    ws = moe.Workspace("cpu")
+    for n in (2000, 4000, 8000):
+        ws.get(n)
+    assert [b.numel() for b in ws.buffers()] == [8000]
+
+
+def test_a_buffer_allocated_in_a_capture_stays_the_graphs(stream):
+    ws = moe.Workspace("cpu")
+    own = ws.get(1024)
+    stream["capturing"] = True
+    g = ws.get(5000)
+    assert g is not own and ws.get(4000) is g
+    stream["capturing"] = False
+    assert ws.get(1000) is own and ws.get(4000) is not g
+    assert any(b is g for b in ws.buffers())
+
+
+def test_buffers_start_zeroed(stream):
+    ws = moe.Workspace("cpu")
+    assert ws.buffers() == [] and ws.buf is None
+    assert ws.get(1).numel() >= 1024 and not ws.get(1).any()
