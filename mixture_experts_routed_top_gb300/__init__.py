@@ -227,8 +227,11 @@ class Workspace:
     def get(self, nbytes: int) -> torch.Tensor:
         if _capturing():
             return self._for_graph(nbytes)
-        if self.buf is None or self.buf.numel() < nbytes:
+        old = self.buf
+        if old is None or old.numel() < nbytes:
             self.buf = self._new(nbytes)
+            if old is not None and not any(b is old for b in self.captured):
+                self.buf[:4].copy_(old[:4])     # errors that nobody has read yet
         return self.buf
 
     def _new(self, nbytes: int) -> torch.Tensor:

@@ -54,3 +54,19 @@ def test_a_graph_keeps_its_workspace_when_a_larger_call_follows(moe, default, mo
         assert torch.equal(a, b)
     assert all(bool((o == 7).all()) for o in others)
     moe.workspace_status(after)
+
+
+def test_an_error_is_reported_after_the_workspace_has_grown(moe):
+    """An expert index out of range, then a call that needs a larger buffer, then the status."""
+    ws = moe.Workspace("cuda")
+    h = _randn(16, 128, seed=6)
+    idx = torch.full((16, 1), 9, dtype=torch.int32, device="cuda")
+    wgu, wd = _randn(4, 256, 128, seed=7), _randn(4, 128, 128, seed=8)
+    moe.experts_forward(h, idx, torch.ones(16, 1, device="cuda"), wgu, wd, workspace=ws)
+    before = ws.buf.numel()
+    moe.linear(_randn(64, 64, seed=9), _randn(64, 64, seed=10), workspace=ws)
+    assert ws.buf.numel() > before
+    with pytest.raises(moe.MoEError) as e:
+        moe.workspace_status(ws)
+    assert e.value.status == 1
+    moe.workspace_status(ws)

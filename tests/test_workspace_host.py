@@ -59,3 +59,16 @@ def test_buffers_start_zeroed(stream):
     ws = moe.Workspace("cpu")
     assert ws.buffers() == [] and ws.buf is None
     assert ws.get(1).numel() >= 1024 and not ws.get(1).any()
+
+
+def test_errors_survive_growth(stream):
+    """The error word of a buffer that is given back moves on; the counters behind it start
+    at zero; a captured buffer keeps its own."""
+    ws = moe.Workspace("cpu")
+    ws.get(1024)[:12].view(torch.int32).copy_(torch.tensor([5, 3, 1]))
+    assert ws.get(4096)[:12].view(torch.int32).tolist() == [5, 0, 0]
+    stream["capturing"] = True
+    kept = ws.get(100)
+    stream["capturing"] = False
+    assert not ws.get(9000).any()
+    assert kept[:4].view(torch.int32).item() == 5 and any(b is kept for b in ws.buffers())
