@@ -246,7 +246,25 @@ class Workspace:
         return buf
 
 
+# Workspaces of the calls that are given none: one per device and stream, since
+# calls on different streams run at the same time.
 _DEFAULT_WS = {}
+
+
+def _default_ws(dev: int) -> Workspace:
+    """The default workspace of the device's current stream."""
+    key = (dev, _raw_stream(dev))
+    ws = _DEFAULT_WS.get(key)
+    if ws is not None:
+        return ws
+    if _capturing():
+        # a stream that only captures has none; the calls were tried on another one, and what
+        # was allocated now would be zeroed, error word and all, in every replay
+        for (d, _), other in list(_DEFAULT_WS.items()):
+            if d == dev:
+                return other
+    return _DEFAULT_WS.setdefault(key, Workspace(torch.device("cuda", dev)))
+
 
 # moe_activation values
 ACTIVATIONS = {"silu": 0, "gelu": 1, "relu": 2}
@@ -290,10 +308,7 @@ def experts_forward(hidden: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.
         out = torch.empty(T, H, dtype=torch.bfloat16, device=hidden.device)
     nbytes = workspace_size(T, H, I, E, k, wdtype)
     if workspace is None:
-        key = hidden.device
-        workspace = _DEFAULT_WS.get(key)
-        if workspace is None:
-            workspace = _DEFAULT_WS.setdefault(key, Workspace(key))
+        workspace = _default_ws(hidden.get_device())
     ws = workspace.get(nbytes)
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
@@ -326,10 +341,12 @@ def accumulator(workspace, T: int, H: int, I: int, E: int, k: int,
 
 
 def default_workspace(device="cuda") -> Workspace:
+    """The workspace of calls on the device's current stream that are given none.
+    A graph captured without a workspace uses the one of the stream that it was
+    captured on, or if that has none the device's first: replays and the calls
+    that share it have to be ordered."""
     d = torch.device(device)
-    if d.index is None:
-        d = torch.device("cuda", torch.cuda.current_device())
-    return _DEFAULT_WS.setdefault(d, Workspace(d))
+    return _default_ws(torch.cuda.current_device() if d.index is None else d.index)
 
 
 # ------------------------------------------------------------------ around the experts
@@ -391,12 +408,8 @@ def _call(call, dev: int, stream, *args):
         _check(status)
 
 
-def _workspace(workspace: Optional[Workspace], device, nbytes: int) -> torch.Tensor:
-    if workspace is None:
-        workspace = _DEFAULT_WS.get(device)
-        if workspace is None:
-            workspace = _DEFAULT_WS.setdefault(device, Workspace(device))
-    return workspace.get(nbytes)
+def _workspace(workspace: Optional[Workspace], dev: int, nbytes: int) -> torch.Tensor:
+    return (_default_ws(dev) if workspace is None else workspace).get(nbytes)
 
 
 def _matrix_of(name: str, t: torch.Tensor):
@@ -560,7 +573,7 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
     bf16 [T,H], or None where pre_norm was off; residual: the residual_out that
     block_norm returned; the rest as it was called with.  What does not apply
     comes back as None.  d_gate is fp32 for a per-channel gate, else of the
-    gate's type; the weights' gradients are fp32 [H]."""
+    gate's type; the weights' gradients are fp32 [H].  workspace: as in linear."""
     dev, shape = _matrix_of("residual", residual)
     ld_r = _mat("residual", residual, _DT, shape, dev)
     T, H = shape
@@ -587,7 +600,7 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
     if pre:
         d_pre = torch.empty(H, dtype=_F32, device=device)
         pdpre = d_pre.data_ptr()
-    ws = _workspace(workspace, device, (_LIB or lib()).moe_block_norm_backward_workspace_size(H))
+    ws = _workspace(workspace, dev, (_LIB or lib()).moe_block_norm_backward_workspace_size(H))
     _call(_NORM_BWD, dev, stream, pgr, ld_gr, pgn, ld_gn, residual.data_ptr() if pgn else 0, _DT[residual.dtype],
           ld_r, py, ld_y, pg, kind, gate_dt, ld_g, scale, post_norm, post, pre, wdt, eps, T, H, d_res.data_ptr(),
           pdy, pdg, pdpost, pdpre, ws.data_ptr(), ws.numel())
@@ -612,8 +625,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
     activation None, 'silu', 'gelu' (exact) or 'relu'; out_dtype bf16 or fp32
     (router logits), which residual and the pre-activation share.  out: the
     tensor to write into (rows contiguous); it may be residual.  Calls that
-    share a workspace (by default all of a device) must be ordered on one
-    stream."""
+    share a workspace must be ordered on one stream; without one they use
+    their stream's."""
     global _LINEAR_WS
     dev, xs = _matrix_of("x", x)
     T, K = xs
@@ -641,7 +654,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
         z = torch.empty_strided(shape, (ld_o, 1), dtype=out_dtype, device=x.device)
         pz = z.data_ptr()
     _LINEAR_WS = _LINEAR_WS or lib().moe_linear_workspace_size()
-    ws = _workspace(workspace, x.device, _LINEAR_WS)
+    ws = _workspace(workspace, dev, _LINEAR_WS)
     _call(_LINEAR, dev, stream, x.data_ptr(), ld_x, w.data_ptr(), ld_w, pb, bdt, _act(activation), pr, ld_r, T, K, N,
           out.data_ptr(), dt, ld_o, pz, ws.data_ptr(), ws.numel())
     return (out, z) if preact else out
@@ -656,7 +669,7 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
     grad_y [T,N] of linear's output type (it is also the residual's gradient);
     preact: what linear(..., preact=True) returned, with an activation; bias:
     as passed to linear (None: dbias is None).  need_x / need_w = False leave
-    that gradient out (None)."""
+    that gradient out (None).  workspace: as in linear."""
     dev, xs = _matrix_of("x", x)
     T, K = xs
     ld_x = _mat("x", x, _ONLY_BF16, xs, dev)
@@ -681,7 +694,7 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
     if need_w:
         dw = torch.empty((N, K), dtype=_BF16, device=x.device)
         pdw = dw.data_ptr()
-    ws = _workspace(workspace, x.device, (_LIB or lib()).moe_linear_backward_workspace_size(T, N))
+    ws = _workspace(workspace, dev, (_LIB or lib()).moe_linear_backward_workspace_size(T, N))
     _call(_LINEAR_BWD, dev, stream, grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(),
           ld_w, act, pz, ld_z, T, K, N, pdx, pdw, pdb, ws.data_ptr(), ws.numel())
     return dx, dw, db

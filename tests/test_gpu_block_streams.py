@@ -70,3 +70,32 @@ def test_an_error_is_reported_after_the_workspace_has_grown(moe):
         moe.workspace_status(ws)
     assert e.value.status == 1
     moe.workspace_status(ws)
+
+
+def test_streams_do_not_share_the_default_workspace(moe):
+    """Split products and gradients on two streams at once give what they give one by one."""
+    cases = [(_randn(64, 4096, seed=20 + i), _randn(256, 4096, seed=30 + i), _randn(64, 256, seed=40 + i))
+             for i in range(2)]
+
+    def step(x, w, gy):
+        return moe.linear(x, w), *moe.linear_backward(gy, x, w, bias=w[:, 0].contiguous())
+
+    want = [step(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    spaces = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            spaces.append(moe.default_workspace())
+    assert spaces[0] is not spaces[1] and moe.default_workspace() not in spaces
+    got = [[], []]
+    for _ in range(40):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(*cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+    for ws in spaces:
+        moe.workspace_status(ws)

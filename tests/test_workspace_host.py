@@ -72,3 +72,25 @@ def test_errors_survive_growth(stream):
     stream["capturing"] = False
     assert not ws.get(9000).any()
     assert kept[:4].view(torch.int32).item() == 5 and any(b is kept for b in ws.buffers())
+
+
+def test_default_workspaces_per_stream(stream, monkeypatch):
+    """Each device and stream has its own; a capturing stream without one shares the device's
+    first, so that nothing is allocated in the capture."""
+    now = {}
+    monkeypatch.setattr(moe, "_DEFAULT_WS", {})
+    monkeypatch.setattr(moe, "_raw_stream", lambda dev: now["handle"])
+    made = {}
+    for dev, handle in ((0, 0), (0, 11), (1, 0)):
+        now["handle"] = handle
+        made[dev, handle] = moe._default_ws(dev)
+        assert moe._default_ws(dev) is made[dev, handle]
+    assert len({id(w) for w in made.values()}) == 3
+    stream["capturing"] = True
+    now["handle"] = 99
+    assert moe._default_ws(0) is made[0, 0] and moe._default_ws(1) is made[1, 0]
+    now["handle"] = 11
+    assert moe._default_ws(0) is made[0, 11]
+    stream["capturing"] = False
+    now["handle"] = 99
+    assert moe._default_ws(0) not in made.values()
