@@ -149,6 +149,37 @@ def _stream(stream=None):
     return _raw_stream(_raw_device()) if stream is None else stream.cuda_stream
 
 
+def _tensors(values):
+    for v in values:
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif isinstance(v, (tuple, list)):
+            yield from _tensors(v)
+
+
+def _on_stream(call, args: dict):
+    """call(**args) on args["stream"], as under torch.cuda.stream(): results and
+    workspaces are allocated, and workspaces zeroed, in that stream's order.
+    Tensors are marked as used by the stream that is not their own, so that
+    letting go of one gives its memory to nobody while either still works on it.
+    Waiting for what the arguments come from is the caller's, as ever."""
+    stream = args.pop("stream")
+    given = list(_tensors(args.values()))
+    for t in given:
+        if t.is_cuda and t.device != stream.device:
+            raise ValueError(f"stream on {stream.device}, a tensor on {t.device}")
+    before = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        result = call(**args)
+    if stream != before:
+        for t in given:
+            if t.is_cuda:
+                t.record_stream(stream)
+        for t in _tensors((result,)):
+            t.record_stream(before)
+    return result
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -158,13 +189,15 @@ def _need_cuda(*ts):
 # ------------------------------------------------------------------ router
 def route(logits: torch.Tensor, k: int, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Top-k routing of fp32 logits [T, E] -> (topk_idx int32 [T,k], topk_w fp32 [T,k])."""
+    if stream is not None:
+        return _on_stream(route, locals())
     _need_cuda(logits)
     if logits.dtype != torch.float32 or logits.dim() != 2:
         raise ValueError("logits must be fp32 [T, E]")
     T, E = logits.shape
     idx = torch.empty(T, k, dtype=torch.int32, device=logits.device)
     w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
-    _check(lib().moe_route(_ptr(logits), T, E, k, _ptr(idx), _ptr(w), _stream(stream)))
+    _check(lib().moe_route(_ptr(logits), T, E, k, _ptr(idx), _ptr(w), _stream()))
     return idx, w
 
 
@@ -175,6 +208,8 @@ def dispatch_workspace_size(T: int, E: int, k: int) -> int:
 
 def dispatch(topk_idx: torch.Tensor, E: int, stream=None):
     """Expert-contiguous ordering -> (counts [E], offsets [E+1], sorted_f [T*k], row_of [T*k])."""
+    if stream is not None:
+        return _on_stream(dispatch, locals())
     _need_cuda(topk_idx)
     if topk_idx.dtype != torch.int32 or topk_idx.dim() != 2:
         raise ValueError("topk_idx must be int32 [T, k]")
@@ -187,8 +222,8 @@ def dispatch(topk_idx: torch.Tensor, E: int, stream=None):
     nbytes = dispatch_workspace_size(T, E, k)
     ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=dev)
     _check(lib().moe_dispatch(_ptr(topk_idx), T, E, k, _ptr(counts), _ptr(offsets),
-                              _ptr(sorted_f), _ptr(row_of), _ptr(ws), nbytes, _stream(stream)))
-    _check(lib().moe_workspace_status(_ptr(ws), _stream(stream)))
+                              _ptr(sorted_f), _ptr(row_of), _ptr(ws), nbytes, _stream()))
+    _check(lib().moe_workspace_status(_ptr(ws), _stream()))
     return counts, offsets, sorted_f, row_of
 
 
@@ -201,7 +236,7 @@ def workspace_size(T: int, H: int, I: int, E: int, k: int, wdtype: int = W_BF16)
 
 def _capturing() -> bool:
     """Whether the current stream is being captured (the default stream cannot be)."""
-    return _raw_stream(_raw_device()) != 0 and torch.cuda.is_current_stream_capturing()
+    return _stream() != 0 and torch.cuda.is_current_stream_capturing()
 
 
 class Workspace:
@@ -217,6 +252,7 @@ class Workspace:
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
         self.buf = None
+        self.home = None        # the stream in whose order buf's memory is given back
         self.captured = []      # buffers that graphs use
 
     def buffers(self):
@@ -227,9 +263,11 @@ class Workspace:
     def get(self, nbytes: int) -> torch.Tensor:
         if _capturing():
             return self._for_graph(nbytes)
-        old = self.buf
+        old, now = self.buf, _stream()
+        if self.home != now and old is not None:
+            old.record_stream(torch.cuda.current_stream(self.device))
         if old is None or old.numel() < nbytes:
-            self.buf = self._new(nbytes)
+            self.buf, self.home = self._new(nbytes), now
             if old is not None and not any(b is old for b in self.captured):
                 self.buf[:4].copy_(old[:4])     # errors that nobody has read yet
         return self.buf
@@ -284,6 +322,8 @@ def experts_forward(hidden: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.
     or packed e2m1 bytes (uint8 or int8) [E,2I,H/2] and [E,H,I/2] with 1x32
     UE8M0 scales from quantize_fp4_blocks; activation: the gate activation,
     'silu' (SwiGLU), 'gelu' (GeGLU, exact erf GELU) or 'relu' (ReGLU)."""
+    if stream is not None:
+        return _on_stream(experts_forward, locals())
     _need_cuda(hidden, topk_idx, topk_w, w_gate_up, w_down, scale_gate_up, scale_down, out)
     T, H = hidden.shape
     k = topk_idx.shape[1]
@@ -315,14 +355,21 @@ def experts_forward(hidden: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.
     _check(lib().moe_experts_forward_act(
         _ptr(hidden), T, H, _ptr(topk_idx), _ptr(topk_w), E, k, I, _ptr(w_gate_up),
         _ptr(w_down), wdtype, _ptr(scale_gate_up), _ptr(scale_down), sf, ACTIVATIONS[activation],
-        _ptr(out), _ptr(ws), ws.numel(), _stream(stream)))
+        _ptr(out), _ptr(ws), ws.numel(), _stream()))
     return out
 
 
-def workspace_status(workspace, stream=None):
+def workspace_status(workspace=None, stream=None):
     """Synchronise and raise MoEError if a kernel flagged an error in ws (a
-    Workspace: in any of its buffers, those of captured graphs among them)."""
-    bufs = (workspace.buffers() or [None]) if isinstance(workspace, Workspace) else [workspace]
+    Workspace: in any of its buffers, those of captured graphs among them;
+    None: in a default workspace of any stream of the device, which is
+    synchronised)."""
+    if workspace is None:
+        torch.cuda.synchronize()
+        dev = torch.cuda.current_device()
+        bufs = [b for (d, _), ws in list(_DEFAULT_WS.items()) if d == dev for b in ws.buffers()]
+    else:
+        bufs = (workspace.buffers() or [None]) if isinstance(workspace, Workspace) else [workspace]
     for ws in bufs:
         _check(lib().moe_workspace_status(_ptr(ws), _stream(stream)))
 
@@ -340,11 +387,14 @@ def accumulator(workspace, T: int, H: int, I: int, E: int, k: int,
     return ws[off:off + T * H * 4].view(torch.float32).view(T, H)
 
 
-def default_workspace(device="cuda") -> Workspace:
-    """The workspace of calls on the device's current stream that are given none.
+def default_workspace(device="cuda", stream=None) -> Workspace:
+    """The workspace of calls on the device's current stream (or stream) that are given none.
     A graph captured without a workspace uses the one of the stream that it was
     captured on, or if that has none the device's first: replays and the calls
     that share it have to be ordered."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return default_workspace(stream.device)
     d = torch.device(device)
     return _default_ws(torch.cuda.current_device() if d.index is None else d.index)
 
@@ -352,7 +402,8 @@ def default_workspace(device="cuda") -> Workspace:
 # ------------------------------------------------------------------ around the experts
 # Activations, logits and their gradients may have rows further apart than
 # they are long (a slice of columns of a larger matrix); everything else is
-# contiguous.  Each call is asynchronous on the current stream (or stream=).
+# contiguous.  Each call is asynchronous on the current stream; with stream= it
+# runs as under torch.cuda.stream(stream).
 _BF16, _F32 = torch.bfloat16, torch.float32
 _DT = {_BF16: 0, _F32: 1}
 _SCORES = {"softmax": 0, "sigmoid": 1}
@@ -396,14 +447,14 @@ def _dense(name: str, t: torch.Tensor, dtypes, shape, dev: int) -> int:
     return t.data_ptr()
 
 
-def _call(call, dev: int, stream, *args):
-    """One of the packed calls on device `dev`: the stream appended, the device made current."""
+def _call(call, dev: int, *args):
+    """One of the packed calls on device `dev`: its current stream appended, the device made current."""
     L = _LIB or lib()
     if _raw_device() == dev:
-        status = L.moe_call_packed(call[0], call[1](*args, _raw_stream(dev) if stream is None else stream.cuda_stream))
+        status = L.moe_call_packed(call[0], call[1](*args, _raw_stream(dev)))
     else:
         with torch.cuda.device(dev):
-            status = L.moe_call_packed(call[0], call[1](*args, _raw_stream(dev) if stream is None else stream.cuda_stream))
+            status = L.moe_call_packed(call[0], call[1](*args, _raw_stream(dev)))
     if status:
         _check(status)
 
@@ -440,6 +491,8 @@ def route_scored(logits: torch.Tensor, k: int, *, score: str = "sigmoid",
     (1 or 2) best; the chosen scores are divided by their sum if renormalise,
     then multiplied by scale.  Experts with a logit of -inf or NaN are masked.
     out: (topk_idx, topk_w) to write into."""
+    if stream is not None:
+        return _on_stream(route_scored, locals())
     dev, shape = _matrix_of("logits", logits)
     ld = _mat("logits", logits, _DT, shape, dev)
     T, E = shape
@@ -451,7 +504,7 @@ def route_scored(logits: torch.Tensor, k: int, *, score: str = "sigmoid",
         idx, w = out
         pi = _dense("topk_idx", idx, _ONLY_I32, (T, k), dev)
         pw = _dense("topk_w", w, _ONLY_F32, (T, k), dev)
-    _call(_ROUTE, dev, stream, logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _score_of(score),
+    _call(_ROUTE, dev, logits.data_ptr(), _DT[logits.dtype], ld, T, E, k, _score_of(score),
           0 if bias is None else _dense("bias", bias, _ONLY_F32, (E,), dev), n_group, topk_group, group_top,
           renormalise, scale, pi, pw)
     return idx, w
@@ -467,6 +520,8 @@ def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: 
     logits, score, bias, renormalise, scale as route_scored was called with;
     topk_idx, topk_w what it returned; grad_w fp32 [T,k].  out: a tensor to
     write into, its rows contiguous."""
+    if stream is not None:
+        return _on_stream(route_scored_backward, locals())
     dev, shape = _matrix_of("logits", logits)
     ld = _mat("logits", logits, _DT, shape, dev)
     T, E = shape
@@ -478,7 +533,7 @@ def route_scored_backward(logits: torch.Tensor, topk_idx: torch.Tensor, topk_w: 
         ldo = E
     else:
         ldo = _mat("out", out, (logits.dtype,), shape, dev)
-    _call(_ROUTE_BWD, dev, stream, logits.data_ptr(), _DT[logits.dtype], ld, T, E, slots[1], _score_of(score),
+    _call(_ROUTE_BWD, dev, logits.data_ptr(), _DT[logits.dtype], ld, T, E, slots[1], _score_of(score),
           0 if bias is None else _dense("bias", bias, _ONLY_F32, (E,), dev), renormalise, scale,
           _dense("topk_idx", topk_idx, _ONLY_I32, slots, dev), _dense("topk_w", topk_w, _ONLY_F32, slots, dev),
           _dense("grad_w", grad_w, _ONLY_F32, slots, dev), out.data_ptr(), ldo)
@@ -533,6 +588,8 @@ def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     [T] / [T,1] or [T,H], bf16 or fp32; weights [H], both bf16 or both fp32.
     out: (residual_out, normed) to write into, either of them None for a new
     tensor; residual_out may be residual."""
+    if stream is not None:
+        return _on_stream(block_norm, locals())
     dev, shape = _matrix_of("residual", residual)
     ld_r = _mat("residual", residual, _DT, shape, dev)
     T, H = shape
@@ -556,7 +613,7 @@ def block_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
         pn = n.data_ptr()
     else:
         pn = _dense("normed", n, _ONLY_BF16, shape, dev)
-    _call(_NORM, dev, stream, residual.data_ptr(), _DT[residual.dtype], ld_r, py, ld_y, pg, kind, gate_dt, ld_g,
+    _call(_NORM, dev, residual.data_ptr(), _DT[residual.dtype], ld_r, py, ld_y, pg, kind, gate_dt, ld_g,
           scale, post_norm, post, pre_norm, pre, wdt, eps, T, H, pres, pn)
     return res, n
 
@@ -574,6 +631,8 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
     block_norm returned; the rest as it was called with.  What does not apply
     comes back as None.  d_gate is fp32 for a per-channel gate, else of the
     gate's type; the weights' gradients are fp32 [H].  workspace: as in linear."""
+    if stream is not None:
+        return _on_stream(block_norm_backward, locals())
     dev, shape = _matrix_of("residual", residual)
     ld_r = _mat("residual", residual, _DT, shape, dev)
     T, H = shape
@@ -601,7 +660,7 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
         d_pre = torch.empty(H, dtype=_F32, device=device)
         pdpre = d_pre.data_ptr()
     ws = _workspace(workspace, dev, (_LIB or lib()).moe_block_norm_backward_workspace_size(H))
-    _call(_NORM_BWD, dev, stream, pgr, ld_gr, pgn, ld_gn, residual.data_ptr() if pgn else 0, _DT[residual.dtype],
+    _call(_NORM_BWD, dev, pgr, ld_gr, pgn, ld_gn, residual.data_ptr() if pgn else 0, _DT[residual.dtype],
           ld_r, py, ld_y, pg, kind, gate_dt, ld_g, scale, post_norm, post, pre, wdt, eps, T, H, d_res.data_ptr(),
           pdy, pdg, pdpost, pdpre, ws.data_ptr(), ws.numel())
     return d_res, d_y, d_gate, d_post, d_pre
@@ -628,6 +687,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
     share a workspace must be ordered on one stream; without one they use
     their stream's."""
     global _LINEAR_WS
+    if stream is not None:
+        return _on_stream(linear, locals())
     dev, xs = _matrix_of("x", x)
     T, K = xs
     ld_x = _mat("x", x, _ONLY_BF16, xs, dev)
@@ -655,7 +716,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = N
         pz = z.data_ptr()
     _LINEAR_WS = _LINEAR_WS or lib().moe_linear_workspace_size()
     ws = _workspace(workspace, dev, _LINEAR_WS)
-    _call(_LINEAR, dev, stream, x.data_ptr(), ld_x, w.data_ptr(), ld_w, pb, bdt, _act(activation), pr, ld_r, T, K, N,
+    _call(_LINEAR, dev, x.data_ptr(), ld_x, w.data_ptr(), ld_w, pb, bdt, _act(activation), pr, ld_r, T, K, N,
           out.data_ptr(), dt, ld_o, pz, ws.data_ptr(), ws.numel())
     return (out, z) if preact else out
 
@@ -670,6 +731,8 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
     preact: what linear(..., preact=True) returned, with an activation; bias:
     as passed to linear (None: dbias is None).  need_x / need_w = False leave
     that gradient out (None).  workspace: as in linear."""
+    if stream is not None:
+        return _on_stream(linear_backward, locals())
     dev, xs = _matrix_of("x", x)
     T, K = xs
     ld_x = _mat("x", x, _ONLY_BF16, xs, dev)
@@ -695,7 +758,7 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
         dw = torch.empty((N, K), dtype=_BF16, device=x.device)
         pdw = dw.data_ptr()
     ws = _workspace(workspace, dev, (_LIB or lib()).moe_linear_backward_workspace_size(T, N))
-    _call(_LINEAR_BWD, dev, stream, grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(),
+    _call(_LINEAR_BWD, dev, grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(),
           ld_w, act, pz, ld_z, T, K, N, pdx, pdw, pdb, ws.data_ptr(), ws.numel())
     return dx, dw, db
 
@@ -704,6 +767,8 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
 def quantize_fp8_blocks(w: torch.Tensor, scale_fmt: str = "f32", stream=None):
     """bf16 [..., R, C] -> (e4m3 codes uint8 [..., R, C], scales [..., R/128, C/128]
     as fp32 ('f32') or uint8 exponent bytes ('ue8m0'))."""
+    if stream is not None:
+        return _on_stream(quantize_fp8_blocks, locals())
     _need_cuda(w)
     if w.dtype != torch.bfloat16:
         raise ValueError("w must be bf16")
@@ -717,7 +782,7 @@ def quantize_fp8_blocks(w: torch.Tensor, scale_fmt: str = "f32", stream=None):
     s = torch.empty(*lead, R // 128 if R % 128 == 0 else 0, C // 128 if C % 128 == 0 else 0,
                     dtype=sdt, device=w.device)
     _check(lib().moe_quantize_fp8_blocks(_ptr(w), nmat, R, C, sf, _ptr(q), _ptr(s),
-                                         _stream(stream)))
+                                         _stream()))
     return q, s
 
 
@@ -725,6 +790,8 @@ def quantize_fp4_blocks(w: torch.Tensor, stream=None):
     """bf16 [..., R, C] -> (packed e2m1 codes uint8 [..., R, C/2], two per
     byte with the even element in the low nibble; UE8M0 exponent bytes
     uint8 [..., R, C/32], one per 1x32 block)."""
+    if stream is not None:
+        return _on_stream(quantize_fp4_blocks, locals())
     _need_cuda(w)
     if w.dtype != torch.bfloat16:
         raise ValueError("w must be bf16")
@@ -734,7 +801,7 @@ def quantize_fp4_blocks(w: torch.Tensor, stream=None):
         nmat *= d
     q = torch.empty(*lead, R, C // 2, dtype=torch.uint8, device=w.device)
     s = torch.empty(*lead, R, C // 32, dtype=torch.uint8, device=w.device)
-    _check(lib().moe_quantize_fp4_blocks(_ptr(w), nmat, R, C, _ptr(q), _ptr(s), _stream(stream)))
+    _check(lib().moe_quantize_fp4_blocks(_ptr(w), nmat, R, C, _ptr(q), _ptr(s), _stream()))
     return q, s
 
 
@@ -858,6 +925,8 @@ def launch_count() -> int:
 def selftest_wait_timeout(limit_us: int = 2000, stream=None) -> int:
     """Run the bounded-wait self-test; returns the status that
     moe_workspace_status reports afterwards (expected MOE_ERR_TIMEOUT)."""
+    if stream is not None:
+        return _on_stream(selftest_wait_timeout, locals())
     ws = torch.zeros(1024, dtype=torch.uint8, device="cuda")
-    _check(lib().moe_selftest_wait_timeout(_ptr(ws), ws.numel(), int(limit_us), _stream(stream)))
-    return int(lib().moe_workspace_status(_ptr(ws), _stream(stream)))
+    _check(lib().moe_selftest_wait_timeout(_ptr(ws), ws.numel(), int(limit_us), _stream()))
+    return int(lib().moe_workspace_status(_ptr(ws), _stream()))

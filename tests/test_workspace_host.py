@@ -13,6 +13,7 @@ def stream(monkeypatch):
     """Whether the current stream is being captured, as the test sets it."""
     state = dict(capturing=False)
     monkeypatch.setattr(moe, "_capturing", lambda: state["capturing"], raising=False)
+    monkeypatch.setattr(moe, "_stream", lambda stream=None: 0)
     return state
 
 
@@ -94,3 +95,56 @@ def test_default_workspaces_per_stream(stream, monkeypatch):
     stream["capturing"] = False
     now["handle"] = 99
     assert moe._default_ws(0) not in made.values()
+
+
+def test_calls_on_a_stream(monkeypatch):
+    """stream= makes it the current one for the whole call, and both streams are recorded."""
+    log = []
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+        def __init__(self, name):
+            self.name = name
+
+    class Under:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            log.append(("enter", self.s.name))
+
+        def __exit__(self, *exc):
+            log.append(("leave", self.s.name))
+
+    class Fake(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cuda", 0)
+
+        def record_stream(self, s):
+            log.append((self.label, s.name))
+
+    def tensor(label):
+        t = torch.zeros(2).as_subclass(Fake)
+        t.label = label
+        return t
+
+    main, side = Stream("main"), Stream("side")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: main)
+    monkeypatch.setattr(torch.cuda, "stream", Under)
+    result = (tensor("y"), None)
+
+    def call(x, k, *, out=None, bias=None):
+        log.append(("call", k))
+        return result
+
+    args = dict(x=tensor("x"), k=3, out=(tensor("o"), None), bias=None, stream=side)
+    assert moe._on_stream(call, args) is result
+    assert log == [("enter", "side"), ("call", 3), ("leave", "side"), ("x", "side"), ("o", "side"), ("y", "main")]
+    log.clear()
+    moe._on_stream(call, dict(x=tensor("x"), k=4, stream=main))         # the current one: nothing to record
+    assert log == [("enter", "main"), ("call", 4), ("leave", "main")]
+    other = Stream("other")
+    other.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError):
+        moe._on_stream(call, dict(x=tensor("x"), k=4, stream=other))
