@@ -106,17 +106,16 @@ struct Cols {
   }
 };
 
-// Sums of N values over the TX threads of one row (TX a multiple of 32; the
-// block's other rows take part in the barriers).  Every thread gets the
+// Sums of N values over a block of whole warps.  Every thread gets the
 // same bits: the warps' sums are added in warp order.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* s_red, int warps, int row_warp0) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float* s_red, int warps) {
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v[n] += __shfl_xor_sync(0xffffffffu, v[n], off);
   if (warps == 1) return;
-  const int warp = (threadIdx.x + threadIdx.y * blockDim.x) >> 5;
+  const int warp = threadIdx.x >> 5;
   __syncthreads();  // the previous sums have been read
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
@@ -127,13 +126,13 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* s_red, int warps,
   for (int n = 0; n < N; ++n) v[n] = 0.f;
   for (int w = 0; w < warps; ++w)
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] += s_red[(row_warp0 + w) * N + n];
+    for (int n = 0; n < N; ++n) v[n] += s_red[w * N + n];
 }
 
 constexpr int kMaxRed = 32 * 4;  // warps of a block x values of a reduction
 
 // Forward, the rows that the streamed kernels below do not take (above 8192
-// columns): a row per group of TX threads, held in registers.  4778 x 12288 bf16
+// columns): a row per block, held in registers.  4778 x 12288 bf16
 // with both norms and a gate per channel 152 us (3.1 TB/s), bound by the
 // latency of its three dependent trips with one row per block in flight.
 template <typename RT, bool VEC, int NV>
@@ -141,12 +140,10 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
   pdl_launch_dependents();
   __shared__ float s_red[kMaxRed];
   const Cols<VEC, NV> c{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.H};
-  const int warps = blockDim.x >> 5, warp0 = threadIdx.y * warps;
+  const int warps = blockDim.x >> 5;
   const float inv_h = 1.f / static_cast<float>(a.H);
   pdl_wait();
-  const long t_raw = static_cast<long>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const bool on = t_raw < a.T;  // a row past the end still meets the barriers
-  const long t = on ? t_raw : a.T - 1;
+  const long t = blockIdx.x;
   const RT* r_in = static_cast<const RT*>(a.residual) + t * a.ld_res;
   const __nv_bfloat16* y_in =
       a.y ? static_cast<const __nv_bfloat16*>(a.y) + t * a.ld_y : nullptr;
@@ -168,7 +165,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[0] += y[v][e] * y[v][e];
-      row_sums<1>(sum, s_red, warps, warp0);
+      row_sums<1>(sum, s_red, warps);
       rstd = rsqrtf(sum[0] * inv_h + a.eps);
     }
     coef *= rstd;
@@ -191,7 +188,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) r[v][e] += coef * y[v][e];
-      if (on) c.store(static_cast<RT*>(a.residual_out) + t * a.H, v, r[v]);
+      c.store(static_cast<RT*>(a.residual_out) + t * a.H, v, r[v]);
     }
   }
   if (a.pre_norm) {
@@ -200,7 +197,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[0] += r[v][e] * r[v][e];
-    row_sums<1>(sum, s_red, warps, warp0);
+    row_sums<1>(sum, s_red, warps);
     const float rstd = rsqrtf(sum[0] * inv_h + a.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -212,7 +209,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[v][e] *= m[e];
       }
-      if (on) c.store(static_cast<__nv_bfloat16*>(a.normed) + t * a.H, v, r[v]);
+      c.store(static_cast<__nv_bfloat16*>(a.normed) + t * a.H, v, r[v]);
     }
   }
 }
@@ -221,8 +218,9 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
 // each thread keeps the sums over its rows for its own columns (dw_pre,
 // dw_post and a per-channel dg) and leaves them as one partial row per
 // block; block_norm_partials_kernel adds those in block order, so the
-// result does not depend on timing.  For rows above 8192 columns, and rows of fp32
-// with an fp32 gate per element whose ring would not fit.  4778 x 12288 bf16 with
+// result does not depend on timing.  For rows above 8192 columns, and rows of
+// 2049 columns or more whose ring of two stages would not fit: fp32 streams with
+// both gradients and a gate per element, of either type.  4778 x 12288 bf16 with
 // both norms and a gate per channel 652 us (1.1 TB/s): a column's sums and values
 // take more registers than its threads have.
 template <typename RT, bool VEC, int NV>
@@ -260,7 +258,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
           sum[1] += q[v][e] * r[v][e] * (a.pre_weight != nullptr ? m[e] : 1.f);
         }
       }
-      row_sums<2>(sum, s_red, warps, 0);
+      row_sums<2>(sum, s_red, warps);
       const float rstd = rsqrtf(sum[0] * inv_h + a.eps);
       const float corr = sum[1] * inv_h * rstd * rstd * rstd;
 #pragma unroll
@@ -308,7 +306,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNor
       }
     }
     float rstd = 1.f;
-    if (a.post_norm || a.gate_kind == MOE_GATE_TOKEN) row_sums<3>(sum, s_red, warps, 0);
+    if (a.post_norm || a.gate_kind == MOE_GATE_TOKEN) row_sums<3>(sum, s_red, warps);
     if (a.post_norm) rstd = rsqrtf(sum[0] * inv_h + a.eps);
     if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) {
       const float dg = a.scale * rstd * sum[2];
@@ -1179,14 +1177,9 @@ template <typename RT, bool VEC>
 cudaError_t fwd(const BlockNormArgs& a, int num_sms, cudaStream_t s) {
   if (a.H <= 8192)
     return a.H <= 2048 ? fwd_nv<RT, 1, VEC>(a, num_sms, s) : fwd_nv<RT, 2, VEC>(a, num_sms, s);
-  // one piece of 8 columns per thread up to 8192 columns, two above
-  const int pieces = ceil_div(a.H, 8);
-  const int nv = pieces <= 1024 ? 1 : 2;
-  const int tx = ceil_div(ceil_div(pieces, nv), 32) * 32;
-  const int ty = tx >= 256 ? 1 : 256 / tx;
-  const dim3 grid(ceil_div(a.T, ty)), block(tx, ty);
-  return nv == 1 ? launch_pdl(block_norm_kernel<RT, VEC, 1>, grid, block, 0, s, a)
-                 : launch_pdl(block_norm_kernel<RT, VEC, 2>, grid, block, 0, s, a);
+  // two pieces of 8 columns per thread
+  const dim3 block(ceil_div(ceil_div(a.H, 8), 64) * 32);
+  return launch_pdl(block_norm_kernel<RT, VEC, 2>, dim3(a.T), block, 0, s, a);
 }
 
 template <typename RT, bool VEC>
@@ -1195,7 +1188,11 @@ cudaError_t bwd(const BlockNormBwdArgs& a, int num_sms, int* blocks_used, cudaSt
     const int pr = static_cast<int>(sizeof(RT) / 2);
     const int pv = (a.grad_normed ? pr + 1 : 0) + (a.grad_res ? pr : 0) + (a.y != nullptr) +
                    (a.gate_kind == MOE_GATE_ELEMENT ? (a.gate_bf16 ? 1 : 2) : 0);
-    // two stages fit: every case but wide rows with fp32 streams and fp32 element gates
+    // two stages fit: every case up to 2048 columns; above, all but fp32 streams with both
+    // gradients and a gate per element: 7 or 8 pieces, 224 or 256 KB, as a stage is laid out
+    // for 512 threads whatever the block has.  Rows that are not whole vectors take what
+    // they need, and of the same calls only those of 2049 to 2560, 3585 to 4096 and 7169 to
+    // 8192 columns (fp32 gates: from 3073 and from 6145) do not fit.
     const int nv = a.H <= 2048 ? 1 : 2;
     const size_t stage =
         VEC ? stage_bytes(pv, nv)

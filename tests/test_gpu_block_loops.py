@@ -231,3 +231,19 @@ def test_many_slots_in_groups(moe, T, E, k, ng, tg, gt, score):
     assert sure.sum() >= T // 2
     assert np.array_equal(idx.cpu().numpy()[sure], ridx[sure])
     _close(w[torch.from_numpy(sure).cuda()], rw[sure], np.abs(rw[sure]), False)
+
+
+# ------------------------------------------------------------------ wide rows
+# a row per block forward; backward two or three rows per block, whole vectors and not
+@pytest.mark.parametrize("T,H", [(700, 9000), (650, 8193), (340, 12289), (310, 16383), (310, 16384)])
+@pytest.mark.parametrize("stream", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gate", ["channel", "token", "element32"])
+def test_block_norm_of_wide_rows(moe, T, H, stream, gate):
+    test_block_norm_over_many_steps(moe, T, H, stream, gate, True, True)
+
+
+# fp32 streams with a gate per element above 2048 columns: rows that have no ring in the backward pass
+@pytest.mark.parametrize("T,H", [(700, 2049), (700, 4096), (650, 4099), (320, 7168), (320, 8191)])
+@pytest.mark.parametrize("gate", ["element", "element32"])
+def test_block_norm_of_fp32_streams_with_element_gates(moe, T, H, gate):
+    test_block_norm_over_many_steps(moe, T, H, torch.float32, gate, True, True)
