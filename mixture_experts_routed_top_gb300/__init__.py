@@ -235,8 +235,9 @@ def workspace_size(T: int, H: int, I: int, E: int, k: int, wdtype: int = W_BF16)
 
 
 def _capturing() -> bool:
-    """Whether the current stream is being captured (the default stream cannot be)."""
-    return _stream() != 0 and torch.cuda.is_current_stream_capturing()
+    """Whether the current stream is being captured; the default stream (handle 0) cannot be
+    and is not asked."""
+    return torch.cuda.is_current_stream_capturing()
 
 
 class Workspace:
@@ -260,10 +261,13 @@ class Workspace:
         own = [] if self.buf is None or any(b is self.buf for b in self.captured) else [self.buf]
         return own + self.captured
 
-    def get(self, nbytes: int) -> torch.Tensor:
-        if _capturing():
+    def get(self, nbytes: int, now: Optional[int] = None) -> torch.Tensor:
+        """A buffer of at least nbytes for a call on the current stream (its handle: now)."""
+        if now is None:
+            now = _stream()
+        old = self.buf
+        if now and _capturing():
             return self._for_graph(nbytes)
-        old, now = self.buf, _stream()
         if self.home != now and old is not None:
             old.record_stream(torch.cuda.current_stream(self.device))
         if old is None or old.numel() < nbytes:
@@ -295,7 +299,7 @@ def _default_ws(dev: int) -> Workspace:
     ws = _DEFAULT_WS.get(key)
     if ws is not None:
         return ws
-    if _capturing():
+    if key[1] and _capturing():
         # a stream that only captures has none; the calls were tried on another one, and what
         # was allocated now would be zeroed, error word and all, in every replay
         for (d, _), other in list(_DEFAULT_WS.items()):
@@ -347,9 +351,7 @@ def experts_forward(hidden: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=hidden.device)
     nbytes = workspace_size(T, H, I, E, k, wdtype)
-    if workspace is None:
-        workspace = _default_ws(hidden.get_device())
-    ws = workspace.get(nbytes)
+    ws = _workspace(workspace, hidden.get_device(), nbytes)
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
     _check(lib().moe_experts_forward_act(
@@ -460,7 +462,10 @@ def _call(call, dev: int, *args):
 
 
 def _workspace(workspace: Optional[Workspace], dev: int, nbytes: int) -> torch.Tensor:
-    return (_default_ws(dev) if workspace is None else workspace).get(nbytes)
+    now = _raw_stream(dev)
+    if workspace is None:
+        workspace = _DEFAULT_WS.get((dev, now)) or _default_ws(dev)
+    return workspace.get(nbytes, now)
 
 
 def _matrix_of(name: str, t: torch.Tensor):

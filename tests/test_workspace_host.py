@@ -13,7 +13,7 @@ def stream(monkeypatch):
     """Whether the current stream is being captured, as the test sets it."""
     state = dict(capturing=False)
     monkeypatch.setattr(moe, "_capturing", lambda: state["capturing"], raising=False)
-    monkeypatch.setattr(moe, "_stream", lambda stream=None: 0)
+    monkeypatch.setattr(moe, "_stream", lambda stream=None: 7)
     return state
 
 
@@ -82,7 +82,7 @@ def test_default_workspaces_per_stream(stream, monkeypatch):
     monkeypatch.setattr(moe, "_DEFAULT_WS", {})
     monkeypatch.setattr(moe, "_raw_stream", lambda dev: now["handle"])
     made = {}
-    for dev, handle in ((0, 0), (0, 11), (1, 0)):
+    for dev, handle in ((0, 0), (0, 11), (1, 0)):     # handle 0: the default stream
         now["handle"] = handle
         made[dev, handle] = moe._default_ws(dev)
         assert moe._default_ws(dev) is made[dev, handle]
