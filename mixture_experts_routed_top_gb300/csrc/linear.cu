@@ -1324,9 +1324,11 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
 // in order by linear_colsum_kernel.
 // One exponential per slope, with the fast exponential and division: at most
 // a few units of 2^-22, far below the rounding of dz (2^-9 on average) and
-// averaged out in the sums.  With the accurate forms the kernel spent 57
-// instructions per element and took 40 us for 8191 x 2048, three times what
-// its loads and stores need; now 21 (100 MB, 4.8 TB/s), bound by issue.
+// averaged out in the sums.  With the accurate forms the kernel took 40 us for
+// 8191 x 2048 with silu, three times what its loads and stores need; now 22
+// (100 MB, 4.6 TB/s, 19 instructions an element).
+// SPLIT, the second part of few dz, is a constant of the code: as a test in the
+// loop that large gradients run it cost 15 registers and 12 us.
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == MOE_ACT_SILU) {  // s (1 + z (1 - s)), 1 - s = e^-z s; below -80 (-1.4e-33) as at -80
@@ -1340,7 +1342,7 @@ __device__ __forceinline__ float act_slope(float z) {
   return z > 0.f ? 1.f : 0.f;
 }
 
-template <int ACT, bool F32>
+template <int ACT, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzArgs a) {
   pdl_launch_dependents();
   __shared__ float s_sum[8][256];
@@ -1357,7 +1359,7 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzArgs a) {
       sum[j] += d[j];
     }
     if (a.dz != nullptr) st8(a.dz, t * a.ld_dz + n, false, d);  // rows padded to 8: always whole
-    if (a.dz_lo != nullptr) {
+    if (SPLIT) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // nothing is left of one that bf16 has no finite value for
         const float hi = __bfloat162float(__float2bfloat16_rn(d[j]));
@@ -1557,6 +1559,16 @@ cudaError_t launch_vector(const LinearStreamArgs& a, int num_sms, cudaStream_t s
   return launch_vector_w<8>(a, s);
 }
 
+template <int ACT>
+cudaError_t launch_dz(const LinearDzArgs& a, dim3 grid, cudaStream_t s) {
+  const dim3 block(256);
+  if (a.dz_lo != nullptr)
+    return a.f32 ? launch_pdl(linear_dz_kernel<ACT, true, true>, grid, block, 0, s, a)
+                 : launch_pdl(linear_dz_kernel<ACT, false, true>, grid, block, 0, s, a);
+  return a.f32 ? launch_pdl(linear_dz_kernel<ACT, true, false>, grid, block, 0, s, a)
+               : launch_pdl(linear_dz_kernel<ACT, false, false>, grid, block, 0, s, a);
+}
+
 template <int NT>
 cudaError_t launch_stream(LinearStreamArgs a, int num_sms, cudaStream_t s) {
   // warps of a block per tile, then blocks: until every SM has WANT warps, as
@@ -1681,20 +1693,12 @@ int linear_dz_slices(long T, long N, int num_sms) {
 }
 
 cudaError_t launch_linear_dz(const LinearDzArgs& a, int slices, float* dbias, cudaStream_t s) {
-  const dim3 grid(ceil_div(a.N, 256), slices), block(256);
+  const dim3 grid(ceil_div(a.N, 256), slices);
   cudaError_t e;
-  auto go = [&](auto kern_f32, auto kern_bf16) {
-    return a.f32 ? launch_pdl(kern_f32, grid, block, 0, s, a)
-                 : launch_pdl(kern_bf16, grid, block, 0, s, a);
-  };
-  if (a.act == MOE_ACT_SILU)
-    e = go(linear_dz_kernel<MOE_ACT_SILU, true>, linear_dz_kernel<MOE_ACT_SILU, false>);
-  else if (a.act == MOE_ACT_GELU)
-    e = go(linear_dz_kernel<MOE_ACT_GELU, true>, linear_dz_kernel<MOE_ACT_GELU, false>);
-  else if (a.act == MOE_ACT_RELU)
-    e = go(linear_dz_kernel<MOE_ACT_RELU, true>, linear_dz_kernel<MOE_ACT_RELU, false>);
-  else
-    e = go(linear_dz_kernel<MOE_ACT_NONE, true>, linear_dz_kernel<MOE_ACT_NONE, false>);
+  if (a.act == MOE_ACT_SILU) e = launch_dz<MOE_ACT_SILU>(a, grid, s);
+  else if (a.act == MOE_ACT_GELU) e = launch_dz<MOE_ACT_GELU>(a, grid, s);
+  else if (a.act == MOE_ACT_RELU) e = launch_dz<MOE_ACT_RELU>(a, grid, s);
+  else e = launch_dz<MOE_ACT_NONE>(a, grid, s);
   count_launches(1);
   if (e != cudaSuccess) return e;
   if (dbias != nullptr && slices > 1) {  // one slice has written dbias itself
