@@ -172,7 +172,7 @@ moe_status moe_experts_forward(const void* hidden, int T, int H,
  * relu map to SwiGLU, GeGLU and ReGLU): h = act(gate x) * (up x).
  *   MOE_ACT_SILU  silu(x) = x / (1 + e^-x)            (SwiGLU)
  *   MOE_ACT_GELU  exact GELU x/2 (1 + erf(x / sqrt 2)) (GeGLU)
- *   MOE_ACT_RELU  max(x, 0)                            (ReGLU)
+ *   MOE_ACT_RELU  max(x, 0), NaN for NaN               (ReGLU)
  */
 typedef enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1, MOE_ACT_RELU = 2 } moe_activation;
 

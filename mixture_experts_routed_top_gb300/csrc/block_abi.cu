@@ -152,9 +152,12 @@ struct LinearWs {
 };
 // dz is rounded to bf16 for the products of the gradient.  Over many dz that adds
 // to the error of a gradient what its own rounding to bf16 does, 1.41 times in
-// all; of a few dz the roundings do not average out (T = 1, N = 24: 1.53 times),
-// and the products are small.  So up to this many dz the rest of the rounding is
-// kept too and multiplied first, and the gradients are as those of an fp32 dz.
+// all.  Of a few dz the roundings do not average out: the squares of n rounding
+// errors, of normal gradients times silu's slope, have a mean that varies by 3.4
+// / sqrt(n) of itself, so 24 dz leave 1.35 times in the median of draws and 2.1
+// in one of a hundred, 256 dz 1.6 and 1024 dz 1.5.  So up to this many dz the rest
+// of the rounding is kept too and multiplied first, in two more small products,
+// and the gradients are as those of an fp32 dz; beyond, 1.41 within 7 %.
 constexpr int64_t kLinearDzSplit = 1024;
 LinearWs linear_ws(int T, int N) {
   LinearWs w;

@@ -133,8 +133,9 @@ constexpr int kMaxRed = 32 * 4;  // warps of a block x values of a reduction
 
 // Forward, the rows that the streamed kernels below do not take (above 8192
 // columns): a row per block, held in registers.  4778 x 12288 bf16
-// with both norms and a gate per channel 152 us (3.1 TB/s), bound by the
-// latency of its three dependent trips with one row per block in flight.
+// with both norms and a gate per channel 142 us (3.3 TB/s), bound by the
+// latency of its three dependent trips with one row per block in flight; 12289
+// columns, in single elements and with 250 bytes of spills a thread, 334.
 template <typename RT, bool VEC, int NV>
 __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a) {
   pdl_launch_dependents();
@@ -221,8 +222,10 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(const BlockNormArgs a)
 // result does not depend on timing.  For rows above 8192 columns, and rows of
 // 2049 columns or more whose ring of two stages would not fit: fp32 streams with
 // both gradients and a gate per element, of either type.  4778 x 12288 bf16 with
-// both norms and a gate per channel 652 us (1.1 TB/s): a column's sums and values
-// take more registers than its threads have.
+// both norms and a gate per channel 537 us (1.3 TB/s): a column's sums and values
+// take more registers than its threads have (1 KB of spills a thread; 4.5 KB where
+// rows are not whole vectors, 1945 us at 12289 columns).  An fp32 stream with a
+// gate per element 134 us at 4096 x 4096, 229 at 4096 x 7168 (2.8 TB/s).
 template <typename RT, bool VEC, int NV>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const BlockNormBwdArgs a) {
   pdl_launch_dependents();
@@ -622,9 +625,10 @@ constexpr int ring_blocks(int nv) { return nv == 1 ? 2 : 1; }
 // MID: a call between two blocks (y given, norm before the next block, no
 // gate per element), whose options are then constants of the code.
 // 8192 x 7168 bf16 with both norms and a gate per channel: 80 us (470 MB, 5.9
-// TB/s, 86 % of a copy), bound by memory; 4099 x 2048 with an fp32 stream 18.5
-// (101 MB, 5.4 TB/s); one token 3.7, three dependent trips (row, two sums).
-// EDGE: 8192 x 7167 139 us (3.4 TB/s), bound by issue; a row per block without a
+// TB/s, 86 % of a copy), bound by memory; 4099 x 2048 with an fp32 stream 22 (101
+// MB, 4.6 TB/s: a block walks over seven steps of two rows that share its barriers,
+// so filling and draining the ring counts); one token 3.7, three dependent trips
+// (row, two sums).  EDGE: 8192 x 7167 137 us (3.4 TB/s), bound by issue; a row per block without a
 // ring 309.
 template <typename RT, int NV, int STAGES, bool MID, bool EDGE>
 __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV))
@@ -791,7 +795,7 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV))
 // MID: both gradients and y given, no gate per element.
 // 8192 x 7168 bf16 with both norms and a gate per channel: 117 us and 7 for the
 // partial rows' sums (705 MB, 5.7 TB/s over both, 84 % of a copy), bound by
-// memory and nearly as much by issue.  EDGE: 8192 x 7167 255 us (2.8 TB/s), by
+// memory and nearly as much by issue.  EDGE: 8192 x 7167 246 us (2.9 TB/s), by
 // issue; without a ring 1684.
 template <typename RT, int NV, int STAGES, bool MID, bool EDGE>
 __global__ void __launch_bounds__(kRingThreads, 1)
