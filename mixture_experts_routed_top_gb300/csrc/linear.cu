@@ -1564,9 +1564,12 @@ cudaError_t launch_vector(const LinearStreamArgs& a, int num_sms, cudaStream_t s
 template <int ACT>
 cudaError_t launch_dz(const LinearDzArgs& a, dim3 grid, cudaStream_t s) {
   const dim3 block(256);
-  if (a.dz_lo != nullptr)
-    return a.f32 ? launch_pdl(linear_dz_kernel<ACT, true, true>, grid, block, 0, s, a)
-                 : launch_pdl(linear_dz_kernel<ACT, false, true>, grid, block, 0, s, a);
+  if (a.dz_lo != nullptr) {
+    if (a.f32) return launch_pdl(linear_dz_kernel<ACT, true, true>, grid, block, 0, s, a);
+    if constexpr (ACT == MOE_ACT_SILU || ACT == MOE_ACT_GELU)
+      return launch_pdl(linear_dz_kernel<ACT, false, true>, grid, block, 0, s, a);
+    return cudaErrorInvalidValue;  // bf16 gradients times 0 or 1 have no second part
+  }
   return a.f32 ? launch_pdl(linear_dz_kernel<ACT, true, false>, grid, block, 0, s, a)
                : launch_pdl(linear_dz_kernel<ACT, false, false>, grid, block, 0, s, a);
 }
