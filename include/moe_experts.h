@@ -591,11 +591,52 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
                                void* dw, float* dbias, void* ws, size_t ws_bytes, void* stream);
 
 /*
- * moe_call_packed - one of the six calls above with its arguments in a block of
+ * moe_gated_linear - both projections of a gated feed-forward, the activation and
+ * the product in one kernel: with z = x w^T + bias, out = act(z[:, :I]) * z[:, I:].
+ *   x         device bf16 [T, K];  w  device bf16 [2 I, K]: I gate rows, then I up
+ *             rows (an expert's w_gate_up)
+ *   bias      device [2 I] bf16 or fp32 (bias_dt), or NULL
+ *   act       a moe_activation, of the gate half
+ *   out       device bf16 [T, I], rows ld_out apart, rounded once from fp32
+ *   preact    device bf16 [T, 2 I], rows 2 I apart, or NULL: out, z rounded once
+ *             (what the backward pass needs; out is made from the unrounded z)
+ *   ws        device scratch, 256-byte aligned, at least
+ *             moe_linear_workspace_size() bytes; head as in moe_linear
+ * K % 8 == 0 and strides of x and w multiples of 8, else MOE_ERR_UNSUPPORTED; any
+ * T, any I < 2^30.  T = 0 or I = 0 is a no-op.
+ */
+moe_status moe_gated_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w,
+                            const void* bias, moe_dtype bias_dt, int act, int T, int K, int I,
+                            void* out, int64_t ld_out, void* preact, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/*
+ * moe_gated_linear_backward - gradients of moe_gated_linear.  With zg, zu the halves
+ * of z, dz = (grad_h * zu * act'(zg), grad_h * act(zg)): dx = dz w, dw = dz^T x,
+ * dbias = sum over tokens of dz.  dz enters the two products rounded to bf16 (up to
+ * 1024 of them, T * 2 I, as the sum of two), and dbias unrounded.
+ *   grad_h   device bf16 [T, I];  preact  device bf16 [T, 2 I], as the forward
+ *            stored it, rows ld_z apart
+ *   dx       out, bf16 [T, K], rows K apart, or NULL
+ *   dw       out, bf16 [2 I, K], rows K apart, or NULL
+ *   dbias    out, fp32 [2 I], or NULL
+ *   ws       at least moe_gated_linear_backward_workspace_size() bytes, 256-byte
+ *            aligned, head as above
+ * The same requirements as moe_gated_linear.  T = 0 writes zeros to dw and dbias.
+ */
+size_t moe_gated_linear_backward_workspace_size(int T, int I);
+moe_status moe_gated_linear_backward(const void* grad_h, int64_t ld_gh, const void* x, int64_t ld_x,
+                                     const void* w, int64_t ld_w, int act, const void* preact,
+                                     int64_t ld_z, int T, int K, int I, void* dx, void* dw,
+                                     float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_call_packed - one of the calls above with its arguments in a block of
  * 8-byte slots in the function's order: pointers and integers as int64_t,
  * floats as double.  For bindings that pay per argument.
  *   call   0 moe_route_scored, 1 moe_route_scored_backward, 2 moe_block_norm,
- *          3 moe_block_norm_backward, 4 moe_linear, 5 moe_linear_backward;
+ *          3 moe_block_norm_backward, 4 moe_linear, 5 moe_linear_backward,
+ *          7 moe_gated_linear, 8 moe_gated_linear_backward;
  *          any other: MOE_ERR_INVALID_ARG
  *   block  the slots; a size that no int holds: MOE_ERR_UNSUPPORTED
  */

@@ -26,6 +26,7 @@ __all__ = [
     "get_decode_single", "set_tile_group", "get_tile_group", "set_pair_gemm", "get_pair_gemm", "set_down_l2_hints", "get_down_l2_hints", "set_down_phases",
     "get_down_phases",
     "route_scored", "route_scored_backward", "block_norm", "block_norm_backward", "linear", "linear_backward",
+    "gated_linear", "gated_linear_backward",
     "Workspace", "STATUS", "STAGES", "W_BF16", "W_FP8_E4M3", "W_FP4_E2M1", "SCALE_NONE", "SCALE_F32",
     "SCALE_UE8M0", "ACTIVATIONS",
 ]
@@ -97,6 +98,10 @@ _SIGS = {
     "moe_linear_workspace_size": ([], _SZ),
     "moe_linear": ([_P, _L, _P, _L, _P, _I, _I, _P, _L, _I, _I, _I, _P, _I, _L, _P, _P, _SZ, _P], _I),
     "moe_linear_backward_workspace_size": ([_I, _I], _SZ),
+    "moe_gated_linear": ([_P, _L, _P, _L, _P, _I, _I, _I, _I, _I, _P, _L, _P, _P, _SZ, _P], _I),
+    "moe_gated_linear_backward_workspace_size": ([_I, _I], _SZ),
+    "moe_gated_linear_backward": ([_P, _L, _P, _L, _P, _L, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _SZ,
+                                   _P], _I),
     "moe_linear_backward": ([_P, _I, _L, _P, _L, _P, _L, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _SZ,
                              _P], _I),
 }
@@ -422,6 +427,8 @@ _NORM = (2, struct.Struct("=9qd5qd5q").pack)
 _NORM_BWD = (3, struct.Struct("=13qd4qd10q").pack)
 _LINEAR = (4, struct.Struct("=19q").pack)
 _LINEAR_BWD = (5, struct.Struct("=19q").pack)
+_GATED = (7, struct.Struct("=16q").pack)
+_GATED_BWD = (8, struct.Struct("=18q").pack)
 
 
 def _bad(name: str, what: str):
@@ -765,6 +772,93 @@ def linear_backward(grad_y: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *,
     ws = _workspace(workspace, dev, (_LIB or lib()).moe_linear_backward_workspace_size(T, N))
     _call(_LINEAR_BWD, dev, grad_y.data_ptr(), _DT[grad_y.dtype], ld_g, x.data_ptr(), ld_x, w.data_ptr(),
           ld_w, act, pz, ld_z, T, K, N, pdx, pdw, pdb, ws.data_ptr(), ws.numel())
+    return dx, dw, db
+
+
+def _gate_act(activation: str) -> int:
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[activation]
+
+
+def _halves(w: torch.Tensor) -> int:
+    """-> the rows of each half of gate and up weights."""
+    if w.dim() != 2 or w.shape[0] % 2:
+        _bad("w", "[2 I, K]: gate rows, then as many up rows")
+    return w.shape[0] // 2
+
+
+def gated_linear(x: torch.Tensor, w: torch.Tensor, *, bias: Optional[torch.Tensor] = None,
+                 activation: str = "silu", preact: bool = False, out: Optional[torch.Tensor] = None,
+                 workspace: Optional[Workspace] = None, stream=None):
+    """act(z[:, :I]) * z[:, I:] with z = x w^T + bias -> bf16 [T,I], or (that, z) if preact.
+
+    Both projections of a gated feed-forward, its activation and product in one
+    kernel.  x bf16 [T,K]; w bf16 [2I,K]: I gate rows, then I up rows (an
+    expert's w_gate_up); K a multiple of 8; bias [2I] bf16 or fp32; activation
+    'silu', 'gelu' (exact) or 'relu'; z bf16 [T,2I], for the backward pass.
+    out: the tensor to write into (rows contiguous).  workspace: as in linear."""
+    global _LINEAR_WS
+    if stream is not None:
+        return _on_stream(gated_linear, locals())
+    dev, xs = _matrix_of("x", x)
+    T, K = xs
+    ld_x = _mat("x", x, _ONLY_BF16, xs, dev)
+    I = _halves(w)
+    ld_w = _mat("w", w, _ONLY_BF16, (2 * I, K), dev)
+    act = _gate_act(activation)
+    pb = bdt = pz = 0
+    z = None
+    if bias is not None:
+        pb, bdt = _dense("bias", bias, _DT, (2 * I,), dev), _DT[bias.dtype]
+    if out is None:
+        out = torch.empty((T, I), dtype=_BF16, device=x.device)
+        ld_o = I
+    else:
+        ld_o = _mat("out", out, _ONLY_BF16, (T, I), dev)
+    if preact:
+        z = torch.empty((T, 2 * I), dtype=_BF16, device=x.device)
+        pz = z.data_ptr()
+    _LINEAR_WS = _LINEAR_WS or lib().moe_linear_workspace_size()
+    ws = _workspace(workspace, dev, _LINEAR_WS)
+    _call(_GATED, dev, x.data_ptr(), ld_x, w.data_ptr(), ld_w, pb, bdt, act, T, K, I, out.data_ptr(), ld_o, pz,
+          ws.data_ptr(), ws.numel())
+    return (out, z) if preact else out
+
+
+def gated_linear_backward(grad_h: torch.Tensor, x: torch.Tensor, w: torch.Tensor, preact: torch.Tensor, *,
+                          bias: Optional[torch.Tensor] = None, activation: str = "silu", need_x: bool = True,
+                          need_w: bool = True, workspace: Optional[Workspace] = None, stream=None):
+    """Gradients of gated_linear -> (dx bf16 [T,K], dw bf16 [2I,K], dbias fp32 [2I]).
+
+    grad_h bf16 [T,I]; preact: the z that gated_linear(..., preact=True)
+    returned; bias: as passed to gated_linear (None: dbias is None).  need_x /
+    need_w = False leave that gradient out (None).  workspace: as in linear."""
+    if stream is not None:
+        return _on_stream(gated_linear_backward, locals())
+    dev, xs = _matrix_of("x", x)
+    T, K = xs
+    ld_x = _mat("x", x, _ONLY_BF16, xs, dev)
+    I = _halves(w)
+    ld_w = _mat("w", w, _ONLY_BF16, (2 * I, K), dev)
+    ld_g = _mat("grad_h", grad_h, _ONLY_BF16, (T, I), dev)
+    ld_z = _mat("preact", preact, _ONLY_BF16, (T, 2 * I), dev)
+    act = _gate_act(activation)
+    pdx = pdw = pdb = 0
+    dx = dw = db = None
+    if bias is not None:
+        _dense("bias", bias, _DT, (2 * I,), dev)
+        db = torch.empty(2 * I, dtype=_F32, device=x.device)
+        pdb = db.data_ptr()
+    if need_x:
+        dx = torch.empty(xs, dtype=_BF16, device=x.device)
+        pdx = dx.data_ptr()
+    if need_w:
+        dw = torch.empty((2 * I, K), dtype=_BF16, device=x.device)
+        pdw = dw.data_ptr()
+    ws = _workspace(workspace, dev, (_LIB or lib()).moe_gated_linear_backward_workspace_size(T, I))
+    _call(_GATED_BWD, dev, grad_h.data_ptr(), ld_g, x.data_ptr(), ld_x, w.data_ptr(), ld_w, act, preact.data_ptr(),
+          ld_z, T, K, I, pdx, pdw, pdb, ws.data_ptr(), ws.numel())
     return dx, dw, db
 
 

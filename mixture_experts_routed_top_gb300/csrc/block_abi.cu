@@ -146,6 +146,20 @@ moe_status run_linear(const void* a, int64_t ld_a, bool a_mn, const void* b, int
   return e == cudaSuccess ? MOE_OK : cuda_error(e, what);
 }
 
+// The gated product x [T, K] by w [2 I, K].
+moe_status run_gated(const void* x, int64_t ld_x, const void* w, int64_t ld_w, const LinearDev& p,
+                     cudaStream_t s, const char* what) {
+  const int T = p.epi.M, I = p.epi.N, K = p.K;
+  const LinearPath path = gated_path(T, I, K, device_sms());
+  CUtensorMap tx, tw;
+  moe_status st = make_map_bf16_2d(&tx, x, K, T, ld_x, 64, 128);
+  if (st != MOE_OK) return st;
+  st = make_map_bf16_2d(&tw, w, K, 2ull * I, ld_w, 64, path.kind == LinearPath::kTile ? 64 : 128);
+  if (st != MOE_OK) return st;
+  const cudaError_t e = launch_gated(tx, tw, p, path, s);
+  return e == cudaSuccess ? MOE_OK : cuda_error(e, what);
+}
+
 struct LinearWs {
   int64_t ld_dz;
   size_t dz, dz_lo, partials, total;
@@ -169,6 +183,50 @@ LinearWs linear_ws(int T, int N) {
   w.partials = (w.dz_lo + (split ? bytes : 0) + 1023) / 1024 * 1024;
   w.total = w.partials + static_cast<size_t>(kLinearDzSlices) * N * 4;
   return w;
+}
+
+// The products of a gradient: dx = dz w and dw = dz^T x for dz [T, N] in bf16, dz_lo what
+// its rounding left or null.
+moe_status gradient_products(const void* dz, const void* dz_lo, int64_t ld_dz, const void* x,
+                             int64_t ld_x, const void* w, int64_t ld_w, int T, int K, int N,
+                             void* dx, void* dw, uint8_t* wsb, cudaStream_t s, const char* fn) {
+  LinearEpi e{};
+  e.act = MOE_ACT_NONE;
+  e.ld_out = K;
+  e.N = K;
+  e.vec = true;  // K % 8 == 0
+  LinearDev p{};
+  p.err = reinterpret_cast<int*>(wsb);
+  p.parts = reinterpret_cast<float*>(wsb + 1024);
+  e.ld_res = K;
+  // dz_lo's product first, then dz's on top of it
+  auto product = [&](void* out, int M, int contraction, bool a_mn, const void* b, int64_t ld_b) {
+    e.M = M;
+    e.out = out;
+    p.K = contraction;
+    moe_status r = MOE_OK;
+    if (dz_lo) {
+      e.residual = nullptr;
+      p.epi = e;
+      r = run_linear(dz_lo, ld_dz, a_mn, b, ld_b, true, p, s, fn);
+      if (r != MOE_OK) return r;
+    }
+    e.residual = dz_lo ? out : nullptr;
+    p.epi = e;
+    return run_linear(dz, ld_dz, a_mn, b, ld_b, true, p, s, fn);
+  };
+  moe_status st = MOE_OK;
+  if (dx && (st = product(dx, T, N, false, w, ld_w)) != MOE_OK) return st;
+  if (dw && (st = product(dw, N, T, true, x, ld_x)) != MOE_OK) return st;
+  return MOE_OK;
+}
+
+constexpr int kGatedMaxI = (1 << 30) - 1;  // 2 I is an int
+moe_status check_gated(const char* fn, int64_t ld_x, int64_t ld_w, int act, int T, int K, int I) {
+  if (act == MOE_ACT_NONE)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: a gate has an activation", fn);
+  if (I > kGatedMaxI) return set_last_error(MOE_ERR_UNSUPPORTED, "%s: I above 2^30 - 1", fn);
+  return check_linear(fn, ld_x, ld_w, act, T, K, I);
 }
 
 }  // namespace
@@ -562,34 +620,109 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
       ld_dz = L.ld_dz;
     }
   }
+  return gradient_products(dz, dz_lo, ld_dz, x, ld_x, w, ld_w, T, K, N, dx, dw, wsb, s, fn);
+}
+
+moe_status moe_gated_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w,
+                            const void* bias, moe_dtype bias_dt, int act, int T, int K, int I,
+                            void* out, int64_t ld_out, void* preact, void* ws, size_t ws_bytes,
+                            void* stream) {
+  const char* fn = "moe_gated_linear";
+  moe_status st = check_gated(fn, ld_x, ld_w, act, T, K, I);
+  if (st != MOE_OK) return st;
+  if (bias && !is_dtype(bias_dt))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  if (ld_out < I) return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride below I", fn);
+  if (T == 0 || I == 0) return MOE_OK;
+  if (!x || !w || !out) return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (preact && preact == out)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: preact needs a buffer of its own", fn);
+  if (!all16(x, w, bias, out, preact))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
+  if ((st = check_ws(fn, ws, ws_bytes, kLinearWsBytes)) != MOE_OK) return st;
   LinearEpi e{};
-  e.act = MOE_ACT_NONE;
-  e.ld_out = K;
-  e.N = K;
-  e.vec = true;  // K % 8 == 0
-  LinearDev p{};
+  e.bias = bias;
+  e.out = out;
+  e.preact = preact;
+  e.ld_out = ld_out;
+  e.M = T;
+  e.N = I;
+  e.act = act;
+  e.bias_bf16 = bias_dt == MOE_DT_BF16;
+  e.vec = I % 8 == 0 && ld_out % 8 == 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (linear_streams(T, 2 * I)) {
+    LinearStreamArgs g;
+    g.x = static_cast<const __nv_bfloat16*>(x);
+    g.w = static_cast<const __nv_bfloat16*>(w);
+    g.ld_x = ld_x;
+    g.ld_w = ld_w;
+    g.K = K;
+    g.epi = e;
+    const cudaError_t r = launch_gated_stream(g, device_sms(), s);
+    return r == cudaSuccess ? MOE_OK : cuda_error(r, fn);
+  }
+  LinearDev p;
+  p.epi = e;
+  p.K = K;
+  p.split = 1;
+  p.group = 0;
   p.err = static_cast<int*>(ws);
-  p.parts = reinterpret_cast<float*>(wsb + 1024);
-  e.ld_res = K;
-  // dz_lo's product first, then dz's on top of it
-  auto product = [&](void* out, int M, int contraction, bool a_mn, const void* b, int64_t ld_b) {
-    e.M = M;
-    e.out = out;
-    p.K = contraction;
-    moe_status r = MOE_OK;
-    if (dz_lo) {
-      e.residual = nullptr;
-      p.epi = e;
-      r = run_linear(dz_lo, ld_dz, a_mn, b, ld_b, true, p, s, fn);
-      if (r != MOE_OK) return r;
-    }
-    e.residual = dz_lo ? out : nullptr;
-    p.epi = e;
-    return run_linear(dz, ld_dz, a_mn, b, ld_b, true, p, s, fn);
-  };
-  if (dx && (st = product(dx, T, N, false, w, ld_w)) != MOE_OK) return st;
-  if (dw && (st = product(dw, N, T, true, x, ld_x)) != MOE_OK) return st;
-  return MOE_OK;
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 1024);
+  return run_gated(x, ld_x, w, ld_w, p, s, fn);
+}
+
+size_t moe_gated_linear_backward_workspace_size(int T, int I) {
+  return T < 0 || I < 0 || I > kGatedMaxI ? 0 : linear_ws(T, 2 * I).total;
+}
+
+moe_status moe_gated_linear_backward(const void* grad_h, int64_t ld_gh, const void* x, int64_t ld_x,
+                                     const void* w, int64_t ld_w, int act, const void* preact,
+                                     int64_t ld_z, int T, int K, int I, void* dx, void* dw,
+                                     float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_gated_linear_backward";
+  moe_status st = check_gated(fn, ld_x, ld_w, act, T, K, I);
+  if (st != MOE_OK) return st;
+  if (ld_gh < I || ld_z < 2ll * I)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride too small", fn);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int N = 2 * I;
+  if (I == 0 || T == 0) {
+    cudaError_t e = cudaSuccess;
+    if (dx && T > 0) e = cudaMemsetAsync(dx, 0, static_cast<size_t>(T) * K * 2, s);
+    if (e == cudaSuccess && dw && I > 0) e = cudaMemsetAsync(dw, 0, static_cast<size_t>(N) * K * 2, s);
+    if (e == cudaSuccess && dbias && I > 0) e = cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * 4, s);
+    return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+  }
+  if (!grad_h || !preact || (dx && !w) || (dw && !x))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!all16(grad_h, x, w, preact, dx, dw, dbias))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
+  const LinearWs L = linear_ws(T, N);
+  if ((st = check_ws(fn, ws, ws_bytes, L.total)) != MOE_OK) return st;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  const bool products = dx || dw;
+  if (!products && !dbias) return MOE_OK;
+  LinearDzArgs a;
+  a.dy = grad_h;
+  a.preact = preact;
+  a.dz = products ? reinterpret_cast<__nv_bfloat16*>(wsb + L.dz) : nullptr;
+  a.dz_lo = products && static_cast<int64_t>(T) * N <= kLinearDzSplit
+                ? reinterpret_cast<__nv_bfloat16*>(wsb + L.dz_lo) : nullptr;
+  a.ld_dy = ld_gh;
+  a.ld_z = ld_z;
+  a.ld_dz = L.ld_dz;
+  a.T = T;
+  a.N = I;
+  a.act = act;
+  a.f32 = false;
+  a.vec = I % 8 == 0 && ld_gh % 8 == 0 && ld_z % 8 == 0;
+  const int slices = std::min(linear_dz_slices(T, I, device_sms()), kLinearDzSlices);
+  a.partials = !dbias ? nullptr : slices == 1 ? dbias : reinterpret_cast<float*>(wsb + L.partials);
+  const cudaError_t r = launch_gated_dz(a, slices, dbias, s);
+  if (r != cudaSuccess) return cuda_error(r, fn);
+  if (!products) return MOE_OK;
+  return gradient_products(a.dz, a.dz_lo, L.ld_dz, x, ld_x, w, ld_w, T, K, N, dx, dw, wsb, s, fn);
 }
 
 // The Python binding's way in: converting 14 to 29 arguments one by one took longer
@@ -605,6 +738,8 @@ moe_status moe_call_packed(int call, const void* block) {
     case 3: return a.call(moe_block_norm_backward);
     case 4: return a.call(moe_linear);
     case 5: return a.call(moe_linear_backward);
+    case 7: return a.call(moe_gated_linear);
+    case 8: return a.call(moe_gated_linear_backward);
   }
   return set_last_error(MOE_ERR_INVALID_ARG, "moe_call_packed: unknown call %d", call);
 }

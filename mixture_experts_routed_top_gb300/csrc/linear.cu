@@ -26,427 +26,10 @@
 #include <atomic>
 #include <type_traits>
 
-#include "moe_device.cuh"
-#include "moe_internal.h"
+#include "linear_device.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int BK = 64;  // bf16 elements per 128-byte swizzled row
-
-// Shared-memory descriptor of an MN-major tile with 128-byte swizzling: 64
-// rows (of M or N) contiguous in a 128-byte line, lines along the
-// contraction, 8 lines (1024 bytes) per swizzle atom; the next 64 rows
-// `slab_bytes` away.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t slab_bytes) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);    // start address / 16
-  d |= static_cast<uint64_t>(slab_bytes >> 4) << 16;      // leading byte offset: next 64 rows
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;            // stride byte offset: next 8 lines
-  d |= static_cast<uint64_t>(1) << 46;                    // descriptor version (sm_100 family)
-  d |= static_cast<uint64_t>(2) << 61;                    // swizzle mode: 128 B
-  return d;
-}
-
-// Instruction descriptor of idesc_bf16_f32 with the operands' orders.
-__host__ __device__ constexpr uint32_t idesc_bf16_order(int M, int N, bool a_mn, bool b_mn) {
-  return idesc_bf16_f32(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
-}
-
-// Bounded waits as mbar_wait_bounded, on the SM's cycle counter: reading the
-// global timer takes longer than most of these waits.  2e9 cycles are a second
-// at the card's 2 GHz; each try itself blocks for a while.
-constexpr long long kWaitCycles = 2000000000ll, kDrainCycles = 40000000ll;
-template <bool kCluster>
-__device__ __forceinline__ bool wait_cycles(uint32_t bar, uint32_t parity, volatile int* abort,
-                                            int* err, int code, long long limit) {
-  long long t0 = 0;
-  for (int i = 0;; ++i) {
-    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if ((i & 15) == 15) {
-      if (*abort) return false;
-      const long long now = clock64();
-      if (i == 15) t0 = now;
-      else if (now - t0 > limit) {
-        atomicOr(err, code);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort,
-                                          int* err, int code, long long limit = kWaitCycles) {
-  return wait_cycles<true>(bar, parity, abort, err, code, limit);
-}
-__device__ __forceinline__ bool wait_cta(uint32_t bar, uint32_t parity, volatile int* abort,
-                                         int* err, int code, long long limit = kWaitCycles) {
-  return wait_cycles<false>(bar, parity, abort, err, code, limit);
-}
-
-// 2-D load counted on an mbarrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint32_t bar,
-                                                 uint32_t dst, int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
-      : "memory");
-}
-
-__device__ __forceinline__ float ldf(const void* p, long i, bool bf16) {
-  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i])
-              : static_cast<const float*>(p)[i];
-}
-__device__ __forceinline__ void stf(void* p, long i, bool f32, float v) {
-  if (f32) static_cast<float*>(p)[i] = v;
-  else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
-__device__ __forceinline__ void ld8(const void* p, long i, bool bf16, float (&v)[8]) {
-  if (bf16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-  } else {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    const float4 a = q[0], b = q[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-}
-__device__ __forceinline__ void st8(void* p, long i, bool f32, const float (&v)[8]) {
-  if (f32) {
-    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint4 u;
-    u.x = pack_bf16x2(v[0], v[1]);
-    u.y = pack_bf16x2(v[2], v[3]);
-    u.z = pack_bf16x2(v[4], v[5]);
-    u.w = pack_bf16x2(v[6], v[7]);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = u;
-  }
-}
-
-// The activation in fp32; silu_f's fast division only where the result is
-// rounded to bf16.
-__device__ __forceinline__ float act_f(float z, int act, bool f32) {
-  if (act == MOE_ACT_NONE) return z;
-  if (act == MOE_ACT_SILU && f32) return z / (1.f + expf(-z));
-  return gate_act(z, act);
-}
-// 8 elements from 16 bytes of bf16 or 32 of fp32.
-template <bool F32>
-__device__ __forceinline__ void bits8(const uint4 (&x)[F32 ? 2 : 1], float (&v)[8]) {
-  const uint4 a = x[0], b = x[F32 ? 1 : 0];
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    v[j] = __uint_as_float(F32 ? w[j] : j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
-}
-// A result and the residual.  REST (the gradients' products): the residual is the
-// product of what rounding an operand left, and it joins only finite results.  Times
-// an infinity that rest, 0 or of either sign, would make the infinite result a NaN.
-template <bool REST>
-__device__ __forceinline__ float plus(float v, float r) {
-  return REST && !(fabsf(v) < INFINITY) ? v : v + r;
-}
-// The epilogue on 8 consecutive columns n.. of row m (m < M) where N % 8 == 0 and
-// every row is 16-byte aligned: pre-activation z = v + bias, y = residual +
-// act(z).  ACT and F32 are constants of the code: kernels hold several copies of
-// this, and with every activation and type in each the code was so long that
-// fetching it took longer than a small product (33 us for 64 x 256 x 256),
-// while one copy called as a function took 300 ns a call.
-// b: the bias there; x: the residual's bits.
-template <int ACT, bool F32, bool REST>
-__device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, const float (&b)[8],
-                                          const uint4 (&x)[F32 ? 2 : 1], float (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] += b[j];
-  if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, F32, v);
-  if (ACT != MOE_ACT_NONE) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = act_f(v[j], ACT, F32);
-  }
-  if (p.residual != nullptr) {
-    float r[8];
-    bits8<F32>(x, r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = plus<REST>(v[j], r[j]);
-  }
-  st8(p.out, m * p.ld_out + n, F32, v);
-}
-// 32 consecutive columns of 32 rows from a warp's TMEM load (lane: row m).  The
-// values go through `buf` (32 x 32 floats of this warp, 16-byte pieces of a row
-// in the order of their index xor the row's, so that neither side meets a bank
-// twice), after which lanes hold neighbouring columns: 4 lanes of 8 columns a
-// row, or where rows are not whole aligned vectors (p.vec off) 32 of one.
-// Straight from the lanes every access touched 32 rows, and the epilogue of a
-// 256 x 256 tile took 6 us, as long as 1152 of the contraction.
-constexpr int kTurn = 32 * 32;
-template <int ACT, bool F32, bool REST>
-__device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
-                                           const uint32_t (&v)[32], float* buf) {
-  const int lane = threadIdx.x & 31;
-  const long m0 = m - lane;
-  // bias and residual of 8 columns of 4 rows, every load on its way before the
-  // first store, which the compiler may not move loads across
-  const int nv = n + 8 * (lane & 3);
-  float bv[8] = {};
-  uint4 xv[4][F32 ? 2 : 1] = {};
-  if (p.vec && nv < p.N) {
-    if (p.residual != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const long row = m0 + 8 * i + (lane >> 2);
-        if (row < p.M) {
-          const uint4* q = reinterpret_cast<const uint4*>(
-              static_cast<const char*>(p.residual) + (row * p.ld_res + nv) * (F32 ? 4 : 2));
-          xv[i][0] = q[0];
-          if (F32) xv[i][F32 ? 1 : 0] = q[1];
-        }
-      }
-    }
-    if (p.bias != nullptr) ld8(p.bias, nv, p.bias_bf16, bv);
-  }
-  __syncwarp();  // the previous step's values have been read
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(buf + lane * 32 + 4 * (c ^ (lane & 7))) =
-        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-  __syncwarp();
-  if (p.vec) {
-    const int c = 2 * (lane & 3);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 8 * i + (lane >> 2);
-      const float4 x = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * (c ^ (row & 7)));
-      const float4 y = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * ((c + 1) ^ (row & 7)));
-      float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-      if (m0 + row < p.M && nv < p.N) epilogue8<ACT, F32, REST>(p, m0 + row, nv, bv, xv[i], f);
-    }
-  } else if (n + lane < p.N) {
-    const int rows = static_cast<int>(min(32l, p.M - m0)), col = n + lane;
-    const float b = p.bias != nullptr ? ldf(p.bias, col, p.bias_bf16) : 0.f;
-    using U = std::conditional_t<F32, uint32_t, uint16_t>;  // the residual's bits
-#pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-      U x[8] = {};
-      if (p.residual != nullptr) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (r0 + k < rows) x[k] = static_cast<const U*>(p.residual)[(m0 + r0 + k) * p.ld_res + col];
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = r0 + k;
-        if (r >= rows) break;
-        const float z = buf[r * 32 + 4 * ((lane >> 2) ^ k) + (lane & 3)] + b;
-        const float res = __uint_as_float(static_cast<uint32_t>(x[k]) << (F32 ? 0 : 16));
-        if (p.preact != nullptr) stf(p.preact, (m0 + r) * p.ld_out + col, F32, z);
-        stf(p.out, (m0 + r) * p.ld_out + col, F32, __fadd_rn(act_f(z, ACT, F32), res));
-      }
-    }
-  }
-  __syncwarp();
-}
-
-// Joining a split contraction.  The CTAs of a cluster share a tile and each owns
-// some of its rows.  A CTA has its sums in its shared memory ([128][STRIDE]
-// floats); it writes the other owners' rows to its part of the workspace
-// ([CTA][128][8 * CHUNKS] floats, whole lines, into L2), and after a cluster
-// barrier each owner adds its rows over all CTAs in their order (so the
-// result does not depend on timing), its own from shared memory, and runs the
-// epilogue on them: 8 columns of a row per thread, neighbouring threads along
-// the row, the loads of two rows from up to four CTAs in flight together.
-// Through distributed shared memory instead, reading or writing, the same
-// exchange ran at 17 to 30 GB/s per SM and took 5 us of a router product of
-// 8192 tokens and 10 of a 256 x 2048 x 2048 one.
-template <int THREADS, int CHUNKS, int STRIDE>
-__device__ __forceinline__ void hand_over(const float* stg, float* part, int row0, int rows) {
-  constexpr int C4 = 2 * CHUNKS;  // float4s of a row
-  for (int i = threadIdx.x; i < (128 - rows) * C4; i += THREADS) {
-    int row = i / C4;
-    row += row >= row0 ? rows : 0;  // the rows before and after the CTA's own
-    const int c = (i % C4) * 4;
-    __stcg(reinterpret_cast<float4*>(part + row * (4 * C4) + c),
-           *reinterpret_cast<const float4*>(stg + row * STRIDE + c));
-  }
-}
-// v[row][8] += parts k0 .. k0 + PARTS - 1 of the first R of a thread's 4 rows,
-// `count` of which there are.  own: its columns of the rows in shared memory,
-// other: in the first CTA's part of the workspace, the next one's `step`
-// floats further on; `mine` is the part in shared memory.
-template <int R, int PARTS>
-__device__ __forceinline__ void add_parts(const float* own, int own_step, const float* other,
-                                          int other_step, long step, int k0, int mine, int count,
-                                          float (&v)[4][8]) {
-  float4 x[PARTS][R][2];
-#pragma unroll
-  for (int i = 0; i < PARTS; ++i)
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      x[i][r][0] = x[i][r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r >= count) continue;
-      if (k0 + i == mine) {
-        const float4* q = reinterpret_cast<const float4*>(own + r * own_step);
-        x[i][r][0] = q[0];
-        x[i][r][1] = q[1];
-      } else {
-        const float4* q = reinterpret_cast<const float4*>(other + step * (k0 + i) + r * other_step);
-        x[i][r][0] = __ldcg(q);
-        x[i][r][1] = __ldcg(q + 1);
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < PARTS; ++i)
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      v[r][0] += x[i][r][0].x, v[r][1] += x[i][r][0].y, v[r][2] += x[i][r][0].z;
-      v[r][3] += x[i][r][0].w, v[r][4] += x[i][r][1].x, v[r][5] += x[i][r][1].y;
-      v[r][6] += x[i][r][1].z, v[r][7] += x[i][r][1].w;
-    }
-}
-// RB rows of a warp, a lane every 32nd column: sums `from` (this lane's, rows
-// `stride` apart; -1: no row), bias b.  The type and whether there is an
-// activation are constants: tested per element they took most of its time.
-template <bool F32, bool ACT, int RB>
-__device__ __forceinline__ void single_rows(const LinearEpi& p, const float* from, int stride,
-                                            const int (&row)[RB], long m0, int n0,
-                                            const float (&b)[8]) {
-  constexpr int COLS = 8 / RB;
-  using T = std::conditional_t<F32, float, __nv_bfloat16>;
-  const int n = n0 + (threadIdx.x & 31);
-  // the residual's bits, every load on its way before the first is used (with the
-  // conversion beside the load each waited for its own, 7 us at 391 x 224 x 706)
-  using U = std::conditional_t<F32, uint32_t, uint16_t>;
-  U y[RB][COLS];
-#pragma unroll
-  for (int k = 0; k < RB; ++k)
-#pragma unroll
-    for (int j = 0; j < COLS; ++j) y[k][j] = 0;
-  if (p.residual != nullptr) {
-#pragma unroll
-    for (int k = 0; k < RB; ++k)
-#pragma unroll
-      for (int j = 0; j < COLS; ++j)
-        if (row[k] >= 0 && n + 32 * j < p.N)
-          y[k][j] = static_cast<const U*>(p.residual)[(m0 + row[k]) * p.ld_res + n + 32 * j];
-  }
-#pragma unroll
-  for (int k = 0; k < RB; ++k) {
-    if (row[k] < 0) continue;
-    const float* const v = from + row[k] * stride;
-    const long at = (m0 + row[k]) * p.ld_out + n;
-#pragma unroll
-    for (int j = 0; j < COLS; ++j) {
-      if (n + 32 * j >= p.N) continue;
-      const float z = v[32 * j] + b[j];
-      if (p.preact != nullptr) stf(static_cast<T*>(p.preact) + at, 32 * j, F32, z);
-      // not fused into the activation, which would depend on the other options
-      const float res = __uint_as_float(static_cast<uint32_t>(y[k][j]) << (F32 ? 0 : 16));
-      stf(static_cast<T*>(p.out) + at, 32 * j, F32, __fadd_rn(res, ACT ? act_f(z, p.act, F32) : z));
-    }
-  }
-}
-
-// The rows row0 .. row0 + rows of a tile whose first row is m0, columns n0 ..
-// n0 + 8 * CHUNKS.  parts: number of CTAs (1, 2, 4 or 8), mine: this one's place
-// among them; part0: the first one's part of the workspace, the next ones'
-// `step` floats further on.  Rows that are not whole aligned vectors go back into
-// stg and leave it with a warp's lanes along a row (391 x 224 x 706 from the
-// threads' 8 columns 22.5 us, so 12.1; x 704 9.2).
-template <int THREADS, int CHUNKS, int STRIDE, bool REST>
-__device__ __forceinline__ void join_rows(const LinearEpi& p, float* stg, const float* part0,
-                                          long step, int parts, int mine, int row0, int rows,
-                                          long m0, int n0) {
-  static_assert(THREADS % CHUNKS == 0 && 32 % CHUNKS == 0, "a thread keeps its columns");
-  constexpr int STEP = THREADS / CHUNKS, WROWS = 32 / CHUNKS, WCOLS = CHUNKS / 4;
-  constexpr int RB = 8 / WCOLS;
-  const int lane = threadIdx.x & 31;
-  const int col = (threadIdx.x % CHUNKS) * 8, n = n0 + col;
-  if (p.vec && n >= p.N) return;
-  float b[8];  // of the thread's columns; without vectors of lane, lane + 32, ..
-#pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = 0.f;
-  if (p.bias != nullptr) {
-    if (p.vec) {
-      ld8(p.bias, n, p.bias_bf16, b);
-    } else {
-#pragma unroll
-      for (int j = 0; j < WCOLS; ++j)
-        if (n0 + lane + 32 * j < p.N) b[j] = ldf(p.bias, n0 + lane + 32 * j, p.bias_bf16);
-    }
-  }
-  // rows in flight: 4 of up to two parts, 2 of four (twice as many measured slower)
-  const int R = parts <= 2 ? 4 : 2;
-  const int end = static_cast<int>(min(static_cast<long>(rows), p.M - m0 - row0));
-#pragma unroll 1
-  for (int iw = threadIdx.x / 32 * WROWS; iw < end; iw += R * STEP) {  // the warp's first row
-    const int i = iw + lane / CHUNKS;
-    const int count = max(0, min(R, (end - i + STEP - 1) / STEP)), ra = row0 + i;
-    float* const own = stg + ra * STRIDE + col;
-    const float* const other = part0 + ra * (8 * CHUNKS) + col;
-    constexpr int OS = STEP * STRIDE, PS = STEP * 8 * CHUNKS;
-    float v[4][8];
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[r][j] = 0.f;
-    if (parts == 1) add_parts<4, 1>(own, OS, other, PS, step, 0, mine, count, v);
-    else if (parts == 2) add_parts<4, 2>(own, OS, other, PS, step, 0, mine, count, v);
-    else
-      for (int k = 0; k < parts; k += 4)
-        add_parts<2, 4>(own, OS, other, PS, step, k, mine, count, v);
-    if (!p.vec) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        if (r >= count) continue;
-        float4* q = reinterpret_cast<float4*>(own + r * OS);
-        q[0] = make_float4(v[r][0], v[r][1], v[r][2], v[r][3]);
-        q[1] = make_float4(v[r][4], v[r][5], v[r][6], v[r][7]);
-      }
-      __syncwarp();
-      for (int r = 0; r < R * WROWS; r += RB) {
-        int rows_at[RB];
-#pragma unroll
-        for (int k = 0; k < RB; ++k) {
-          const int row = iw + (r + k) / WROWS * STEP + (r + k) % WROWS;
-          rows_at[k] = row < end ? row0 + row : -1;
-        }
-        const float* from = stg + lane;
-        if (p.out_f32) {
-          if (p.act == MOE_ACT_NONE) single_rows<true, false>(p, from, STRIDE, rows_at, m0, n0, b);
-          else single_rows<true, true>(p, from, STRIDE, rows_at, m0, n0, b);
-        } else {
-          if (p.act == MOE_ACT_NONE) single_rows<false, false>(p, from, STRIDE, rows_at, m0, n0, b);
-          else single_rows<false, true>(p, from, STRIDE, rows_at, m0, n0, b);
-        }
-      }
-      continue;
-    }
-#pragma unroll 1
-    for (int r = 0; r < count; ++r) {
-      const long m = m0 + ra + r * STEP;
-      float z[8], y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        z[j] = (r == 0 ? v[0][j] : r == 1 ? v[1][j] : r == 2 ? v[2][j] : v[3][j]) + b[j];
-        y[j] = 0.f;
-      }
-      if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + n, !p.out_f32, y);
-      if (p.preact != nullptr) st8(p.preact, m * p.ld_out + n, p.out_f32, z);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = plus<REST>(act_f(z[j], p.act, p.out_f32), y[j]);
-      st8(p.out, m * p.ld_out + n, p.out_f32, y);
-    }
-  }
-}
 
 // ====================================================== CTA-pair kernel
 // tcgen05.mma.cta_group::2, M = 256 (128 rows of A in each CTA), N = 256
@@ -478,18 +61,9 @@ static_assert(kPOffTurn % 16 == 0 && kPOffMisc % 8 == 0, "aligned");
 constexpr int kPSmem = kPOffTurn + 8 * kTurn * 4 + 1024;
 static_assert(kPSmem <= 227 * 1024, "shared memory budget");
 
-// Tile order: groups of `group` row tiles, all column tiles of a group
-// before the next, so the tiles in flight share operand rows in L2.
-__device__ __forceinline__ void pair_tile(int tile, int mt, int nt, int group, int* mi, int* ni) {
-  const int per = group * nt;
-  const int g = tile / per;
-  const int rows = min(group, mt - g * group);
-  const int r = tile - g * per;
-  *ni = r / rows;
-  *mi = g * group + (r - *ni * rows);
-}
-
-template <bool A_MN, bool B_MN, int ACT>
+// GATED: the pair's B is 128 gate rows (rank 0's half) and their 128 up rows (rank 1's),
+// the tile's outputs their 128 columns.
+template <bool A_MN, bool B_MN, int ACT, bool GATED>
 __global__ void __launch_bounds__(kPThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
                        const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ LinearDev p) {
@@ -534,7 +108,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  const int mt = (p.epi.M + 255) >> 8, nt = (p.epi.N + 255) >> 8;
+  constexpr int kCols = GATED ? 128 : 256;  // outputs of a tile
+  const int mt = (p.epi.M + 255) >> 8, nt = (p.epi.N + kCols - 1) / kCols;
   const int total = mt * nt;
   const int KB = (p.K + 2 * BK - 1) / (2 * BK);
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
@@ -548,7 +123,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         int mi, ni;
         pair_tile(tile, mt, nt, p.group, &mi, &ni);
         const int arow = mi * 256 + 128 * static_cast<int>(rank);
-        const int brow = ni * 256 + 128 * static_cast<int>(rank);
+        const int brow = ni * kCols + (GATED ? p.epi.N : 128) * static_cast<int>(rank);
         for (int kb = 0; kb < KB; ++kb) {
           if (!wait_pair(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err,
                                              ERR_TIMEOUT_PRODUCER)) {
@@ -634,7 +209,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, column half
-    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 128 * half;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + (GATED ? 64 : 128) * half;
     float* const turn = reinterpret_cast<float*>(smem + kPOffTurn) + (warp - 2) * kTurn;
     int it = 0;
     for (int tile = cid; tile < total; tile += ncl, ++it) {
@@ -649,20 +224,33 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const long m = static_cast<long>(mi) * 256 + 128 * rank + 32 * q + lane;
-      const int n0 = ni * 256 + 128 * half;
+      const int n0 = ni * kCols + kCols / 2 * half;
+      auto release = [&] {  // every column read: hand the accumulator back
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(smem_u32(&tempty[acc]));
+          else mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
+        }
+      };
+      if (GATED) {
+#pragma unroll 1
+        for (int s = 0; s < 2; ++s) {
+          uint32_t g[32], u[32];
+          tmem_ld_32x32b_x32(tl + acc * 256 + 32 * s, g);
+          tmem_ld_32x32b_x32(tl + acc * 256 + 128 + 32 * s, u);
+          tmem_ld_wait();
+          if (s == 1) release();
+          if (n0 + 32 * s < p.epi.N) epilogue32_gated<ACT>(p.epi, m, n0 + 32 * s, g, u, turn);
+        }
+        continue;
+      }
 #pragma unroll 1
       for (int s = 0; s < 4; ++s) {
         uint32_t v[32];
         tmem_ld_32x32b_x32(tl + acc * 256 + 32 * s, v);
         tmem_ld_wait();
-        if (s == 3) {  // every column read: hand the accumulator back
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (rank == 0) mbar_arrive(smem_u32(&tempty[acc]));
-            else mbar_arrive_remote(mapa_shared(smem_u32(&tempty[acc]), 0));
-          }
-        }
+        if (s == 3) release();
         if (n0 + 32 * s < p.epi.N) epilogue32<ACT, false, B_MN>(p.epi, m, n0 + 32 * s, v, turn);
       }
     }
@@ -965,7 +553,8 @@ constexpr int kTSmem = kTOffMisc + 16 + 1024;
 constexpr int kTStride = 132;                    // floats per staged row: 128 + 4 (no bank conflicts)
 static_assert(128 * kTStride * 4 <= kTOffBar, "staged tile fits the ring");
 
-template <bool A_MN, bool B_MN>
+// GATED: 64 gate rows of w and their 64 up rows, for 64 outputs.
+template <bool A_MN, bool B_MN, bool GATED>
 __global__ void __launch_bounds__(kTThreads)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
                        const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ LinearDev p) {
@@ -1030,6 +619,9 @@ __global__ void __launch_bounds__(kTThreads)
         if (B_MN) {
           tma_load_2d(&tm_b, fb, b_dst, ni * 128, k0);
           tma_load_2d(&tm_b, fb, b_dst + kTOper / 2, ni * 128 + BK, k0);
+        } else if (GATED) {
+          tma_load_2d(&tm_b, fb, b_dst, k0, ni * 64);
+          tma_load_2d(&tm_b, fb, b_dst + kTOper / 2, k0, p.epi.N + ni * 64);
         } else {
           tma_load_2d(&tm_b, fb, b_dst, k0, ni * 128);
         }
@@ -1116,10 +708,13 @@ __global__ void __launch_bounds__(kTThreads)
   }
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 256);
-  if (ok)
-    join_rows<kTThreads, 16, kTStride, B_MN>(
-        p.epi, stg, p.parts + static_cast<long>(blockIdx.x - rank) * 128 * 128, 128l * 128, S, rank,
-        rank * rows, rows, static_cast<long>(mi) * 128, ni * 128);
+  const float* const part0 = p.parts + static_cast<long>(blockIdx.x - rank) * 128 * 128;
+  if (ok && GATED)
+    join_rows_gated<kTThreads, kTStride>(p.epi, stg, part0, 128l * 128, S, rank, rank * rows, rows,
+                                         static_cast<long>(mi) * 128, ni * 64);
+  else if (ok)
+    join_rows<kTThreads, 16, kTStride, B_MN>(p.epi, stg, part0, 128l * 128, S, rank, rank * rows, rows,
+                                             static_cast<long>(mi) * 128, ni * 128);
 }
 
 // ====================================================== one token
@@ -1127,7 +722,8 @@ __global__ void __launch_bounds__(kTThreads)
 // block share two rows of w, each lane multiplying 16-byte pieces of them with
 // the token's, and add their sums in order.  2048 x 7168 6.3 us from memory
 // (4.7 TB/s, 2 us more than the bytes need), 3.7 from L2.
-template <int WPR>
+// GATED: the two rows are a gate row and its up row, and give one output.
+template <int WPR, bool GATED>
 __global__ void __launch_bounds__(256)
     linear_vector_kernel(const __grid_constant__ LinearStreamArgs a) {
   constexpr int R = 2;                // rows of w per warp: they share the token's loads
@@ -1136,13 +732,13 @@ __global__ void __launch_bounds__(256)
   __shared__ float s_part[8][R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp / WPR, part = warp % WPR;
-  const int n0 = (blockIdx.x * GROUPS + grp) * R;
+  const int n0 = (blockIdx.x * GROUPS + grp) * (GATED ? 1 : R);
   pdl_wait();
   float acc[R] = {};
   const int chunks = a.K / 8;
   if (n0 < a.epi.N) {
     const __nv_bfloat16* w0 = a.w + static_cast<long>(n0) * a.ld_w;
-    const __nv_bfloat16* w1 = a.w + static_cast<long>(min(n0 + 1, a.epi.N - 1)) * a.ld_w;
+    const __nv_bfloat16* w1 = a.w + (GATED ? static_cast<long>(a.epi.N) + n0 : min(n0 + 1, a.epi.N - 1)) * a.ld_w;
 #pragma unroll 4
     for (int c = part * 32 + lane; c < chunks; c += WPR * 32) {
       float f[R][8], x[8];
@@ -1162,12 +758,23 @@ __global__ void __launch_bounds__(256)
     if (lane == 0) s_part[warp][r] = acc[r];
   }
   __syncthreads();
+  const LinearEpi& p = a.epi;
+  if (GATED) {
+    const int i = threadIdx.x, n = blockIdx.x * GROUPS + i;
+    if (i < GROUPS && n < p.N) {
+      float zg = 0.f, zu = 0.f;
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) zg += s_part[i * WPR + w][0], zu += s_part[i * WPR + w][1];
+      if (p.bias != nullptr) zg += ldf(p.bias, n, p.bias_bf16), zu += ldf(p.bias, p.N + n, p.bias_bf16);
+      gated1<MOE_ACT_NONE>(p, 0, n, zg, zu);
+    }
+    return;
+  }
   const int i = threadIdx.x, n = blockIdx.x * GROUPS * R + i;
   if (i < GROUPS * R && n < a.epi.N) {
     float z = 0.f;
 #pragma unroll
     for (int w = 0; w < WPR; ++w) z += s_part[i / R * WPR + w][i % R];
-    const LinearEpi& p = a.epi;
     if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
     if (p.preact != nullptr) stf(p.preact, n, p.out_f32, z);
     z = act_f(z, p.act, p.out_f32);
@@ -1224,10 +831,12 @@ template <int NT>
 struct StreamLay {
   static constexpr int G = NT == 1 ? 8 : 4, TOK = 8 * NT;
 };
-template <int NT>
+// GATED: the 16 rows are 8 gate rows and their 8 up rows, for 8 outputs.
+template <int NT, bool GATED>
 __global__ void __launch_bounds__(kStreamWarps * 32)
     linear_stream_kernel(const __grid_constant__ LinearStreamArgs a) {
   constexpr int G = StreamLay<NT>::G, TOK = StreamLay<NT>::TOK;
+  constexpr int OUT = GATED ? 8 : 16;  // outputs of a tile
   pdl_launch_dependents();
   __shared__ float s_part[kStreamWarps][TOK][17];
   __shared__ float s_sum[kStreamWarps][TOK][16];  // of a tile, over this block's warps
@@ -1235,15 +844,15 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
   const int wpr = a.wpr, S = a.split, rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tiles = kStreamWarps / wpr;  // of a block
   const int tile0 = blockIdx.x / S * tiles, part = rank * wpr + warp % wpr;
-  const int n0 = (tile0 + warp / wpr) * 16;
+  const int n0 = (tile0 + warp / wpr) * OUT;
   const int N = a.epi.N, T = a.epi.M, K = a.K;
   pdl_wait();
   float sum[NT][4] = {};
   if (n0 < N) {
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const bool on0 = n0 + g < N, on1 = n0 + 8 + g < N;
+    const bool on0 = n0 + g < N, on1 = GATED ? on0 : n0 + 8 + g < N;
     const __nv_bfloat16* w0 = a.w + static_cast<long>(n0 + g) * a.ld_w;
-    const __nv_bfloat16* w1 = w0 + 8 * a.ld_w;
+    const __nv_bfloat16* w1 = w0 + (GATED ? static_cast<long>(N) : 8l) * a.ld_w;
 #pragma unroll 1
     for (int k0 = part * (32 * G); k0 < K; k0 += wpr * S * (32 * G)) {
       uint4 wv[G][2], xv[G][NT];
@@ -1295,19 +904,31 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
     __syncwarp();
     cluster_sync_all();
   }
-  // the blocks of a cluster share the results out among them
-  for (int i = threadIdx.x + rank * (kStreamWarps * 32); i < count; i += S * (kStreamWarps * 32)) {
-    const int tl = i / (TOK * 16), tok = i / 16 % TOK, r = i % 16, n = (tile0 + tl) * 16 + r;
-    if (n >= N || tok >= T) continue;
+  // the sum of one (tile, token, row) over the blocks or the warps
+  auto total = [&](int tl, int tok, int r) {
     float z = 0.f;
     if (S > 1) {
-      const uint32_t at = smem_u32(&s_sum[0][0][0] + i);
+      const uint32_t at = smem_u32(&s_sum[0][0][0] + (tl * TOK + tok) * 16 + r);
 #pragma unroll 8
       for (int q = 0; q < S; ++q) z += ld_cluster_f32(mapa_shared(at, q));
     } else {
       for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
     }
+    return z;
+  };
+  // the blocks of a cluster share the results out among them
+  const int results = tiles * TOK * OUT;
+  for (int i = threadIdx.x + rank * (kStreamWarps * 32); i < results; i += S * (kStreamWarps * 32)) {
+    const int tl = i / (TOK * OUT), tok = i / OUT % TOK, r = i % OUT, n = (tile0 + tl) * OUT + r;
+    if (n >= N || tok >= T) continue;
+    float z = total(tl, tok, r);
     if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
+    if (GATED) {
+      float zu = total(tl, tok, 8 + r);
+      if (p.bias != nullptr) zu += ldf(p.bias, N + n, p.bias_bf16);
+      gated1<MOE_ACT_NONE>(p, tok, n, z, zu);
+      continue;
+    }
     if (p.preact != nullptr) stf(p.preact, tok * p.ld_out + n, p.out_f32, z);
     z = act_f(z, p.act, p.out_f32);
     if (p.residual != nullptr) z += ldf(p.residual, tok * p.ld_res + n, !p.out_f32);
@@ -1403,6 +1024,94 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzArgs a) {
   }
 }
 
+// The gated product's: from dh and z = (zg, zu), dzg = dh zu act'(zg) and dzu = dh
+// act(zg), side by side in rows of 2 N (`ld_dz` apart), with the same column sums.
+// A block covers 256 outputs.
+template <int ACT, bool SPLIT>
+__global__ void __launch_bounds__(256) gated_dz_kernel(const LinearDzArgs a) {
+  pdl_launch_dependents();
+  __shared__ float s_sum[2][8][256];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int n = blockIdx.x * 256 + x * 8, N = a.N;
+  pdl_wait();
+  const long t0 = static_cast<long>(a.T) * blockIdx.y / gridDim.y;
+  const long t1 = static_cast<long>(a.T) * (blockIdx.y + 1) / gridDim.y;
+  float sg[8] = {}, su[8] = {};
+  const __nv_bfloat16* const dh = static_cast<const __nv_bfloat16*>(a.dy);
+  const __nv_bfloat16* const z = static_cast<const __nv_bfloat16*>(a.preact);
+  auto slopes = [&](float (&d)[8], float (&zg)[8], float (&zu)[8]) {  // zg, zu become dzg, dzu
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // not fused into the sums, which would then depend on whether dz is stored
+      const float g = __fmul_rn(d[j] * zu[j], act_slope<ACT>(zg[j]));
+      zu[j] = __fmul_rn(d[j], gate_act(zg[j], ACT));
+      zg[j] = g;
+      sg[j] += zg[j];
+      su[j] += zu[j];
+    }
+  };
+  auto rest = [](float v) {  // nothing is left of one that bf16 has no finite value for
+    const float hi = __bfloat162float(__float2bfloat16_rn(v));
+    return fabsf(hi) < INFINITY ? v - hi : 0.f;
+  };
+  if (n < N && a.vec) {
+#pragma unroll 2
+    for (long t = t0 + y; t < t1; t += 8) {
+      float d[8], zg[8], zu[8];
+      ld8(dh, t * a.ld_dy + n, true, d);
+      ld8(z, t * a.ld_z + n, true, zg);
+      ld8(z, t * a.ld_z + N + n, true, zu);
+      slopes(d, zg, zu);
+      if (a.dz == nullptr) continue;
+      st8(a.dz, t * a.ld_dz + n, false, zg);
+      st8(a.dz, t * a.ld_dz + N + n, false, zu);
+      if (SPLIT) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) zg[j] = rest(zg[j]), zu[j] = rest(zu[j]);
+        st8(a.dz_lo, t * a.ld_dz + n, false, zg);
+        st8(a.dz_lo, t * a.ld_dz + N + n, false, zu);
+      }
+    }
+  } else if (n < N) {
+    for (long t = t0 + y; t < t1; t += 8) {
+      float d[8], zg[8], zu[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = n + j < N;
+        d[j] = in ? ldf(dh, t * a.ld_dy + n + j, true) : 0.f;
+        zg[j] = in ? ldf(z, t * a.ld_z + n + j, true) : 0.f;
+        zu[j] = in ? ldf(z, t * a.ld_z + N + n + j, true) : 0.f;
+      }
+      slopes(d, zg, zu);
+      if (a.dz == nullptr) continue;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (n + j >= N) continue;
+        stf(a.dz, t * a.ld_dz + n + j, false, zg[j]);
+        stf(a.dz, t * a.ld_dz + N + n + j, false, zu[j]);
+        if (SPLIT) {
+          stf(a.dz_lo, t * a.ld_dz + n + j, false, rest(zg[j]));
+          stf(a.dz_lo, t * a.ld_dz + N + n + j, false, rest(zu[j]));
+        }
+      }
+    }
+  }
+  if (a.partials == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s_sum[0][y][x * 8 + j] = sg[j], s_sum[1][y][x * 8 + j] = su[j];
+  __syncthreads();
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  if (col < N) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += s_sum[h][i][threadIdx.x];
+      a.partials[static_cast<long>(blockIdx.y) * (2l * N) + static_cast<long>(h) * N + col] = v;
+    }
+  }
+}
+
 // Sums of the slices' partial rows: 32 columns x 8 parts of the slices per
 // block, each part added in order, then the parts.
 __global__ void __launch_bounds__(256)
@@ -1426,10 +1135,10 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <bool A_MN, bool B_MN, int ACT>
+template <bool A_MN, bool B_MN, int ACT, bool GATED = false>
 cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, LinearDev p,
                         cudaStream_t s) {
-  auto kern = linear_pair_kernel<A_MN, B_MN, ACT>;
+  auto kern = linear_pair_kernel<A_MN, B_MN, ACT, GATED>;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -1457,7 +1166,7 @@ cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Linear
     if (nc < 1) return cudaErrorLaunchOutOfResources;
     max_clusters[dev].store(nc, std::memory_order_release);
   }
-  const long tiles = static_cast<long>(ceil_div(p.epi.M, 256)) * ceil_div(p.epi.N, 256);
+  const long tiles = static_cast<long>(ceil_div(p.epi.M, 256)) * ceil_div(p.epi.N, GATED ? 128 : 256);
   p.group = 8;
   cfg.gridDim = dim3(2 * static_cast<int>(std::min<long>(nc, tiles)));
   cfg.stream = s;
@@ -1514,10 +1223,10 @@ cudaError_t launch_sums(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Linear
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-template <bool A_MN, bool B_MN>
+template <bool A_MN, bool B_MN, bool GATED = false>
 cudaError_t launch_tile(const CUtensorMap& tm_a, const CUtensorMap& tm_b, LinearDev p, int split,
                         cudaStream_t s) {
-  auto kern = linear_tile_kernel<A_MN, B_MN>;
+  auto kern = linear_tile_kernel<A_MN, B_MN, GATED>;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -1537,7 +1246,7 @@ cudaError_t launch_tile(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Linear
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   p.split = split;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ceil_div(p.epi.M, 128) * ceil_div(p.epi.N, 128) * split);
+  cfg.gridDim = dim3(ceil_div(p.epi.M, 128) * ceil_div(p.epi.N, GATED ? 64 : 128) * split);
   cfg.blockDim = dim3(kTThreads);
   cfg.dynamicSmemBytes = kTSmem;
   cfg.stream = s;
@@ -1548,17 +1257,19 @@ cudaError_t launch_tile(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Linear
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-template <int WPR>
+template <int WPR, bool GATED>
 cudaError_t launch_vector_w(const LinearStreamArgs& a, cudaStream_t s) {
-  return launch_pdl(linear_vector_kernel<WPR>, dim3(ceil_div(a.epi.N, 8 / WPR * 2)), dim3(256), 0, s, a);
+  return launch_pdl(linear_vector_kernel<WPR, GATED>, dim3(ceil_div(a.epi.N, 8 / WPR * (GATED ? 1 : 2))),
+                    dim3(256), 0, s, a);
 }
+template <bool GATED>
 cudaError_t launch_vector(const LinearStreamArgs& a, int num_sms, cudaStream_t s) {
   // warps per row pair: enough that every SM has 40 warps, at most 8
-  const long pairs = (a.epi.N + 1) / 2, want = 40L * num_sms;
-  if (pairs >= want) return launch_vector_w<1>(a, s);
-  if (2 * pairs >= want) return launch_vector_w<2>(a, s);
-  if (4 * pairs >= want) return launch_vector_w<4>(a, s);
-  return launch_vector_w<8>(a, s);
+  const long pairs = GATED ? a.epi.N : (a.epi.N + 1) / 2, want = 40L * num_sms;
+  if (pairs >= want) return launch_vector_w<1, GATED>(a, s);
+  if (2 * pairs >= want) return launch_vector_w<2, GATED>(a, s);
+  if (4 * pairs >= want) return launch_vector_w<4, GATED>(a, s);
+  return launch_vector_w<8, GATED>(a, s);
 }
 
 template <int ACT>
@@ -1574,13 +1285,13 @@ cudaError_t launch_dz(const LinearDzArgs& a, dim3 grid, cudaStream_t s) {
                : launch_pdl(linear_dz_kernel<ACT, false, false>, grid, block, 0, s, a);
 }
 
-template <int NT>
+template <int NT, bool GATED>
 cudaError_t launch_stream(LinearStreamArgs a, int num_sms, cudaStream_t s) {
   // warps of a block per tile, then blocks: until every SM has WANT warps, as
   // long as each has a group of the contraction
   constexpr long WANT = 16;
   constexpr int kGroup = 32 * StreamLay<NT>::G;
-  const long tiles = ceil_div(a.epi.N, 16);
+  const long tiles = ceil_div(a.epi.N, GATED ? 8 : 16);
   a.wpr = a.split = 1;
   while (a.wpr < kStreamWarps && tiles * a.wpr < WANT * num_sms && a.wpr * kGroup < a.K) a.wpr *= 2;
   while (a.split < 8 && tiles * a.wpr * a.split < WANT * num_sms && a.wpr * a.split * kGroup < a.K)
@@ -1598,7 +1309,7 @@ cudaError_t launch_stream(LinearStreamArgs a, int num_sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = a.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<NT>, a);
+  return cudaLaunchKernelEx(&cfg, linear_stream_kernel<NT, GATED>, a);
 }
 
 }  // namespace
@@ -1614,7 +1325,7 @@ cudaError_t launch_stream(LinearStreamArgs a, int num_sms, cudaStream_t s) {
 // 36, but 8192 x 7168 x 64 31 against 28), or where an fp32 result would have more
 // than 1024 of the contraction in one accumulator (unless the split of the small
 // tiles is at its end: from K = 16384 on, with few tiles, it has more).
-LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms) {
+LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms, bool sums) {
   LinearPath r;
   const long big = static_cast<long>(ceil_div(M, 256)) * ceil_div(N, 256);
   const long pairs = std::min(num_sms, kLinearMaxParts / 2) / 2;
@@ -1627,8 +1338,8 @@ LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms) {
   const long tiles = static_cast<long>(ceil_div(M, 128)) * ceil_div(N, 128);
   while (r.split < 8 && tiles * r.split * 2 <= 4 * pairs && K / (r.split * 2) >= 4 * BK)
     r.split *= 2;
-  if ((big * 8 >= pairs * 3 && 3 * big <= tiles && K >= 64 * BK) ||
-      (out_f32 && K / (2 * r.split) > 16 * BK && r.split < 8)) {
+  if (sums && ((big * 8 >= pairs * 3 && 3 * big <= tiles && K >= 64 * BK) ||
+               (out_f32 && K / (2 * r.split) > 16 * BK && r.split < 8))) {
     r.kind = LinearPath::kSums;  // 2 * big <= pairs here
     r.split = 2;
   }
@@ -1681,14 +1392,42 @@ cudaError_t launch_linear(const CUtensorMap& tm_a, const CUtensorMap& tm_b, cons
 
 bool linear_streams(int T, int N) { return T <= 16 || (T <= 32 && N <= 1024); }
 
-cudaError_t launch_linear_stream(const LinearStreamArgs& a, int num_sms, cudaStream_t s) {
+namespace {
+template <bool GATED>
+cudaError_t launch_few(const LinearStreamArgs& a, int num_sms, cudaStream_t s) {
   cudaError_t e;
-  if (a.epi.M == 1) e = launch_vector(a, num_sms, s);
-  else if (a.epi.M <= 8) e = launch_stream<1>(a, num_sms, s);
-  else if (a.epi.M <= 16) e = launch_stream<2>(a, num_sms, s);
-  else e = launch_stream<4>(a, num_sms, s);
+  if (a.epi.M == 1) e = launch_vector<GATED>(a, num_sms, s);
+  else if (a.epi.M <= 8) e = launch_stream<1, GATED>(a, num_sms, s);
+  else if (a.epi.M <= 16) e = launch_stream<2, GATED>(a, num_sms, s);
+  else e = launch_stream<4, GATED>(a, num_sms, s);
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+}  // namespace
+cudaError_t launch_linear_stream(const LinearStreamArgs& a, int num_sms, cudaStream_t s) {
+  return launch_few<false>(a, num_sms, s);
+}
+cudaError_t launch_gated_stream(const LinearStreamArgs& a, int num_sms, cudaStream_t s) {
+  return launch_few<true>(a, num_sms, s);
+}
+
+// Which kernel of the gated product: 2 N columns of accumulators in the same two
+// kinds of tiles.
+LinearPath gated_path(long M, long N, long K, int num_sms) {
+  return linear_path(M, 2 * N, K, false, num_sms, false);
+}
+cudaError_t launch_gated(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const LinearDev& p,
+                         const LinearPath& path, cudaStream_t s) {
+  const long parts = static_cast<long>(path.split) * ceil_div(p.epi.M, 128) * ceil_div(p.epi.N, 64);
+  if (path.kind == LinearPath::kSums || (path.kind == LinearPath::kPair && path.split != 1) ||
+      (path.split != 1 && path.split != 2 && path.split != 4 && path.split != 8) ||
+      (path.split > 1 && (path.split > ceil_div(p.K, BK) || parts > kLinearMaxParts)))
+    return cudaErrorInvalidValue;
+  if (path.kind == LinearPath::kTile)
+    return launch_tile<false, false, true>(tm_x, tm_w, p, path.split, s);
+  if (p.epi.act == MOE_ACT_SILU) return launch_pair<false, false, MOE_ACT_SILU, true>(tm_x, tm_w, p, s);
+  if (p.epi.act == MOE_ACT_GELU) return launch_pair<false, false, MOE_ACT_GELU, true>(tm_x, tm_w, p, s);
+  return launch_pair<false, false, MOE_ACT_RELU, true>(tm_x, tm_w, p, s);
 }
 
 int linear_dz_slices(long T, long N, int num_sms) {
@@ -1709,6 +1448,29 @@ cudaError_t launch_linear_dz(const LinearDzArgs& a, int slices, float* dbias, cu
   if (dbias != nullptr && slices > 1) {  // one slice has written dbias itself
     e = launch_pdl(linear_colsum_kernel, dim3(ceil_div(a.N, 32)), dim3(256), 0, s,
                    static_cast<const float*>(a.partials), slices, a.N, dbias);
+    count_launches(1);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+namespace {
+template <int ACT>
+cudaError_t launch_gated_dz_act(const LinearDzArgs& a, dim3 grid, cudaStream_t s) {
+  return a.dz_lo != nullptr ? launch_pdl(gated_dz_kernel<ACT, true>, grid, dim3(256), 0, s, a)
+                            : launch_pdl(gated_dz_kernel<ACT, false>, grid, dim3(256), 0, s, a);
+}
+}  // namespace
+cudaError_t launch_gated_dz(const LinearDzArgs& a, int slices, float* dbias, cudaStream_t s) {
+  const dim3 grid(ceil_div(a.N, 256), slices);
+  cudaError_t e;
+  if (a.act == MOE_ACT_SILU) e = launch_gated_dz_act<MOE_ACT_SILU>(a, grid, s);
+  else if (a.act == MOE_ACT_GELU) e = launch_gated_dz_act<MOE_ACT_GELU>(a, grid, s);
+  else e = launch_gated_dz_act<MOE_ACT_RELU>(a, grid, s);
+  count_launches(1);
+  if (e != cudaSuccess) return e;
+  if (dbias != nullptr && slices > 1) {
+    e = launch_pdl(linear_colsum_kernel, dim3(ceil_div(2 * a.N, 32)), dim3(256), 0, s,
+                   static_cast<const float*>(a.partials), slices, 2 * a.N, dbias);
     count_launches(1);
   }
   return e != cudaSuccess ? e : cudaGetLastError();

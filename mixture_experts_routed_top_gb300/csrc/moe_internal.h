@@ -404,7 +404,8 @@ struct LinearPath {
   enum Kind { kPair, kSums, kTile } kind;
   int split;
 };
-LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms);
+// sums: whether split pairs (kSums) may be chosen.
+LinearPath linear_path(long M, long N, long K, bool out_f32, int num_sms, bool sums = true);
 // D[M, N] = A B^T with the operands' orders (a_mn, b_mn: false, false /
 // false, true / true, true).  The maps' boxes: 64 of the contraction x 128 rows
 // of a K-major operand; 64 rows x 64 (kTile) or 128 of the contraction of an
@@ -434,5 +435,16 @@ struct LinearDzArgs {
 constexpr int kLinearDzSlices = 608;
 int linear_dz_slices(long T, long N, int num_sms);
 cudaError_t launch_linear_dz(const LinearDzArgs& a, int slices, float* dbias, cudaStream_t s);
+
+// The gated product, weights [2 N, K]: act(x wg^T + bg) (x wu^T + bu) for N outputs; p.epi.N
+// = N, out bf16, preact rows 2 N apart, no residual.  tm_w's box: 64 of the contraction x
+// 64 (kTile) or 128 rows.
+LinearPath gated_path(long M, long N, long K, int num_sms);
+cudaError_t launch_gated(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const LinearDev& p,
+                         const LinearPath& path, cudaStream_t s);
+cudaError_t launch_gated_stream(const LinearStreamArgs& a, int num_sms, cudaStream_t s);
+// dz of the gated product: dy = dh [T, N], preact = z [T, 2 N], both bf16; dz, partials
+// and dbias of 2 N columns.
+cudaError_t launch_gated_dz(const LinearDzArgs& a, int slices, float* dbias, cudaStream_t s);
 
 }  // namespace moe

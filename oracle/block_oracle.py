@@ -203,3 +203,20 @@ def linear_backward(grad_y, x, w, activation=None, preact=None):
     if activation is not None:
         dz = dz * _slope(_f64(preact), activation)
     return dz @ _f64(w), dz.T @ _f64(x), dz.sum(0), dz
+
+
+def gated_linear(x, w, bias=None, activation="silu"):
+    """act(z[:, :I]) * z[:, I:] with z = x w^T + bias -> (that, z)."""
+    z = _f64(x) @ _f64(w).T
+    if bias is not None:
+        z = z + _f64(bias)
+    I = z.shape[1] // 2
+    return _act(z[:, :I], activation) * z[:, I:], z
+
+
+def gated_linear_backward(grad_h, x, w, preact, activation="silu"):
+    """-> (dx, dw, dbias, dz)."""
+    z, dh = _f64(preact), _f64(grad_h)
+    zg, zu = np.split(z, 2, axis=1)
+    dz = np.concatenate([dh * zu * _slope(zg, activation), dh * _act(zg, activation)], 1)
+    return dz @ _f64(w), dz.T @ _f64(x), dz.sum(0), dz

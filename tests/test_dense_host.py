@@ -1,0 +1,85 @@
+"""The operators of the dense half of a block without a GPU: pins of their float64 oracle
+(closed forms, and central differences for the gradients) and refusals of the C entries,
+which come back as a status before anything touches the device."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import block_oracle as B
+
+NUL = ctypes.c_void_p(0)
+P = ctypes.c_void_p(1 << 20)        # never dereferenced: the calls below stop before a launch
+ODD = ctypes.c_void_p((1 << 20) + 8)
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 5
+EPS = 1e-5          # step of the central differences: truncation ~ EPS^2, rounding ~ 1e-16 / EPS
+TOL = 1e-6          # a hundred times the larger of the two, for values of order 1
+
+
+@pytest.fixture(scope="module")
+def L():
+    from mixture_experts_routed_top_gb300 import build, lib
+    build.build()
+    return lib()
+
+
+def _diff(f, v, direction):
+    return (f(v + EPS * direction) - f(v - EPS * direction)) / (2 * EPS)
+
+
+# ------------------------------------------------------------------ gated products
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gated_gradient_against_differences(act):
+    g = np.random.default_rng(4)
+    x, w, b, gh = g.normal(size=(5, 8)), g.normal(size=(6, 8)), g.normal(size=6), g.normal(size=(5, 3))
+    _, z = B.gated_linear(x, w, b, act)
+    dx, dw, db, _ = B.gated_linear_backward(gh, x, w, z, act)
+    for val, grad, f in ((x, dx, lambda a: B.gated_linear(a, w, b, act)), (w, dw, lambda a: B.gated_linear(x, a, b, act)),
+                         (b, db, lambda a: B.gated_linear(x, w, a, act))):
+        u = g.normal(size=val.shape)
+        assert abs(_diff(lambda a: (f(a)[0] * gh).sum(), val, u) - (grad * u).sum()) < TOL
+
+
+def test_gated_closed_forms():
+    x, w = np.array([[2.0, -3.0]]), np.array([[1.0, 0], [0, 1], [0, 1], [1, 0]])       # gates 2, -3; ups -3, 2
+    h, z = B.gated_linear(x, w, activation="relu")
+    assert z.tolist() == [[2.0, -3.0, -3.0, 2.0]] and h.tolist() == [[-6.0, 0.0]]
+    assert B.gated_linear_backward([[1, 1]], x, w, z, "relu")[3].tolist() == [[-3.0, 0.0, 2.0, 0.0]]
+
+
+def gated(L, x=P, ld_x=64, w=P, ld_w=64, bias=NUL, bdt=0, act=0, T=4, K=64, I=32, out=P, ld_out=32, z=NUL, ws=P,
+          wsb=1 << 30):
+    return L.moe_gated_linear(x, ld_x, w, ld_w, bias, bdt, act, T, K, I, out, ld_out, z, ws, wsb, NUL)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(I=-1), INVALID), (dict(K=0), UNSUPPORTED), (dict(K=60), UNSUPPORTED),
+    (dict(ld_x=68), UNSUPPORTED), (dict(ld_w=56), INVALID), (dict(act=3), INVALID), (dict(act=-1), INVALID),
+    (dict(bias=P, bdt=2), INVALID), (dict(ld_out=31), INVALID), (dict(x=NUL), INVALID), (dict(w=NUL), INVALID),
+    (dict(out=NUL), INVALID), (dict(x=ODD), INVALID), (dict(bias=ODD), INVALID), (dict(z=P), INVALID),
+    (dict(ws=NUL), INVALID), (dict(wsb=128), WORKSPACE), (dict(I=1 << 30, ld_out=1 << 30), UNSUPPORTED),
+    (dict(T=0, x=NUL), OK), (dict(I=0, x=NUL), OK)])
+def test_gated_linear_refusals(L, kw, status):
+    assert gated(L, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(act=-1), INVALID), (dict(z=NUL), INVALID), (dict(K=60), UNSUPPORTED), (dict(ld_gh=31), INVALID),
+    (dict(ld_z=63), INVALID), (dict(gh=NUL), INVALID), (dict(wsb=64), WORKSPACE), (dict(x=ODD), INVALID)])
+def test_gated_linear_backward_refusals(L, kw, status):
+    need = L.moe_gated_linear_backward_workspace_size(4, 32)
+    assert need >= 4 * 64 * 2 and L.moe_gated_linear_backward_workspace_size(4, 1 << 30) == 0
+    a = dict(gh=P, ld_gh=32, x=P, act=0, z=P, ld_z=64, K=64, wsb=need)
+    a.update(kw)
+    assert L.moe_gated_linear_backward(a["gh"], a["ld_gh"], a["x"], 64, P, 64, a["act"], a["z"], a["ld_z"], 4, a["K"],
+                                       32, P, P, NUL, P, a["wsb"], NUL) == status
+
+
+def test_the_bindings_refuse_host_tensors():
+    import torch
+
+    import mixture_experts_routed_top_gb300 as m
+    t = torch.zeros(4, 8)
+    for call in (lambda: m.gated_linear(t, t), lambda: m.gated_linear_backward(t, t, t, t)):
+        with pytest.raises(ValueError):
+            call()
