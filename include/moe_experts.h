@@ -631,12 +631,50 @@ moe_status moe_gated_linear_backward(const void* grad_h, int64_t ld_gh, const vo
                                      float* dbias, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * moe_quantize_fp8_rows - e4m3 codes of rows, a scale per 1 x 128 of them.
+ *   x         device bf16 [T, K], rows ld_x apart
+ *   q         device e4m3 bytes [T, K] out, rows K apart
+ *   scale     device out, fp32 or UE8M0 bytes (scale_fmt): that of row t and block kb at
+ *             scale[t * s_row + kb * s_kb]
+ * The scale is amax / 448 in fp32, at least 2^-126, or the smallest power of two that is no
+ * smaller; 1 where amax is 0, infinite (byte 255) where it is.  Codes round x * (1 / scale)
+ * to nearest, ties to even.
+ * K % 128 == 0 and ld_x a multiple of 8, else MOE_ERR_UNSUPPORTED.  T = 0 is a no-op.
+ */
+moe_status moe_quantize_fp8_rows(const void* x, int64_t ld_x, int T, int K, moe_scale_fmt scale_fmt,
+                                 void* q, void* scale, int64_t s_row, int64_t s_kb, void* stream);
+
+/*
+ * moe_linear_fp8 - out = residual + act(x w^T + bias) of e4m3 operands with a scale per 1 x
+ * 128 of x and per 128 x 128 of w.  The sums of a block of 128 are the tensor core's, scaled
+ * and added in fp32.
+ *   x         device e4m3 bytes [T, K] with x_scale (strides as above, of scale_fmt); or,
+ *             where x_scale is NULL, bf16 [T, K], which is quantised as
+ *             moe_quantize_fp8_rows does
+ *   w         device e4m3 bytes [N, K], rows ld_w apart
+ *   w_scale   device [ceil(N / 128), K / 128] of scale_fmt
+ *   bias, act, residual, out   as in moe_linear
+ *   ws        device scratch, 256-byte aligned, at least moe_linear_fp8_workspace_size()
+ *             bytes (where x_scale is given moe_linear_workspace_size() do); head as in
+ *             moe_linear
+ * K % 128 == 0 and rows of x and w 16-byte aligned, else MOE_ERR_UNSUPPORTED; any T, N.
+ * T = 0 or N = 0 is a no-op.
+ */
+size_t moe_linear_fp8_workspace_size(int T, int K);
+moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int64_t s_row, int64_t s_kb,
+                          const void* w, int64_t ld_w, const void* w_scale,
+                          moe_scale_fmt scale_fmt, const void* bias, moe_dtype bias_dt, int act,
+                          const void* residual, int64_t ld_res, int T, int K, int N, void* out,
+                          moe_dtype out_dt, int64_t ld_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * moe_call_packed - one of the calls above with its arguments in a block of
  * 8-byte slots in the function's order: pointers and integers as int64_t,
  * floats as double.  For bindings that pay per argument.
  *   call   0 moe_route_scored, 1 moe_route_scored_backward, 2 moe_block_norm,
  *          3 moe_block_norm_backward, 4 moe_linear, 5 moe_linear_backward,
- *          7 moe_gated_linear, 8 moe_gated_linear_backward;
+ *          7 moe_gated_linear, 8 moe_gated_linear_backward, 9 moe_quantize_fp8_rows,
+ *          10 moe_linear_fp8;
  *          any other: MOE_ERR_INVALID_ARG
  *   block  the slots; a size that no int holds: MOE_ERR_UNSUPPORTED
  */

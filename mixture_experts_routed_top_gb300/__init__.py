@@ -26,7 +26,7 @@ __all__ = [
     "get_decode_single", "set_tile_group", "get_tile_group", "set_pair_gemm", "get_pair_gemm", "set_down_l2_hints", "get_down_l2_hints", "set_down_phases",
     "get_down_phases",
     "route_scored", "route_scored_backward", "block_norm", "block_norm_backward", "linear", "linear_backward",
-    "gated_linear", "gated_linear_backward",
+    "gated_linear", "gated_linear_backward", "quantize_fp8_rows", "linear_fp8",
     "Workspace", "STATUS", "STAGES", "W_BF16", "W_FP8_E4M3", "W_FP4_E2M1", "SCALE_NONE", "SCALE_F32",
     "SCALE_UE8M0", "ACTIVATIONS",
 ]
@@ -102,6 +102,10 @@ _SIGS = {
     "moe_gated_linear_backward_workspace_size": ([_I, _I], _SZ),
     "moe_gated_linear_backward": ([_P, _L, _P, _L, _P, _L, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _SZ,
                                    _P], _I),
+    "moe_quantize_fp8_rows": ([_P, _L, _I, _I, _I, _P, _P, _L, _L, _P], _I),
+    "moe_linear_fp8_workspace_size": ([_I, _I], _SZ),
+    "moe_linear_fp8": ([_P, _L, _P, _L, _L, _P, _L, _P, _I, _P, _I, _I, _P, _L, _I, _I, _I, _P, _I, _L, _P,
+                        _SZ, _P], _I),
     "moe_linear_backward": ([_P, _I, _L, _P, _L, _P, _L, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _SZ,
                              _P], _I),
 }
@@ -429,6 +433,8 @@ _LINEAR = (4, struct.Struct("=19q").pack)
 _LINEAR_BWD = (5, struct.Struct("=19q").pack)
 _GATED = (7, struct.Struct("=16q").pack)
 _GATED_BWD = (8, struct.Struct("=18q").pack)
+_FP8_ROWS = (9, struct.Struct("=10q").pack)
+_LINEAR_FP8 = (10, struct.Struct("=23q").pack)
 
 
 def _bad(name: str, what: str):
@@ -860,6 +866,97 @@ def gated_linear_backward(grad_h: torch.Tensor, x: torch.Tensor, w: torch.Tensor
     _call(_GATED_BWD, dev, grad_h.data_ptr(), ld_g, x.data_ptr(), ld_x, w.data_ptr(), ld_w, act, preact.data_ptr(),
           ld_z, T, K, I, pdx, pdw, pdb, ws.data_ptr(), ws.numel())
     return dx, dw, db
+
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+_SCALE_DT = {_F32: SCALE_F32, torch.uint8: SCALE_UE8M0}
+
+
+def quantize_fp8_rows(x: torch.Tensor, scale_fmt: str = "f32", *,
+                      out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None, stream=None):
+    """bf16 [T,K] -> (e4m3 codes uint8 [T,K], scales [T,K/128] of its 1x128 blocks as
+    fp32 ('f32') or uint8 exponent bytes ('ue8m0')), for linear_fp8.
+
+    K a multiple of 128.  The scales lie by K block (strides (1, T)), as
+    linear_fp8 reads them best.  out: (codes, scales) to write into, codes
+    contiguous, scales with any positive strides."""
+    if stream is not None:
+        return _on_stream(quantize_fp8_rows, locals())
+    dev, xs = _matrix_of("x", x)
+    T, K = xs
+    ld_x = _mat("x", x, _ONLY_BF16, xs, dev)
+    sf = _SCALE_BY_NAME.get(scale_fmt, SCALE_NONE)
+    if sf == SCALE_NONE:
+        raise ValueError("scale_fmt must be 'f32' or 'ue8m0'")
+    if out is None:
+        q = torch.empty(xs, dtype=torch.uint8, device=x.device)
+        pq = q.data_ptr()
+        s = torch.empty((K // 128, T), dtype=_F32 if sf == SCALE_F32 else torch.uint8, device=x.device).t()
+    else:
+        q, s = out
+        pq = _dense("codes", q, _E4M3, xs, dev)
+    ps, s_row, s_kb = _row_scales("scales", s, sf, xs, dev)
+    _call(_FP8_ROWS, dev, x.data_ptr(), ld_x, T, K, sf, pq, ps, s_row, s_kb)
+    return q, s
+
+
+def _row_scales(name: str, s: torch.Tensor, sf: int, xs, dev: int):
+    """Checks the scales of a matrix's 1x128 blocks; -> (address, strides of row and block)."""
+    shape = (xs[0], xs[1] // 128)
+    if s.shape != shape or _SCALE_DT.get(s.dtype) != sf or s.get_device() != dev:
+        _bad(name, f"a tensor {list(shape)} of {'float32' if sf == SCALE_F32 else 'uint8'} on CUDA device {dev}")
+    a, b = s.stride()
+    return s.data_ptr(), max(a, 1) if shape[0] == 1 else a, max(b, 1) if shape[1] == 1 else b
+
+
+def linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
+               x_scale: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               workspace: Optional[Workspace] = None, stream=None) -> torch.Tensor:
+    """residual + act(x w^T + bias) -> [T,N] of 8-bit operands with block scales.
+
+    w e4m3 [N,K] (uint8 or float8_e4m3fn), K a multiple of 128, N any; w_scale
+    [ceil(N/128), K/128] of its 128x128 blocks: fp32, or uint8 UE8M0 exponent
+    bytes (quantize_fp8_blocks).  x bf16 [T,K], quantised in 1x128 blocks with
+    scales of w_scale's format on the way; or e4m3 with x_scale [T,K/128] of
+    that format (quantize_fp8_rows), any strides.  bias, activation, residual,
+    out_dtype, out, workspace: as in linear."""
+    global _LINEAR_WS
+    if stream is not None:
+        return _on_stream(linear_fp8, locals())
+    dev, xs = _matrix_of("x", x)
+    T, K = xs
+    ld_x = _mat("x", x, _ONLY_BF16 if x_scale is None else _E4M3, xs, dev)
+    N = w.shape[0]
+    ld_w = _mat("w", w, _E4M3, (N, K), dev)
+    sf = _SCALE_DT.get(w_scale.dtype)
+    pws = _dense("w_scale", w_scale, _SCALE_DT, ((N + 127) // 128, K // 128), dev)
+    px, s_row, s_kb = (0, 0, 0) if x_scale is None else _row_scales("x_scale", x_scale, sf, xs, dev)
+    shape = (T, N)
+    if out is None:
+        dt = _DT.get(out_dtype)
+        if dt is None:
+            _bad("out_dtype", _names(_DT))
+        out = torch.empty(shape, dtype=out_dtype, device=x.device)
+        ld_o = N
+    else:
+        ld_o = _mat("out", out, _DT, shape, dev)
+        out_dtype = out.dtype
+        dt = _DT[out_dtype]
+    pb = bdt = pr = ld_r = 0
+    if bias is not None:
+        pb, bdt = _dense("bias", bias, _DT, (N,), dev), _DT[bias.dtype]
+    if residual is not None:
+        pr, ld_r = residual.data_ptr(), _mat("residual", residual, (out_dtype,), shape, dev)
+    if x_scale is None:
+        need = (_LIB or lib()).moe_linear_fp8_workspace_size(T, K)
+    else:
+        need = _LINEAR_WS = _LINEAR_WS or lib().moe_linear_workspace_size()
+    ws = _workspace(workspace, dev, need)
+    _call(_LINEAR_FP8, dev, x.data_ptr(), ld_x, px, s_row, s_kb, w.data_ptr(), ld_w, pws, sf, pb, bdt,
+          _act(activation), pr, ld_r, T, K, N, out.data_ptr(), dt, ld_o, ws.data_ptr(), ws.numel())
+    return out
 
 
 # ------------------------------------------------------------------ FP8

@@ -36,8 +36,10 @@ int device_sms() {
 
 bool ptr_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-moe_status make_map_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
-                            uint64_t ld, uint32_t box_inner, uint32_t box_outer) {
+namespace {
+moe_status make_map_2d(CUtensorMap* m, CUtensorMapDataType type, uint64_t size, const void* base,
+                       uint64_t inner, uint64_t outer, uint64_t ld, uint32_t box_inner,
+                       uint32_t box_outer) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -51,16 +53,25 @@ moe_status make_map_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, ui
   if (!fn)
     return set_last_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {ld * 2};
+  cuuint64_t strides[1] = {ld * size};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = fn(m, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return set_last_error(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return MOE_OK;
+}
+}  // namespace
+
+moe_status make_map_bf16_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                            uint64_t ld, uint32_t box_inner, uint32_t box_outer) {
+  return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, inner, outer, ld, box_inner, box_outer);
+}
+moe_status make_map_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                          uint64_t ld) {
+  return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, inner, outer, ld, 128, 128);
 }
 
 }  // namespace moe
@@ -228,6 +239,33 @@ moe_status check_gated(const char* fn, int64_t ld_x, int64_t ld_w, int act, int 
   if (I > kGatedMaxI) return set_last_error(MOE_ERR_UNSUPPORTED, "%s: I above 2^30 - 1", fn);
   return check_linear(fn, ld_x, ld_w, act, T, K, I);
 }
+
+moe_status check_fp8(const char* fn, int64_t ld_x, int align, int T, int K, int scale_fmt) {
+  if (T < 0) return set_last_error(MOE_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (K < 128 || K % 128)
+    return set_last_error(MOE_ERR_UNSUPPORTED, "%s: K must be a positive multiple of 128", fn);
+  if (scale_fmt != MOE_SCALE_F32 && scale_fmt != MOE_SCALE_UE8M0)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: unknown scale format %d", fn, scale_fmt);
+  if (ld_x < K) return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride below K", fn);
+  if (ld_x % align)
+    return set_last_error(MOE_ERR_UNSUPPORTED, "%s: row strides must be multiples of 16 bytes", fn);
+  return MOE_OK;
+}
+
+bool scale_aligned(const void* p, int fmt) { return ptr_aligned(p, fmt == MOE_SCALE_F32 ? 4 : 1); }
+
+struct Fp8Ws {
+  size_t codes, scales, total;
+};
+Fp8Ws fp8_ws(int T, int K) {
+  Fp8Ws w;
+  w.codes = kLinearWsBytes;
+  w.scales = w.codes + (static_cast<size_t>(T) * K + 1023) / 1024 * 1024;
+  w.total = w.scales + static_cast<size_t>(T) * (K / 128) * 4;
+  return w;
+}
+// Up to this many tokens the kernel that streams the weights quantises them itself.
+constexpr int kFp8QuantiseOnTheWay = 8;
 
 }  // namespace
 
@@ -725,6 +763,112 @@ moe_status moe_gated_linear_backward(const void* grad_h, int64_t ld_gh, const vo
   return gradient_products(a.dz, a.dz_lo, L.ld_dz, x, ld_x, w, ld_w, T, K, N, dx, dw, wsb, s, fn);
 }
 
+moe_status moe_quantize_fp8_rows(const void* x, int64_t ld_x, int T, int K, moe_scale_fmt scale_fmt,
+                                 void* q, void* scale, int64_t s_row, int64_t s_kb, void* stream) {
+  const char* fn = "moe_quantize_fp8_rows";
+  moe_status st = check_fp8(fn, ld_x, 8, T, K, scale_fmt);
+  if (st != MOE_OK) return st;
+  if (s_row < 1 || s_kb < 1)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: scale strides must be positive", fn);
+  if (T == 0) return MOE_OK;
+  if (!x || !q || !scale) return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!all16(x, q) || !scale_aligned(scale, scale_fmt))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: x and q must be 16-byte aligned, scales as their type", fn);
+  const cudaError_t e = launch_fp8_rows({static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(q),
+                                         scale, ld_x, s_row, s_kb, T, K / 128,
+                                         scale_fmt == MOE_SCALE_UE8M0},
+                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+}
+
+size_t moe_linear_fp8_workspace_size(int T, int K) { return T < 0 || K < 0 ? 0 : fp8_ws(T, K).total; }
+
+moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int64_t s_row, int64_t s_kb,
+                          const void* w, int64_t ld_w, const void* w_scale,
+                          moe_scale_fmt scale_fmt, const void* bias, moe_dtype bias_dt, int act,
+                          const void* residual, int64_t ld_res, int T, int K, int N, void* out,
+                          moe_dtype out_dt, int64_t ld_out, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_linear_fp8";
+  moe_status st = check_fp8(fn, ld_x, x_scale ? 16 : 8, T, K, scale_fmt);
+  if (st != MOE_OK) return st;
+  if (N < 0) return set_last_error(MOE_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (!is_act(act)) return set_last_error(MOE_ERR_INVALID_ARG, "%s: unknown activation %d", fn, act);
+  if (!is_dtype(out_dt) || (bias && !is_dtype(bias_dt)))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  if (ld_w < K) return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride below K", fn);
+  if (ld_w % 16)
+    return set_last_error(MOE_ERR_UNSUPPORTED, "%s: row strides must be multiples of 16 bytes", fn);
+  if (x_scale && (s_row < 1 || s_kb < 1))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: scale strides must be positive", fn);
+  if (ld_out < N || (residual && ld_res < N))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride below N", fn);
+  if (T == 0 || N == 0) return MOE_OK;
+  if (!x || !w || !w_scale || !out) return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (residual == out && ld_res != ld_out)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: in place only with the same row stride", fn);
+  if (!all16(x, w, bias, residual, out) || !scale_aligned(x_scale, scale_fmt) ||
+      !scale_aligned(w_scale, scale_fmt))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned, scales as their type", fn);
+  const Fp8Ws L = fp8_ws(T, K);
+  if ((st = check_ws(fn, ws, ws_bytes, x_scale ? kLinearWsBytes : L.total)) != MOE_OK) return st;
+  uint8_t* const wsb = static_cast<uint8_t*>(ws);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  LinearEpi e{};
+  e.bias = bias;
+  e.residual = residual;
+  e.out = out;
+  e.ld_res = ld_res;
+  e.ld_out = ld_out;
+  e.M = T;
+  e.N = N;
+  e.act = act;
+  e.bias_bf16 = bias_dt == MOE_DT_BF16;
+  e.out_f32 = out_dt == MOE_DT_F32;
+  e.vec = N % 8 == 0 && rows16(ld_out, size_of(out_dt)) &&
+          (!residual || rows16(ld_res, size_of(out_dt)));
+  Fp8Scales sc{x_scale, w_scale, s_row, s_kb, scale_fmt == MOE_SCALE_UE8M0};
+  const int KB = K / 128;
+  const bool streams = fp8_streams(T, N);
+  if (!x_scale && !(streams && T <= kFp8QuantiseOnTheWay)) {
+    // codes, and scales by K block: what neighbouring rows need lies together
+    const cudaError_t r = launch_fp8_rows({static_cast<const __nv_bfloat16*>(x), wsb + L.codes,
+                                           wsb + L.scales, ld_x, 1, T, T, KB, sc.ue8m0 != 0}, s);
+    if (r != cudaSuccess) return cuda_error(r, fn);
+    x = wsb + L.codes;
+    ld_x = K;
+    sc.x = wsb + L.scales;
+    sc.x_row = 1;
+    sc.x_kb = T;
+  }
+  if (streams) {
+    Fp8StreamArgs g;
+    g.x = x;
+    g.w = static_cast<const uint8_t*>(w);
+    g.ld_x = ld_x;
+    g.ld_w = ld_w;
+    g.sc = sc;
+    g.KB = KB;
+    g.codes = sc.x != nullptr;
+    g.wpr = g.split = 1;
+    g.epi = e;
+    const cudaError_t r = launch_fp8_stream(g, device_sms(), s);
+    return r == cudaSuccess ? MOE_OK : cuda_error(r, fn);
+  }
+  CUtensorMap tx, tw;
+  if ((st = make_map_u8_2d(&tx, x, K, T, ld_x)) != MOE_OK) return st;
+  if ((st = make_map_u8_2d(&tw, w, K, N, ld_w)) != MOE_OK) return st;
+  Fp8LinearDev p;
+  p.epi = e;
+  p.sc = sc;
+  p.KB = KB;
+  p.split = 1;
+  p.group = 0;
+  p.parts = reinterpret_cast<float*>(wsb + 1024);
+  p.err = static_cast<int*>(ws);
+  const cudaError_t r = launch_fp8_linear(tx, tw, p, fp8_path(T, N, K, device_sms()), s);
+  return r == cudaSuccess ? MOE_OK : cuda_error(r, fn);
+}
+
 // The Python binding's way in: converting 14 to 29 arguments one by one took longer
 // there than launching the kernel.
 moe_status moe_call_packed(int call, const void* block) {
@@ -740,6 +884,8 @@ moe_status moe_call_packed(int call, const void* block) {
     case 5: return a.call(moe_linear_backward);
     case 7: return a.call(moe_gated_linear);
     case 8: return a.call(moe_gated_linear_backward);
+    case 9: return a.call(moe_quantize_fp8_rows);
+    case 10: return a.call(moe_linear_fp8);
   }
   return set_last_error(MOE_ERR_INVALID_ARG, "moe_call_packed: unknown call %d", call);
 }

@@ -819,13 +819,6 @@ __device__ __forceinline__ void warp_mma(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-constexpr int kStreamWarps = 8;
 // NT: groups of 8 tokens; G: steps of 32 of the contraction per group.
 template <int NT>
 struct StreamLay {
@@ -892,52 +885,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s_part[warp][8 * q + 2 * t + (i & 1)][g + 8 * (i >> 1)] = sum[q][i];
   __syncthreads();
-  const LinearEpi& p = a.epi;
-  const int count = tiles * TOK * 16;  // (tile, token, row), the row fastest
-  if (S > 1) {
-    for (int i = threadIdx.x; i < count; i += kStreamWarps * 32) {
-      const int tl = i / (TOK * 16), tok = i / 16 % TOK, r = i % 16;
-      float z = 0.f;
-      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
-      (&s_sum[0][0][0])[i] = z;
-    }
-    __syncwarp();
-    cluster_sync_all();
-  }
-  // the sum of one (tile, token, row) over the blocks or the warps
-  auto total = [&](int tl, int tok, int r) {
-    float z = 0.f;
-    if (S > 1) {
-      const uint32_t at = smem_u32(&s_sum[0][0][0] + (tl * TOK + tok) * 16 + r);
-#pragma unroll 8
-      for (int q = 0; q < S; ++q) z += ld_cluster_f32(mapa_shared(at, q));
-    } else {
-      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
-    }
-    return z;
-  };
-  // the blocks of a cluster share the results out among them
-  const int results = tiles * TOK * OUT;
-  for (int i = threadIdx.x + rank * (kStreamWarps * 32); i < results; i += S * (kStreamWarps * 32)) {
-    const int tl = i / (TOK * OUT), tok = i / OUT % TOK, r = i % OUT, n = (tile0 + tl) * OUT + r;
-    if (n >= N || tok >= T) continue;
-    float z = total(tl, tok, r);
-    if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
-    if (GATED) {
-      float zu = total(tl, tok, 8 + r);
-      if (p.bias != nullptr) zu += ldf(p.bias, N + n, p.bias_bf16);
-      gated1<MOE_ACT_NONE>(p, tok, n, z, zu);
-      continue;
-    }
-    if (p.preact != nullptr) stf(p.preact, tok * p.ld_out + n, p.out_f32, z);
-    z = act_f(z, p.act, p.out_f32);
-    if (p.residual != nullptr) z += ldf(p.residual, tok * p.ld_res + n, !p.out_f32);
-    stf(p.out, tok * p.ld_out + n, p.out_f32, z);
-  }
-  if (S > 1) {
-    __syncwarp();
-    cluster_sync_all();  // the others have read this block's sums
-  }
+  stream_results<TOK, GATED>(a.epi, s_part, s_sum, wpr, S, rank, tiles, tile0);
 }
 
 // ====================================================== dz and dbias

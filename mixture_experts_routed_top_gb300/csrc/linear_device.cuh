@@ -596,6 +596,70 @@ __device__ __forceinline__ void join_rows_gated(const LinearEpi& p, float* stg, 
   }
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// The end of the kernels of few tokens.  s_part: each warp's sums [token][row] of its
+// tile of 16 weight rows; `wpr` warps of each of the S blocks of a cluster share a
+// tile.  The warps' sums are added in order, then the blocks', through the
+// cluster's shared memory (half a kilobyte each), and the results shared out.
+constexpr int kStreamWarps = 8;
+template <int TOK, bool GATED>
+__device__ __forceinline__ void stream_results(const LinearEpi& p, const float (*s_part)[TOK][17],
+                                               float (*s_sum)[TOK][16], int wpr, int S, int rank,
+                                               int tiles, int tile0) {
+  constexpr int OUT = GATED ? 8 : 16;  // outputs of a tile
+  const int count = tiles * TOK * 16;  // (tile, token, row), the row fastest
+  const int N = p.N, T = p.M;
+  if (S > 1) {
+    for (int i = threadIdx.x; i < count; i += kStreamWarps * 32) {
+      const int tl = i / (TOK * 16), tok = i / 16 % TOK, r = i % 16;
+      float z = 0.f;
+      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
+      (&s_sum[0][0][0])[i] = z;
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
+  // the sum of one (tile, token, row) over the blocks or the warps
+  auto total = [&](int tl, int tok, int r) {
+    float z = 0.f;
+    if (S > 1) {
+      const uint32_t at = smem_u32(&s_sum[0][0][0] + (tl * TOK + tok) * 16 + r);
+#pragma unroll 8
+      for (int q = 0; q < S; ++q) z += ld_cluster_f32(mapa_shared(at, q));
+    } else {
+      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
+    }
+    return z;
+  };
+  // the blocks of a cluster share the results out among them
+  const int results = tiles * TOK * OUT;
+  for (int i = threadIdx.x + rank * (kStreamWarps * 32); i < results; i += S * (kStreamWarps * 32)) {
+    const int tl = i / (TOK * OUT), tok = i / OUT % TOK, r = i % OUT, n = (tile0 + tl) * OUT + r;
+    if (n >= N || tok >= T) continue;
+    float z = total(tl, tok, r);
+    if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
+    if (GATED) {
+      float zu = total(tl, tok, 8 + r);
+      if (p.bias != nullptr) zu += ldf(p.bias, N + n, p.bias_bf16);
+      gated1<MOE_ACT_NONE>(p, tok, n, z, zu);
+      continue;
+    }
+    if (p.preact != nullptr) stf(p.preact, tok * p.ld_out + n, p.out_f32, z);
+    z = act_f(z, p.act, p.out_f32);
+    if (p.residual != nullptr) z += ldf(p.residual, tok * p.ld_res + n, !p.out_f32);
+    stf(p.out, tok * p.ld_out + n, p.out_f32, z);
+  }
+  if (S > 1) {
+    __syncwarp();
+    cluster_sync_all();  // the others have read this block's sums
+  }
+}
+
 // Tile order: groups of `group` row tiles, all column tiles of a group
 // before the next, so the tiles in flight share operand rows in L2.
 __device__ __forceinline__ void pair_tile(int tile, int mt, int nt, int group, int* mi, int* ni) {

@@ -1,0 +1,772 @@
+// Dense products of 8-bit operands: y = residual + act(x w^T + bias) with e4m3 codes, a
+// scale per 1 x 128 of x (a token, 128 of the contraction) and one per 128 x 128 of w,
+// and the quantiser of such rows:
+//   z[t, n] = sum_kb sx[t, kb] sw[n / 128, kb] (sum_{k in kb} qx[t, k] qw[n, k])
+// A block of 128 of the contraction is one 128-byte swizzled row of an operand and one
+// scale of each: the inner sums come from the tensor core (products of e4m3 are exact
+// in it), and are multiplied by their scales and added in fp32 registers.
+//
+// The kernels, chosen by fp8_streams() and fp8_path():
+//   fp8_pair_kernel    256 x 256 tiles on CTA pairs, persistent: large products
+//   fp8_tile_kernel    128 x 128 tiles, the contraction split over a cluster: few tiles
+//   fp8_stream_kernel  a few tokens: the weights streamed into registers
+//   fp8_rows_kernel    the rows' codes and scales, before the first two
+#include <algorithm>
+#include <atomic>
+
+#include "linear_device.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kB = 128;  // e4m3 per 128-byte swizzled row = one scale block
+
+__device__ __forceinline__ float scale_at(const void* base, long i, int ue8m0) {
+  if (ue8m0) {
+    const uint32_t b = __ldg(static_cast<const uint8_t*>(base) + i);
+    return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
+  }
+  return __ldg(static_cast<const float*>(base) + i);
+}
+// Of a block of a row from its absolute maximum, as the weights' quantiser, but no
+// less than 2^-126, whose reciprocal is still a number; *stored: bits or exponent byte.
+// An infinity makes an infinite scale (byte 255), which makes its row NaN.
+__device__ __forceinline__ float row_scale(float amax, bool ue8m0, uint32_t* stored) {
+  if (amax == 0.f) {
+    *stored = ue8m0 ? 127u : __float_as_uint(1.0f);
+    return 1.0f;
+  }
+  const float q = fmaxf(amax / 448.0f, __uint_as_float(0x00800000u));
+  if (!ue8m0) {
+    *stored = __float_as_uint(q);
+    return q;
+  }
+  if (!(q < INFINITY)) {
+    *stored = 255u;
+    return INFINITY;
+  }
+  return ue8m0_ceil(q, stored);
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return static_cast<uint32_t>(e4m3x2(a, b)) | (static_cast<uint32_t>(e4m3x2(c, d)) << 16);
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ float amax8(const uint4& u) {
+  float v[8], m = 0.f;
+  unpack8(u, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  return m;
+}
+__device__ __forceinline__ uint2 codes8(const uint4& u, float inv) {
+  float v[8];
+  unpack8(u, v);
+  return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                    e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+
+// ====================================================== rows of codes
+// Bound by memory.  A block takes 32 rows x 512 columns; 16 lanes hold a 1 x 128 block,
+// 16 bytes each, and a thread's 8 loads are on their way before the first is used.  The
+// scales leave through shared memory, so that those of a K block, neighbours in the
+// layout that the products read best, are written in whole lines.
+__global__ void __launch_bounds__(256) fp8_rows_kernel(const __grid_constant__ Fp8RowsArgs a) {
+  pdl_launch_dependents();
+  __shared__ uint32_t s_scale[4][32];
+  const int hw = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const int t0 = blockIdx.x * 32, kb0 = blockIdx.y * 4;
+  pdl_wait();
+  uint4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int u = hw + 16 * i, t = t0 + (u >> 2), kb = kb0 + (u & 3);
+    v[i] = t < a.T && kb < a.KB
+               ? __ldg(reinterpret_cast<const uint4*>(a.x + t * a.ld_x + kb * kB) + l)
+               : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int u = hw + 16 * i, t = t0 + (u >> 2), kb = kb0 + (u & 3);
+    float m = amax8(v[i]);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    uint32_t stored;
+    const float inv = 1.0f / row_scale(m, a.ue8m0, &stored);
+    if (t < a.T && kb < a.KB)
+      reinterpret_cast<uint2*>(a.q + (static_cast<long>(t) * a.KB + kb) * kB)[l] = codes8(v[i], inv);
+    if (l == 0) s_scale[u & 3][u >> 2] = stored;
+  }
+  __syncthreads();
+  const int i = threadIdx.x;
+  if (i >= 128) return;
+  const int t = t0 + (i & 31), kb = kb0 + (i >> 5);
+  if (t >= a.T || kb >= a.KB) return;
+  const long at = t * a.s_row + kb * a.s_kb;
+  if (a.ue8m0) static_cast<uint8_t*>(a.scale)[at] = static_cast<uint8_t>(s_scale[i >> 5][i & 31]);
+  else static_cast<uint32_t*>(a.scale)[at] = s_scale[i >> 5][i & 31];
+}
+
+// ====================================================== promotion
+// The sums of one K block, 64 columns of this thread's row, from TMEM at `taddr`, times
+// s, added to acc.  `release` runs once all of them have been read.
+template <typename Release>
+__device__ __forceinline__ void promote(uint32_t taddr, float s, float (&acc)[64], Release release) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint32_t v[16];
+    tmem_ld_32x32b_x16(taddr + 16 * h, v);
+    tmem_ld_wait_x16(v);
+    if (h == 3) release();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[16 * h + i] = fmaf(__uint_as_float(v[i]), s, acc[16 * h + i]);
+  }
+}
+
+// ====================================================== CTA-pair kernel
+// 256 x 256 tiles, cta_group::2: each CTA holds 128 rows of x and 128 of w per stage, and
+// 128 rows x 256 columns of the sums of two K blocks in TMEM, one of them being filled
+// while the other is promoted.  Roles (576 threads): warp 0 loads, warp 1 MMAs (rank
+// 0), warps 2-17 promotion and epilogue: thread = row, four groups of 64 columns.
+// Barriers as in the bf16 pair kernel; every wait is bounded.
+constexpr int kStages = 5;
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kOper = 128 * kB;                    // 16 KB: one operand's part of a stage
+constexpr int kOffBar = 2 * kStages * kOper;
+constexpr int kBars = 2 * kStages + 5;
+constexpr int kOffMisc = kOffBar + kBars * 8;
+constexpr int kOffTurn = (kOffMisc + 8 + 15) / 16 * 16;
+constexpr int kSmem = kOffTurn + kEpiWarps * kTurn * 4 + 1024;
+static_assert(kOffMisc % 8 == 0 && kSmem <= 227 * 1024, "shared memory");
+
+template <int ACT, bool F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                    const __grid_constant__ Fp8LinearDev p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);  // rank 0: both CTAs' loads landed
+  uint64_t* empty = full + kStages;        // both: the stage's MMAs are done
+  uint64_t* pfull = empty + kStages;       // both: sums of a K block complete
+  uint64_t* pempty = pfull + 2;            // rank 0: both CTAs have read them
+  uint64_t* fin = pempty + 2;              // rank 0: every MMA done
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank() & 1u);
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&pfull[b]), 1);
+      mbar_init(smem_u32(&pempty[b]), 2 * kEpiWarps);
+    }
+    mbar_init(smem_u32(fin), 1);
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  cluster_sync_all();  // the pair's barriers are up
+  if (warp == 1) tmem_alloc_pair(smem_u32(s_tmem), 512);
+  pdl_wait();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the pair's TMEM is allocated in both CTAs
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int mt = (p.epi.M + 255) >> 8, nt = (p.epi.N + 255) >> 8;
+  const int total = mt * nt, KB = p.KB;
+  const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 0, issued = 0, last_par = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < total; tile += ncl) {
+        int mi, ni;
+        pair_tile(tile, mt, nt, p.group, &mi, &ni);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait_pair(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err, ERR_TIMEOUT_PRODUCER)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb_local = smem_u32(&full[stage]);
+          if (rank == 0) mbar_arrive_expect_tx(fb_local, 4u * kOper);
+          const uint32_t fb = mapa_shared(fb_local, 0);
+          const uint32_t a_dst = smem_u32(smem + 2 * stage * kOper);
+          tma_load_2d_pair(&tm_a, fb, a_dst, kb * kB, mi * 256 + 128 * rank);
+          tma_load_2d_pair(&tm_b, fb, a_dst + kOper, kb * kB, ni * 256 + 128 * rank);
+          issued |= 1u << stage;
+          last_par = (last_par & ~(1u << stage)) | (ph << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      // drain: rank 0 until every issued stage's loads (both CTAs') landed,
+      // rank 1 until its last loads of each stage were consumed
+      for (int s = 0; s < kStages; ++s) {
+        if ((issued >> s) & 1u) {
+          volatile int no_abort = 0;
+          wait_pair(smem_u32(rank == 0 ? &full[s] : &empty[s]), (last_par >> s) & 1u, &no_abort,
+                    p.err, ERR_TIMEOUT_PRODUCER, kDrainCycles);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(256, 256);
+      int stage = 0;
+      uint32_t ph = 0, g = 0;  // g: K blocks so far, which select the buffer
+      bool ok = true;
+      for (int tile = cid; ok && tile < total; tile += ncl) {
+        for (int kb = 0; kb < KB; ++kb, ++g) {
+          const int b = g & 1;
+          if (!wait_pair(smem_u32(&pempty[b]), ((g >> 1) & 1) ^ 1u, s_abort, p.err, ERR_TIMEOUT_MMA) ||
+              !wait_pair(smem_u32(&full[stage]), ph, s_abort, p.err, ERR_TIMEOUT_MMA)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t as = smem_u32(smem + 2 * stage * kOper);
+          const uint64_t ad = sdesc_k_sw128(as), bd = sdesc_k_sw128(as + kOper);
+#pragma unroll
+          for (int kk = 0; kk < kB / 32; ++kk)
+            umma_f8_pair(tmem + b * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+          umma_commit_pair_both(smem_u32(&empty[stage]));
+          umma_commit_pair_both(smem_u32(&pfull[b]));
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (g > 0) {
+        umma_commit_pair_local(smem_u32(fin));
+        volatile int no_abort = 0;
+        wait_pair(smem_u32(fin), 0, &no_abort, p.err, ERR_TIMEOUT_MMA);
+      }
+    }
+  } else {
+    const int q = warp & 3, grp = (warp - 2) >> 2;  // TMEM lane quarter, 64 columns
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64 * grp;
+    float* const turn = reinterpret_cast<float*>(smem + kOffTurn) + (warp - 2) * kTurn;
+    const int nb = (p.epi.N + kB - 1) / kB;  // rows of weight scales
+    uint32_t g = 0;
+    int ok = 1;
+    for (int tile = cid; tile < total; tile += ncl) {
+      int mi, ni;
+      pair_tile(tile, mt, nt, p.group, &mi, &ni);
+      const long m = static_cast<long>(mi) * 256 + 128 * rank + 32 * q + lane;
+      const bool valid = m < p.epi.M;
+      const long wbase = static_cast<long>(min(2 * ni + (grp >> 1), nb - 1)) * KB;
+      float acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+      // the scales of a K block are loaded while the one before it is promoted
+      float sx = valid ? scale_at(p.sc.x, m * p.sc.x_row, p.sc.ue8m0) : 0.f;
+      float sw = scale_at(p.sc.w, wbase, p.sc.ue8m0);
+#pragma unroll 1
+      for (int kb = 0; kb < KB; ++kb, ++g) {
+        const int b = g & 1;
+        const float s = sx * sw;
+        if (kb + 1 < KB) {
+          sx = valid ? scale_at(p.sc.x, m * p.sc.x_row + (kb + 1) * p.sc.x_kb, p.sc.ue8m0) : 0.f;
+          sw = scale_at(p.sc.w, wbase + kb + 1, p.sc.ue8m0);
+        }
+        if (lane == 0)
+          ok = wait_pair(smem_u32(&pfull[b]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        promote(tl + b * 256, s, acc, [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (rank == 0) mbar_arrive(smem_u32(&pempty[b]));
+            else mbar_arrive_remote(mapa_shared(smem_u32(&pempty[b]), 0));
+          }
+        });
+      }
+      if (!ok) break;
+      const int n0 = ni * 256 + 64 * grp;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        uint32_t v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * s + i]);
+        if (n0 + 32 * s < p.epi.N) epilogue32<ACT, F32, false>(p.epi, m, n0 + 32 * s, v, turn);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the other may touch its shared memory
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ====================================================== split tile kernel
+// One 128 x 128 tile per cluster of S CTAs; CTA r takes the r-th part of the contraction
+// (at least one K block).  Two CTAs fit an SM (256 TMEM columns each).  8 promotion
+// warps: thread = row, two halves of 64 columns; the CTAs' sums are joined as the bf16
+// kernel's.
+constexpr int kTStages = 3;
+constexpr int kTEpiWarps = 8;
+constexpr int kTThreads = 64 + 32 * kTEpiWarps;
+constexpr int kTOffBar = 2 * kTStages * kOper;
+constexpr int kTBars = 2 * kTStages + 4;
+constexpr int kTOffMisc = kTOffBar + kTBars * 8;
+constexpr int kTSmem = kTOffMisc + 16 + 1024;
+constexpr int kTStride = 132;  // floats per staged row: 128 + 4 (no bank conflicts)
+static_assert(128 * kTStride * 4 <= kTOffBar, "staged tile fits the ring");
+
+__global__ void __launch_bounds__(kTThreads, 2)
+    fp8_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                    const __grid_constant__ Fp8LinearDev p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTOffBar);
+  uint64_t* empty = full + kTStages;
+  uint64_t* pfull = empty + kTStages;
+  uint64_t* pempty = pfull + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kTOffMisc);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kTOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.split;
+  const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&pfull[b]), 1);
+      mbar_init(smem_u32(&pempty[b]), kTEpiWarps);
+    }
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+  }
+  if (warp == 1) tmem_alloc(smem_u32(s_tmem), 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  const uint32_t tmem = *s_tmem;
+  const int mt = (p.epi.M + 127) >> 7;
+  const int tile = blockIdx.x / S;
+  const int mi = tile % mt, ni = tile / mt;
+  const int kb0 = static_cast<int>(static_cast<long>(p.KB) * rank / S);
+  const int kb1 = static_cast<int>(static_cast<long>(p.KB) * (rank + 1) / S);
+  float* const stg = reinterpret_cast<float*>(smem);
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 0, issued = 0, last_par = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait_cta(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err, ERR_TIMEOUT_PRODUCER)) break;
+        const uint32_t fb = smem_u32(&full[stage]);
+        mbar_arrive_expect_tx(fb, 2u * kOper);
+        const uint32_t a_dst = smem_u32(smem + 2 * stage * kOper);
+        tma_load_2d(&tm_a, fb, a_dst, kb * kB, mi * 128);
+        tma_load_2d(&tm_b, fb, a_dst + kOper, kb * kB, ni * 128);
+        issued |= 1u << stage;
+        last_par = (last_par & ~(1u << stage)) | (ph << stage);
+        if (++stage == kTStages) {
+          stage = 0;
+          ph ^= 1u;
+        }
+      }
+      for (int s = 0; s < kTStages; ++s) {  // nothing in flight when the ring is reused
+        if ((issued >> s) & 1u) {
+          volatile int no_abort = 0;
+          wait_cta(smem_u32(&full[s]), (last_par >> s) & 1u, &no_abort, p.err, ERR_TIMEOUT_PRODUCER,
+                   kDrainCycles);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(128, 128);
+      int stage = 0;
+      uint32_t ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const int g = kb - kb0, b = g & 1;
+        if (!wait_cta(smem_u32(&pempty[b]), ((g >> 1) & 1) ^ 1u, s_abort, p.err, ERR_TIMEOUT_MMA) ||
+            !wait_cta(smem_u32(&full[stage]), ph, s_abort, p.err, ERR_TIMEOUT_MMA))
+          break;
+        tc_fence_after();
+        const uint32_t as = smem_u32(smem + 2 * stage * kOper);
+        const uint64_t ad = sdesc_k_sw128(as), bd = sdesc_k_sw128(as + kOper);
+#pragma unroll
+        for (int kk = 0; kk < kB / 32; ++kk)
+          umma_f8(tmem + b * 128, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+        umma_commit(smem_u32(&empty[stage]));
+        umma_commit(smem_u32(&pfull[b]));
+        if (++stage == kTStages) {
+          stage = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  }
+  float acc[64];
+  int ok = 1;
+  const int q = warp & 3, half = (warp - 2) >> 2;
+  if (warp >= 2) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) acc[i] = 0.f;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64 * half;
+    const long m = static_cast<long>(mi) * 128 + 32 * q + lane;
+    const bool valid = m < p.epi.M;
+    const long wbase = static_cast<long>(ni) * p.KB;  // ni * 128 < N
+    float sx = valid ? scale_at(p.sc.x, m * p.sc.x_row + kb0 * p.sc.x_kb, p.sc.ue8m0) : 0.f;
+    float sw = scale_at(p.sc.w, wbase + kb0, p.sc.ue8m0);
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int g = kb - kb0, b = g & 1;
+      const float s = sx * sw;
+      if (kb + 1 < kb1) {
+        sx = valid ? scale_at(p.sc.x, m * p.sc.x_row + (kb + 1) * p.sc.x_kb, p.sc.ue8m0) : 0.f;
+        sw = scale_at(p.sc.w, wbase + kb + 1, p.sc.ue8m0);
+      }
+      if (lane == 0)
+        ok = wait_cta(smem_u32(&pfull[b]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      promote(tl + b * 128, s, acc, [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&pempty[b]));
+      });
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();  // every K block has been promoted, so every load and product is done
+  tc_fence_after();
+  if (warp >= 2) {
+    float* row = stg + (32 * q + lane) * kTStride + 64 * half;
+#pragma unroll
+    for (int j = 0; j < 64; j += 4)
+      *reinterpret_cast<float4*>(row + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+  }
+  __syncthreads();
+  const int rows = 128 / S;
+  if (S > 1) {
+    hand_over<kTThreads, 16, kTStride>(stg, p.parts + static_cast<long>(blockIdx.x) * 128 * 128,
+                                       rank * rows, rows);
+    __syncwarp();
+    cluster_sync_all();  // sums handed over
+  }
+  if (warp == 1) tmem_dealloc(tmem, 256);
+  if (!*s_abort)
+    join_rows<kTThreads, 16, kTStride, false>(
+        p.epi, stg, p.parts + static_cast<long>(blockIdx.x - rank) * 128 * 128, 128l * 128, S, rank,
+        rank * rows, rows, static_cast<long>(mi) * 128, ni * 128);
+}
+
+// ====================================================== few tokens
+// As the bf16 kernel of few tokens: the codes of w go from memory into the registers of a
+// warp-level product (16 weight rows x 8 tokens x 32).  A lane's 16-byte loads are its
+// fragments: of 64 consecutive codes of a row, lane 4 g + t holds 16 t .. 16 t + 15 of
+// row g, the first 8 of them in one instruction and the others in the next; any order of
+// the contraction does, as long as both operands count it alike.  Tokens in bf16 are
+// quantised on the way by every warp that multiplies them: the four lanes of a token
+// hold a whole 1 x 128 block of it.
+__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void warp_mma_f8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+constexpr int kStreamBlocks = 2;  // K blocks that a warp asks for at once
+template <int NT, bool CODES>
+__global__ void __launch_bounds__(kStreamWarps * 32)
+    fp8_stream_kernel(const __grid_constant__ Fp8StreamArgs a) {
+  constexpr int G = kStreamBlocks, TOK = 8 * NT;
+  pdl_launch_dependents();
+  __shared__ float s_part[kStreamWarps][TOK][17];
+  __shared__ float s_sum[kStreamWarps][TOK][16];  // of a tile, over this block's warps
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wpr = a.wpr, S = a.split, rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tiles = kStreamWarps / wpr;  // of a block
+  const int tile0 = blockIdx.x / S * tiles, part = rank * wpr + warp % wpr;
+  const int n0 = (tile0 + warp / wpr) * 16;
+  const int N = a.epi.N, T = a.epi.M, KB = a.KB;
+  pdl_wait();
+  float sum[NT][4] = {};
+  if (n0 < N) {
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const bool on0 = n0 + g < N, on1 = n0 + 8 + g < N;
+    const uint8_t* w0 = a.w + static_cast<long>(n0 + g) * a.ld_w + 16 * t;
+    const uint8_t* w1 = w0 + 8 * a.ld_w;
+    const long wbase = static_cast<long>(n0 / kB) * KB;  // 16 rows lie in one scale block
+#pragma unroll 1
+    for (int kb0 = part * G; kb0 < KB; kb0 += wpr * S * G) {
+      uint4 wv[G][2][2];
+      float sw[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        const bool in = kb0 + j < KB;
+        const long k = static_cast<long>(kb0 + j) * kB;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          wv[j][h][0] = on0 && in ? ld_codes(w0 + k + 64 * h) : zero;
+          wv[j][h][1] = on1 && in ? ld_codes(w1 + k + 64 * h) : zero;
+        }
+        sw[j] = in ? scale_at(a.sc.w, wbase + kb0 + j, a.sc.ue8m0) : 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < G; ++j) {
+        if (kb0 + j >= KB) break;  // the same for the whole warp
+        const long k = static_cast<long>(kb0 + j) * kB + 16 * t;
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          const int tok = 8 * q + g;
+          uint4 xc[2] = {zero, zero};
+          float sx = 0.f;
+          if (CODES) {
+            if (tok < T) {
+              const uint8_t* x = static_cast<const uint8_t*>(a.x) + tok * a.ld_x + k;
+              xc[0] = __ldg(reinterpret_cast<const uint4*>(x));
+              xc[1] = __ldg(reinterpret_cast<const uint4*>(x + 64));
+              sx = scale_at(a.sc.x, tok * a.sc.x_row + (kb0 + j) * a.sc.x_kb, a.sc.ue8m0);
+            }
+          } else {
+            uint4 v[4] = {zero, zero, zero, zero};
+            if (tok < T) {
+              const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + tok * a.ld_x + k;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                v[i] = __ldg(reinterpret_cast<const uint4*>(x + 64 * (i >> 1) + 8 * (i & 1)));
+            }
+            float m = fmaxf(fmaxf(amax8(v[0]), amax8(v[1])), fmaxf(amax8(v[2]), amax8(v[3])));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            uint32_t stored;
+            sx = row_scale(m, a.sc.ue8m0 != 0, &stored);
+            const float inv = 1.0f / sx;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint2 lo = codes8(v[2 * h], inv), hi = codes8(v[2 * h + 1], inv);
+              xc[h] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            }
+          }
+          float c[4] = {};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 lo = wv[j][h][0], hi = wv[j][h][1], x = xc[h];
+            warp_mma_f8(c, lo.x, hi.x, lo.y, hi.y, x.x, x.y);
+            warp_mma_f8(c, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
+          }
+          // a lane's sums: rows g and g + 8, tokens 2 t and 2 t + 1 of each 8
+          const float s0 = sw[j] * __shfl_sync(0xffffffffu, sx, 8 * t);
+          const float s1 = sw[j] * __shfl_sync(0xffffffffu, sx, 8 * t + 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[q][i] = fmaf(c[i], i & 1 ? s1 : s0, sum[q][i]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_part[warp][8 * q + 2 * t + (i & 1)][g + 8 * (i >> 1)] = sum[q][i];
+  __syncthreads();
+  stream_results<TOK, false>(a.epi, s_part, s_sum, wpr, S, rank, tiles, tile0);
+}
+
+template <int ACT, bool F32>
+cudaError_t launch_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Fp8LinearDev p, cudaStream_t s) {
+  auto kern = fp8_pair_kernel<ACT, F32>;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  static std::atomic<int> max_clusters[64] = {};
+  int nc = max_clusters[dev].load(std::memory_order_acquire);
+  if (nc == 0) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (err != cudaSuccess) return err;
+    err = cudaOccupancyMaxActiveClusters(&nc, kern, &cfg);
+    if (err != cudaSuccess) return err;
+    if (nc < 1) return cudaErrorLaunchOutOfResources;
+    max_clusters[dev].store(nc, std::memory_order_release);
+  }
+  const long tiles = static_cast<long>(ceil_div(p.epi.M, 256)) * ceil_div(p.epi.N, 256);
+  p.group = 8;
+  cfg.gridDim = dim3(2 * static_cast<int>(std::min<long>(nc, tiles)));
+  cfg.stream = s;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, kern, tm_a, tm_b, p);
+  count_launches(1);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <int ACT>
+cudaError_t launch_pair_act(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const Fp8LinearDev& p,
+                            cudaStream_t s) {
+  return p.epi.out_f32 ? launch_pair<ACT, true>(tm_a, tm_b, p, s) : launch_pair<ACT, false>(tm_a, tm_b, p, s);
+}
+
+cudaError_t launch_tile(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Fp8LinearDev p, int split,
+                        cudaStream_t s) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64) return cudaErrorInvalidDevice;
+  static std::atomic<int> ready[64] = {};
+  if (!ready[dev].load(std::memory_order_acquire)) {
+    err = cudaFuncSetAttribute(fp8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmem);
+    if (err != cudaSuccess) return err;
+    ready[dev].store(1, std::memory_order_release);
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  p.split = split;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(p.epi.M, 128) * ceil_div(p.epi.N, 128) * split);
+  cfg.blockDim = dim3(kTThreads);
+  cfg.dynamicSmemBytes = kTSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  err = cudaLaunchKernelEx(&cfg, fp8_tile_kernel, tm_a, tm_b, p);
+  count_launches(1);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <int NT, bool CODES>
+cudaError_t launch_stream(Fp8StreamArgs a, int num_sms, cudaStream_t s) {
+  // as the bf16 kernel: warps of a block per tile, then blocks, until every SM has 16
+  // warps, as long as each has a group of the contraction
+  const long tiles = ceil_div(a.epi.N, 16);
+  a.wpr = a.split = 1;
+  while (a.wpr < kStreamWarps && tiles * a.wpr < 16l * num_sms && a.wpr * kStreamBlocks < a.KB) a.wpr *= 2;
+  while (a.split < 8 && tiles * a.wpr * a.split < 16l * num_sms && a.wpr * a.split * kStreamBlocks < a.KB)
+    a.split *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(tiles, kStreamWarps / a.wpr) * a.split);
+  cfg.blockDim = dim3(kStreamWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fp8_stream_kernel<NT, CODES>, a);
+}
+template <bool CODES>
+cudaError_t launch_stream_tokens(const Fp8StreamArgs& a, int num_sms, cudaStream_t s) {
+  if (a.epi.M <= 8) return launch_stream<1, CODES>(a, num_sms, s);
+  if (a.epi.M <= 16) return launch_stream<2, CODES>(a, num_sms, s);
+  return launch_stream<4, CODES>(a, num_sms, s);
+}
+
+}  // namespace
+
+// As linear_path: pairs from half a wave of their tiles, below it 128 x 128 tiles with the
+// contraction split until the grid covers the GPU twice, each part at least two K
+// blocks long.
+LinearPath fp8_path(long M, long N, long K, int num_sms) {
+  LinearPath r;
+  const long big = static_cast<long>(ceil_div(M, 256)) * ceil_div(N, 256);
+  const long pairs = std::min(num_sms, kLinearMaxParts / 2) / 2;
+  r.split = 1;
+  if (big >= pairs / 2) {
+    r.kind = LinearPath::kPair;
+    return r;
+  }
+  r.kind = LinearPath::kTile;
+  const long tiles = static_cast<long>(ceil_div(M, 128)) * ceil_div(N, 128);
+  while (r.split < 8 && tiles * r.split * 2 <= 4 * pairs && K / (r.split * 2) >= 2 * kB) r.split *= 2;
+  return r;
+}
+
+cudaError_t launch_fp8_linear(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const Fp8LinearDev& p,
+                              const LinearPath& path, cudaStream_t s) {
+  const long parts = static_cast<long>(path.split) * ceil_div(p.epi.M, 128) * ceil_div(p.epi.N, 128);
+  if (path.kind == LinearPath::kSums || (path.kind == LinearPath::kPair && path.split != 1) ||
+      (path.split != 1 && path.split != 2 && path.split != 4 && path.split != 8) ||
+      (path.split > 1 && (path.split > p.KB || parts > kLinearMaxParts)))
+    return cudaErrorInvalidValue;
+  if (path.kind == LinearPath::kTile) return launch_tile(tm_x, tm_w, p, path.split, s);
+  if (p.epi.act == MOE_ACT_SILU) return launch_pair_act<MOE_ACT_SILU>(tm_x, tm_w, p, s);
+  if (p.epi.act == MOE_ACT_GELU) return launch_pair_act<MOE_ACT_GELU>(tm_x, tm_w, p, s);
+  if (p.epi.act == MOE_ACT_RELU) return launch_pair_act<MOE_ACT_RELU>(tm_x, tm_w, p, s);
+  return launch_pair_act<MOE_ACT_NONE>(tm_x, tm_w, p, s);
+}
+
+bool fp8_streams(int T, int N) { return T <= 16 || (T <= 32 && N <= 1024); }
+
+cudaError_t launch_fp8_stream(const Fp8StreamArgs& a, int num_sms, cudaStream_t s) {
+  const cudaError_t e = a.codes ? launch_stream_tokens<true>(a, num_sms, s)
+                                : launch_stream_tokens<false>(a, num_sms, s);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_fp8_rows(const Fp8RowsArgs& a, cudaStream_t s) {
+  const cudaError_t e = launch_pdl(fp8_rows_kernel, dim3(ceil_div(a.T, 32), ceil_div(a.KB, 4)), dim3(256), 0, s, a);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace moe

@@ -447,4 +447,51 @@ cudaError_t launch_gated_stream(const LinearStreamArgs& a, int num_sms, cudaStre
 // and dbias of 2 N columns.
 cudaError_t launch_gated_dz(const LinearDzArgs& a, int slices, float* dbias, cudaStream_t s);
 
+// 2-D matrix of bytes, box 128 x 128 of them, otherwise as make_map_bf16_2d.
+moe_status make_map_u8_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                          uint64_t ld);
+
+// 8-bit products (linear_fp8.cu): x w^T of e4m3 codes, one scale per 1 x 128 of x and per
+// 128 x 128 of w, fp32 or UE8M0.
+struct Fp8Scales {
+  const void* x;           // of token t and block kb: x[t * x_row + kb * x_kb]
+  const void* w;           // [ceil(N / 128), K / 128]
+  long x_row, x_kb;
+  int ue8m0;
+};
+struct Fp8LinearDev {
+  LinearEpi epi;           // preact null
+  Fp8Scales sc;
+  int KB;                  // K / 128
+  int split, group;
+  float* parts;            // as LinearDev::parts
+  int* err;
+};
+LinearPath fp8_path(long M, long N, long K, int num_sms);      // kPair or kTile
+cudaError_t launch_fp8_linear(const CUtensorMap& tm_x, const CUtensorMap& tm_w,
+                              const Fp8LinearDev& p, const LinearPath& path, cudaStream_t s);
+struct Fp8StreamArgs {
+  const void* x;           // bf16, quantised on the way, or (codes) e4m3
+  const uint8_t* w;
+  long ld_x, ld_w;
+  Fp8Scales sc;            // sc.x null unless codes
+  int KB;
+  bool codes;
+  int wpr, split;          // as LinearStreamArgs
+  LinearEpi epi;
+};
+bool fp8_streams(int T, int N);
+cudaError_t launch_fp8_stream(const Fp8StreamArgs& a, int num_sms, cudaStream_t s);
+// bf16 [T, K] -> e4m3 codes [T, K] (rows K apart) and a scale per 1 x 128, at
+// scale[t * s_row + kb * s_kb].
+struct Fp8RowsArgs {
+  const __nv_bfloat16* x;
+  uint8_t* q;
+  void* scale;
+  long ld_x, s_row, s_kb;
+  int T, KB;
+  bool ue8m0;
+};
+cudaError_t launch_fp8_rows(const Fp8RowsArgs& a, cudaStream_t s);
+
 }  // namespace moe

@@ -12,6 +12,8 @@ Definitions (the tests pin them against finite differences and closed forms):
 * block_norm: z = y/rms(y) w_post (or y), r' = r + scale g z,
   n = r'/rms(r') w_pre, rms(v) = sqrt(mean v^2 + eps).
 * linear: residual + act(x w^T + b).
+* gated_linear: act(z_g) z_u with z = x w^T + b, its first half z_g.
+* linear_fp8: linear of x = qx sx, w = qw sw, codes times the scales of their blocks.
 """
 from __future__ import annotations
 
@@ -19,8 +21,10 @@ import math
 
 import numpy as np
 
+from .moe_oracle import e4m3_decode
+
 __all__ = ["scores", "route_scored", "route_scored_backward", "block_norm", "block_norm_backward",
-           "linear", "linear_backward"]
+           "linear", "linear_backward", "gated_linear", "gated_linear_backward", "linear_fp8"]
 
 _erf = np.vectorize(math.erf, otypes=[np.float64])
 
@@ -220,3 +224,14 @@ def gated_linear_backward(grad_h, x, w, preact, activation="silu"):
     zg, zu = np.split(z, 2, axis=1)
     dz = np.concatenate([dh * zu * _slope(zg, activation), dh * _act(zg, activation)], 1)
     return dz @ _f64(w), dz.T @ _f64(x), dz.sum(0), dz
+
+
+def linear_fp8(qx, sx, qw, sw, bias=None, activation=None, residual=None):
+    """e4m3 codes with scale values: sx [T, K/128], sw [ceil(N/128), K/128] -> (y, z, sum of magnitudes)."""
+    x = e4m3_decode(qx).astype(np.float64) * np.repeat(_f64(sx), 128, 1)
+    w = e4m3_decode(qw).astype(np.float64) * np.repeat(np.repeat(_f64(sw), 128, 0)[: len(qw)], 128, 1)
+    z = x @ w.T
+    if bias is not None:
+        z = z + _f64(bias)
+    y = _act(z, activation)
+    return (y if residual is None else y + _f64(residual)), z, np.abs(x) @ np.abs(w).T

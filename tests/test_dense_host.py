@@ -75,11 +75,60 @@ def test_gated_linear_backward_refusals(L, kw, status):
                                        32, P, P, NUL, P, a["wsb"], NUL) == status
 
 
+# ------------------------------------------------------------------ 8-bit products
+def test_linear_fp8_closed_forms():
+    qx, qw = np.full((1, 256), 0x38, np.uint8), np.full((130, 256), 0x38, np.uint8)       # ones
+    y, z, mag = B.linear_fp8(qx, [[2.0, 0.5]], qw, [[1.0, 4.0], [8.0, 0.0]], bias=np.arange(130.0), activation="relu",
+                             residual=np.ones((1, 130)))
+    assert z[0, 0] == 128 * (2 + 2) and z[0, 129] == 128 * 16 + 129 and y[0, 129] == z[0, 129] + 1 and mag[0, 127] == 512
+
+
+def rows8(L, x=P, ld_x=256, T=4, K=256, fmt=1, q=P, s=P, s_row=2, s_kb=1):
+    return L.moe_quantize_fp8_rows(x, ld_x, T, K, fmt, q, s, s_row, s_kb, NUL)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(K=0), UNSUPPORTED), (dict(K=200), UNSUPPORTED), (dict(ld_x=255), INVALID),
+    (dict(ld_x=260), UNSUPPORTED), (dict(fmt=0), INVALID), (dict(fmt=3), INVALID), (dict(s_row=0), INVALID),
+    (dict(s_kb=-1), INVALID), (dict(x=NUL), INVALID), (dict(q=NUL), INVALID), (dict(s=NUL), INVALID),
+    (dict(x=ODD), INVALID), (dict(q=ODD), INVALID), (dict(s=ctypes.c_void_p((1 << 20) + 2)), INVALID),
+    (dict(T=0, x=NUL), OK)])
+def test_quantize_fp8_rows_refusals(L, kw, status):
+    assert rows8(L, **kw) == status
+
+
+def lin8(L, x=P, ld_x=256, xs=NUL, s_row=0, s_kb=0, w=P, ld_w=256, ws8=P, fmt=1, bias=NUL, bdt=0, act=-1, res=NUL,
+         ld_res=0, T=4, K=256, N=32, out=P, odt=0, ld_out=32, ws=P, wsb=1 << 30):
+    return L.moe_linear_fp8(x, ld_x, xs, s_row, s_kb, w, ld_w, ws8, fmt, bias, bdt, act, res, ld_res, T, K, N, out, odt,
+                            ld_out, ws, wsb, NUL)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(N=-1), INVALID), (dict(K=0), UNSUPPORTED), (dict(K=192), UNSUPPORTED),
+    (dict(ld_x=260), UNSUPPORTED), (dict(ld_x=264, xs=P, s_row=2, s_kb=1), UNSUPPORTED), (dict(ld_w=255), INVALID),
+    (dict(ld_w=264), UNSUPPORTED), (dict(fmt=0), INVALID), (dict(fmt=3), INVALID), (dict(xs=P, s_row=0, s_kb=1), INVALID),
+    (dict(act=3), INVALID), (dict(odt=2), INVALID), (dict(bias=P, bdt=2), INVALID), (dict(ld_out=31), INVALID),
+    (dict(res=P, ld_res=31), INVALID), (dict(res=P, ld_res=40), INVALID), (dict(x=NUL), INVALID), (dict(w=NUL), INVALID),
+    (dict(ws8=NUL), INVALID), (dict(out=NUL), INVALID), (dict(x=ODD), INVALID), (dict(w=ODD), INVALID),
+    (dict(ws=NUL), INVALID), (dict(wsb=128), WORKSPACE), (dict(T=0, x=NUL), OK), (dict(N=0, x=NUL), OK)])
+def test_linear_fp8_refusals(L, kw, status):
+    assert lin8(L, **kw) == status
+
+
+def test_linear_fp8_workspace(L):
+    """Given codes need the products' part alone; bf16 rows their codes and scales too."""
+    small, need = L.moe_linear_workspace_size(), L.moe_linear_fp8_workspace_size(4, 256)
+    assert need >= small + 4 * 256 + 4 * 2 * 4 and L.moe_linear_fp8_workspace_size(-1, 256) == 0
+    assert lin8(L, wsb=need - 1) == WORKSPACE
+    assert lin8(L, xs=P, s_row=2, s_kb=1, wsb=small - 1) == WORKSPACE
+
+
 def test_the_bindings_refuse_host_tensors():
     import torch
 
     import mixture_experts_routed_top_gb300 as m
     t = torch.zeros(4, 8)
-    for call in (lambda: m.gated_linear(t, t), lambda: m.gated_linear_backward(t, t, t, t)):
+    for call in (lambda: m.gated_linear(t, t), lambda: m.gated_linear_backward(t, t, t, t),
+                 lambda: m.quantize_fp8_rows(t), lambda: m.linear_fp8(t, t, t)):
         with pytest.raises(ValueError):
             call()

@@ -1,4 +1,5 @@
-"""The dense half of a block on the GPU against the float64 oracle: gated products.
+"""The dense half of a block on the GPU against the float64 oracle: gated products, 8-bit
+products with block scales.
 
 Tolerances as in test_gpu_block_ops.py, from the arithmetic: a bf16 result is one
 rounding, at most 2^-8 of it (BF); a tensor-core sum of K products is off by at most
@@ -9,6 +10,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from oracle import block_oracle as B
 
 pytestmark = pytest.mark.gpu
@@ -156,3 +158,146 @@ def test_gated_linear_not_finite(moe, T, K, I):
     want[T // 2], want[:, I // 2], want[:, I + I // 3] = True, True, True
     assert np.array_equal(np.isnan(_np(z)), want)
     assert np.array_equal(np.isnan(_np(h)), want[:, :I] | want[:, I:])
+
+
+# ------------------------------------------------------------------ 8-bit products
+def _acc8(K):
+    """Sums of 128 on the tensor core (at most 128 / 16 + 16 additions, 2^-23 each of the sum of
+    magnitudes), then K / 128 fp32 products and additions, half of 2^-23 each."""
+    return (24 + K / 128 + 1) * 2.0 ** -23
+
+
+def _weights8(g, N, K, fmt):
+    w = g.normal(size=(-(-N // 128) * 128, K)) / K ** 0.5 * (1 + 9 * (g.random((1, K)) < 0.02))
+    w[N:] = 0
+    codes, stored, scale = O.quantize_blocks(w.astype(np.float32), 128, 128, fmt)
+    return torch.from_numpy(codes[:N].copy()).cuda(), torch.from_numpy(stored).cuda(), codes[:N], scale
+
+
+def _rows8(g, T, K):
+    return _dev(g.normal(size=(T, K)) * (0.1 + 3 * g.random((T, 1))) * (1 + 20 * (g.random((1, K)) < 0.02)), torch.bfloat16)
+
+
+@pytest.mark.parametrize("T,K", [(1, 128), (31, 640), (33, 512), (64, 128), (7, 1152), (129, 2048)])
+@pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
+def test_quantize_fp8_rows(moe, T, K, fmt):
+    """Codes and scales bit for bit, in both orders of the scales and from strided rows."""
+    g = _rng(T, K)
+    x = _rows8(g, T, K)
+    x[T // 2, :128] = 0
+    codes, stored, _ = O.quantize_blocks(_np(x).astype(np.float32), 1, 128, fmt)
+    q, s = moe.quantize_fp8_rows(x, fmt)
+    assert s.stride() == (1, T) or T == 1 or K == 128
+    assert np.array_equal(q.cpu().numpy(), codes) and np.array_equal(s.cpu().numpy(), stored)
+    big = torch.zeros(T, K + 24, dtype=torch.bfloat16, device="cuda")
+    big[:, 8:8 + K] = x
+    o = (torch.zeros(T, K, dtype=torch.float8_e4m3fn, device="cuda"), torch.zeros(T, K // 128, dtype=s.dtype, device="cuda"))
+    moe.quantize_fp8_rows(big[:, 8:8 + K], fmt, out=o)
+    assert torch.equal(o[0].view(torch.uint8), q) and torch.equal(o[1], s)
+
+
+FP8 = [  # T, K, N: a token, few tokens, tiles and split contractions, ragged, CTA pairs
+    (1, 128, 1), (1, 2048, 7168), (2, 256, 33), (8, 7168, 100), (9, 128, 16), (16, 1152, 129), (17, 640, 1025),
+    (30, 384, 700), (32, 512, 17), (33, 128, 130), (100, 7168, 576), (129, 1024, 129), (300, 512, 264), (257, 256, 3),
+    (700, 2048, 1000), (2050, 256, 1536), (2049, 384, 1601), (1301, 2048, 2041), (4500, 128, 900)]
+
+
+@pytest.mark.parametrize("T,K,N", FP8)
+@pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
+def test_linear_fp8(moe, T, K, N, fmt):
+    g = _rng(T, K, N, 8)
+    x = _rows8(g, T, K)
+    w, ws, wc, wsv = _weights8(g, N, K, fmt)
+    q, s = moe.quantize_fp8_rows(x, fmt)
+    xc, xs, xsv = O.quantize_blocks(_np(x).astype(np.float32), 1, 128, fmt)
+    for act, dt, bdt, res in (("silu", torch.bfloat16, torch.float32, True), (None, torch.float32, None, False),
+                              ("gelu", torch.float32, torch.bfloat16, True), ("relu", torch.bfloat16, None, False),
+                              ("silu", torch.float32, torch.bfloat16, False), (None, torch.bfloat16, None, True),
+                              ("gelu", torch.bfloat16, None, False), ("relu", torch.float32, None, True)):
+        b = None if bdt is None else _dev(g.normal(size=N), bdt)
+        r = _dev(g.normal(size=(T, N)), dt) if res else None
+        ry, rz, mag = B.linear_fp8(xc, xsv, wc, wsv, None if b is None else _np(b), act, None if r is None else _np(r))
+        m = mag + np.abs(rz) + (0 if r is None else np.abs(_np(r)))
+        y = moe.linear_fp8(x, w, ws, bias=b, activation=act, residual=r, out_dtype=dt)
+        _close(y, ry, 1.2 * m, dt == torch.bfloat16, _acc8(K) + 2.0 ** -21)     # |act'| < 1.2
+        # the same codes, however they come
+        for qq, ss in ((q, s), (q.view(torch.float8_e4m3fn), s.contiguous())):
+            y2 = moe.linear_fp8(qq, w.view(torch.float8_e4m3fn), ws, x_scale=ss, bias=b, activation=act, residual=r, out_dtype=dt)
+            assert torch.equal(y2, y)
+    moe.workspace_status(moe.default_workspace())
+
+
+def test_linear_fp8_strides_in_place_and_empty(moe):
+    g = _rng(31)
+    x = _rows8(g, 70, 256)
+    w, ws, wc, wsv = _weights8(g, 90, 256, "f32")
+    ref = moe.linear_fp8(x, w, ws)
+    big, wbig = torch.zeros(70, 400, dtype=torch.bfloat16, device="cuda"), torch.zeros(90, 320, dtype=torch.uint8, device="cuda")
+    big[:, 16:272], wbig[:, 32:288] = x, w
+    out = torch.zeros(70, 104, dtype=torch.bfloat16, device="cuda")
+    moe.linear_fp8(big[:, 16:272], wbig[:, 32:288], ws, out=out[:, :90])
+    assert torch.equal(out[:, :90], ref) and (out[:, 90:] == 0).all()
+    q, s = moe.quantize_fp8_rows(x)
+    qbig = torch.zeros(70, 288, dtype=torch.uint8, device="cuda")
+    qbig[:, 16:272] = q
+    sbig = torch.zeros(141, 5, device="cuda")
+    sbig[1::2, 1:5:2] = s
+    assert torch.equal(moe.linear_fp8(qbig[:, 16:272], w, ws, x_scale=sbig[1::2, 1:5:2]), ref)
+    acc = ref.clone()
+    moe.linear_fp8(x, w, ws, residual=acc, out=acc)
+    _close(acc, 2 * _np(ref), 4 * np.abs(_np(ref)), True, BF)
+    assert moe.linear_fp8(x[:0], w, ws).shape == (0, 90) and moe.linear_fp8(x, w[:0], ws[:0]).shape == (70, 0)
+    q0, s0 = moe.quantize_fp8_rows(x[:0])
+    assert q0.shape == (0, 256) and s0.shape == (0, 2)
+    e8 = torch.zeros(1, 2, dtype=torch.uint8, device="cuda")
+    for bad in (lambda: moe.linear_fp8(x, w, ws[:, :1]), lambda: moe.linear_fp8(x, w, ws, x_scale=s),
+                lambda: moe.linear_fp8(q, w, ws), lambda: moe.linear_fp8(q, w, e8, x_scale=s),
+                lambda: moe.linear_fp8(x, w, ws, activation="tanh"), lambda: moe.linear_fp8(x, w.float(), ws),
+                lambda: moe.linear_fp8(x, w, ws, out=out), lambda: moe.quantize_fp8_rows(x, "none"),
+                lambda: moe.quantize_fp8_rows(x.float()), lambda: moe.quantize_fp8_rows(x, out=(q, s[:, :1]))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(moe.MoEError):
+        moe.quantize_fp8_rows(x[:, :136])             # K not a multiple of 128
+    with pytest.raises(moe.MoEError):
+        moe.linear_fp8(q, w, ws, x_scale=s[:1].expand(70, 2))     # one scale for all rows: a stride of 0
+
+
+@pytest.mark.parametrize("T,N", [(3, 40), (40, 40), (2050, 1540)])
+@pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
+def test_linear_fp8_extremes(moe, T, N, fmt):
+    """Rows of zeros give zeros, the smallest and largest bf16 values keep their sign and size, and
+    an infinity or NaN stays in its row; a NaN code of w stays in its column."""
+    K = 256
+    g = _rng(T, N)
+    x = _rows8(g, T, K)
+    w, ws, wc, wsv = _weights8(g, N, K, fmt)
+    x[0] = 0
+    x[1] = 2.0 ** -132                                  # below the smallest scale's reach: a code of 2^-6 or none
+    x[2] = 0
+    x[2, :4] = 3.3e38
+    y = moe.linear_fp8(x, w, ws, out_dtype=torch.float32)
+    assert (y[0] == 0).all() and (y[1].abs() <= K * 2.0 ** -126 * 20).all()
+    assert (torch.isfinite(y[2]) | (y[2].abs() == float("inf"))).all()
+    rows = torch.ones(T, dtype=torch.bool)
+    x[T - 1, 5], x[2, 7] = float("nan"), float("inf")
+    rows[T - 1], rows[2] = False, False
+    wn = w.clone()
+    wn[N // 2, 3] = 0x7F
+    y2 = moe.linear_fp8(x, wn, ws, out_dtype=torch.float32)
+    cols = torch.arange(N) != N // 2
+    assert torch.isnan(y2[T - 1]).all() and torch.isnan(y2[:, N // 2]).all() and not torch.isfinite(y2[2]).any()
+    a, b = y[rows.cuda()][:, cols.cuda()], y2[rows.cuda()][:, cols.cuda()]
+    assert torch.equal(a, b)
+
+
+def test_linear_fp8_long_rows_of_one_sign(moe):
+    """Without cancellation the sums stay as near as fp32 ones: 2^-19 of the result over 7168."""
+    g = _rng(5)
+    for T, N in ((4, 64), (64, 256), (2048, 1536)):
+        x = _dev(np.abs(g.normal(size=(T, 7168))), torch.bfloat16)
+        w, ws, wc, wsv = _weights8(g, N, 7168, "f32")
+        y = moe.linear_fp8(x, w & 0x7F, ws, out_dtype=torch.float32)
+        xc, _, xsv = O.quantize_blocks(_np(x).astype(np.float32), 1, 128, "f32")
+        ry = B.linear_fp8(xc, xsv, wc & 0x7F, wsv)[0]
+        assert np.linalg.norm(_np(y) - ry) < 2.0 ** -19 * np.linalg.norm(ry)
