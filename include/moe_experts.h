@@ -668,13 +668,53 @@ moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int6
                           moe_dtype out_dt, int64_t ld_out, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * moe_layer_norm - the residual sum and the layer norm after it in one pass:
+ *   residual_out = residual + y
+ *   normed       = (residual_out - mean) / sqrt(var + eps) * weight + bias
+ * with the mean and variance of a row, held in fp32 (the variance as the mean of squared
+ * differences from the mean).  residual_out is rounded once on its way out; normed is
+ * made from the unrounded residual_out.
+ *   residual      device [T, H], bf16 or fp32 (res_dt)
+ *   y             device bf16 [T, H], or NULL: residual_out = residual is not written
+ *   weight, bias  device [H] bf16 or fp32 (weight_dt, both), or NULL: 1 and 0
+ *   residual_out  device [T, H] of residual's type, rows H apart; may be residual itself
+ *                 where ld_res = H
+ *   normed        device bf16 [T, H], rows H apart
+ * 1 <= H <= 16384 (else MOE_ERR_UNSUPPORTED), any strides >= H, buffers aligned to 16
+ * bytes.  T = 0 is a no-op.
+ */
+moe_status moe_layer_norm(const void* residual, moe_dtype res_dt, int64_t ld_res, const void* y,
+                          int64_t ld_y, const void* weight, const void* bias, moe_dtype weight_dt,
+                          float eps, int T, int H, void* residual_out, void* normed, void* stream);
+
+/*
+ * moe_layer_norm_backward - gradients of moe_layer_norm.
+ *   grad_residual  dL/d residual_out, of res_dt, or NULL (zero)
+ *   grad_normed    dL/d normed, bf16
+ *   residual       the residual_out that was stored
+ *   d_residual     out, dL/d residual, of res_dt, rows H apart; may be grad_residual itself
+ *                  where ld_gres = H
+ *   d_y            out, bf16 [T, H], or NULL: d_residual rounded to bf16 (y's gradient)
+ *   d_weight, d_bias   out, fp32 [H], summed over tokens; or NULL
+ *   ws             at least moe_layer_norm_backward_workspace_size(H) bytes, 256-byte
+ *                  aligned (partial sums; its first 256 bytes are left alone)
+ * The sums over tokens are added in a fixed order.  T = 0 writes zeros to them.
+ */
+size_t moe_layer_norm_backward_workspace_size(int H);
+moe_status moe_layer_norm_backward(const void* grad_residual, int64_t ld_gres, const void* grad_normed,
+                                   int64_t ld_gn, const void* residual, moe_dtype res_dt,
+                                   int64_t ld_res, const void* weight, moe_dtype weight_dt, float eps,
+                                   int T, int H, void* d_residual, void* d_y, float* d_weight,
+                                   float* d_bias, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * moe_call_packed - one of the calls above with its arguments in a block of
  * 8-byte slots in the function's order: pointers and integers as int64_t,
  * floats as double.  For bindings that pay per argument.
  *   call   0 moe_route_scored, 1 moe_route_scored_backward, 2 moe_block_norm,
  *          3 moe_block_norm_backward, 4 moe_linear, 5 moe_linear_backward,
  *          7 moe_gated_linear, 8 moe_gated_linear_backward, 9 moe_quantize_fp8_rows,
- *          10 moe_linear_fp8;
+ *          10 moe_linear_fp8, 11 moe_layer_norm, 12 moe_layer_norm_backward;
  *          any other: MOE_ERR_INVALID_ARG
  *   block  the slots; a size that no int holds: MOE_ERR_UNSUPPORTED
  */

@@ -27,6 +27,7 @@ __all__ = [
     "get_down_phases",
     "route_scored", "route_scored_backward", "block_norm", "block_norm_backward", "linear", "linear_backward",
     "gated_linear", "gated_linear_backward", "quantize_fp8_rows", "linear_fp8",
+    "layer_norm", "layer_norm_backward",
     "Workspace", "STATUS", "STAGES", "W_BF16", "W_FP8_E4M3", "W_FP4_E2M1", "SCALE_NONE", "SCALE_F32",
     "SCALE_UE8M0", "ACTIVATIONS",
 ]
@@ -106,6 +107,9 @@ _SIGS = {
     "moe_linear_fp8_workspace_size": ([_I, _I], _SZ),
     "moe_linear_fp8": ([_P, _L, _P, _L, _L, _P, _L, _P, _I, _P, _I, _I, _P, _L, _I, _I, _I, _P, _I, _L, _P,
                         _SZ, _P], _I),
+    "moe_layer_norm": ([_P, _I, _L, _P, _L, _P, _P, _I, _F, _I, _I, _P, _P, _P], _I),
+    "moe_layer_norm_backward_workspace_size": ([_I], _SZ),
+    "moe_layer_norm_backward": ([_P, _L, _P, _L, _P, _I, _L, _P, _I, _F, _I, _I, _P, _P, _P, _P, _P, _SZ, _P], _I),
     "moe_linear_backward": ([_P, _I, _L, _P, _L, _P, _L, _I, _P, _L, _I, _I, _I, _P, _P, _P, _P, _SZ,
                              _P], _I),
 }
@@ -435,6 +439,8 @@ _GATED = (7, struct.Struct("=16q").pack)
 _GATED_BWD = (8, struct.Struct("=18q").pack)
 _FP8_ROWS = (9, struct.Struct("=10q").pack)
 _LINEAR_FP8 = (10, struct.Struct("=23q").pack)
+_LAYER_NORM = (11, struct.Struct("=8qd5q").pack)
+_LAYER_NORM_BWD = (12, struct.Struct("=9qd9q").pack)
 
 
 def _bad(name: str, what: str):
@@ -682,6 +688,99 @@ def block_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: Opti
           ld_r, py, ld_y, pg, kind, gate_dt, ld_g, scale, post_norm, post, pre, wdt, eps, T, H, d_res.data_ptr(),
           pdy, pdg, pdpost, pdpre, ws.data_ptr(), ws.numel())
     return d_res, d_y, d_gate, d_post, d_pre
+
+
+def layer_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+               weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, eps: float = 1e-5,
+               out: Optional[Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]] = None,
+               stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The residual sum and the layer norm after it in one pass -> (residual_out, normed).
+
+    residual_out = residual + y;
+    normed = (residual_out - mean) / sqrt(var + eps) * weight + bias over a row.
+
+    residual bf16 or fp32 [T,H] (residual_out alike); y bf16 [T,H], or None:
+    only the norm, and residual itself is returned; normed bf16; weight and
+    bias [H] or None, both bf16 or both fp32.  out: (residual_out, normed) to
+    write into, either of them None for a new tensor; residual_out may be
+    residual."""
+    if stream is not None:
+        return _on_stream(layer_norm, locals())
+    dev, shape = _matrix_of("residual", residual)
+    ld_r = _mat("residual", residual, _DT, shape, dev)
+    T, H = shape
+    pw, pb, wdt = _weight_and_bias(weight, bias, H, dev)
+    res, n = (None, None) if out is None else out
+    py = ld_y = pres = 0
+    if y is None:
+        res = residual
+    else:
+        py, ld_y = y.data_ptr(), _mat("y", y, _ONLY_BF16, shape, dev)
+        if res is None:
+            res = torch.empty(shape, dtype=residual.dtype, device=residual.device)
+            pres = res.data_ptr()
+        else:
+            pres = _dense("residual_out", res, (residual.dtype,), shape, dev)
+    if n is None:
+        n = torch.empty(shape, dtype=_BF16, device=residual.device)
+        pn = n.data_ptr()
+    else:
+        pn = _dense("normed", n, _ONLY_BF16, shape, dev)
+    _call(_LAYER_NORM, dev, residual.data_ptr(), _DT[residual.dtype], ld_r, py, ld_y, pw, pb, wdt, eps, T, H, pres, pn)
+    return res, n
+
+
+def _weight_and_bias(weight, bias, H: int, dev: int):
+    """-> the addresses of a layer norm's weight and bias (0: none), their dtype."""
+    pw = pb = dt = 0
+    if weight is not None:
+        pw, dt = _dense("weight", weight, _DT, (H,), dev), _DT[weight.dtype]
+    if bias is not None:
+        pb = _dense("bias", bias, _DT, (H,), dev)
+        if pw and _DT[bias.dtype] != dt:
+            raise ValueError("weight and bias must have one dtype")
+        dt = _DT[bias.dtype]
+    return pw, pb, dt
+
+
+def layer_norm_backward(grad_residual: Optional[torch.Tensor], grad_normed: torch.Tensor, residual: torch.Tensor, *,
+                        weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                        eps: float = 1e-5, need_y: bool = False, workspace: Optional[Workspace] = None, stream=None):
+    """Gradients of layer_norm -> (d_residual, d_y, d_weight, d_bias).
+
+    grad_residual: dL/d residual_out [T,H] or None; grad_normed: dL/d normed
+    bf16 [T,H]; residual: the residual_out that layer_norm returned; weight,
+    bias, eps as it was called with (None: that gradient is None).  need_y:
+    also y's gradient, which is d_residual in bf16 (the same tensor where that
+    is bf16).  d_weight and d_bias are fp32 [H].  workspace: as in linear."""
+    if stream is not None:
+        return _on_stream(layer_norm_backward, locals())
+    dev, shape = _matrix_of("residual", residual)
+    ld_r = _mat("residual", residual, _DT, shape, dev)
+    T, H = shape
+    device = residual.device
+    pgr = ld_gr = pdy = pdw = pdb = 0
+    d_y = d_w = d_b = None
+    if grad_residual is not None:
+        pgr, ld_gr = grad_residual.data_ptr(), _mat("grad_residual", grad_residual, (residual.dtype,), shape, dev)
+    ld_gn = _mat("grad_normed", grad_normed, _ONLY_BF16, shape, dev)
+    pw, pb, wdt = _weight_and_bias(weight, bias, H, dev)
+    d_res = torch.empty(shape, dtype=residual.dtype, device=device)
+    if need_y and residual.dtype == _BF16:
+        d_y = d_res
+    elif need_y:
+        d_y = torch.empty(shape, dtype=_BF16, device=device)
+        pdy = d_y.data_ptr()
+    if pw:
+        d_w = torch.empty(H, dtype=_F32, device=device)
+        pdw = d_w.data_ptr()
+    if pb:
+        d_b = torch.empty(H, dtype=_F32, device=device)
+        pdb = d_b.data_ptr()
+    ws = _workspace(workspace, dev, (_LIB or lib()).moe_layer_norm_backward_workspace_size(H))
+    _call(_LAYER_NORM_BWD, dev, pgr, ld_gr, grad_normed.data_ptr(), ld_gn, residual.data_ptr(), _DT[residual.dtype],
+          ld_r, pw, wdt, eps, T, H, d_res.data_ptr(), pdy, pdw, pdb, ws.data_ptr(), ws.numel())
+    return d_res, d_y, d_w, d_b
 
 
 def _act(activation: Optional[str]) -> int:

@@ -869,6 +869,104 @@ moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int6
   return r == cudaSuccess ? MOE_OK : cuda_error(r, fn);
 }
 
+moe_status moe_layer_norm(const void* residual, moe_dtype res_dt, int64_t ld_res, const void* y,
+                          int64_t ld_y, const void* weight, const void* bias, moe_dtype weight_dt,
+                          float eps, int T, int H, void* residual_out, void* normed, void* stream) {
+  const char* fn = "moe_layer_norm";
+  if (T < 0) return set_last_error(MOE_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (H < 1 || H > kNormMaxH)
+    return set_last_error(MOE_ERR_UNSUPPORTED, "%s: H must be in [1, %d]", fn, kNormMaxH);
+  if (!is_dtype(res_dt) || !is_dtype(weight_dt))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  if (T == 0) return MOE_OK;  // before the pointers: empty buffers may have none
+  if (ld_res < H || (y && ld_y < H))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride below H", fn);
+  if (!residual || (y && !residual_out) || !normed)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (residual_out == residual && y && ld_res != H)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: in place only where the row stride is H", fn);
+  if (normed == residual || (y && (normed == residual_out || normed == y || residual_out == y)))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
+  if (!all16(residual, y, weight, bias, residual_out, normed))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
+  LayerNormArgs a;
+  a.residual = residual;
+  a.y = y;
+  a.weight = weight;
+  a.bias = bias;
+  a.residual_out = residual_out;
+  a.normed = normed;
+  a.ld_res = ld_res;
+  a.ld_y = ld_y;
+  a.T = T;
+  a.H = H;
+  a.weight_bf16 = weight_dt == MOE_DT_BF16;
+  a.eps = eps;
+  const bool vec = H % 8 == 0 && ld_res % 8 == 0 && (!y || ld_y % 8 == 0);
+  const cudaError_t e =
+      launch_layer_norm(a, res_dt == MOE_DT_BF16, vec, device_sms(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+}
+
+size_t moe_layer_norm_backward_workspace_size(int H) {
+  return H < 1 ? 0 : 1024 + static_cast<size_t>(kNormBwdBlocks) * 2 * H * 4;
+}
+
+moe_status moe_layer_norm_backward(const void* grad_residual, int64_t ld_gres, const void* grad_normed,
+                                   int64_t ld_gn, const void* residual, moe_dtype res_dt,
+                                   int64_t ld_res, const void* weight, moe_dtype weight_dt, float eps,
+                                   int T, int H, void* d_residual, void* d_y, float* d_weight,
+                                   float* d_bias, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_layer_norm_backward";
+  if (T < 0) return set_last_error(MOE_ERR_INVALID_ARG, "%s: negative size", fn);
+  if (H < 1 || H > kNormMaxH)
+    return set_last_error(MOE_ERR_UNSUPPORTED, "%s: H must be in [1, %d]", fn, kNormMaxH);
+  if (!is_dtype(res_dt) || !is_dtype(weight_dt))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: unknown dtype", fn);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {  // before the pointers: empty buffers may have none
+    for (float* p : {d_weight, d_bias}) {
+      const cudaError_t e = p ? cudaMemsetAsync(p, 0, static_cast<size_t>(H) * 4, s) : cudaSuccess;
+      if (e != cudaSuccess) return cuda_error(e, fn);
+    }
+    return MOE_OK;
+  }
+  if ((grad_residual && ld_gres < H) || ld_gn < H || ld_res < H)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride below H", fn);
+  if (!grad_normed || !residual || !d_residual)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (d_residual == grad_residual && ld_gres != H)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: in place only where the row stride is H", fn);
+  if (d_residual == residual || d_residual == grad_normed || d_residual == d_y ||
+      (d_y && (d_y == residual || d_y == grad_normed || d_y == grad_residual)))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
+  moe_status st = check_ws(fn, ws, ws_bytes, moe_layer_norm_backward_workspace_size(H));
+  if (st != MOE_OK) return st;
+  if (!all16(grad_residual, grad_normed, residual, weight, d_residual, d_y, d_weight, d_bias))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
+  LayerNormBwdArgs a;
+  a.grad_res = grad_residual;
+  a.grad_normed = grad_normed;
+  a.residual = residual;
+  a.weight = weight;
+  a.d_res = d_residual;
+  a.d_y = d_y;
+  a.d_w = d_weight;
+  a.d_b = d_bias;
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 1024);
+  a.ld_gres = ld_gres;
+  a.ld_gn = ld_gn;
+  a.ld_res = ld_res;
+  a.T = T;
+  a.H = H;
+  a.n_part = (d_weight != nullptr) + (d_bias != nullptr);
+  a.weight_bf16 = weight_dt == MOE_DT_BF16;
+  a.eps = eps;
+  const bool vec = H % 8 == 0 && (!grad_residual || ld_gres % 8 == 0) && ld_gn % 8 == 0 && ld_res % 8 == 0;
+  const cudaError_t e = launch_layer_norm_backward(a, res_dt == MOE_DT_BF16, vec, device_sms(), s);
+  return e == cudaSuccess ? MOE_OK : cuda_error(e, fn);
+}
+
 // The Python binding's way in: converting 14 to 29 arguments one by one took longer
 // there than launching the kernel.
 moe_status moe_call_packed(int call, const void* block) {
@@ -886,6 +984,8 @@ moe_status moe_call_packed(int call, const void* block) {
     case 8: return a.call(moe_gated_linear_backward);
     case 9: return a.call(moe_quantize_fp8_rows);
     case 10: return a.call(moe_linear_fp8);
+    case 11: return a.call(moe_layer_norm);
+    case 12: return a.call(moe_layer_norm_backward);
   }
   return set_last_error(MOE_ERR_INVALID_ARG, "moe_call_packed: unknown call %d", call);
 }

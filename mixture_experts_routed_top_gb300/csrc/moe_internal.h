@@ -379,6 +379,38 @@ constexpr int kNormBwdBlocks = 304;   // most blocks of the backward pass (2 per
 cudaError_t launch_block_norm_backward(const BlockNormBwdArgs& a, bool res_bf16, bool vec,
                                        int num_sms, cudaStream_t s);
 
+struct LayerNormArgs {
+  const void* residual;
+  const void* y;           // or null
+  const void* weight;      // or null
+  const void* bias;        // or null; of weight_bf16's type
+  void* residual_out;      // [T, H], null without y
+  void* normed;            // [T, H]
+  long ld_res, ld_y;
+  int T, H;
+  bool weight_bf16;
+  float eps;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs& a, bool res_bf16, bool vec, int num_sms,
+                              cudaStream_t s);
+struct LayerNormBwdArgs {
+  const void* grad_res;    // or null
+  const void* grad_normed;
+  const void* residual;    // the stored r
+  const void* weight;      // or null
+  void* d_res;
+  void* d_y;               // bf16 or null
+  float* d_w;              // or null
+  float* d_b;              // or null
+  float* partials;         // [blocks, n_part, H]
+  long ld_gres, ld_gn, ld_res;
+  int T, H, n_part;
+  bool weight_bf16;
+  float eps;
+};
+cudaError_t launch_layer_norm_backward(const LayerNormBwdArgs& a, bool res_bf16, bool vec,
+                                       int num_sms, cudaStream_t s);
+
 // Epilogue of the linear kernels.
 struct LinearEpi {
   const void* bias;        // [N] or null

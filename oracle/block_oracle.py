@@ -13,6 +13,7 @@ Definitions (the tests pin them against finite differences and closed forms):
   n = r'/rms(r') w_pre, rms(v) = sqrt(mean v^2 + eps).
 * linear: residual + act(x w^T + b).
 * gated_linear: act(z_g) z_u with z = x w^T + b, its first half z_g.
+* layer_norm: r = residual + y, n = (r - mean) / sqrt(var + eps) w + b.
 * linear_fp8: linear of x = qx sx, w = qw sw, codes times the scales of their blocks.
 """
 from __future__ import annotations
@@ -24,7 +25,8 @@ import numpy as np
 from .moe_oracle import e4m3_decode
 
 __all__ = ["scores", "route_scored", "route_scored_backward", "block_norm", "block_norm_backward",
-           "linear", "linear_backward", "gated_linear", "gated_linear_backward", "linear_fp8"]
+           "linear", "linear_backward", "gated_linear", "gated_linear_backward", "linear_fp8",
+           "layer_norm", "layer_norm_backward"]
 
 _erf = np.vectorize(math.erf, otypes=[np.float64])
 
@@ -235,3 +237,26 @@ def linear_fp8(qx, sx, qw, sw, bias=None, activation=None, residual=None):
         z = z + _f64(bias)
     y = _act(z, activation)
     return (y if residual is None else y + _f64(residual)), z, np.abs(x) @ np.abs(w).T
+
+
+# ------------------------------------------------------------------ layer norm
+def _centred(r, eps):
+    d = r - r.mean(1, keepdims=True)
+    return d, _rstd(d, eps)
+
+
+def layer_norm(residual, y=None, weight=None, bias=None, eps=1e-5):
+    """-> (r, n)."""
+    r = _f64(residual) if y is None else _f64(residual) + _f64(y)
+    d, rs = _centred(r, eps)
+    n = d * rs * (1.0 if weight is None else _f64(weight))
+    return r, n if bias is None else n + _f64(bias)
+
+
+def layer_norm_backward(grad_residual, grad_normed, residual, weight=None, eps=1e-5):
+    """-> (d_residual, d_weight, d_bias)."""
+    dn = _f64(grad_normed)
+    d, rs = _centred(_f64(residual), eps)
+    h, q = d * rs, dn * (1.0 if weight is None else _f64(weight))
+    out = rs * (q - q.mean(1, keepdims=True) - h * (q * h).mean(1, keepdims=True))
+    return (out if grad_residual is None else out + _f64(grad_residual)), (dn * h).sum(0), dn.sum(0)

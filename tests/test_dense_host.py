@@ -123,12 +123,88 @@ def test_linear_fp8_workspace(L):
     assert lin8(L, xs=P, s_row=2, s_kb=1, wsb=small - 1) == WORKSPACE
 
 
+# ------------------------------------------------------------------ layer norm
+def test_layer_norm_gradient_against_differences():
+    g = np.random.default_rng(6)
+    v = dict(residual=g.normal(size=(4, 10)) + 3, y=g.normal(size=(4, 10)), weight=g.normal(size=10), bias=g.normal(size=10))
+    gr, gn = g.normal(size=(4, 10)), g.normal(size=(4, 10))
+
+    def loss(**q):
+        r, n = B.layer_norm(**q)
+        return (r * gr).sum() + (n * gn).sum()
+    dr, dw, db = B.layer_norm_backward(gr, gn, B.layer_norm(**v)[0], v["weight"])
+    for name, d in (("residual", dr), ("y", dr), ("weight", dw), ("bias", db)):
+        u = g.normal(size=v[name].shape)
+        assert abs(_diff(lambda a: loss(**{**v, name: a}), v[name], u) - (d * u).sum()) < TOL, name
+
+
+def test_layer_norm_closed_forms():
+    r, n = B.layer_norm([[1.0, 2.0]], [[1.0, 4.0]], weight=[2.0, 3.0], bias=[1.0, -1.0], eps=0.0)
+    assert r.tolist() == [[2.0, 6.0]] and n.tolist() == [[-1.0, 2.0]]
+    # shifts and scales of the row have no gradient through the norm
+    dr = B.layer_norm_backward(None, [[1.0, 5.0, -2.0]], [[1.0, 2.0, 4.0]], eps=0.0)[0]
+    assert abs(dr.sum()) < 1e-12 and abs((dr * [[1.0, 2.0, 4.0]]).sum()) < 1e-12
+
+
+def lnorm(L, res=P, res_dt=0, ld_res=64, y=P, ld_y=64, w=P, b=P, wdt=0, T=4, H=64, out=P, n=None):
+    n = ctypes.c_void_p(1 << 21) if n is None else n
+    return L.moe_layer_norm(res, res_dt, ld_res, y, ld_y, w, b, wdt, 1e-5, T, H, out, n, NUL)
+
+
+Q = ctypes.c_void_p(1 << 22)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(H=0), UNSUPPORTED), (dict(H=16385, ld_res=16385, ld_y=16385), UNSUPPORTED),
+    (dict(res_dt=3), INVALID), (dict(wdt=3), INVALID), (dict(ld_res=63), INVALID), (dict(ld_y=63), INVALID),
+    (dict(res=NUL), INVALID), (dict(out=NUL), INVALID), (dict(n=NUL), INVALID), (dict(ld_res=72), INVALID),
+    (dict(n=P), INVALID), (dict(y=Q, out=Q), INVALID), (dict(y=NUL, n=P), INVALID), (dict(y=ODD), INVALID),
+    (dict(w=ODD), INVALID), (dict(b=ODD), INVALID), (dict(T=0, res=NUL), OK)])
+def test_layer_norm_refusals(L, kw, status):
+    a = dict(y=ctypes.c_void_p(1 << 23))
+    a.update(kw)
+    assert lnorm(L, **a) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INVALID), (dict(H=0), UNSUPPORTED), (dict(H=16385), UNSUPPORTED), (dict(res_dt=2), INVALID),
+    (dict(ld_gr=63), INVALID), (dict(ld_gn=63), INVALID), (dict(ld_res=63), INVALID), (dict(gn=NUL), INVALID),
+    (dict(res=NUL), INVALID), (dict(dr=NUL), INVALID), (dict(ws=NUL), INVALID), (dict(wsb=16), WORKSPACE),
+    (dict(dr=Q, gr=Q, ld_gr=72), INVALID), (dict(dr=Q, res=Q), INVALID), (dict(dr=Q, dy=Q), INVALID),
+    (dict(dr=Q, dy=P), INVALID), (dict(gr=ODD), INVALID), (dict(dw=ODD), INVALID)])
+def test_layer_norm_backward_refusals(L, kw, status):
+    a = dict(gr=P, ld_gr=64, gn=P, ld_gn=64, res=P, res_dt=0, ld_res=64, T=4, H=64, dr=Q, dy=NUL, dw=NUL, ws=P,
+             wsb=L.moe_layer_norm_backward_workspace_size(64))
+    a.update(kw)
+    assert a["wsb"] == 16 or a["wsb"] >= 2 * 64 * 4
+    assert L.moe_layer_norm_backward(a["gr"], a["ld_gr"], a["gn"], a["ld_gn"], a["res"], a["res_dt"], a["ld_res"], P, 0,
+                                     1e-5, a["T"], a["H"], a["dr"], a["dy"], a["dw"], NUL, a["ws"], a["wsb"], NUL) == status
+
+
+def test_packed_calls(L):
+    """The calls of the dense half by number: each one's own refusals come back."""
+    import struct
+
+    def block(*v):
+        return struct.pack("=" + "".join("d" if isinstance(x, float) else "q" for x in v), *v)
+    p = P.value
+    assert L.moe_call_packed(7, block(p, 60, p, 60, 0, 0, 0, 4, 60, 8, p, 8, 0, p, 1 << 25, 0)) == UNSUPPORTED
+    assert L.moe_call_packed(8, block(p, 8, p, 64, p, 64, -1, p, 16, 4, 64, 8, p, p, 0, p, 1 << 25, 0)) == INVALID
+    assert L.moe_call_packed(9, block(p, 64, 4, 64, 1, p, p, 1, 1, 0)) == UNSUPPORTED
+    assert L.moe_call_packed(10, block(p, 128, 0, 0, 0, p, 128, p, 1, 0, 0, -1, 0, 0, 4, 128, 8, p, 0, 7, p, 1 << 25, 0)) == INVALID
+    assert L.moe_call_packed(11, block(p, 0, 8, 0, 0, 0, 0, 0, 1e-5, 4, 0, 0, p, 0)) == UNSUPPORTED
+    assert L.moe_call_packed(12, block(0, 0, p, 8, p, 0, 8, 0, 0, 1e-5, 1 << 33, 8, p, 0, 0, 0, p, 1 << 25, 0)) == UNSUPPORTED
+    for call in (6, 13, 99):
+        assert L.moe_call_packed(call, block(*([0] * 30))) == INVALID
+
+
 def test_the_bindings_refuse_host_tensors():
     import torch
 
     import mixture_experts_routed_top_gb300 as m
     t = torch.zeros(4, 8)
     for call in (lambda: m.gated_linear(t, t), lambda: m.gated_linear_backward(t, t, t, t),
-                 lambda: m.quantize_fp8_rows(t), lambda: m.linear_fp8(t, t, t)):
+                 lambda: m.quantize_fp8_rows(t), lambda: m.linear_fp8(t, t, t), lambda: m.layer_norm(t),
+                 lambda: m.layer_norm_backward(t, t, t)):
         with pytest.raises(ValueError):
             call()

@@ -1,5 +1,5 @@
 """The dense half of a block on the GPU against the float64 oracle: gated products, 8-bit
-products with block scales.
+products with block scales, layer norm.
 
 Tolerances as in test_gpu_block_ops.py, from the arithmetic: a bf16 result is one
 rounding, at most 2^-8 of it (BF); a tensor-core sum of K products is off by at most
@@ -301,3 +301,107 @@ def test_linear_fp8_long_rows_of_one_sign(moe):
         xc, _, xsv = O.quantize_blocks(_np(x).astype(np.float32), 1, 128, "f32")
         ry = B.linear_fp8(xc, xsv, wc & 0x7F, wsv)[0]
         assert np.linalg.norm(_np(y) - ry) < 2.0 ** -19 * np.linalg.norm(ry)
+
+
+# ------------------------------------------------------------------ layer norm
+NORMS = [  # T, H: rows in part of a warp, a block's several rows, odd widths, one row, the widest, several turns of the ring
+    (1, 1), (1, 7168), (3, 8), (5, 7), (37, 72), (64, 2048), (33, 2049), (19, 2056), (2, 8192), (9, 7167), (130, 264),
+    (2600, 2048), (700, 7168), (5000, 77), (320, 4100), (3, 8200), (200, 12288), (170, 8193), (2, 16384), (2, 16383)]
+
+
+@pytest.mark.parametrize("T,H", NORMS)
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_layer_norm_and_gradient(moe, T, H, dt):
+    g = _rng(T, H)
+    bf = dt == torch.bfloat16
+    for i, (wdt, bdt, add) in enumerate(((torch.bfloat16, True, True), (torch.float32, True, False), (None, False, True),
+                                         (torch.float32, False, True), (None, True, False))):
+        x = _dev(g.normal(size=(T, H)) * 2 + 4 * g.normal(size=(T, 1)), dt)
+        y = _dev(g.normal(size=(T, H)), torch.bfloat16) if add else None
+        w = None if wdt is None else _dev(1 + 0.3 * g.normal(size=H), wdt)
+        b = _dev(g.normal(size=H), torch.float32 if wdt is None else wdt) if bdt else None
+        r, n = moe.layer_norm(x, y, weight=w, bias=b)
+        f = lambda t: None if t is None else _np(t)
+        rr, rn = B.layer_norm(_np(x), f(y), f(w), f(b))
+        if add:
+            _close(r, rr, np.abs(_np(x)) + np.abs(_np(y)), bf, 2.0 ** -23)
+        else:
+            assert r is x
+        # the mean is off by F32 of the row's magnitudes, and with it every difference from it
+        aw = 1.0 if w is None else np.abs(_np(w))
+        rs = 1 / np.sqrt(rr.var(1, keepdims=True) + 1e-5)
+        hm = (np.abs(rr) + np.abs(rr).mean(1, keepdims=True)) * rs
+        _close(n, rn, hm * aw + np.abs(rn) + (0 if b is None else np.abs(_np(b))), True)
+        gn, gr = _dev(g.normal(size=(T, H)), torch.bfloat16), _dev(g.normal(size=(T, H)), dt) if i % 2 == 0 else None
+        need = add or not bf
+        dr, dy, dw, db = moe.layer_norm_backward(gr, gn, r, weight=w, bias=b, need_y=need)
+        rdr, rdw, rdb = B.layer_norm_backward(f(gr), _np(gn), _np(r), f(w))
+        v = _np(r)
+        rs = 1 / np.sqrt(v.var(1, keepdims=True) + 1e-5)
+        hm = (np.abs(v) + np.abs(v).mean(1, keepdims=True)) * rs
+        q = np.abs(_np(gn)) * aw
+        mag = rs * (q + q.mean(1, keepdims=True) + hm * (q * hm).mean(1, keepdims=True)) + (0 if gr is None else np.abs(_np(gr)))
+        _close(dr, rdr, mag, bf)
+        assert (dy is dr) if bf and need else (dy is None) if not need else torch.equal(dy, dr.bfloat16())
+        if w is None:
+            assert dw is None
+        else:
+            _close(dw, rdw, (np.abs(_np(gn)) * hm).sum(0), False)
+        if b is None:
+            assert db is None
+        else:
+            _close(db, rdb, np.abs(_np(gn)).sum(0), False)
+
+
+def test_layer_norm_far_from_zero(moe):
+    """A stream at 4096 with a spread of one: the variance is that of the differences, not a difference of squares."""
+    g = _rng(9)
+    for T, H in ((5, 300), (4, 2048), (3, 7167), (2, 12288)):
+        x = _dev(4096 + np.round(g.normal(size=(T, H)) * 64) / 64)
+        _, n = moe.layer_norm(x)
+        # the mean is off by at most 2^-18 of 4096 = 2^-6; on average by the trees' few roundings of 2^-12
+        ref = B.layer_norm(_np(x))[1]
+        assert np.abs(_np(n) - ref).max() <= 2.0 ** -8 * np.abs(ref).max() + 2.0 ** -9
+
+
+def test_layer_norm_strides_in_place_and_empty(moe):
+    g = _rng(41)
+    for H, lead, T in ((264, 8, 37), (264, 16, 37), (77, 8, 300)):
+        x, y = _dev(g.normal(size=(T, H)), torch.bfloat16), _dev(g.normal(size=(T, H)), torch.bfloat16)
+        w, b = _dev(g.normal(size=H)), _dev(g.normal(size=H))
+        r, n = moe.layer_norm(x, y, weight=w, bias=b)
+        big = torch.zeros(T, 400, dtype=torch.bfloat16, device="cuda")
+        big[:, lead:lead + H] = x
+        r2, n2 = moe.layer_norm(big[:, lead:lead + H], y, weight=w, bias=b)
+        assert torch.equal(r2, r) and torch.equal(n2, n)
+        copy, nn = x.clone(), torch.empty_like(n)
+        r3, n3 = moe.layer_norm(copy, y, weight=w, bias=b, out=(copy, nn))
+        assert r3 is copy and n3 is nn and torch.equal(copy, r) and torch.equal(nn, n)
+        gr, gn = _dev(g.normal(size=(T, H)), torch.bfloat16), _dev(g.normal(size=(T, H)), torch.bfloat16)
+        full = moe.layer_norm_backward(gr, gn, r, weight=w, bias=b)
+        big2 = torch.zeros(T, 408, dtype=torch.bfloat16, device="cuda")
+        big2[:, lead:lead + H] = gn
+        again = moe.layer_norm_backward(gr, big2[:, lead:lead + H], r, weight=w, bias=b)
+        assert all(torch.equal(p, q) for p, q in zip((full[0], *full[2:]), (again[0], *again[2:])))
+        e = moe.layer_norm_backward(gr[:0], gn[:0], r[:0], weight=w, bias=b, need_y=True)
+        assert e[0].shape == (0, H) and (e[2] == 0).all() and (e[3] == 0).all()
+        assert moe.layer_norm(x[:0], y[:0])[1].shape == (0, H)
+    for bad in (lambda: moe.layer_norm(x, y.float()), lambda: moe.layer_norm(x, weight=w[1:]),
+                lambda: moe.layer_norm(x, weight=w, bias=b.bfloat16()), lambda: moe.layer_norm(x.half()),
+                lambda: moe.layer_norm_backward(gr.float(), gn, r), lambda: moe.layer_norm_backward(gr, gn[1:], r)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(moe.MoEError):
+        moe.layer_norm(torch.zeros(2, 16392, device="cuda"))
+
+
+def test_layer_norm_rows_stay_apart(moe):
+    """Equal columns have variance 0 and give the bias; a NaN or an infinity stays in its row."""
+    for H in (64, 77, 7168, 12288):
+        x = torch.full((6, H), 3.0, device="cuda")
+        x[1, H // 2], x[4, H - 1] = float("nan"), float("inf")
+        b = torch.arange(H, device="cuda") * 1.0
+        _, n = moe.layer_norm(x, bias=b)
+        assert torch.isnan(n[1]).all() and torch.isnan(n[4]).any() and not torch.isfinite(n[4, H - 1])
+        for i in (0, 2, 3, 5):
+            assert torch.equal(n[i], b.bfloat16())
