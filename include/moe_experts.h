@@ -637,7 +637,7 @@ moe_status moe_gated_linear_backward(const void* grad_h, int64_t ld_gh, const vo
  *   scale     device out, fp32 or UE8M0 bytes (scale_fmt): that of row t and block kb at
  *             scale[t * s_row + kb * s_kb]
  * The scale is amax / 448 in fp32, at least 2^-126, or the smallest power of two that is no
- * smaller; 1 where amax is 0, infinite (byte 255) where it is.  Codes round x * (1 / scale)
+ * smaller; 1 where amax is 0, not finite (byte 255) where it is not.  Codes round x * (1 / scale)
  * to nearest, ties to even.
  * K % 128 == 0 and ld_x a multiple of 8, else MOE_ERR_UNSUPPORTED.  T = 0 is a no-op.
  */

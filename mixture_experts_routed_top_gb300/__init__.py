@@ -976,9 +976,8 @@ def quantize_fp8_rows(x: torch.Tensor, scale_fmt: str = "f32", *,
     """bf16 [T,K] -> (e4m3 codes uint8 [T,K], scales [T,K/128] of its 1x128 blocks as
     fp32 ('f32') or uint8 exponent bytes ('ue8m0')), for linear_fp8.
 
-    K a multiple of 128.  The scales lie by K block (strides (1, T)), as
-    linear_fp8 reads them best.  out: (codes, scales) to write into, codes
-    contiguous, scales with any positive strides."""
+    K a multiple of 128.  out: (codes, scales) to write into, codes contiguous,
+    scales with any positive strides."""
     if stream is not None:
         return _on_stream(quantize_fp8_rows, locals())
     dev, xs = _matrix_of("x", x)
@@ -990,7 +989,7 @@ def quantize_fp8_rows(x: torch.Tensor, scale_fmt: str = "f32", *,
     if out is None:
         q = torch.empty(xs, dtype=torch.uint8, device=x.device)
         pq = q.data_ptr()
-        s = torch.empty((K // 128, T), dtype=_F32 if sf == SCALE_F32 else torch.uint8, device=x.device).t()
+        s = torch.empty((T, K // 128), dtype=_F32 if sf == SCALE_F32 else torch.uint8, device=x.device)
     else:
         q, s = out
         pq = _dense("codes", q, _E4M3, xs, dev)
@@ -1019,7 +1018,8 @@ def linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
     [ceil(N/128), K/128] of its 128x128 blocks: fp32, or uint8 UE8M0 exponent
     bytes (quantize_fp8_blocks).  x bf16 [T,K], quantised in 1x128 blocks with
     scales of w_scale's format on the way; or e4m3 with x_scale [T,K/128] of
-    that format (quantize_fp8_rows), any strides.  bias, activation, residual,
+    that format (quantize_fp8_rows), any strides; a row's side by side are
+    read best.  bias, activation, residual,
     out_dtype, out, workspace: as in linear."""
     global _LINEAR_WS
     if stream is not None:

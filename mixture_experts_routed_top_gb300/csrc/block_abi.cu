@@ -261,7 +261,7 @@ Fp8Ws fp8_ws(int T, int K) {
   Fp8Ws w;
   w.codes = kLinearWsBytes;
   w.scales = w.codes + (static_cast<size_t>(T) * K + 1023) / 1024 * 1024;
-  w.total = w.scales + static_cast<size_t>(T) * (K / 128) * 4;
+  w.total = w.scales + static_cast<size_t>(T) * ((K / 128 + 3) / 4 * 4) * 4;
   return w;
 }
 // Up to this many tokens the kernel that streams the weights quantises them itself.
@@ -830,15 +830,16 @@ moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int6
   const int KB = K / 128;
   const bool streams = fp8_streams(T, N);
   if (!x_scale && !(streams && T <= kFp8QuantiseOnTheWay)) {
-    // codes, and scales by K block: what neighbouring rows need lies together
+    // rows of scales padded to 4: a 16-byte load brings those of four K blocks
+    const int64_t row = (KB + 3) / 4 * 4;
     const cudaError_t r = launch_fp8_rows({static_cast<const __nv_bfloat16*>(x), wsb + L.codes,
-                                           wsb + L.scales, ld_x, 1, T, T, KB, sc.ue8m0 != 0}, s);
+                                           wsb + L.scales, ld_x, row, 1, T, KB, sc.ue8m0 != 0}, s);
     if (r != cudaSuccess) return cuda_error(r, fn);
     x = wsb + L.codes;
     ld_x = K;
     sc.x = wsb + L.scales;
-    sc.x_row = 1;
-    sc.x_kb = T;
+    sc.x_row = row;
+    sc.x_kb = 1;
   }
   if (streams) {
     Fp8StreamArgs g;

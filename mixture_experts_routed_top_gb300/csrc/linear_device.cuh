@@ -171,8 +171,8 @@ __device__ __forceinline__ void epilogue8(const LinearEpi& p, long m, int n, con
 constexpr int kTurn = 32 * 32;
 template <int ACT, bool F32, bool REST>
 __device__ __forceinline__ void epilogue32(const LinearEpi& p, long m, int n,
-                                           const uint32_t (&v)[32], float* buf) {
-  const int lane = threadIdx.x & 31;
+                                           const uint32_t (&v)[32], float* buf,
+                                           const int lane = threadIdx.x & 31) {
   const long m0 = m - lane;
   // bias and residual of 8 columns of 4 rows, every load on its way before the
   // first store, which the compiler may not move loads across

@@ -21,22 +21,23 @@ namespace {
 
 constexpr int kB = 128;  // e4m3 per 128-byte swizzled row = one scale block
 
+__device__ __forceinline__ float ue8m0_value(uint32_t b) {
+  return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
+}
 __device__ __forceinline__ float scale_at(const void* base, long i, int ue8m0) {
-  if (ue8m0) {
-    const uint32_t b = __ldg(static_cast<const uint8_t*>(base) + i);
-    return b == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(b << 23);
-  }
-  return __ldg(static_cast<const float*>(base) + i);
+  return ue8m0 ? ue8m0_value(__ldg(static_cast<const uint8_t*>(base) + i))
+               : __ldg(static_cast<const float*>(base) + i);
 }
 // Of a block of a row from its absolute maximum, as the weights' quantiser, but no
 // less than 2^-126, whose reciprocal is still a number; *stored: bits or exponent byte.
-// An infinity makes an infinite scale (byte 255), which makes its row NaN.
+// An infinity or NaN makes an infinite or NaN scale (byte 255), which makes its row NaN.
 __device__ __forceinline__ float row_scale(float amax, bool ue8m0, uint32_t* stored) {
   if (amax == 0.f) {
     *stored = ue8m0 ? 127u : __float_as_uint(1.0f);
     return 1.0f;
   }
-  const float q = fmaxf(amax / 448.0f, __uint_as_float(0x00800000u));
+  float q = amax / 448.0f;
+  q = q < __uint_as_float(0x00800000u) ? __uint_as_float(0x00800000u) : q;  // a NaN stays one
   if (!ue8m0) {
     *stored = __float_as_uint(q);
     return q;
@@ -58,12 +59,14 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
     v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ float amax8(const uint4& u) {
-  float v[8], m = 0.f;
-  unpack8(u, v);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-  return m;
+// The largest absolute value of 8, as bits: those of bf16 without a sign are ordered as
+// integers, NaN above all.
+__device__ __forceinline__ uint32_t amax8(const uint4& u) {
+  const uint32_t m = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
+}
+__device__ __forceinline__ float amax_value(uint32_t pair) {  // of both halves
+  return __uint_as_float(max(pair << 16, pair & 0xffff0000u));
 }
 __device__ __forceinline__ uint2 codes8(const uint4& u, float inv) {
   float v[8];
@@ -91,17 +94,27 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __grid_constant__ F
                ? __ldg(reinterpret_cast<const uint4*>(a.x + t * a.ld_x + kb * kB) + l)
                : make_uint4(0u, 0u, 0u, 0u);
   }
+  // lane l of the 16 keeps the maximum of unit l % 8, so that each scale is made once
+  uint32_t mine = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t m = amax8(v[i]);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if ((l & 7) == i) mine = m;
+  }
+  uint32_t stored;
+  const float inv_mine = 1.0f / row_scale(amax_value(mine), a.ue8m0, &stored);
+  if (l < 8) {
+    const int u = hw + 16 * l;
+    s_scale[u & 3][u >> 2] = stored;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int u = hw + 16 * i, t = t0 + (u >> 2), kb = kb0 + (u & 3);
-    float m = amax8(v[i]);
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    uint32_t stored;
-    const float inv = 1.0f / row_scale(m, a.ue8m0, &stored);
+    const float inv = __shfl_sync(0xffffffffu, inv_mine, i, 16);
     if (t < a.T && kb < a.KB)
       reinterpret_cast<uint2*>(a.q + (static_cast<long>(t) * a.KB + kb) * kB)[l] = codes8(v[i], inv);
-    if (l == 0) s_scale[u & 3][u >> 2] = stored;
   }
   __syncthreads();
   const int i = threadIdx.x;
@@ -114,37 +127,109 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const __grid_constant__ F
 }
 
 // ====================================================== promotion
-// The sums of one K block, 64 columns of this thread's row, from TMEM at `taddr`, times
-// s, added to acc.  `release` runs once all of them have been read.
-template <typename Release>
-__device__ __forceinline__ void promote(uint32_t taddr, float s, float (&acc)[64], Release release) {
+// 32 of a K block's sums in this thread's row, times s, added to acc[AT ..].
+template <int AT, int N>
+__device__ __forceinline__ void promote(const uint32_t (&v)[32], float s, float (&acc)[N]) {
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    uint32_t v[16];
-    tmem_ld_32x32b_x16(taddr + 16 * h, v);
-    tmem_ld_wait_x16(v);
-    if (h == 3) release();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) acc[16 * h + i] = fmaf(__uint_as_float(v[i]), s, acc[16 * h + i]);
-  }
+  for (int i = 0; i < 32; ++i) acc[AT + i] = fmaf(__uint_as_float(v[i]), s, acc[AT + i]);
 }
+
+// The scales of a row of x, four K blocks at a time: one 16-byte load where they lie side by
+// side (fp32; 4 bytes of UE8M0), four loads where they do not.
+struct ScaleRow {
+  const char* x;
+  long step;
+  bool valid, side, ue8m0;
+  __device__ __forceinline__ ScaleRow(const Fp8Scales& sc, long m, bool valid_)
+      : valid(valid_), ue8m0(sc.ue8m0 != 0) {
+    const int size = ue8m0 ? 1 : 4;
+    x = static_cast<const char*>(sc.x) + m * sc.x_row * size;
+    step = sc.x_kb * size;
+    side = sc.x_kb == 1 && (reinterpret_cast<uintptr_t>(x) & (4 * size - 1)) == 0;
+  }
+  // of the blocks kb .. kb + 3, kb a multiple of 4, those below KB
+  __device__ __forceinline__ void four(int kb, int KB, float (&s)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = 0.f;
+    if (!valid) return;
+    const char* p = x + kb * step;
+    if (side && kb + 4 <= KB) {
+      if (!ue8m0) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+        s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+      } else {
+        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = ue8m0_value((v >> (8 * i)) & 255u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (kb + i < KB) s[i] = scale_at(p + i * step, 0, ue8m0);
+    }
+  }
+};
 
 // ====================================================== CTA-pair kernel
 // 256 x 256 tiles, cta_group::2: each CTA holds 128 rows of x and 128 of w per stage, and
 // 128 rows x 256 columns of the sums of two K blocks in TMEM, one of them being filled
-// while the other is promoted.  Roles (576 threads): warp 0 loads, warp 1 MMAs (rank
-// 0), warps 2-17 promotion and epilogue: thread = row, four groups of 64 columns.
+// while the other is promoted.  Roles (384 threads):
+//   warp 0     TMA producer
+//   warp 1     MMA issuer (rank 0); the whole warp walks and one lane issues
+//   warps 2-3  the scale products of 8 K blocks at a time, into a ring of two such slabs
+//   warps 4-11 promotion and epilogue: thread = row, two halves of 128 columns.  Columns go
+//              32 at a time, the next load on its way while the last one is multiplied,
+//              also from one K block to the next.  128 sums and 64 loaded values take the
+//              registers that the first four warps give up (4 x 56 + 8 x 224 a lane of the
+//              12 x 168 that the block is launched with).
 // Barriers as in the bf16 pair kernel; every wait is bounded.
 constexpr int kStages = 5;
-constexpr int kEpiWarps = 16;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kRegsFew = 56, kRegsMany = 224;
+static_assert(4 * kRegsFew + kEpiWarps * kRegsMany <= (4 + kEpiWarps) * 168, "registers of the launch");
+constexpr int kSlab = 8;                           // K blocks of scale products
 constexpr int kOper = 128 * kB;                    // 16 KB: one operand's part of a stage
 constexpr int kOffBar = 2 * kStages * kOper;
-constexpr int kBars = 2 * kStages + 5;
+constexpr int kBars = 2 * kStages + 9;
 constexpr int kOffMisc = kOffBar + kBars * 8;
 constexpr int kOffTurn = (kOffMisc + 8 + 15) / 16 * 16;
-constexpr int kSmem = kOffTurn + kEpiWarps * kTurn * 4 + 1024;
+constexpr int kOffScale = kOffTurn + kEpiWarps * kTurn * 4;  // [2][kSlab][2 halves][128 rows]
+constexpr int kSmem = kOffScale + 2 * kSlab * 256 * 4 + 1024;
 static_assert(kOffMisc % 8 == 0 && kSmem <= 227 * 1024, "shared memory");
+
+// 64 columns of 32 rows of bf16 results without a residual, rows of whole aligned vectors:
+// bias and activation where the sums are, 16-byte pieces of the rounded rows through the
+// turn buffer (in the order of their index xor the row's), then 8 lanes along a row, so
+// that a store fills lines.
+template <int ACT>
+__device__ __forceinline__ void epilogue64_bf16(const LinearEpi& p, int m0, int n, float* z, float* buf, int lane) {
+  uint4* const b4 = reinterpret_cast<uint4*>(buf);
+  __syncwarp();  // the previous step's values have been read
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    if (p.bias != nullptr && n + 8 * c < p.N) {
+      float b[8];
+      ld8(p.bias, n + 8 * c, p.bias_bf16, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[8 * c + j] += b[j];
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = pack_bf16x2(act_f(z[8 * c + 2 * j], ACT, false), act_f(z[8 * c + 2 * j + 1], ACT, false));
+    b4[lane * 8 + (c ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  const int c = lane & 7, r0 = lane >> 3;
+  if (n + 8 * c >= p.N) return;
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (static_cast<long>(m0) + r0) * p.ld_out + n + 8 * c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 4 * i;
+    if (m0 + r < p.M) *reinterpret_cast<uint4*>(to + 4 * i * p.ld_out) = b4[r * 8 + (c ^ (r & 7))];
+  }
+}
 
 template <int ACT, bool F32>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -158,6 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* pfull = empty + kStages;       // both: sums of a K block complete
   uint64_t* pempty = pfull + 2;            // rank 0: both CTAs have read them
   uint64_t* fin = pempty + 2;              // rank 0: every MMA done
+  uint64_t* sfull = fin + 1;               // a slab of scale products is there
+  uint64_t* sempty = sfull + 2;            // it has been read
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -171,6 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&pfull[b]), 1);
       mbar_init(smem_u32(&pempty[b]), 2 * kEpiWarps);
+      mbar_init(smem_u32(&sfull[b]), 64);
+      mbar_init(smem_u32(&sempty[b]), kEpiWarps);
     }
     mbar_init(smem_u32(fin), 1);
     *s_abort = 0;
@@ -191,9 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int mt = (p.epi.M + 255) >> 8, nt = (p.epi.N + 255) >> 8;
   const int total = mt * nt, KB = p.KB;
   const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
+  float* const slabs = reinterpret_cast<float*>(smem + kOffScale);
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    regs_fewer<kRegsFew>();
+    if (warp == 0 && lane == 0) {
       int stage = 0;
       uint32_t ph = 0, issued = 0, last_par = 0;
       bool ok = true;
@@ -201,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int mi, ni;
         pair_tile(tile, mt, nt, p.group, &mi, &ni);
         for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_pair(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err, ERR_TIMEOUT_PRODUCER)) {
+          if (!wait_cta(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err, ERR_TIMEOUT_PRODUCER)) {
             ok = false;
             break;
           }
@@ -224,94 +315,158 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < kStages; ++s) {
         if ((issued >> s) & 1u) {
           volatile int no_abort = 0;
-          wait_pair(smem_u32(rank == 0 ? &full[s] : &empty[s]), (last_par >> s) & 1u, &no_abort,
+          wait_cta(smem_u32(rank == 0 ? &full[s] : &empty[s]), (last_par >> s) & 1u, &no_abort,
                     p.err, ERR_TIMEOUT_PRODUCER, kDrainCycles);
         }
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+      // one K block is like the next, whatever tile it is of
       constexpr uint32_t idesc = idesc_e4m3_f32(256, 256);
+      const uint32_t count = static_cast<uint32_t>(cid < total ? (total - cid + ncl - 1) / ncl : 0) * KB;
+      const uint64_t d0 = sdesc_k_sw128(smem_u32(smem));
       int stage = 0;
-      uint32_t ph = 0, g = 0;  // g: K blocks so far, which select the buffer
-      bool ok = true;
-      for (int tile = cid; ok && tile < total; tile += ncl) {
-        for (int kb = 0; kb < KB; ++kb, ++g) {
-          const int b = g & 1;
-          if (!wait_pair(smem_u32(&pempty[b]), ((g >> 1) & 1) ^ 1u, s_abort, p.err, ERR_TIMEOUT_MMA) ||
-              !wait_pair(smem_u32(&full[stage]), ph, s_abort, p.err, ERR_TIMEOUT_MMA)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t as = smem_u32(smem + 2 * stage * kOper);
-          const uint64_t ad = sdesc_k_sw128(as), bd = sdesc_k_sw128(as + kOper);
+      uint32_t ph = 0;
+      for (uint32_t g = 0; g < count; ++g) {
+        const uint32_t b = g & 1, eph = ((g >> 1) & 1) ^ 1u;
+        const uint32_t fbar = smem_u32(&full[stage]), ebar = smem_u32(&pempty[b]);
+        const bool f = mbar_try_wait(fbar, ph), e = mbar_try_wait(ebar, eph);  // both on their way
+        const bool ok = (f || wait_cta(fbar, ph, s_abort, p.err, ERR_TIMEOUT_MMA)) &&
+                        (e || wait_cta(ebar, eph, s_abort, p.err, ERR_TIMEOUT_MMA));
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint64_t ad = d0 + static_cast<uint32_t>(stage * (2 * kOper >> 4)), bd = ad + (kOper >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kB / 32; ++kk)
             umma_f8_pair(tmem + b * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u);
-          umma_commit_pair_both(smem_u32(&empty[stage]));
           umma_commit_pair_both(smem_u32(&pfull[b]));
-          if (++stage == kStages) {
-            stage = 0;
-            ph ^= 1u;
-          }
+          umma_commit_pair_both(smem_u32(&empty[stage]));
+        }
+        __syncwarp();
+        if (++stage == kStages) {
+          stage = 0;
+          ph ^= 1u;
         }
       }
-      if (g > 0) {
-        umma_commit_pair_local(smem_u32(fin));
+      if (count > 0) {
+        if (elect_one()) umma_commit_pair_local(smem_u32(fin));
         volatile int no_abort = 0;
-        wait_pair(smem_u32(fin), 0, &no_abort, p.err, ERR_TIMEOUT_MMA);
+        wait_cta(smem_u32(fin), 0, &no_abort, p.err, ERR_TIMEOUT_MMA);
+      }
+    } else if (warp >= 2) {
+      const int r = threadIdx.x - 64;  // rows r and r + 64
+      const int nb = (p.epi.N + kB - 1) / kB;  // rows of weight scales
+      uint32_t slab = 0;
+      bool ok = true;
+      for (int tile = cid; ok && tile < total; tile += ncl) {
+        int mi, ni;
+        pair_tile(tile, mt, nt, p.group, &mi, &ni);
+        const long m = static_cast<long>(mi) * 256 + 128 * rank + r;
+        ScaleRow x0(p.sc, m, m < p.epi.M), x1(p.sc, m + 64, m + 64 < p.epi.M);
+        const long w0 = static_cast<long>(min(2 * ni, nb - 1)) * KB, w1 = static_cast<long>(min(2 * ni + 1, nb - 1)) * KB;
+        for (int kb = 0; kb < KB; kb += kSlab, ++slab) {
+          const int b = slab & 1;
+          if (!wait_cta(smem_u32(&sempty[b]), ((slab >> 1) & 1) ^ 1u, s_abort, p.err, ERR_TIMEOUT_EPILOGUE)) {
+            ok = false;
+            break;
+          }
+          float* to = slabs + b * kSlab * 256 + r;
+#pragma unroll 1
+          for (int j = 0; j < kSlab && kb + j < KB; j += 4) {
+            float a[4], c[4];
+            x0.four(kb + j, KB, a);
+            x1.four(kb + j, KB, c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (kb + j + i >= KB) continue;
+              const float u0 = scale_at(p.sc.w, w0 + kb + j + i, p.sc.ue8m0),
+                          u1 = scale_at(p.sc.w, w1 + kb + j + i, p.sc.ue8m0);
+              float* const at = to + (j + i) * 256;
+              at[0] = a[i] * u0;
+              at[64] = c[i] * u0;
+              at[128] = a[i] * u1;
+              at[192] = c[i] * u1;
+            }
+          }
+          mbar_arrive(smem_u32(&sfull[b]));
+        }
       }
     }
+    __syncwarp();
   } else {
-    const int q = warp & 3, grp = (warp - 2) >> 2;  // TMEM lane quarter, 64 columns
-    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64 * grp;
-    float* const turn = reinterpret_cast<float*>(smem + kOffTurn) + (warp - 2) * kTurn;
-    const int nb = (p.epi.N + kB - 1) / kB;  // rows of weight scales
-    uint32_t g = 0;
-    int ok = 1;
+    regs_more<kRegsMany>();
+    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lane quarter, column half
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 128 * half;
+    float* const turn = reinterpret_cast<float*>(smem + kOffTurn) + (warp - 4) * kTurn;
+    const uint32_t pempty0 = rank == 0 ? smem_u32(pempty) : mapa_shared(smem_u32(pempty), 0);
+    const float* const mine = slabs + 128 * half + 32 * q + lane;
+    uint32_t g = 0, slab = 0;  // K blocks and slabs so far
+    uint32_t v[2][32];
+    // waits for block g's sums and asks for the first 32 of them
+    auto begin = [&] {
+      const bool ready = wait_cta(smem_u32(&pfull[g & 1]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
+      if (!__all_sync(0xffffffffu, ready)) return false;
+      tc_fence_after();
+      tmem_ld_32x32b_x32(tl + (g & 1) * 256, v[0]);
+      return true;
+    };
     for (int tile = cid; tile < total; tile += ncl) {
       int mi, ni;
       pair_tile(tile, mt, nt, p.group, &mi, &ni);
-      const long m = static_cast<long>(mi) * 256 + 128 * rank + 32 * q + lane;
-      const bool valid = m < p.epi.M;
-      const long wbase = static_cast<long>(min(2 * ni + (grp >> 1), nb - 1)) * KB;
-      float acc[64];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0.f;
-      // the scales of a K block are loaded while the one before it is promoted
-      float sx = valid ? scale_at(p.sc.x, m * p.sc.x_row, p.sc.ue8m0) : 0.f;
-      float sw = scale_at(p.sc.w, wbase, p.sc.ue8m0);
-#pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb, ++g) {
-        const int b = g & 1;
-        const float s = sx * sw;
-        if (kb + 1 < KB) {
-          sx = valid ? scale_at(p.sc.x, m * p.sc.x_row + (kb + 1) * p.sc.x_kb, p.sc.ue8m0) : 0.f;
-          sw = scale_at(p.sc.w, wbase + kb + 1, p.sc.ue8m0);
-        }
-        if (lane == 0)
-          ok = wait_pair(smem_u32(&pfull[b]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      bool ok = true;
+      for (int kb0 = 0; ok && kb0 < KB; kb0 += kSlab, ++slab) {
+        ok = wait_cta(smem_u32(&sfull[slab & 1]), (slab >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        tc_fence_after();
-        promote(tl + b * 256, s, acc, [&] {
+        const float* from = mine + (slab & 1) * kSlab * 256;
+        const int count = min(kSlab, KB - kb0);
+        if (kb0 == 0) ok = begin();
+#pragma unroll 1
+        for (int j = 0; ok && j < count; ++j) {
+          const float s = from[j * 256];
+          const uint32_t tb = tl + (g & 1) * 256;
+          tmem_ld_wait_x32(v[0]);
+          tmem_ld_32x32b_x32(tb + 32, v[1]);
+          promote<0>(v[0], s, acc);
+          tmem_ld_wait_x32(v[1]);
+          tmem_ld_32x32b_x32(tb + 64, v[0]);
+          promote<32>(v[1], s, acc);
+          tmem_ld_wait_x32(v[0]);
+          tmem_ld_32x32b_x32(tb + 96, v[1]);
+          promote<64>(v[0], s, acc);
+          tmem_ld_wait_x32(v[1]);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (rank == 0) mbar_arrive(smem_u32(&pempty[b]));
-            else mbar_arrive_remote(mapa_shared(smem_u32(&pempty[b]), 0));
+            if (rank == 0) mbar_arrive(pempty0 + 8 * (g & 1));
+            else mbar_arrive_remote_relaxed(pempty0 + 8 * (g & 1));
           }
-        });
+          ++g;
+          if (kb0 + j + 1 < KB) ok = begin();
+          promote<96>(v[1], s, acc);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sempty[slab & 1]));
       }
       if (!ok) break;
-      const int n0 = ni * 256 + 64 * grp;
+      // what the epilogue derives from these is not worth a register while blocks are promoted
+      int ln = lane, n0 = ni * 256 + 128 * half;
+      asm volatile("" : "+r"(mi), "+r"(n0), "+r"(ln));
+      const int m0 = mi * 256 + 128 * rank + 32 * q;
+      if (!F32 && p.epi.vec && p.epi.residual == nullptr) {
+        epilogue64_bf16<ACT>(p.epi, m0, n0, acc, turn, ln);
+        if (n0 + 64 < p.epi.N) epilogue64_bf16<ACT>(p.epi, m0, n0 + 64, acc + 64, turn, ln);
+        continue;
+      }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint32_t v[32];
+      for (int s = 0; s < 4; ++s) {
+        uint32_t u[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(acc[32 * s + i]);
-        if (n0 + 32 * s < p.epi.N) epilogue32<ACT, F32, false>(p.epi, m, n0 + 32 * s, v, turn);
+        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(acc[32 * s + i]);
+        if (n0 + 32 * s < p.epi.N) epilogue32<ACT, F32, false>(p.epi, static_cast<long>(m0) + ln, n0 + 32 * s, u, turn, ln);
       }
     }
   }
@@ -325,10 +480,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ====================================================== split tile kernel
 // One 128 x 128 tile per cluster of S CTAs; CTA r takes the r-th part of the contraction
-// (at least one K block).  Two CTAs fit an SM (256 TMEM columns each).  8 promotion
+// (at least one K block).  8 promotion
 // warps: thread = row, two halves of 64 columns; the CTAs' sums are joined as the bf16
 // kernel's.
-constexpr int kTStages = 3;
+constexpr int kTStages = 5;
 constexpr int kTEpiWarps = 8;
 constexpr int kTThreads = 64 + 32 * kTEpiWarps;
 constexpr int kTOffBar = 2 * kTStages * kOper;
@@ -338,7 +493,7 @@ constexpr int kTSmem = kTOffMisc + 16 + 1024;
 constexpr int kTStride = 132;  // floats per staged row: 128 + 4 (no bank conflicts)
 static_assert(128 * kTStride * 4 <= kTOffBar, "staged tile fits the ring");
 
-__global__ void __launch_bounds__(kTThreads, 2)
+__global__ void __launch_bounds__(kTThreads, 1)
     fp8_tile_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                     const __grid_constant__ Fp8LinearDev p) {
   extern __shared__ uint8_t smem_raw[];
@@ -434,35 +589,47 @@ __global__ void __launch_bounds__(kTThreads, 2)
     }
   }
   float acc[64];
-  int ok = 1;
   const int q = warp & 3, half = (warp - 2) >> 2;
   if (warp >= 2) {
 #pragma unroll
     for (int i = 0; i < 64; ++i) acc[i] = 0.f;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16) + 64 * half;
     const long m = static_cast<long>(mi) * 128 + 32 * q + lane;
-    const bool valid = m < p.epi.M;
-    const long wbase = static_cast<long>(ni) * p.KB;  // ni * 128 < N
-    float sx = valid ? scale_at(p.sc.x, m * p.sc.x_row + kb0 * p.sc.x_kb, p.sc.ue8m0) : 0.f;
-    float sw = scale_at(p.sc.w, wbase + kb0, p.sc.ue8m0);
-#pragma unroll 1
-    for (int kb = kb0; kb < kb1; ++kb) {
-      const int g = kb - kb0, b = g & 1;
-      const float s = sx * sw;
-      if (kb + 1 < kb1) {
-        sx = valid ? scale_at(p.sc.x, m * p.sc.x_row + (kb + 1) * p.sc.x_kb, p.sc.ue8m0) : 0.f;
-        sw = scale_at(p.sc.w, wbase + kb + 1, p.sc.ue8m0);
-      }
-      if (lane == 0)
-        ok = wait_cta(smem_u32(&pfull[b]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+    const ScaleRow row(p.sc, m, m < p.epi.M);
+    const long w_row = static_cast<long>(ni) * p.KB;  // ni * 128 < N
+    uint32_t v[2][32];
+    // waits for the sums of block g of this part and asks for the first 32 of them
+    auto begin = [&](int g) {
+      const bool ready = wait_cta(smem_u32(&pfull[g & 1]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
+      if (!__all_sync(0xffffffffu, ready)) return false;
       tc_fence_after();
-      promote(tl + b * 128, s, acc, [&] {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&pempty[b]));
-      });
+      tmem_ld_32x32b_x32(tl + (g & 1) * 128, v[0]);
+      return true;
+    };
+    float sx[4], nx[4], sw = scale_at(p.sc.w, w_row + kb0, p.sc.ue8m0);
+    row.four(kb0 & ~3, p.KB, nx);  // the scales of four blocks, those ahead on their way
+    bool ok = true;
+#pragma unroll 1
+    for (int kb = kb0; ok && kb < kb1; ++kb) {
+      const int g = kb - kb0, b = g & 1;
+      if (g == 0 || (kb & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sx[i] = nx[i];
+        if ((kb | 3) + 1 < kb1) row.four((kb | 3) + 1, p.KB, nx);
+      }
+      const float s = sw * ((kb & 2) ? ((kb & 1) ? sx[3] : sx[2]) : ((kb & 1) ? sx[1] : sx[0]));
+      if (kb + 1 < kb1) sw = scale_at(p.sc.w, w_row + kb + 1, p.sc.ue8m0);
+      if (g == 0) ok = begin(0);
+      if (!ok) break;
+      tmem_ld_wait_x32(v[0]);
+      tmem_ld_32x32b_x32(tl + b * 128 + 32, v[1]);
+      promote<0>(v[0], s, acc);
+      tmem_ld_wait_x32(v[1]);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&pempty[b]));
+      if (kb + 1 < kb1) ok = begin(g + 1);
+      promote<32>(v[1], s, acc);
     }
   }
   __syncwarp();
@@ -575,11 +742,11 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
               for (int i = 0; i < 4; ++i)
                 v[i] = __ldg(reinterpret_cast<const uint4*>(x + 64 * (i >> 1) + 8 * (i & 1)));
             }
-            float m = fmaxf(fmaxf(amax8(v[0]), amax8(v[1])), fmaxf(amax8(v[2]), amax8(v[3])));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            uint32_t m = __vmaxu2(__vmaxu2(amax8(v[0]), amax8(v[1])), __vmaxu2(amax8(v[2]), amax8(v[3])));
+            m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
             uint32_t stored;
-            sx = row_scale(m, a.sc.ue8m0 != 0, &stored);
+            sx = row_scale(amax_value(m), a.sc.ue8m0 != 0, &stored);
             const float inv = 1.0f / sx;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -723,8 +890,7 @@ cudaError_t launch_stream_tokens(const Fp8StreamArgs& a, int num_sms, cudaStream
 }  // namespace
 
 // As linear_path: pairs from half a wave of their tiles, below it 128 x 128 tiles with the
-// contraction split until the grid covers the GPU twice, each part at least two K
-// blocks long.
+// contraction split until the grid covers the GPU, each part at least two K blocks long.
 LinearPath fp8_path(long M, long N, long K, int num_sms) {
   LinearPath r;
   const long big = static_cast<long>(ceil_div(M, 256)) * ceil_div(N, 256);
@@ -736,7 +902,7 @@ LinearPath fp8_path(long M, long N, long K, int num_sms) {
   }
   r.kind = LinearPath::kTile;
   const long tiles = static_cast<long>(ceil_div(M, 128)) * ceil_div(N, 128);
-  while (r.split < 8 && tiles * r.split * 2 <= 4 * pairs && K / (r.split * 2) >= 2 * kB) r.split *= 2;
+  while (r.split < 8 && tiles * r.split * 2 <= 2 * pairs && K / (r.split * 2) >= 2 * kB) r.split *= 2;
   return r;
 }
 
