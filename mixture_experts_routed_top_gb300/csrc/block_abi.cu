@@ -841,20 +841,28 @@ moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int6
     sc.x_row = row;
     sc.x_kb = 1;
   }
-  if (streams) {
+  // rows t0 .. T by the kernel of few tokens
+  auto stream_rows = [&](int64_t t0) {
+    auto rows = [](const void* p, int64_t bytes) { return static_cast<const uint8_t*>(p) + bytes; };
     Fp8StreamArgs g;
-    g.x = x;
+    g.codes = sc.x != nullptr;
+    g.x = rows(x, t0 * ld_x * (g.codes ? 1 : 2));
     g.w = static_cast<const uint8_t*>(w);
     g.ld_x = ld_x;
     g.ld_w = ld_w;
     g.sc = sc;
+    if (sc.x) g.sc.x = rows(sc.x, t0 * sc.x_row * (sc.ue8m0 ? 1 : 4));
     g.KB = KB;
-    g.codes = sc.x != nullptr;
     g.wpr = g.split = 1;
     g.epi = e;
+    g.epi.M = static_cast<int>(T - t0);
+    g.epi.out = static_cast<uint8_t*>(out) + t0 * ld_out * size_of(out_dt);
+    if (residual) g.epi.residual = rows(residual, t0 * ld_res * size_of(out_dt));
     const cudaError_t r = launch_fp8_stream(g, device_sms(), s);
     return r == cudaSuccess ? MOE_OK : cuda_error(r, fn);
-  }
+  };
+  if (streams) return stream_rows(0);
+  const LinearPath path = fp8_path(T, N, K, device_sms());
   CUtensorMap tx, tw;
   if ((st = make_map_u8_2d(&tx, x, K, T, ld_x)) != MOE_OK) return st;
   if ((st = make_map_u8_2d(&tw, w, K, N, ld_w)) != MOE_OK) return st;
@@ -866,8 +874,11 @@ moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int6
   p.group = 0;
   p.parts = reinterpret_cast<float*>(wsb + 1024);
   p.err = static_cast<int*>(ws);
-  const cudaError_t r = launch_fp8_linear(tx, tw, p, fp8_path(T, N, K, device_sms()), s);
-  return r == cudaSuccess ? MOE_OK : cuda_error(r, fn);
+  const int rest = fp8_rest(T, N, path, device_sms());
+  p.epi.M = T - rest;
+  const cudaError_t r = launch_fp8_linear(tx, tw, p, path, s);
+  if (r != cudaSuccess) return cuda_error(r, fn);
+  return rest ? stream_rows(T - rest) : MOE_OK;
 }
 
 moe_status moe_layer_norm(const void* residual, moe_dtype res_dt, int64_t ld_res, const void* y,

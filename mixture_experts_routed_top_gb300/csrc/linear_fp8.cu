@@ -681,11 +681,11 @@ __device__ __forceinline__ void warp_mma_f8(float (&c)[4], uint32_t a0, uint32_t
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-constexpr int kStreamBlocks = 2;  // K blocks that a warp asks for at once
-template <int NT, bool CODES>
+// NT: groups of 8 tokens; G: K blocks that a warp asks for at once.
+template <int NT, bool CODES, int G>
 __global__ void __launch_bounds__(kStreamWarps * 32)
     fp8_stream_kernel(const __grid_constant__ Fp8StreamArgs a) {
-  constexpr int G = kStreamBlocks, TOK = 8 * NT;
+  constexpr int TOK = 8 * NT;
   pdl_launch_dependents();
   __shared__ float s_part[kStreamWarps][TOK][17];
   __shared__ float s_sum[kStreamWarps][TOK][16];  // of a tile, over this block's warps
@@ -856,15 +856,15 @@ cudaError_t launch_tile(const CUtensorMap& tm_a, const CUtensorMap& tm_b, Fp8Lin
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-template <int NT, bool CODES>
+template <int NT, bool CODES, int G>
 cudaError_t launch_stream(Fp8StreamArgs a, int num_sms, cudaStream_t s) {
-  // as the bf16 kernel: warps of a block per tile, then blocks, until every SM has 16
-  // warps, as long as each has a group of the contraction
+  // warps of a block per tile until every SM has 16, then two blocks, as long as each has a
+  // group of the contraction (8 tokens at 7168 x 2112: one block 10.9 us, two 8.4, up to
+  // eight 11.1; at 2048 x 7168 8 warps 6.5 us, 4 warps 8.5)
   const long tiles = ceil_div(a.epi.N, 16);
   a.wpr = a.split = 1;
-  while (a.wpr < kStreamWarps && tiles * a.wpr < 16l * num_sms && a.wpr * kStreamBlocks < a.KB) a.wpr *= 2;
-  while (a.split < 8 && tiles * a.wpr * a.split < 16l * num_sms && a.wpr * a.split * kStreamBlocks < a.KB)
-    a.split *= 2;
+  while (a.wpr < kStreamWarps && tiles * a.wpr < 16l * num_sms && a.wpr * G < a.KB) a.wpr *= 2;
+  if (tiles * a.wpr < 16l * num_sms && a.wpr * G < a.KB) a.split = 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -878,13 +878,16 @@ cudaError_t launch_stream(Fp8StreamArgs a, int num_sms, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = a.split > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fp8_stream_kernel<NT, CODES>, a);
+  return cudaLaunchKernelEx(&cfg, fp8_stream_kernel<NT, CODES, G>, a);
 }
 template <bool CODES>
 cudaError_t launch_stream_tokens(const Fp8StreamArgs& a, int num_sms, cudaStream_t s) {
-  if (a.epi.M <= 8) return launch_stream<1, CODES>(a, num_sms, s);
-  if (a.epi.M <= 16) return launch_stream<2, CODES>(a, num_sms, s);
-  return launch_stream<4, CODES>(a, num_sms, s);
+  // 8 tokens and a long contraction: four K blocks at once, 8.4 us against 9.8 at 7168 x 2112
+  // (at 2048 x 7168, where a warp has two, 7.8 against 6.5; 16 tokens 12.9 against 11.0)
+  if (a.epi.M <= 8)
+    return a.KB >= 32 ? launch_stream<1, CODES, 4>(a, num_sms, s) : launch_stream<1, CODES, 2>(a, num_sms, s);
+  if (a.epi.M <= 16) return launch_stream<2, CODES, 2>(a, num_sms, s);
+  return launch_stream<4, CODES, 2>(a, num_sms, s);
 }
 
 }  // namespace
@@ -902,8 +905,18 @@ LinearPath fp8_path(long M, long N, long K, int num_sms) {
   }
   r.kind = LinearPath::kTile;
   const long tiles = static_cast<long>(ceil_div(M, 128)) * ceil_div(N, 128);
-  while (r.split < 8 && tiles * r.split * 2 <= 2 * pairs && K / (r.split * 2) >= 2 * kB) r.split *= 2;
+  while (r.split < 4 && tiles * r.split * 2 <= 2 * pairs && K / (r.split * 2) >= 2 * kB) r.split *= 2;
   return r;
+}
+
+// How many of the last rows the kernel of few tokens takes: up to 16 beyond whole row tiles,
+// where their tiles would begin another wave of pairs.  4099 x 7168 x 2112: 153 tiles on 76
+// pairs 91 us, 144 and 3 rows 70.
+int fp8_rest(int T, int N, const LinearPath& path, int num_sms) {
+  const int rest = T % 256, pairs = std::max(num_sms / 2, 1);
+  if (path.kind != LinearPath::kPair || rest == 0 || rest > 16 || T < 256) return 0;
+  const long nt = ceil_div(N, 256), tiles = (T / 256 + 1) * nt;
+  return (tiles - nt + pairs - 1) / pairs < (tiles + pairs - 1) / pairs ? rest : 0;
 }
 
 cudaError_t launch_fp8_linear(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const Fp8LinearDev& p,

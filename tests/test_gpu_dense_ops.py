@@ -199,7 +199,8 @@ def test_quantize_fp8_rows(moe, T, K, fmt):
 FP8 = [  # T, K, N: a token, few tokens, tiles and split contractions, ragged, CTA pairs
     (1, 128, 1), (1, 2048, 7168), (2, 256, 33), (8, 7168, 100), (9, 128, 16), (16, 1152, 129), (17, 640, 1025),
     (30, 384, 700), (32, 512, 17), (33, 128, 130), (100, 7168, 576), (129, 1024, 129), (300, 512, 264), (257, 256, 3),
-    (700, 2048, 1000), (2050, 256, 1536), (2049, 384, 1601), (1301, 2048, 2041), (4500, 128, 900)]
+    (700, 2048, 1000), (2050, 256, 1536), (2049, 384, 1601), (1301, 2048, 2041), (4500, 128, 900),
+    (2562, 256, 1700), (1298, 384, 3300)]         # the last two: their last rows apart from whole tiles
 
 
 @pytest.mark.parametrize("T,K,N", FP8)
