@@ -198,11 +198,10 @@ constexpr int kOffScale = kOffTurn + kEpiWarps * kTurn * 4;  // [2][kSlab][2 hal
 constexpr int kSmem = kOffScale + 2 * kSlab * 256 * 4 + 1024;
 static_assert(kOffMisc % 8 == 0 && kSmem <= 227 * 1024, "shared memory");
 
-// 64 columns of 32 rows of bf16 results without a residual, rows of whole aligned vectors:
-// bias and activation where the sums are, 16-byte pieces of the rounded rows through the
-// turn buffer (in the order of their index xor the row's), then 8 lanes along a row, so
+// 64 columns of 32 rows of bf16 results without activation and residual, rows of whole
+// aligned vectors: the bias where the sums are, 16-byte pieces of the rounded rows through
+// the turn buffer (in the order of their index xor the row's), then 8 lanes along a row, so
 // that a store fills lines.
-template <int ACT>
 __device__ __forceinline__ void epilogue64_bf16(const LinearEpi& p, int m0, int n, float* z, float* buf, int lane) {
   uint4* const b4 = reinterpret_cast<uint4*>(buf);
   __syncwarp();  // the previous step's values have been read
@@ -216,8 +215,7 @@ __device__ __forceinline__ void epilogue64_bf16(const LinearEpi& p, int m0, int 
     }
     uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = pack_bf16x2(act_f(z[8 * c + 2 * j], ACT, false), act_f(z[8 * c + 2 * j + 1], ACT, false));
+    for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(z[8 * c + 2 * j], z[8 * c + 2 * j + 1]);
     b4[lane * 8 + (c ^ (lane & 7))] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __syncwarp();
@@ -228,6 +226,34 @@ __device__ __forceinline__ void epilogue64_bf16(const LinearEpi& p, int m0, int 
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 4 * i;
     if (m0 + r < p.M) *reinterpret_cast<uint4*>(to + 4 * i * p.ld_out) = b4[r * 8 + (c ^ (r & 7))];
+  }
+}
+// 32 columns of 32 rows of anything else, rows of whole aligned vectors, in little code: 8
+// activations of a loop.  With all 128 of a thread's columns in line, fetching the code took
+// longer than running it (4099 x 7168 x 2112 with gelu 112 us, so 92).
+template <int ACT, bool F32>
+__device__ __forceinline__ void epilogue32_small(const LinearEpi& p, int m0, int n, const uint32_t (&v)[32],
+                                                 float* buf, int lane) {
+  const int nv = n + 8 * (lane & 3), c = 2 * (lane & 3);
+  float b[8] = {};
+  if (p.bias != nullptr && nv < p.N) ld8(p.bias, nv, p.bias_bf16, b);
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(buf + lane * 32 + 4 * (c ^ (lane & 7))) =
+        make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+  __syncwarp();
+  if (nv >= p.N) return;
+#pragma unroll 1
+  for (int row = lane >> 2; row < 32 && m0 + row < p.M; row += 8) {
+    const float4 x = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * (c ^ (row & 7)));
+    const float4 y = *reinterpret_cast<const float4*>(buf + row * 32 + 4 * ((c + 1) ^ (row & 7)));
+    float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}, r[8] = {};
+    const long m = static_cast<long>(m0) + row;
+    if (p.residual != nullptr) ld8(p.residual, m * p.ld_res + nv, !F32, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __fadd_rn(act_f(f[j] + b[j], ACT, F32), r[j]);
+    st8(p.out, m * p.ld_out + nv, F32, f);
   }
 }
 
@@ -456,17 +482,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ln = lane, n0 = ni * 256 + 128 * half;
       asm volatile("" : "+r"(mi), "+r"(n0), "+r"(ln));
       const int m0 = mi * 256 + 128 * rank + 32 * q;
-      if (!F32 && p.epi.vec && p.epi.residual == nullptr) {
-        epilogue64_bf16<ACT>(p.epi, m0, n0, acc, turn, ln);
-        if (n0 + 64 < p.epi.N) epilogue64_bf16<ACT>(p.epi, m0, n0 + 64, acc + 64, turn, ln);
+      constexpr bool kPlain = ACT == MOE_ACT_NONE && !F32;
+      if (kPlain && p.epi.vec && p.epi.residual == nullptr) {
+        epilogue64_bf16(p.epi, m0, n0, acc, turn, ln);
+        if (n0 + 64 < p.epi.N) epilogue64_bf16(p.epi, m0, n0 + 64, acc + 64, turn, ln);
         continue;
       }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      auto step = [&](const float* z, int n) {
         uint32_t u[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(acc[32 * s + i]);
-        if (n0 + 32 * s < p.epi.N) epilogue32<ACT, F32, false>(p.epi, static_cast<long>(m0) + ln, n0 + 32 * s, u, turn, ln);
+        for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(z[i]);
+        if (n >= p.epi.N) return;
+        if (!kPlain && p.epi.vec) epilogue32_small<ACT, F32>(p.epi, m0, n, u, turn, ln);
+        else epilogue32<ACT, F32, false>(p.epi, static_cast<long>(m0) + ln, n, u, turn, ln);
+      };
+      if (kPlain) {  // in a loop, as the others, it cost the promotion registers (222 us against 205)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) step(acc + 32 * s, n0 + 32 * s);
+      } else {
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+          step(acc, n0 + 32 * s);
+#pragma unroll
+          for (int i = 0; i < 96; ++i) acc[i] = acc[i + 32];
+        }
       }
     }
   }
