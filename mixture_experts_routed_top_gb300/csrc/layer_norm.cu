@@ -42,6 +42,9 @@ __device__ __forceinline__ void bias8(const void* p, bool bf16, int col, int H, 
 
 constexpr int ln_blocks(int nv) { return nv == 1 ? 2 : 1; }  // on an SM
 
+// 8192 x 7168 bf16 with the residual sum 77 us (470 MB, 6.1 TB/s, 91 % of a copy), bound by
+// memory; 8 tokens 3.2, three dependent trips (row, two sums).
+
 template <typename RT, int NV, int STAGES, bool EDGE>
 __global__ void __launch_bounds__(kRingThreads, ln_blocks(NV))
     layer_norm_ring_kernel(const LayerNormArgs a) {
@@ -158,7 +161,13 @@ __global__ void __launch_bounds__(kRingThreads, ln_blocks(NV))
 
 // The sums over tokens of a thread's columns stay in registers; a block leaves them as one
 // partial row, and norm_partials_kernel adds those in block order.
-template <typename RT, int NV, int STAGES, bool EDGE>
+// GR: a gradient of the stream beside the norm's, a constant of the code.
+// 8192 x 7168 bf16 with it 94 us and 6 for the partial rows' sums (470 MB, 4.7 TB/s over
+// both), held back by issue (0.54 instructions a cycle and scheduler, 27 a column and row
+// over all) more than by memory; a row's first sums taken together with the last ones of
+// the row before, a barrier a row less, changed nothing.  EDGE: 4099 x 2050 with an fp32
+// stream 34 us with both results (134 MB, 4.0 TB/s).
+template <typename RT, int NV, int STAGES, bool EDGE, bool GR>
 __global__ void __launch_bounds__(kRingThreads, 1)
     layer_norm_backward_ring_kernel(const LayerNormBwdArgs a) {
   pdl_launch_dependents();
@@ -166,9 +175,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   __shared__ __align__(16) F2 s_red[kRedPairs];
   constexpr bool R32 = sizeof(RT) == 4;
   constexpr int PR = R32 ? 2 : 1;
-  const bool has_gr = a.grad_res != nullptr;
+  constexpr bool has_gr = GR;
   // pieces: residual, grad_normed, grad_residual
-  const int pv = PR + 1 + (has_gr ? PR : 0);
+  constexpr int pv = PR + 1 + (has_gr ? PR : 0);
   const int nthr = blockDim.x * blockDim.y, tid = threadIdx.x + threadIdx.y * blockDim.x;
   for (int i = tid; i < kRedPairs; i += nthr) s_red[i] = f2(0.f);
   __syncthreads();
@@ -319,7 +328,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   }
 }
 
-// Rows above 8192 columns: one per block, held in registers.
+// Rows above 8192 columns: one per block, held in registers.  For them only: the backward
+// pass' sums and values of a column take more registers than its threads have (0.4 KB of
+// spills a thread).
 template <typename RT, bool VEC>
 __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs a) {
   pdl_launch_dependents();
@@ -454,12 +465,12 @@ cudaError_t fwd_ring(const LayerNormArgs& a, dim3 block, size_t smem, int grid, 
   if (e != cudaSuccess) return e;
   return launch_pdl(layer_norm_ring_kernel<RT, NV, STAGES, EDGE>, dim3(grid), block, smem, s, a);
 }
-template <typename RT, int NV, int STAGES, bool EDGE>
+template <typename RT, int NV, int STAGES, bool EDGE, bool GR>
 cudaError_t bwd_ring(const LayerNormBwdArgs& a, dim3 block, size_t smem, int grid, cudaStream_t s) {
   static std::atomic<int> ready[64] = {};
-  const cudaError_t e = ring_ready(layer_norm_backward_ring_kernel<RT, NV, STAGES, EDGE>, ready);
+  const cudaError_t e = ring_ready(layer_norm_backward_ring_kernel<RT, NV, STAGES, EDGE, GR>, ready);
   if (e != cudaSuccess) return e;
-  return launch_pdl(layer_norm_backward_ring_kernel<RT, NV, STAGES, EDGE>, dim3(grid), block, smem, s, a);
+  return launch_pdl(layer_norm_backward_ring_kernel<RT, NV, STAGES, EDGE, GR>, dim3(grid), block, smem, s, a);
 }
 
 template <typename RT, int NV, bool VEC>
@@ -476,18 +487,23 @@ cudaError_t fwd_nv(const LayerNormArgs& a, int num_sms, cudaStream_t s) {
   static_assert(ST * stage_bytes(PR + 1, NV) * PER_SM <= kRingBytes, "a ring");
   return fwd_ring<RT, NV, ST, false>(a, block, ST * stage_bytes(PR + (a.y != nullptr), NV), grid, s);
 }
-template <typename RT, int NV, bool VEC>
+template <typename RT, int NV, bool VEC, bool GR>
 cudaError_t bwd_nv(const LayerNormBwdArgs& a, int num_sms, int* blocks, cudaStream_t s) {
-  constexpr int PR = static_cast<int>(sizeof(RT) / 2);
+  constexpr int PR = static_cast<int>(sizeof(RT) / 2), ROWS = 1 + GR;
   const dim3 block = ring_block(a.T, a.H, NV, num_sms);
-  const int rows = 1 + (a.grad_res != nullptr);
-  const size_t stage = VEC ? stage_bytes(PR * rows + 1, NV)
-                           : edge_stage_bytes(PR == 2 ? rows : 0, (PR == 1 ? rows : 0) + 1, NV, block);
+  const size_t stage = VEC ? stage_bytes(PR * ROWS + 1, NV)
+                           : edge_stage_bytes(PR == 2 ? ROWS : 0, (PR == 1 ? ROWS : 0) + 1, NV, block);
   const size_t sums = static_cast<size_t>(block.y) * a.n_part * a.H * 4;  // <= 64 KB
   const int grid = *blocks = std::min(std::min(num_sms, kNormBwdBlocks), ceil_div(a.T, block.y));
+  if (VEC) {  // whole stages of 512 threads, as many as fit: four 99 us at 8192 x 7168, three 102
+    constexpr size_t kStage = stage_bytes(PR * ROWS + 1, NV);
+    constexpr int ST = 4 * kStage <= kRingBytes ? 4 : 3 * kStage <= kRingBytes ? 3 : 2;
+    static_assert(2 * kStage <= kRingBytes, "a ring");
+    return bwd_ring<RT, NV, ST, false, GR>(a, block, std::max(ST * kStage, sums), grid, s);
+  }
   return 3 * stage <= kRingBytes
-             ? bwd_ring<RT, NV, 3, !VEC>(a, block, std::max(3 * stage, sums), grid, s)
-             : bwd_ring<RT, NV, 2, !VEC>(a, block, std::max(2 * stage, sums), grid, s);
+             ? bwd_ring<RT, NV, 3, true, GR>(a, block, std::max(3 * stage, sums), grid, s)
+             : bwd_ring<RT, NV, 2, true, GR>(a, block, std::max(2 * stage, sums), grid, s);
 }
 
 template <typename RT, bool VEC>
@@ -500,7 +516,11 @@ cudaError_t fwd(const LayerNormArgs& a, int num_sms, cudaStream_t s) {
 template <typename RT, bool VEC>
 cudaError_t bwd(const LayerNormBwdArgs& a, int num_sms, int* blocks, cudaStream_t s) {
   if (a.H <= 8192)
-    return a.H <= 2048 ? bwd_nv<RT, 1, VEC>(a, num_sms, blocks, s) : bwd_nv<RT, 2, VEC>(a, num_sms, blocks, s);
+    return a.grad_res != nullptr
+               ? (a.H <= 2048 ? bwd_nv<RT, 1, VEC, true>(a, num_sms, blocks, s)
+                              : bwd_nv<RT, 2, VEC, true>(a, num_sms, blocks, s))
+               : (a.H <= 2048 ? bwd_nv<RT, 1, VEC, false>(a, num_sms, blocks, s)
+                              : bwd_nv<RT, 2, VEC, false>(a, num_sms, blocks, s));
   *blocks = static_cast<int>(std::min<long>(std::min(num_sms, kNormBwdBlocks), a.T));
   const dim3 block(ceil_div(ceil_div(ceil_div(a.H, 8), 4), 32) * 32);
   return launch_pdl(layer_norm_backward_kernel<RT, VEC>, dim3(*blocks), block, 0, s, a);
