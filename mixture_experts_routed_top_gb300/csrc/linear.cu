@@ -885,7 +885,46 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s_part[warp][8 * q + 2 * t + (i & 1)][g + 8 * (i >> 1)] = sum[q][i];
   __syncthreads();
-  stream_results<TOK, GATED>(a.epi, s_part, s_sum, wpr, S, rank, tiles, tile0);
+  if (GATED) {
+    stream_results<TOK, GATED>(a.epi, s_part, s_sum, wpr, S, rank, tiles, tile0, N, T);
+    return;
+  }
+  // the same for plain products, in a copy of its own: with the shared one 16 tokens spilled 44
+  // bytes more a thread and took 11.2 us at 7168 x 2048 instead of 10.5
+  const LinearEpi& p = a.epi;
+  const int count = tiles * TOK * 16;  // (tile, token, row), the row fastest
+  if (S > 1) {
+    for (int i = threadIdx.x; i < count; i += kStreamWarps * 32) {
+      const int tl = i / (TOK * 16), tok = i / 16 % TOK, r = i % 16;
+      float z = 0.f;
+      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
+      (&s_sum[0][0][0])[i] = z;
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
+  // the blocks of a cluster share the results out among them
+  for (int i = threadIdx.x + rank * (kStreamWarps * 32); i < count; i += S * (kStreamWarps * 32)) {
+    const int tl = i / (TOK * 16), tok = i / 16 % TOK, r = i % 16, n = (tile0 + tl) * 16 + r;
+    if (n >= N || tok >= T) continue;
+    float z = 0.f;
+    if (S > 1) {
+      const uint32_t at = smem_u32(&s_sum[0][0][0] + i);
+#pragma unroll 8
+      for (int q = 0; q < S; ++q) z += ld_cluster_f32(mapa_shared(at, q));
+    } else {
+      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
+    }
+    if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
+    if (p.preact != nullptr) stf(p.preact, tok * p.ld_out + n, p.out_f32, z);
+    z = act_f(z, p.act, p.out_f32);
+    if (p.residual != nullptr) z += ldf(p.residual, tok * p.ld_res + n, !p.out_f32);
+    stf(p.out, tok * p.ld_out + n, p.out_f32, z);
+  }
+  if (S > 1) {
+    __syncwarp();
+    cluster_sync_all();  // the others have read this block's sums
+  }
 }
 
 // ====================================================== dz and dbias

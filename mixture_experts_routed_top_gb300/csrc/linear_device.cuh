@@ -608,12 +608,12 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 // cluster's shared memory (half a kilobyte each), and the results shared out.
 constexpr int kStreamWarps = 8;
 template <int TOK, bool GATED>
-__device__ __forceinline__ void stream_results(const LinearEpi& p, const float (*s_part)[TOK][17],
-                                               float (*s_sum)[TOK][16], int wpr, int S, int rank,
-                                               int tiles, int tile0) {
+__device__ __forceinline__ void stream_results(const LinearEpi& p, float (&s_part)[kStreamWarps][TOK][17],
+                                               float (&s_sum)[kStreamWarps][TOK][16], const int wpr,
+                                               const int S, const int rank, const int tiles,
+                                               const int tile0, const int N, const int T) {
   constexpr int OUT = GATED ? 8 : 16;  // outputs of a tile
   const int count = tiles * TOK * 16;  // (tile, token, row), the row fastest
-  const int N = p.N, T = p.M;
   if (S > 1) {
     for (int i = threadIdx.x; i < count; i += kStreamWarps * 32) {
       const int tl = i / (TOK * 16), tok = i / 16 % TOK, r = i % 16;
@@ -624,27 +624,27 @@ __device__ __forceinline__ void stream_results(const LinearEpi& p, const float (
     __syncwarp();
     cluster_sync_all();
   }
-  // the sum of one (tile, token, row) over the blocks or the warps
-  auto total = [&](int tl, int tok, int r) {
-    float z = 0.f;
-    if (S > 1) {
-      const uint32_t at = smem_u32(&s_sum[0][0][0] + (tl * TOK + tok) * 16 + r);
-#pragma unroll 8
-      for (int q = 0; q < S; ++q) z += ld_cluster_f32(mapa_shared(at, q));
-    } else {
-      for (int q = 0; q < wpr; ++q) z += s_part[tl * wpr + q][tok][r];
-    }
-    return z;
-  };
   // the blocks of a cluster share the results out among them
-  const int results = tiles * TOK * OUT;
-  for (int i = threadIdx.x + rank * (kStreamWarps * 32); i < results; i += S * (kStreamWarps * 32)) {
+  for (int i = threadIdx.x + rank * (kStreamWarps * 32); i < (GATED ? count / 2 : count);
+       i += S * (kStreamWarps * 32)) {
     const int tl = i / (TOK * OUT), tok = i / OUT % TOK, r = i % OUT, n = (tile0 + tl) * OUT + r;
     if (n >= N || tok >= T) continue;
-    float z = total(tl, tok, r);
+    float z = 0.f, zu = 0.f;  // GATED: rows r and 8 + r
+    if (S > 1) {
+      const uint32_t at = smem_u32(&s_sum[0][0][0] + (GATED ? (tl * TOK + tok) * 16 + r : i));
+#pragma unroll 8
+      for (int q = 0; q < S; ++q) {
+        z += ld_cluster_f32(mapa_shared(at, q));
+        if (GATED) zu += ld_cluster_f32(mapa_shared(at + 32u, q));
+      }
+    } else {
+      for (int q = 0; q < wpr; ++q) {
+        z += s_part[tl * wpr + q][tok][r];
+        if (GATED) zu += s_part[tl * wpr + q][tok][8 + r];
+      }
+    }
     if (p.bias != nullptr) z += ldf(p.bias, n, p.bias_bf16);
     if (GATED) {
-      float zu = total(tl, tok, 8 + r);
       if (p.bias != nullptr) zu += ldf(p.bias, N + n, p.bias_bf16);
       gated1<MOE_ACT_NONE>(p, tok, n, z, zu);
       continue;

@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s_part[warp][8 * q + 2 * t + (i & 1)][g + 8 * (i >> 1)] = sum[q][i];
   __syncthreads();
-  stream_results<TOK, false>(a.epi, s_part, s_sum, wpr, S, rank, tiles, tile0);
+  stream_results<TOK, false>(a.epi, s_part, s_sum, wpr, S, rank, tiles, tile0, N, T);
 }
 
 template <int ACT, bool F32>
