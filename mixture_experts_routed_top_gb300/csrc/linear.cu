@@ -22,6 +22,8 @@
 //                        of a cluster: few tiles
 //   linear_stream_kernel a few tokens: the weights streamed into registers, and
 //   linear_vector_kernel for one token
+// All but linear_sums_kernel have a GATED form, for the two projections of a gated
+// feed-forward with the activation and product in the epilogue (gated_path()).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -62,7 +64,9 @@ constexpr int kPSmem = kPOffTurn + 8 * kTurn * 4 + 1024;
 static_assert(kPSmem <= 227 * 1024, "shared memory budget");
 
 // GATED: the pair's B is 128 gate rows (rank 0's half) and their 128 up rows (rank 1's),
-// the tile's outputs their 128 columns.
+// the tile's outputs their 128 columns.  8192 x 7168 x 2 x 2048 with silu 254 us from a cool
+// start (1.89 PFLOP/s, tensor cores busy 93 %), 293 in an endless loop; 4099 x 2048 x 2 x 1408
+// with gelu and kept pre-activations 41, where a tile has 16 stages and 187 tiles 3 waves.
 template <bool A_MN, bool B_MN, int ACT, bool GATED>
 __global__ void __launch_bounds__(kPThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -553,7 +557,8 @@ constexpr int kTSmem = kTOffMisc + 16 + 1024;
 constexpr int kTStride = 132;                    // floats per staged row: 128 + 4 (no bank conflicts)
 static_assert(128 * kTStride * 4 <= kTOffBar, "staged tile fits the ring");
 
-// GATED: 64 gate rows of w and their 64 up rows, for 64 outputs.
+// GATED: 64 gate rows of w and their 64 up rows, for 64 outputs: 128 tokens at 7168 x 2 x 2048
+// 18.4 us.
 template <bool A_MN, bool B_MN, bool GATED>
 __global__ void __launch_bounds__(kTThreads)
     linear_tile_kernel(const __grid_constant__ CUtensorMap tm_a,
@@ -722,7 +727,8 @@ __global__ void __launch_bounds__(kTThreads)
 // block share two rows of w, each lane multiplying 16-byte pieces of them with
 // the token's, and add their sums in order.  2048 x 7168 6.3 us from memory
 // (4.7 TB/s, 2 us more than the bytes need), 3.7 from L2.
-// GATED: the two rows are a gate row and its up row, and give one output.
+// GATED: the two rows are a gate row and its up row, and give one output: 7168 x 2 x 2048 13.0
+// us (58.7 MB, 4.5 TB/s).
 template <int WPR, bool GATED>
 __global__ void __launch_bounds__(256)
     linear_vector_kernel(const __grid_constant__ LinearStreamArgs a) {
@@ -824,7 +830,8 @@ template <int NT>
 struct StreamLay {
   static constexpr int G = NT == 1 ? 8 : 4, TOK = 8 * NT;
 };
-// GATED: the 16 rows are 8 gate rows and their 8 up rows, for 8 outputs.
+// GATED: the 16 rows are 8 gate rows and their 8 up rows, for 8 outputs: 8 tokens at 7168 x
+// 2 x 2048 13.9 us, 16 17.6.
 template <int NT, bool GATED>
 __global__ void __launch_bounds__(kStreamWarps * 32)
     linear_stream_kernel(const __grid_constant__ LinearStreamArgs a) {
@@ -1013,7 +1020,8 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const LinearDzArgs a) {
 
 // The gated product's: from dh and z = (zg, zu), dzg = dh zu act'(zg) and dzu = dh
 // act(zg), side by side in rows of 2 N (`ld_dz` apart), with the same column sums.
-// A block covers 256 outputs.
+// A block covers 256 outputs.  257 x 1024 with relu 7 us, most of it launch and two dependent
+// trips; large ones are bound by memory (10 bytes an output).
 template <int ACT, bool SPLIT>
 __global__ void __launch_bounds__(256) gated_dz_kernel(const LinearDzArgs a) {
   pdl_launch_dependents();
