@@ -9,6 +9,7 @@ CUDA device is present the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from typing import Optional, Tuple
@@ -968,6 +969,13 @@ def gated_linear_backward(grad_h: torch.Tensor, x: torch.Tensor, w: torch.Tensor
 
 
 _E4M3 = (torch.uint8, torch.float8_e4m3fn)
+
+
+@functools.lru_cache(maxsize=256)
+def _fp8_workspace(T: int, K: int) -> int:
+    return lib().moe_linear_fp8_workspace_size(T, K)
+
+
 _SCALE_DT = {_F32: SCALE_F32, torch.uint8: SCALE_UE8M0}
 
 
@@ -1049,7 +1057,7 @@ def linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
     if residual is not None:
         pr, ld_r = residual.data_ptr(), _mat("residual", residual, (out_dtype,), shape, dev)
     if x_scale is None:
-        need = (_LIB or lib()).moe_linear_fp8_workspace_size(T, K)
+        need = _fp8_workspace(T, K)
     else:
         need = _LINEAR_WS = _LINEAR_WS or lib().moe_linear_workspace_size()
     ws = _workspace(workspace, dev, need)

@@ -673,8 +673,8 @@ moe_status moe_gated_linear(const void* x, int64_t ld_x, const void* w, int64_t 
   if (ld_out < I) return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride below I", fn);
   if (T == 0 || I == 0) return MOE_OK;
   if (!x || !w || !out) return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (preact && preact == out)
-    return set_last_error(MOE_ERR_INVALID_ARG, "%s: preact needs a buffer of its own", fn);
+  if (out == x || out == w || (preact && (preact == out || preact == x || preact == w)))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
   if (!all16(x, w, bias, out, preact))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
   if ((st = check_ws(fn, ws, ws_bytes, kLinearWsBytes)) != MOE_OK) return st;
@@ -734,6 +734,9 @@ moe_status moe_gated_linear_backward(const void* grad_h, int64_t ld_gh, const vo
   }
   if (!grad_h || !preact || (dx && !w) || (dw && !x))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if ((dx && (dx == grad_h || dx == x || dx == w || dx == preact || dx == dw)) ||
+      (dw && (dw == grad_h || dw == x || dw == w || dw == preact)))
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
   if (!all16(grad_h, x, w, preact, dx, dw, dbias))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
   const LinearWs L = linear_ws(T, N);
@@ -806,6 +809,8 @@ moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int6
   if (!x || !w || !w_scale || !out) return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (residual == out && ld_res != ld_out)
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: in place only with the same row stride", fn);
+  if (out == x || out == w)
+    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
   if (!all16(x, w, bias, residual, out) || !scale_aligned(x_scale, scale_fmt) ||
       !scale_aligned(w_scale, scale_fmt))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned, scales as their type", fn);

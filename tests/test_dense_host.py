@@ -47,7 +47,10 @@ def test_gated_closed_forms():
     assert B.gated_linear_backward([[1, 1]], x, w, z, "relu")[3].tolist() == [[-3.0, 0.0, 2.0, 0.0]]
 
 
-def gated(L, x=P, ld_x=64, w=P, ld_w=64, bias=NUL, bdt=0, act=0, T=4, K=64, I=32, out=P, ld_out=32, z=NUL, ws=P,
+X, W, Z = (ctypes.c_void_p(i << 24) for i in (1, 2, 3))
+
+
+def gated(L, x=X, ld_x=64, w=W, ld_w=64, bias=NUL, bdt=0, act=0, T=4, K=64, I=32, out=P, ld_out=32, z=NUL, ws=P,
           wsb=1 << 30):
     return L.moe_gated_linear(x, ld_x, w, ld_w, bias, bdt, act, T, K, I, out, ld_out, z, ws, wsb, NUL)
 
@@ -57,6 +60,7 @@ def gated(L, x=P, ld_x=64, w=P, ld_w=64, bias=NUL, bdt=0, act=0, T=4, K=64, I=32
     (dict(ld_x=68), UNSUPPORTED), (dict(ld_w=56), INVALID), (dict(act=3), INVALID), (dict(act=-1), INVALID),
     (dict(bias=P, bdt=2), INVALID), (dict(ld_out=31), INVALID), (dict(x=NUL), INVALID), (dict(w=NUL), INVALID),
     (dict(out=NUL), INVALID), (dict(x=ODD), INVALID), (dict(bias=ODD), INVALID), (dict(z=P), INVALID),
+    (dict(out=X), INVALID), (dict(out=W), INVALID), (dict(z=X), INVALID),
     (dict(ws=NUL), INVALID), (dict(wsb=128), WORKSPACE), (dict(I=1 << 30, ld_out=1 << 30), UNSUPPORTED),
     (dict(T=0, x=NUL), OK), (dict(I=0, x=NUL), OK)])
 def test_gated_linear_refusals(L, kw, status):
@@ -65,14 +69,15 @@ def test_gated_linear_refusals(L, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(act=-1), INVALID), (dict(z=NUL), INVALID), (dict(K=60), UNSUPPORTED), (dict(ld_gh=31), INVALID),
-    (dict(ld_z=63), INVALID), (dict(gh=NUL), INVALID), (dict(wsb=64), WORKSPACE), (dict(x=ODD), INVALID)])
+    (dict(ld_z=63), INVALID), (dict(gh=NUL), INVALID), (dict(wsb=64), WORKSPACE), (dict(x=ODD), INVALID),
+    (dict(dx=X), INVALID), (dict(dw=W), INVALID), (dict(dw=P, dx=P), INVALID)])
 def test_gated_linear_backward_refusals(L, kw, status):
     need = L.moe_gated_linear_backward_workspace_size(4, 32)
     assert need >= 4 * 64 * 2 and L.moe_gated_linear_backward_workspace_size(4, 1 << 30) == 0
-    a = dict(gh=P, ld_gh=32, x=P, act=0, z=P, ld_z=64, K=64, wsb=need)
+    a = dict(gh=Z, ld_gh=32, x=X, act=0, z=Z, ld_z=64, K=64, wsb=need, dx=P, dw=ctypes.c_void_p(1 << 21))
     a.update(kw)
-    assert L.moe_gated_linear_backward(a["gh"], a["ld_gh"], a["x"], 64, P, 64, a["act"], a["z"], a["ld_z"], 4, a["K"],
-                                       32, P, P, NUL, P, a["wsb"], NUL) == status
+    assert L.moe_gated_linear_backward(a["gh"], a["ld_gh"], a["x"], 64, W, 64, a["act"], a["z"], a["ld_z"], 4, a["K"],
+                                       32, a["dx"], a["dw"], NUL, P, a["wsb"], NUL) == status
 
 
 # ------------------------------------------------------------------ 8-bit products
@@ -97,7 +102,7 @@ def test_quantize_fp8_rows_refusals(L, kw, status):
     assert rows8(L, **kw) == status
 
 
-def lin8(L, x=P, ld_x=256, xs=NUL, s_row=0, s_kb=0, w=P, ld_w=256, ws8=P, fmt=1, bias=NUL, bdt=0, act=-1, res=NUL,
+def lin8(L, x=X, ld_x=256, xs=NUL, s_row=0, s_kb=0, w=W, ld_w=256, ws8=P, fmt=1, bias=NUL, bdt=0, act=-1, res=NUL,
          ld_res=0, T=4, K=256, N=32, out=P, odt=0, ld_out=32, ws=P, wsb=1 << 30):
     return L.moe_linear_fp8(x, ld_x, xs, s_row, s_kb, w, ld_w, ws8, fmt, bias, bdt, act, res, ld_res, T, K, N, out, odt,
                             ld_out, ws, wsb, NUL)
@@ -109,7 +114,7 @@ def lin8(L, x=P, ld_x=256, xs=NUL, s_row=0, s_kb=0, w=P, ld_w=256, ws8=P, fmt=1,
     (dict(ld_w=264), UNSUPPORTED), (dict(fmt=0), INVALID), (dict(fmt=3), INVALID), (dict(xs=P, s_row=0, s_kb=1), INVALID),
     (dict(act=3), INVALID), (dict(odt=2), INVALID), (dict(bias=P, bdt=2), INVALID), (dict(ld_out=31), INVALID),
     (dict(res=P, ld_res=31), INVALID), (dict(res=P, ld_res=40), INVALID), (dict(x=NUL), INVALID), (dict(w=NUL), INVALID),
-    (dict(ws8=NUL), INVALID), (dict(out=NUL), INVALID), (dict(x=ODD), INVALID), (dict(w=ODD), INVALID),
+    (dict(ws8=NUL), INVALID), (dict(out=NUL), INVALID), (dict(out=X), INVALID), (dict(out=W), INVALID), (dict(x=ODD), INVALID), (dict(w=ODD), INVALID),
     (dict(ws=NUL), INVALID), (dict(wsb=128), WORKSPACE), (dict(T=0, x=NUL), OK), (dict(N=0, x=NUL), OK)])
 def test_linear_fp8_refusals(L, kw, status):
     assert lin8(L, **kw) == status

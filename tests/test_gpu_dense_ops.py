@@ -160,6 +160,24 @@ def test_gated_linear_not_finite(moe, T, K, I):
     assert np.array_equal(np.isnan(_np(h)), want[:, :I] | want[:, I:])
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("T", [1, 40])
+def test_gated_gradient_far_from_zero(moe, act, T):
+    """The gate's activation and slope go to 0 on the left and to z and 1 on the right, as far as bf16 goes."""
+    far = [-3e38, -1e33, -1e20, -1000.0, -88.5, -80.5, -79.0, -20.0, 0.0, 20.0, 90.0, 1000.0, 1e33]
+    I, K = len(far), 64
+    z = torch.cat([torch.tensor(far), torch.ones(I)]).bfloat16().cuda().repeat(T, 1).contiguous()
+    x, w = _dev(np.ones((T, K)), torch.bfloat16), _dev(np.ones((2 * I, K)), torch.bfloat16)
+    gh = torch.ones(T, I, dtype=torch.bfloat16, device="cuda")
+    dx, dw, db = moe.gated_linear_backward(gh, x, w, z, bias=torch.zeros(2 * I, device="cuda"), activation=act)
+    with np.errstate(over="ignore", invalid="ignore"):
+        zg = _np(z)[0, :I]
+        ref = np.concatenate([np.nan_to_num(B._slope(zg, act)), B._act(zg, act)])
+    # fp32 arithmetic, and where e^-z leaves fp32 less than 81 e^-80
+    assert (np.abs(_np(db) - T * ref) <= T * (2.0 ** -18 * np.abs(ref) + 81 * np.exp(-80.0))).all()
+    assert (np.abs(_np(dw)[:, 0] - T * ref) <= T * (2.0 ** -7 * np.abs(ref) + 81 * np.exp(-80.0))).all()
+
+
 # ------------------------------------------------------------------ 8-bit products
 def _acc8(K):
     """Sums of 128 on the tensor core (at most 128 / 16 + 16 additions, 2^-23 each of the sum of
