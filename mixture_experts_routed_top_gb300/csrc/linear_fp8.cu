@@ -190,7 +190,8 @@ struct ScaleRow {
 // block with two warps a scheduler, the reads of TMEM and the tensor core overlap only in
 // part.  Plain multiply-adds: packed ones issue at half the rate and were 5 % slower here.
 // Narrower tiles, which would leave four buffers in TMEM, are bound by shared memory (281 us),
-// 16 promoting warps by their registers (248 and more).
+// 16 promoting warps by their registers (248 and more).  The arrivals that hand a buffer back
+// to rank 0, 8 a K block, are relaxed: released at cluster scope they doubled the time (406).
 constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpiWarps;

@@ -348,8 +348,9 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-// The same where no memory has to be visible to who waits for it (a TMEM buffer that has been
-// read): a release at cluster scope waits for all of the warp's memory operations.
+// The same where no memory has to be visible to who waits for it: the warp's reads of a TMEM
+// buffer have completed (tcgen05.wait::ld, then the fence before this) and others may write
+// it.  A release at cluster scope waits for all of the warp's memory operations.
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
