@@ -37,12 +37,19 @@ __host__ __device__ constexpr uint32_t idesc_bf16_order(int M, int N, bool a_mn,
 // global timer takes longer than most of these waits.  2e9 cycles are a second
 // at the card's 2 GHz; each try itself blocks for a while.
 constexpr long long kWaitCycles = 2000000000ll, kDrainCycles = 40000000ll;
-template <bool kCluster>
+enum class WaitScope { kCta, kPair, kPairTmem };
+template <WaitScope S>
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  return S == WaitScope::kCta    ? mbar_try_wait(bar, parity)
+         : S == WaitScope::kPair ? mbar_try_wait_cluster(bar, parity)
+                                 : mbar_try_wait_cluster_relaxed(bar, parity);
+}
+template <WaitScope S>
 __device__ __forceinline__ bool wait_cycles(uint32_t bar, uint32_t parity, volatile int* abort,
                                             int* err, int code, long long limit) {
   long long t0 = 0;
   for (int i = 0;; ++i) {
-    if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (try_wait<S>(bar, parity)) return true;
     if ((i & 15) == 15) {
       if (*abort) return false;
       const long long now = clock64();
@@ -57,11 +64,16 @@ __device__ __forceinline__ bool wait_cycles(uint32_t bar, uint32_t parity, volat
 }
 __device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort,
                                           int* err, int code, long long limit = kWaitCycles) {
-  return wait_cycles<true>(bar, parity, abort, err, code, limit);
+  return wait_cycles<WaitScope::kPair>(bar, parity, abort, err, code, limit);
+}
+// Where nothing but reads and writes of TMEM is ordered.
+__device__ __forceinline__ bool wait_pair_tmem(uint32_t bar, uint32_t parity, volatile int* abort,
+                                               int* err, int code, long long limit = kWaitCycles) {
+  return wait_cycles<WaitScope::kPairTmem>(bar, parity, abort, err, code, limit);
 }
 __device__ __forceinline__ bool wait_cta(uint32_t bar, uint32_t parity, volatile int* abort,
                                          int* err, int code, long long limit = kWaitCycles) {
-  return wait_cycles<false>(bar, parity, abort, err, code, limit);
+  return wait_cycles<WaitScope::kCta>(bar, parity, abort, err, code, limit);
 }
 
 // 2-D load counted on an mbarrier of either CTA of the pair.

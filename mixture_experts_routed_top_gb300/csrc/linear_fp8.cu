@@ -183,7 +183,10 @@ struct ScaleRow {
 //              also from one K block to the next.  128 sums and 64 loaded values take the
 //              registers that the first four warps give up (4 x 56 + 8 x 224 a lane of the
 //              12 x 168 that the block is launched with).
-// Barriers as in the bf16 pair kernel; every wait is bounded.
+// Barriers as in the bf16 pair kernel.  Those that the other CTA signals are waited for at
+// cluster scope, with an acquire where the loads' data follow and without one where only TMEM
+// changes hands (with one there too 8192 x 16384 x 7168 752 us, so 746); the slabs', of one CTA,
+// at its own.  Every wait is bounded.
 //
 // 8192 x 7168 x 4096 with fp32 scales 207 us (2.33 PFLOP/s).  Bound by the promotion beside
 // the products: without it the same loop takes 138 (3.5 PFLOP/s).  128 multiply-adds a thread and
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int mi, ni;
         pair_tile(tile, mt, nt, p.group, &mi, &ni);
         for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_cta(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err, ERR_TIMEOUT_PRODUCER)) {
+          if (!wait_pair(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err, ERR_TIMEOUT_PRODUCER)) {
             ok = false;
             break;
           }
@@ -350,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < kStages; ++s) {
         if ((issued >> s) & 1u) {
           volatile int no_abort = 0;
-          wait_cta(smem_u32(rank == 0 ? &full[s] : &empty[s]), (last_par >> s) & 1u, &no_abort,
+          wait_pair(smem_u32(rank == 0 ? &full[s] : &empty[s]), (last_par >> s) & 1u, &no_abort,
                     p.err, ERR_TIMEOUT_PRODUCER, kDrainCycles);
         }
       }
@@ -364,9 +367,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t g = 0; g < count; ++g) {
         const uint32_t b = g & 1, eph = ((g >> 1) & 1) ^ 1u;
         const uint32_t fbar = smem_u32(&full[stage]), ebar = smem_u32(&pempty[b]);
-        const bool f = mbar_try_wait(fbar, ph), e = mbar_try_wait(ebar, eph);  // both on their way
-        const bool ok = (f || wait_cta(fbar, ph, s_abort, p.err, ERR_TIMEOUT_MMA)) &&
-                        (e || wait_cta(ebar, eph, s_abort, p.err, ERR_TIMEOUT_MMA));
+        const bool f = mbar_try_wait_cluster(fbar, ph), e = mbar_try_wait_cluster_relaxed(ebar, eph);  // both on their way
+        const bool ok = (f || wait_pair(fbar, ph, s_abort, p.err, ERR_TIMEOUT_MMA)) &&
+                        (e || wait_pair_tmem(ebar, eph, s_abort, p.err, ERR_TIMEOUT_MMA));
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const uint64_t ad = d0 + static_cast<uint32_t>(stage * (2 * kOper >> 4)), bd = ad + (kOper >> 4);
@@ -386,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (count > 0) {
         if (elect_one()) umma_commit_pair_local(smem_u32(fin));
         volatile int no_abort = 0;
-        wait_cta(smem_u32(fin), 0, &no_abort, p.err, ERR_TIMEOUT_MMA);
+        wait_pair(smem_u32(fin), 0, &no_abort, p.err, ERR_TIMEOUT_MMA);
       }
     } else if (warp >= 2) {
       const int r = threadIdx.x - 64;  // rows r and r + 64
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t v[2][32];
     // waits for block g's sums and asks for the first 32 of them
     auto begin = [&] {
-      const bool ready = wait_cta(smem_u32(&pfull[g & 1]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
+      const bool ready = wait_pair_tmem(smem_u32(&pfull[g & 1]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
       if (!__all_sync(0xffffffffu, ready)) return false;
       tc_fence_after();
       tmem_ld_32x32b_x32(tl + (g & 1) * 256, v[0]);
