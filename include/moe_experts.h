@@ -604,6 +604,8 @@ moe_status moe_linear_backward(const void* grad_y, moe_dtype y_dt, int64_t ld_gy
  *             moe_linear_workspace_size() bytes; head as in moe_linear
  * K % 8 == 0 and strides of x and w multiples of 8, else MOE_ERR_UNSUPPORTED; any
  * T, any I < 2^30.  T = 0 or I = 0 is a no-op.
+ * Here and in the calls below results share no memory with operands or with each other, but
+ * where one is named in place (MOE_ERR_INVALID_ARG); columns of one matrix side by side do not.
  */
 moe_status moe_gated_linear(const void* x, int64_t ld_x, const void* w, int64_t ld_w,
                             const void* bias, moe_dtype bias_dt, int act, int T, int K, int I,
@@ -653,7 +655,7 @@ moe_status moe_quantize_fp8_rows(const void* x, int64_t ld_x, int T, int K, moe_
  *             moe_quantize_fp8_rows does
  *   w         device e4m3 bytes [N, K], rows ld_w apart
  *   w_scale   device [ceil(N / 128), K / 128] of scale_fmt
- *   bias, act, residual, out   as in moe_linear
+ *   bias, act, residual, out   as in moe_linear (out may be residual)
  *   ws        device scratch, 256-byte aligned, at least moe_linear_fp8_workspace_size()
  *             bytes (where x_scale is given moe_linear_workspace_size() do); head as in
  *             moe_linear

@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <type_traits>
 #include <utility>
@@ -120,6 +121,60 @@ moe_status check_ws(const char* fn, const void* ws, size_t have, size_t need) {
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: ws must be 256-byte aligned", fn);
   if (have < need)
     return set_last_error(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, have, need);
+  return MOE_OK;
+}
+
+// A matrix in memory: rows of `width` bytes, `pitch` bytes apart.
+struct Region {
+  const void* p;
+  int64_t rows, width, pitch;
+};
+Region matrix_at(const void* p, int64_t rows, int64_t cols, int64_t ld, int size) {
+  return {p, rows, cols * size, rows > 1 ? ld * size : cols * size};
+}
+Region vector_at(const void* p, int64_t n, int size) { return {p, 1, n * size, n * size}; }
+// Scales of any two positive strides: rows or columns where these lie apart from each other,
+// else everything between the first scale and the last.
+Region scales_at(const void* p, int64_t rows, int64_t cols, int64_t s_row, int64_t s_col, int size) {
+  const int64_t row = (cols - 1) * s_col + 1, col = (rows - 1) * s_row + 1;
+  if (rows == 1 || s_row >= row) return matrix_at(p, rows, row, s_row, size);
+  if (cols == 1 || s_col >= col) return matrix_at(p, cols, col, s_col, size);
+  return vector_at(p, (rows - 1) * s_row + row, size);
+}
+int64_t floor_div(int64_t a, int64_t b) { return a / b - (a % b != 0 && (a < 0) != (b < 0)); }
+
+// Whether two of them have a byte in common; one may lie between the columns of another.
+bool overlap(const Region& a, const Region& b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1) return false;
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p)) -
+                    static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p));
+  const int64_t a_end = (a.rows - 1) * a.pitch + a.width, b_end = (b.rows - 1) * b.pitch + b.width;
+  if (d >= a_end || d + b_end <= 0) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  // row j of b meets row i of a where -b.width < d + j b.pitch - i a.pitch < a.width
+  if (a.rows == 1 || b.rows == 1 || a.pitch == b.pitch) {  // by k = j - i
+    const int64_t pitch = a.rows == 1 ? b.pitch : a.pitch;
+    const int64_t first = std::max(floor_div(-b.width - d, pitch) + 1, 1 - a.rows);
+    const int64_t last = std::min(floor_div(a.width - d - 1, pitch), b.rows - 1);
+    return first <= last;
+  }
+  if (a.rows > b.rows) return overlap(b, a);
+  for (int64_t i = 0; i < a.rows; ++i) {
+    const int64_t at = d - i * a.pitch;
+    const int64_t first = std::max<int64_t>(floor_div(-b.width - at, b.pitch) + 1, 0);
+    if (first < b.rows && at + first * b.pitch < a.width) return true;
+  }
+  return false;
+}
+// Results share no memory with operands nor with each other.
+moe_status check_apart(const char* fn, std::initializer_list<Region> results,
+                       std::initializer_list<Region> operands) {
+  for (const Region& r : results) {
+    bool shared = false;
+    for (const Region& o : operands) shared = shared || overlap(r, o);
+    for (const Region& o : results) shared = shared || (&o != &r && overlap(r, o));
+    if (shared) return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
+  }
   return MOE_OK;
 }
 
@@ -673,11 +728,13 @@ moe_status moe_gated_linear(const void* x, int64_t ld_x, const void* w, int64_t 
   if (ld_out < I) return set_last_error(MOE_ERR_INVALID_ARG, "%s: row stride below I", fn);
   if (T == 0 || I == 0) return MOE_OK;
   if (!x || !w || !out) return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (out == x || out == w || (preact && (preact == out || preact == x || preact == w)))
-    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
   if (!all16(x, w, bias, out, preact))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
   if ((st = check_ws(fn, ws, ws_bytes, kLinearWsBytes)) != MOE_OK) return st;
+  if ((st = check_apart(fn, {matrix_at(out, T, I, ld_out, 2), vector_at(preact, T * 2ll * I, 2)},
+                        {matrix_at(x, T, K, ld_x, 2), matrix_at(w, 2ll * I, K, ld_w, 2),
+                         vector_at(bias, 2ll * I, size_of(bias_dt))})) != MOE_OK)
+    return st;
   LinearEpi e{};
   e.bias = bias;
   e.out = out;
@@ -734,13 +791,14 @@ moe_status moe_gated_linear_backward(const void* grad_h, int64_t ld_gh, const vo
   }
   if (!grad_h || !preact || (dx && !w) || (dw && !x))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if ((dx && (dx == grad_h || dx == x || dx == w || dx == preact || dx == dw)) ||
-      (dw && (dw == grad_h || dw == x || dw == w || dw == preact)))
-    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
   if (!all16(grad_h, x, w, preact, dx, dw, dbias))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
   const LinearWs L = linear_ws(T, N);
   if ((st = check_ws(fn, ws, ws_bytes, L.total)) != MOE_OK) return st;
+  if ((st = check_apart(fn, {vector_at(dx, int64_t{T} * K, 2), vector_at(dw, int64_t{N} * K, 2), vector_at(dbias, N, 4)},
+                        {matrix_at(grad_h, T, I, ld_gh, 2), matrix_at(x, T, K, ld_x, 2),
+                         matrix_at(w, N, K, ld_w, 2), matrix_at(preact, T, N, ld_z, 2)})) != MOE_OK)
+    return st;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   const bool products = dx || dw;
   if (!products && !dbias) return MOE_OK;
@@ -777,6 +835,10 @@ moe_status moe_quantize_fp8_rows(const void* x, int64_t ld_x, int T, int K, moe_
   if (!x || !q || !scale) return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (!all16(x, q) || !scale_aligned(scale, scale_fmt))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: x and q must be 16-byte aligned, scales as their type", fn);
+  if ((st = check_apart(fn, {vector_at(q, int64_t{T} * K, 1),
+                             scales_at(scale, T, K / 128, s_row, s_kb, scale_fmt == MOE_SCALE_F32 ? 4 : 1)},
+                        {matrix_at(x, T, K, ld_x, 2)})) != MOE_OK)
+    return st;
   const cudaError_t e = launch_fp8_rows({static_cast<const __nv_bfloat16*>(x), static_cast<uint8_t*>(q),
                                          scale, ld_x, s_row, s_kb, T, K / 128,
                                          scale_fmt == MOE_SCALE_UE8M0},
@@ -809,13 +871,19 @@ moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int6
   if (!x || !w || !w_scale || !out) return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (residual == out && ld_res != ld_out)
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: in place only with the same row stride", fn);
-  if (out == x || out == w)
-    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
   if (!all16(x, w, bias, residual, out) || !scale_aligned(x_scale, scale_fmt) ||
       !scale_aligned(w_scale, scale_fmt))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned, scales as their type", fn);
   const Fp8Ws L = fp8_ws(T, K);
   if ((st = check_ws(fn, ws, ws_bytes, x_scale ? kLinearWsBytes : L.total)) != MOE_OK) return st;
+  const int scale_size = scale_fmt == MOE_SCALE_F32 ? 4 : 1;
+  if ((st = check_apart(fn, {matrix_at(out, T, N, ld_out, size_of(out_dt))},
+                        {matrix_at(x, T, K, ld_x, x_scale ? 1 : 2), matrix_at(w, N, K, ld_w, 1),
+                         scales_at(x_scale, T, K / 128, s_row, s_kb, scale_size),
+                         vector_at(w_scale, (N + 127ll) / 128 * (K / 128), scale_size),
+                         vector_at(bias, N, size_of(bias_dt)),
+                         matrix_at(residual == out ? nullptr : residual, T, N, ld_res, size_of(out_dt))})) != MOE_OK)
+    return st;
   uint8_t* const wsb = static_cast<uint8_t*>(ws);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   LinearEpi e{};
@@ -902,10 +970,15 @@ moe_status moe_layer_norm(const void* residual, moe_dtype res_dt, int64_t ld_res
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (residual_out == residual && y && ld_res != H)
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: in place only where the row stride is H", fn);
-  if (normed == residual || (y && (normed == residual_out || normed == y || residual_out == y)))
-    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
   if (!all16(residual, y, weight, bias, residual_out, normed))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
+  // in place: the same rows as residual's, which then are a result and no operand
+  const Region res = matrix_at(residual, T, H, ld_res, size_of(res_dt));
+  const moe_status st = check_apart(
+      fn, {vector_at(y ? residual_out : nullptr, int64_t{T} * H, size_of(res_dt)), vector_at(normed, int64_t{T} * H, 2)},
+      {y && residual_out == residual ? Region{} : res, matrix_at(y, T, H, ld_y, 2),
+       vector_at(weight, H, size_of(weight_dt)), vector_at(bias, H, size_of(weight_dt))});
+  if (st != MOE_OK) return st;
   LayerNormArgs a;
   a.residual = residual;
   a.y = y;
@@ -954,13 +1027,19 @@ moe_status moe_layer_norm_backward(const void* grad_residual, int64_t ld_gres, c
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (d_residual == grad_residual && ld_gres != H)
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: in place only where the row stride is H", fn);
-  if (d_residual == residual || d_residual == grad_normed || d_residual == d_y ||
-      (d_y && (d_y == residual || d_y == grad_normed || d_y == grad_residual)))
-    return set_last_error(MOE_ERR_INVALID_ARG, "%s: results need buffers of their own", fn);
   moe_status st = check_ws(fn, ws, ws_bytes, moe_layer_norm_backward_workspace_size(H));
   if (st != MOE_OK) return st;
   if (!all16(grad_residual, grad_normed, residual, weight, d_residual, d_y, d_weight, d_bias))
     return set_last_error(MOE_ERR_INVALID_ARG, "%s: buffers must be 16-byte aligned", fn);
+  // in place: as the forward pass; d_weight and d_bias are written after the last read of an operand
+  const int64_t n = int64_t{T} * H;
+  const int rs = size_of(res_dt);
+  st = check_apart(fn, {vector_at(d_residual, n, rs), vector_at(d_y, n, 2)},
+                   {d_residual == grad_residual ? Region{} : matrix_at(grad_residual, T, H, ld_gres, rs),
+                    matrix_at(grad_normed, T, H, ld_gn, 2), matrix_at(residual, T, H, ld_res, rs),
+                    vector_at(weight, H, size_of(weight_dt)), vector_at(d_weight, H, 4), vector_at(d_bias, H, 4)});
+  if (st == MOE_OK) st = check_apart(fn, {vector_at(d_weight, H, 4), vector_at(d_bias, H, 4)}, {});
+  if (st != MOE_OK) return st;
   LayerNormBwdArgs a;
   a.grad_res = grad_residual;
   a.grad_normed = grad_normed;

@@ -32,3 +32,39 @@ def test_linear_fp8_pairs_again_and_again(moe, fmt):
     for _ in range(40):
         assert torch.equal(moe.linear_fp8(q, w, ws, x_scale=s, out_dtype=torch.float32), y)
     moe.workspace_status(moe.default_workspace())
+
+
+# ------------------------------------------------------------------ columns of one matrix
+def test_columns_side_by_side_share_nothing(moe):
+    """Results among the columns of the matrix that their operands are columns of."""
+    T, K, I, N = 300, 256, 40, 72
+    g = _rng(T, K, I, N)
+    x, w = _rows8(g, T, K), torch.from_numpy(g.normal(size=(2 * I, K)) / 16).bfloat16().cuda()
+    big = torch.zeros(T, K + I + N + 32, dtype=torch.bfloat16, device="cuda")
+    big[:, :K] = x
+    a, b, c = big[:, :K], big[:, K:K + I], big[:, K + I:K + I + N]
+    moe.gated_linear(a, w, out=b)
+    assert torch.equal(b, moe.gated_linear(x, w)) and torch.equal(a, x)
+    w8, ws, _, _ = _weights8(g, N, K, "f32")
+    moe.linear_fp8(a, w8, ws, out=c)
+    y = moe.linear_fp8(x, w8, ws)
+    assert torch.equal(c, y)
+    moe.linear_fp8(a, w8, ws, residual=c, out=c)
+    assert torch.equal(c, moe.linear_fp8(x, w8, ws, residual=y)) and torch.equal(a, x)
+    assert (big[:, K + I + N:] == 0).all()
+    # every other row of a matrix, and rows in front of and behind others
+    rows = torch.zeros(2 * T, N, dtype=torch.bfloat16, device="cuda")
+    rows[1::2] = y
+    moe.linear_fp8(x, w8, ws, residual=rows[1::2], out=rows[::2])
+    assert torch.equal(rows[::2], c) and torch.equal(rows[1::2], y)
+    two = torch.zeros(2 * T, K, dtype=torch.bfloat16, device="cuda")
+    two[:T] = x
+    r, n = moe.layer_norm(two[:T], x, out=(None, two[T:]))
+    assert torch.equal(two[:T], x) and torch.equal(n, moe.layer_norm(x, x)[1]) and n.data_ptr() == two[T:].data_ptr()
+    for bad in (lambda: moe.linear_fp8(a, w8, ws, out=big[:, K - 8:K - 8 + N]), lambda: moe.gated_linear(a, w, out=big[:, K - 8:K - 8 + I]),
+                lambda: moe.layer_norm(two[:T], x, out=(None, two[T - 1:-1])), lambda: moe.layer_norm(two[8:T + 8], x, out=(two[:T], None)),
+                lambda: moe.quantize_fp8_rows(x, out=(x.view(torch.uint8).view(-1)[:T * K].view(T, K), torch.zeros(T, 2, device="cuda"))),
+                lambda: moe.linear_fp8(x, w8, ws, residual=rows[1:T + 1], out=rows[:T])):
+        with pytest.raises(moe.MoEError):
+            bad()
+    assert torch.equal(a, x) and torch.equal(two[:T], x)
