@@ -704,7 +704,7 @@ def layer_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     only the norm, and residual itself is returned; normed bf16; weight and
     bias [H] or None, both bf16 or both fp32.  out: (residual_out, normed) to
     write into, either of them None for a new tensor; residual_out may be
-    residual."""
+    residual, and without y is None or residual."""
     if stream is not None:
         return _on_stream(layer_norm, locals())
     dev, shape = _matrix_of("residual", residual)
@@ -714,6 +714,8 @@ def layer_norm(residual: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     res, n = (None, None) if out is None else out
     py = ld_y = pres = 0
     if y is None:
+        if res is not None and res.data_ptr() != residual.data_ptr():
+            raise ValueError("a residual_out to write into needs y: without it residual itself is returned")
         res = residual
     else:
         py, ld_y = y.data_ptr(), _mat("y", y, _ONLY_BF16, shape, dev)

@@ -68,3 +68,16 @@ def test_columns_side_by_side_share_nothing(moe):
         with pytest.raises(moe.MoEError):
             bad()
     assert torch.equal(a, x) and torch.equal(two[:T], x)
+
+
+# ------------------------------------------------------------------ layer norm
+def test_layer_norm_without_a_sum_has_no_residual_out(moe):
+    """A buffer that would stay unwritten is refused; residual itself or none are not."""
+    x = torch.randn(5, 64, device="cuda")
+    n = torch.empty(5, 64, dtype=torch.bfloat16, device="cuda")
+    ref = moe.layer_norm(x)[1]
+    for buf in (None, x, x[:]):
+        r, got = moe.layer_norm(x, out=(buf, n))
+        assert r is x and got is n and torch.equal(n, ref)
+    with pytest.raises(ValueError):
+        moe.layer_norm(x, out=(torch.empty_like(x), n))
