@@ -947,7 +947,7 @@ moe_status moe_linear_fp8(const void* x, int64_t ld_x, const void* x_scale, int6
   p.group = 0;
   p.parts = reinterpret_cast<float*>(wsb + 1024);
   p.err = static_cast<int*>(ws);
-  const int rest = fp8_rest(T, N, path, device_sms());
+  const int rest = fp8_rest(T, N, K, path, device_sms());
   p.epi.M = T - rest;
   const cudaError_t r = launch_fp8_linear(tx, tw, p, path, s);
   if (r != cudaSuccess) return cuda_error(r, fn);

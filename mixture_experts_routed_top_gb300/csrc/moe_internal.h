@@ -500,7 +500,7 @@ struct Fp8LinearDev {
   int* err;
 };
 LinearPath fp8_path(long M, long N, long K, int num_sms);      // kPair or kTile
-int fp8_rest(int T, int N, const LinearPath& path, int num_sms);  // last rows for launch_fp8_stream
+int fp8_rest(int T, int N, int K, const LinearPath& path, int num_sms);  // last rows for launch_fp8_stream
 cudaError_t launch_fp8_linear(const CUtensorMap& tm_x, const CUtensorMap& tm_w,
                               const Fp8LinearDev& p, const LinearPath& path, cudaStream_t s);
 struct Fp8StreamArgs {

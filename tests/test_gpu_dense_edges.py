@@ -34,6 +34,30 @@ def test_linear_fp8_pairs_again_and_again(moe, fmt):
     moe.workspace_status(moe.default_workspace())
 
 
+@pytest.mark.parametrize("T,K,N,launches", [
+    (2051, 2048, 2112, 2), (2064, 2048, 2112, 2), (1040, 2048, 4090, 2),   # the last rows apart from whole tiles
+    (2065, 2048, 2112, 1), (2048, 2048, 2112, 1),                          # none, or too many
+    (1040, 512, 4096, 1), (272, 1024, 18432, 1), (528, 2048, 7168, 1)])    # a second reading of w costs more than the wave
+@pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
+def test_linear_fp8_rows_beyond_whole_tiles(moe, T, K, N, launches, fmt):
+    """Rows that would begin another wave of CTA pairs go to the kernel of few tokens only where
+    that is cheaper, and are right either way."""
+    g = _rng(T, K, N, 12)
+    x = _rows8(g, T, K)
+    w, ws, wc, wsv = _weights8(g, N, K, fmt)
+    q, s = moe.quantize_fp8_rows(x, fmt)
+    r = torch.from_numpy(g.normal(size=(T, N)).astype(np.float32)).cuda()
+    b = torch.from_numpy(g.normal(size=N).astype(np.float32)).cuda()
+    out = r.clone()
+    n0 = moe.launch_count()
+    moe.linear_fp8(q, w, ws, x_scale=s, bias=b, activation="silu", residual=out, out=out)
+    assert moe.launch_count() - n0 == launches
+    at = np.r_[0, 255, T // 256 * 256 - 1:T]          # rows of whole tiles, all beyond them
+    xc, _, xsv = O.quantize_blocks(_np(x)[at].astype(np.float32), 1, 128, fmt)
+    ry, rz, mag = B.linear_fp8(xc, xsv, wc, wsv, _np(b), "silu", _np(r)[at])
+    _close(out[torch.from_numpy(at).cuda()], ry, 1.2 * (mag + np.abs(rz) + np.abs(_np(r)[at])), False, _acc8(K) + 2.0 ** -21)
+
+
 # ------------------------------------------------------------------ columns of one matrix
 def test_columns_side_by_side_share_nothing(moe):
     """Results among the columns of the matrix that their operands are columns of."""
