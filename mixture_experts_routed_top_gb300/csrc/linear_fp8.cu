@@ -939,8 +939,9 @@ cudaError_t launch_stream_tokens(const Fp8StreamArgs& a, int num_sms, cudaStream
   // (at 2048 x 7168, where a warp has two, 7.8 against 6.5; 16 tokens 12.9 against 11.0)
   if (a.epi.M <= 8)
     return a.KB >= 32 ? launch_stream<1, CODES, 4>(a, num_sms, s) : launch_stream<1, CODES, 2>(a, num_sms, s);
-  if (a.epi.M <= 16) return launch_stream<2, CODES, 2>(a, num_sms, s);
-  return launch_stream<4, CODES, 2>(a, num_sms, s);
+  if constexpr (CODES)
+    return a.epi.M <= 16 ? launch_stream<2, CODES, 2>(a, num_sms, s) : launch_stream<4, CODES, 2>(a, num_sms, s);
+  return cudaErrorInvalidValue;  // more bf16 tokens come with their codes made before
 }
 
 }  // namespace
