@@ -648,8 +648,9 @@ moe_status moe_quantize_fp8_rows(const void* x, int64_t ld_x, int T, int K, moe_
 
 /*
  * moe_linear_fp8 - out = residual + act(x w^T + bias) of e4m3 operands with a scale per 1 x
- * 128 of x and per 128 x 128 of w.  The sums of a block of 128 are the tensor core's, scaled
- * and added in fp32.
+ * 128 of x and per 128 x 128 of w.  The sums of a block of 128 are the tensor core's, multiplied
+ * by the fp32 product of both scales and added in fp32.  That product is off by up to 2^-150
+ * where it is below 2^-126, and infinite above fp32's range.
  *   x         device e4m3 bytes [T, K] with x_scale (strides as above, of scale_fmt); or,
  *             where x_scale is NULL, bf16 [T, K], which is quantised as
  *             moe_quantize_fp8_rows does

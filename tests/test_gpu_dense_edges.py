@@ -58,6 +58,45 @@ def test_linear_fp8_rows_beyond_whole_tiles(moe, T, K, N, launches, fmt):
     _close(out[torch.from_numpy(at).cuda()], ry, 1.2 * (mag + np.abs(rz) + np.abs(_np(r)[at])), False, _acc8(K) + 2.0 ** -21)
 
 
+@pytest.mark.parametrize("T,N", [(3, 40), (12, 40), (40, 40), (2050, 1540)])
+@pytest.mark.parametrize("fmt,down", [("f32", 0), ("f32", 20), ("f32", 33), ("ue8m0", 0), ("ue8m0", 20), ("ue8m0", 33)])
+def test_linear_fp8_ends_of_the_range(moe, T, N, fmt, down):
+    """Tokens of the smallest and the largest values against the oracle, with weights of ordinary size
+    and 2^-20 and 2^-33 of it.  The scales' product is made in fp32: where it is below 2^-126 it is off
+    by at most 2^-150, which times the block's sum of codes is far below the smallest result of
+    ordinary tokens; so is a result below 2^-126."""
+    K = 256
+    g = _rng(T, N, 5, down)
+    x = _rows8(g, T, K)
+    w, ws, wc, wsv = _weights8(g, N, K, fmt)
+    ws, wsv = (ws * 2.0 ** -down if fmt == "f32" else ws - down), wsv * 2.0 ** -down
+    x[0], x[2] = 0, 0
+    x[1] = torch.where(torch.arange(K, device="cuda") % 3 == 0, -(2.0 ** -132), 2.0 ** -131)
+    x[2, :4] = torch.tensor([3.3e38, -3.3e38, 1e38, 3.3e38])
+    q, s = moe.quantize_fp8_rows(x, fmt)
+    sx = s.double().cpu().numpy() if fmt == "f32" else np.exp2(s.double().cpu().numpy() - 127)
+    assert (sx[1] == 2.0 ** -126).all() and sx[2, 1] == 1                      # the least scale; a block of zeros
+    largest = _np(x)[2, 0] / 448
+    assert sx[2, 0] == (np.float32(largest) if fmt == "f32" else np.exp2(np.ceil(np.log2(largest))))
+    xc = q.cpu().numpy()
+    assert set(xc[1]) == {0x88, 0x10} and (xc[0] == 0).all()                   # -2^-6 and 2^-5, exactly
+    ry, _, mag = B.linear_fp8(xc, sx, wc, wsv)
+    codes = np.abs(O.moe_oracle.e4m3_decode(xc).astype(np.float64)) @ np.abs(O.moe_oracle.e4m3_decode(wc).astype(np.float64)).T
+    tol = _acc8(K) * mag + 2.0 ** -23 * np.abs(ry) + (codes + 3) * 2.0 ** -150
+    for dt, half in ((torch.float32, 0.0), (torch.bfloat16, 2.0 ** -8)):
+        y = moe.linear_fp8(x, w, ws, out_dtype=dt)
+        assert torch.equal(moe.linear_fp8(q, w, ws, x_scale=s, out_dtype=dt), y)
+        got, lim = _np(y), tol + half * (np.abs(ry) + tol) + (2.0 ** -134 if half else 0)
+        over = np.abs(ry) - lim >= torch.finfo(dt).max                         # infinities, with their sign
+        assert (got[over] == np.sign(ry[over]) * np.inf).all()
+        near = (np.abs(ry) + lim >= torch.finfo(dt).max) & ~over               # either is right
+        ok = ~(over | near)
+        assert (np.abs(got - ry)[ok] <= lim[ok]).all()
+        assert (got[0] == 0).all() and np.isfinite(got[1]).all() and not np.isnan(got).any()
+    # the bound leaves row 1, of some 2^-131 with ordinary weights, its signs and sizes
+    assert down > 0 or (np.abs(ry[1]) > 8 * tol[1]).mean() > 0.8
+
+
 # ------------------------------------------------------------------ columns of one matrix
 def test_columns_side_by_side_share_nothing(moe):
     """Results among the columns of the matrix that their operands are columns of."""
@@ -105,3 +144,24 @@ def test_layer_norm_without_a_sum_has_no_residual_out(moe):
         assert r is x and got is n and torch.equal(n, ref)
     with pytest.raises(ValueError):
         moe.layer_norm(x, out=(torch.empty_like(x), n))
+
+
+# ------------------------------------------------------------------ gated products
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+@pytest.mark.parametrize("T", [1, 40])
+def test_gated_gradient_of_x_far_from_zero(moe, act, T):
+    """dx where each dz has a column of its own: activation and slope go to 0 on the left and to z and 1
+    on the right, as far as bf16 goes.  A rounding of dz and one of dx that finds it exact, or of few dz
+    two parts (2^-17 is left) and a rounding; fp32 arithmetic; where e^-z leaves fp32 81 e^-80."""
+    far = [-3e38, -1e33, -1e20, -1000.0, -88.5, -80.5, -79.0, -20.0, -1.0, 0.0, 0.5, 20.0, 90.0, 1000.0, 1e33]
+    I, K = len(far), 64
+    z = torch.cat([torch.tensor(far), torch.linspace(-2, 2, I)]).bfloat16().cuda().repeat(T, 1).contiguous()
+    x, w = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda"), torch.eye(2 * I, K, dtype=torch.bfloat16, device="cuda")
+    gh = torch.linspace(-1, 1.5, T * I, device="cuda").view(T, I).bfloat16()
+    dx, dw, _ = moe.gated_linear_backward(gh, x, w, z, activation=act)
+    zg, zu = _np(z)[:, :I], _np(z)[:, I:]
+    with np.errstate(over="ignore", invalid="ignore"):
+        terms = np.concatenate([zu * np.nan_to_num(B._slope(zg, act)), B._act(zg, act)], 1)
+    ref = np.concatenate([_np(gh), _np(gh)], 1) * terms
+    assert (np.abs(_np(dx)[:, :2 * I] - ref) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(ref) + 250 * np.exp(-80.0)).all()
+    assert (dx[:, 2 * I:] == 0).all() and (dw == 0).all()
