@@ -655,7 +655,8 @@ moe_status moe_quantize_fp8_rows(const void* x, int64_t ld_x, int T, int K, moe_
  *             where x_scale is NULL, bf16 [T, K], which is quantised as
  *             moe_quantize_fp8_rows does
  *   w         device e4m3 bytes [N, K], rows ld_w apart
- *   w_scale   device [ceil(N / 128), K / 128] of scale_fmt
+ *   w_scale   device [ceil(N / 128), K / 128] of scale_fmt (moe_quantize_fp8_blocks of w, with
+ *             rows of zeros up to a multiple of 128; w is the first N rows of its codes)
  *   bias, act, residual, out   as in moe_linear (out may be residual)
  *   ws        device scratch, 256-byte aligned, at least moe_linear_fp8_workspace_size()
  *             bytes (where x_scale is given moe_linear_workspace_size() do); head as in

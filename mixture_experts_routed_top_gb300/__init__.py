@@ -1026,7 +1026,8 @@ def linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
 
     w e4m3 [N,K] (uint8 or float8_e4m3fn), K a multiple of 128, N any; w_scale
     [ceil(N/128), K/128] of its 128x128 blocks: fp32, or uint8 UE8M0 exponent
-    bytes (quantize_fp8_blocks).  x bf16 [T,K], quantised in 1x128 blocks with
+    bytes.  quantize_fp8_blocks makes both of whole blocks: where N is no multiple of
+    128, of w with rows of zeros up to the next one, whose codes [:N] are w.  x bf16 [T,K], quantised in 1x128 blocks with
     scales of w_scale's format on the way; or e4m3 with x_scale [T,K/128] of
     that format (quantize_fp8_rows), any strides; a row's side by side are
     read best.  bias, activation, residual,
@@ -1071,7 +1072,7 @@ def linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
 # ------------------------------------------------------------------ FP8
 def quantize_fp8_blocks(w: torch.Tensor, scale_fmt: str = "f32", stream=None):
     """bf16 [..., R, C] -> (e4m3 codes uint8 [..., R, C], scales [..., R/128, C/128]
-    as fp32 ('f32') or uint8 exponent bytes ('ue8m0'))."""
+    as fp32 ('f32') or uint8 exponent bytes ('ue8m0')).  R and C multiples of 128."""
     if stream is not None:
         return _on_stream(quantize_fp8_blocks, locals())
     _need_cuda(w)

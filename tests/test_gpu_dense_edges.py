@@ -97,6 +97,25 @@ def test_linear_fp8_ends_of_the_range(moe, T, N, fmt, down):
     assert down > 0 or (np.abs(ry[1]) > 8 * tol[1]).mean() > 0.8
 
 
+@pytest.mark.parametrize("N,K", [(2112, 7168), (1, 128), (300, 384)])
+@pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
+def test_linear_fp8_of_weights_that_end_inside_a_block(moe, N, K, fmt):
+    """Weights of any N from quantize_fp8_blocks as documented: padded with rows of zeros, and the
+    first N rows of the codes; a partial last row by itself is refused."""
+    g = _rng(N, K, 21)
+    x, w = _rows8(g, 9, K), torch.from_numpy(g.normal(size=(N, K)) / K ** 0.5).bfloat16().cuda()
+    codes, ws = moe.quantize_fp8_blocks(torch.nn.functional.pad(w, (0, 0, 0, -N % 128)), fmt)
+    padded = np.zeros((-(-N // 128) * 128, K), np.float32)
+    padded[:N] = _np(w)
+    wc, stored, wsv = O.quantize_blocks(padded, 128, 128, fmt)
+    assert np.array_equal(codes.cpu().numpy(), wc) and np.array_equal(ws.cpu().numpy(), stored)
+    xc, _, xsv = O.quantize_blocks(_np(x).astype(np.float32), 1, 128, fmt)
+    ry, _, mag = B.linear_fp8(xc, xsv, wc[:N], wsv)
+    _close(moe.linear_fp8(x, codes[:N], ws, out_dtype=torch.float32), ry, mag, False, _acc8(K))
+    with pytest.raises(moe.MoEError):
+        moe.quantize_fp8_blocks(w, fmt)
+
+
 # ------------------------------------------------------------------ columns of one matrix
 def test_columns_side_by_side_share_nothing(moe):
     """Results among the columns of the matrix that their operands are columns of."""
