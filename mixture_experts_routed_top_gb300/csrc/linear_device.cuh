@@ -37,7 +37,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16_order(int M, int N, bool a_mn,
 // global timer takes longer than most of these waits.  2e9 cycles are a second
 // at the card's 2 GHz; each try itself blocks for a while.
 constexpr long long kWaitCycles = 2000000000ll, kDrainCycles = 40000000ll;
-enum class WaitScope { kCta, kPair, kPairTmem };
+enum class WaitScope { kCta, kPair, kPairRelaxed };
 template <WaitScope S>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   return S == WaitScope::kCta    ? mbar_try_wait(bar, parity)
@@ -66,10 +66,10 @@ __device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatil
                                           int* err, int code, long long limit = kWaitCycles) {
   return wait_cycles<WaitScope::kPair>(bar, parity, abort, err, code, limit);
 }
-// Where nothing but reads and writes of TMEM is ordered.
-__device__ __forceinline__ bool wait_pair_tmem(uint32_t bar, uint32_t parity, volatile int* abort,
-                                               int* err, int code, long long limit = kWaitCycles) {
-  return wait_cycles<WaitScope::kPairTmem>(bar, parity, abort, err, code, limit);
+// Where nothing but reads and writes of TMEM is ordered, or with fence_acquire_shared_cluster.
+__device__ __forceinline__ bool wait_pair_relaxed(uint32_t bar, uint32_t parity, volatile int* abort,
+                                                  int* err, int code, long long limit = kWaitCycles) {
+  return wait_cycles<WaitScope::kPairRelaxed>(bar, parity, abort, err, code, limit);
 }
 __device__ __forceinline__ bool wait_cta(uint32_t bar, uint32_t parity, volatile int* abort,
                                          int* err, int code, long long limit = kWaitCycles) {

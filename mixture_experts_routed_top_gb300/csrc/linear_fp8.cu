@@ -184,9 +184,10 @@ struct ScaleRow {
 //              registers that the first four warps give up (4 x 56 + 8 x 224 a lane of the
 //              12 x 168 that the block is launched with).
 // Barriers as in the bf16 pair kernel.  Those that the other CTA signals are waited for at
-// cluster scope, with an acquire where the loads' data follow and without one where only TMEM
-// changes hands (with one there too 8192 x 16384 x 7168 752 us, so 746); the slabs', of one CTA,
-// at its own.  Every wait is bounded.
+// cluster scope: without an acquire where only TMEM changes hands, with one of shared memory
+// where the loads' stages do.  An acquire of all memory empties the L1, which holds the scales
+// that the warps 2-3 go on with: 8192 x 7168 x 4096 with UE8M0 scales 242 us, so 203.  The slabs'
+// barriers, of one CTA, are waited for at its own scope.  Every wait is bounded.
 //
 // 8192 x 7168 x 4096 with fp32 scales 207 us (2.33 PFLOP/s).  Bound by the promotion beside
 // the products: without it the same loop takes 138 (3.5 PFLOP/s).  128 multiply-adds a thread and
@@ -330,10 +331,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int mi, ni;
         pair_tile(tile, mt, nt, p.group, &mi, &ni);
         for (int kb = 0; kb < KB; ++kb) {
-          if (!wait_pair(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err, ERR_TIMEOUT_PRODUCER)) {
+          if (!wait_pair_relaxed(smem_u32(&empty[stage]), ph ^ 1u, s_abort, p.err, ERR_TIMEOUT_PRODUCER)) {
             ok = false;
             break;
           }
+          fence_acquire_shared_cluster();
           const uint32_t fb_local = smem_u32(&full[stage]);
           if (rank == 0) mbar_arrive_expect_tx(fb_local, 4u * kOper);
           const uint32_t fb = mapa_shared(fb_local, 0);
@@ -367,10 +369,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t g = 0; g < count; ++g) {
         const uint32_t b = g & 1, eph = ((g >> 1) & 1) ^ 1u;
         const uint32_t fbar = smem_u32(&full[stage]), ebar = smem_u32(&pempty[b]);
-        const bool f = mbar_try_wait_cluster(fbar, ph), e = mbar_try_wait_cluster_relaxed(ebar, eph);  // both on their way
-        const bool ok = (f || wait_pair(fbar, ph, s_abort, p.err, ERR_TIMEOUT_MMA)) &&
-                        (e || wait_pair_tmem(ebar, eph, s_abort, p.err, ERR_TIMEOUT_MMA));
+        const bool f = mbar_try_wait_cluster_relaxed(fbar, ph);  // both on their way
+        const bool e = mbar_try_wait_cluster_relaxed(ebar, eph);
+        const bool ok = (f || wait_pair_relaxed(fbar, ph, s_abort, p.err, ERR_TIMEOUT_MMA)) &&
+                        (e || wait_pair_relaxed(ebar, eph, s_abort, p.err, ERR_TIMEOUT_MMA));
         if (!__all_sync(0xffffffffu, ok)) break;
+        fence_acquire_shared_cluster();
         tc_fence_after();
         const uint64_t ad = d0 + static_cast<uint32_t>(stage * (2 * kOper >> 4)), bd = ad + (kOper >> 4);
         if (elect_one()) {
@@ -442,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t v[2][32];
     // waits for block g's sums and asks for the first 32 of them
     auto begin = [&] {
-      const bool ready = wait_pair_tmem(smem_u32(&pfull[g & 1]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
+      const bool ready = wait_pair_relaxed(smem_u32(&pfull[g & 1]), (g >> 1) & 1, s_abort, p.err, ERR_TIMEOUT_EPILOGUE);
       if (!__all_sync(0xffffffffu, ready)) return false;
       tc_fence_after();
       tmem_ld_32x32b_x32(tl + (g & 1) * 256, v[0]);

@@ -90,6 +90,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster_relaxed(uint32_t bar, uint
   return ok != 0;
 }
 
+// After it: an acquire at cluster scope of shared memory alone.  One of all memory empties the
+// L1 as well.
+__device__ __forceinline__ void fence_acquire_shared_cluster() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+
 // The same with a suspend-time hint: the thread may sleep (not poll) for
 // up to kSuspendHintNs until the phase completes, leaving the issue slots of
 // its SM sub-partition to the other roles.  Measured: faster for the bf16
