@@ -969,17 +969,21 @@ LinearPath fp8_path(long M, long N, long K, int num_sms) {
 
 // How many of the last rows the kernel of few tokens takes: up to 16 beyond whole row tiles,
 // where their tiles would begin another wave of pairs and a second reading of all weights costs
-// less than that wave, whose time grows with K alone, the reading's with N too.  With and
-// without, us, 1 | 16 rows beyond whole tiles:
+// less than that wave, whose time grows with K alone, the reading's with N and the rows too.
+// With and without, us, 1 | 16 rows beyond whole tiles:
 //   K 7168   N 2112 51, 68 | 54, 68   4096 58, 68 | 62, 68   7168 65, 68 | 73, 68
 //            N 18432 95, 70 | 105, 70   36864 171, 128 | 208, 128
-//   K 2048   N 1024 31, 33 | 33, 33   4096 31, 33 | 31, 33   7168 31, 33 | 36, 33
+//   K 4096   N 2112 42, 48 | 42, 48   4096 42, 48 | 49, 48
+//   K 2048   N 1024 32, 36 | 36, 36   4096 31, 33 | 36, 33 (8 rows 33, 33)   7168 31, 33 | 36, 33
 //   K 512    N 2112 23, 21 | 27, 21   4096 25, 21 | 27, 21   (a launch is more than the wave)
 //   K 16384  N 4096 101, 134 | 109, 134   9216 124, 134 | 136, 134   18432 170, 136 | 197, 136
-// So up to 4096 columns and from a contraction of 2048 on, where no size was slower.
+// So up to 4096 columns and from a contraction of 2048 on, from 4096 on for more than 8 rows: no
+// size was slower by more than the timer's step of 1 us.
 int fp8_rest(int T, int N, int K, const LinearPath& path, int num_sms) {
   const int rest = T % 256, pairs = std::max(num_sms / 2, 1);
-  if (path.kind != LinearPath::kPair || rest == 0 || rest > 16 || T < 256 || N > 4096 || K < 2048) return 0;
+  if (path.kind != LinearPath::kPair || T < 256 || N > 4096 || K < 2048 || rest == 0 ||
+      rest > (K < 4096 ? 8 : 16))
+    return 0;
   const long nt = ceil_div(N, 256), tiles = (T / 256 + 1) * nt;
   return (tiles - nt + pairs - 1) / pairs < (tiles + pairs - 1) / pairs ? rest : 0;
 }

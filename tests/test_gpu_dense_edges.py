@@ -35,8 +35,8 @@ def test_linear_fp8_pairs_again_and_again(moe, fmt):
 
 
 @pytest.mark.parametrize("T,K,N,launches", [
-    (2051, 2048, 2112, 2), (2064, 2048, 2112, 2), (1040, 2048, 4090, 2),   # the last rows apart from whole tiles
-    (2065, 2048, 2112, 1), (2048, 2048, 2112, 1),                          # none, or too many
+    (2051, 2048, 2112, 2), (2064, 4096, 2112, 2), (1032, 2048, 4090, 2),   # the last rows apart from whole tiles
+    (2064, 2048, 2112, 1), (2065, 4096, 2112, 1), (2048, 2048, 2112, 1),   # too many, or none
     (1040, 512, 4096, 1), (272, 1024, 18432, 1), (528, 2048, 7168, 1)])    # a second reading of w costs more than the wave
 @pytest.mark.parametrize("fmt", ["f32", "ue8m0"])
 def test_linear_fp8_rows_beyond_whole_tiles(moe, T, K, N, launches, fmt):
