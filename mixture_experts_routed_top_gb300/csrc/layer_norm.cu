@@ -43,8 +43,8 @@ __device__ __forceinline__ void bias8(const void* p, bool bf16, int col, int H, 
 constexpr int ln_blocks(int nv) { return nv == 1 ? 2 : 1; }  // on an SM
 
 // 8192 x 7168 bf16 with the residual sum 77 us (470 MB, 6.1 TB/s, 91 % of a copy), bound by
-// memory; 8 tokens 3.2, three dependent trips (row, two sums).
-
+// memory, with an fp32 stream 132 (705 MB, 5.3 TB/s); 8 tokens 3.2, three dependent trips (row,
+// two sums).  EDGE: 8192 x 7167 bf16 127 us (3.7 TB/s), fp32 143 (4.9 TB/s), bound by issue.
 template <typename RT, int NV, int STAGES, bool EDGE>
 __global__ void __launch_bounds__(kRingThreads, ln_blocks(NV))
     layer_norm_ring_kernel(const LayerNormArgs a) {
@@ -328,9 +328,9 @@ __global__ void __launch_bounds__(kRingThreads, 1)
   }
 }
 
-// Rows above 8192 columns: one per block, held in registers.  For them only: the backward
-// pass' sums and values of a column take more registers than its threads have (0.4 KB of
-// spills a thread).
+// Rows above 8192 columns: one per block, held in registers.  Forward 8192 x 12288 bf16 151 us
+// (805 MB, 5.3 TB/s), 8192 x 16384 191 (5.6 TB/s); single columns where rows are not whole
+// vectors: 8192 x 12287 353 (2.3 TB/s).
 template <typename RT, bool VEC>
 __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs a) {
   pdl_launch_dependents();
@@ -386,6 +386,10 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs a)
   }
 }
 
+// The sums over tokens and the values of a column take more registers than its threads have: 328
+// to 432 bytes of spill stores a thread and 472 to 648 of loads, in the loop over rows, and one row
+// in flight an SM (19 % of the warps).  That is what bounds it, at a quarter of the issue slots:
+// 8192 x 12288 bf16 600 us (1.3 TB/s), 8192 x 16384 630, 8192 x 12287 1807.
 template <typename RT, bool VEC>
 __global__ void __launch_bounds__(512) layer_norm_backward_kernel(const LayerNormBwdArgs a) {
   pdl_launch_dependents();

@@ -189,7 +189,7 @@ struct ScaleRow {
 // that the warps 2-3 go on with: 8192 x 7168 x 4096 with UE8M0 scales 242 us, so 203.  The slabs'
 // barriers, of one CTA, are waited for at its own scope.  Every wait is bounded.
 //
-// 8192 x 7168 x 4096 with fp32 scales 207 us (2.33 PFLOP/s).  Bound by the promotion beside
+// 8192 x 7168 x 4096 with either kind of scales 202 to 207 us (2.35 PFLOP/s).  Bound by the promotion beside
 // the products: without it the same loop takes 138 (3.5 PFLOP/s).  128 multiply-adds a thread and
 // block with two warps a scheduler, the reads of TMEM and the tensor core overlap only in
 // part.  Plain multiply-adds: packed ones issue at half the rate and were 5 % slower here.
@@ -537,8 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // One 128 x 128 tile per cluster of S CTAs; CTA r takes the r-th part of the contraction
 // (at least one K block).  8 promotion
 // warps: thread = row, two halves of 64 columns; the CTAs' sums are joined as the bf16
-// kernel's.  Bound by latency: first stages, the exchange of sums.  128 x 7168 x 2112 13 us, 512
-// tokens 20 (0.77 PFLOP/s).
+// kernel's.  Bound by latency: first stages, the exchange of sums, too few blocks.  Codes given
+// and all caches cold 64 x 7168 x 2112 16 us on 68 blocks (15.7 MB, tensor cores busy 15 %), 512
+// tokens 23 on 136 (19 MB, 19 %).
 constexpr int kTStages = 5;
 constexpr int kTEpiWarps = 8;
 constexpr int kTThreads = 64 + 32 * kTEpiWarps;

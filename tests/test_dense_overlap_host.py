@@ -54,19 +54,17 @@ def test_quantize_fp8_rows(L, kw):
     assert L.moe_quantize_fp8_rows(X, 256, 4, 256, 1, a["q"], a["s"], a["s_row"], a["s_kb"], NUL) == INVALID
 
 
-@pytest.mark.parametrize("codes", [False, True])
-@pytest.mark.parametrize("kw", [
-    dict(out=X), dict(out=at(1, 1008)), dict(out=at(2, 32 * 256 - 16)), dict(out=W), dict(out=B), dict(out=at(8, 16)),
-    dict(out=at(6, 16)), dict(res=at(3, 64), ld_res=32), dict(res=at(3, 16), ld_res=40), dict(res=at(3), ld_res=40),
-    dict(out=at(7))])
+FP8 = [dict(out=X), dict(out=at(1, 1008)), dict(out=at(2, 32 * 256 - 16)), dict(out=W), dict(out=B),
+       dict(out=at(8, 16), s=at(8, 12)), dict(out=at(6, 16)), dict(res=at(3, 64), ld_res=32), dict(res=at(3, 16), ld_res=40),
+       dict(res=at(3), ld_res=40)]
+
+
+@pytest.mark.parametrize("codes,kw", [(c, kw) for c in (False, True) for kw in FP8] + [(True, dict(out=Y))])
 def test_linear_fp8(L, codes, kw):
-    if kw.get("out", NUL).value == at(7).value and not codes:
-        pytest.skip("scales of x come with codes")
-    a = dict(out=OUT, res=R, ld_res=32)
+    a = dict(out=OUT, res=R, ld_res=32, s=S)
     a.update(kw)
     # T 4, K 256, N 32: x 1024 bytes of codes, w 8192, out 256, residual 256, x's scales 32, w's 8 (a row of blocks)
-    s = S if a["out"].value != at(8, 16).value else at(8, 12)
-    assert L.moe_linear_fp8(X, 256, Y if codes else NUL, 2, 1, W, 256, s, 1, B, 1, -1, a["res"], a["ld_res"], 4, 256, 32,
+    assert L.moe_linear_fp8(X, 256, Y if codes else NUL, 2, 1, W, 256, a["s"], 1, B, 1, -1, a["res"], a["ld_res"], 4, 256, 32,
                             a["out"], 0, 32, WS, 1 << 30, NUL) == INVALID
 
 
