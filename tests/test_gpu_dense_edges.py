@@ -58,6 +58,35 @@ def test_linear_fp8_rows_beyond_whole_tiles(moe, T, K, N, launches, fmt):
     _close(out[torch.from_numpy(at).cuda()], ry, 1.2 * (mag + np.abs(rz) + np.abs(_np(r)[at])), False, _acc8(K) + 2.0 ** -21)
 
 
+def test_linear_fp8_rows_apart_in_a_graph_and_beside_it(moe):
+    """Codes, whole tiles and the rows beyond them in one graph, replayed on new contents while another
+    stream makes the same product of its own: each as by itself."""
+    T, K, N = 2051, 2048, 2112
+    g = _rng(T, K, N, 14)
+    w, ws, _, _ = _weights8(g, N, K, "ue8m0")
+    xs = [_rows8(g, T, K) for _ in range(4)]
+    want = [moe.linear_fp8(x, w, ws) for x in xs]
+    x, out = xs[0].clone(), torch.empty_like(want[0])
+    one, two, side = moe.Workspace(), moe.Workspace(), torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        moe.linear_fp8(x, w, ws, out=out, workspace=one)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        moe.linear_fp8(x, w, ws, out=out, workspace=one)
+    other = torch.cuda.Stream()
+    for a, b in zip((0, 1, 2, 3, 1, 0), (3, 2, 1, 0, 3, 2)):
+        x.copy_(xs[a])
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(other):
+            y = [moe.linear_fp8(xs[b], w, ws, workspace=two) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[a]) and all(torch.equal(v, want[b]) for v in y)
+    moe.workspace_status(one)
+    moe.workspace_status(two)
+
+
 @pytest.mark.parametrize("T,N", [(3, 40), (12, 40), (40, 40), (2050, 1540)])
 @pytest.mark.parametrize("fmt,down", [("f32", 0), ("f32", 20), ("f32", 33), ("ue8m0", 0), ("ue8m0", 20), ("ue8m0", 33)])
 def test_linear_fp8_ends_of_the_range(moe, T, N, fmt, down):
